@@ -18,6 +18,7 @@ import dataclasses
 import os
 
 __all__ = ["forward", "step", "step_noalloc", "workspace_size", "NOALLOC_SCRATCH_BYTES", "make_problem", "lib", "GdnError", "Tuning", "tuning",
+           "decode", "group_norm", "group_norm_backward",
            "segment_plan", "profile_enable", "profile_reset", "profile_read",
            "FORWARD", "BACKWARD", "BIDIRECTIONAL", "CHUNK_CAUSAL", "ABI_VERSION", "LIB_PATH"]
 
@@ -124,6 +125,8 @@ def lib():
         L.gdn_step.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.gdn_step_noalloc.restype = i32
         L.gdn_step_noalloc.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        from . import sequence
+        sequence.declare(L)
         if L.gdn_abi_version() != ABI_VERSION:
             raise ImportError(f"libgdn ABI {L.gdn_abi_version()} != binding ABI {ABI_VERSION}")
         _lib = L
@@ -165,7 +168,7 @@ def workspace_size(problem: Problem, direction=BIDIRECTIONAL) -> int:
 
 
 KERNELS = ("seg_map_kernel", "seg_chain_kernel", "seg_out_kernel", "recurrent_kernel", "jac_map_kernel",
-           "jac_out_kernel", "prologue_kernel", "scan_prep_kernel", "scan_kernel")
+           "jac_out_kernel", "prologue_kernel", "scan_prep_kernel", "scan_kernel", "decode_kernel", "norm_kernels", "norm_grad_kernels")
 
 
 def profile_enable(on: bool = True) -> None:
@@ -359,3 +362,14 @@ def step_noalloc(q, k, v, log_gate, beta, state_in=None, state_out=None, *, key_
     _check(lib().gdn_step_noalloc(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(beta),
                                   _ptr(state_in), _ptr(state_out), _ptr(out), ctypes.c_void_p(stream)))
     return out, state_out
+
+
+def __getattr__(name):
+    # the sequence operators' binding needs torch at import; the rest of this module does not
+    if name in _SEQUENCE:
+        from . import sequence
+        return getattr(sequence, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+_SEQUENCE = ("decode", "group_norm", "group_norm_backward")

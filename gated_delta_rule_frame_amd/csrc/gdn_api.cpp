@@ -12,6 +12,10 @@ namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
+namespace gdn {
+
 gdn_status fail(gdn_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -21,6 +25,14 @@ gdn_status fail(gdn_status s, const char* fmt, ...) {
   g_last_error = buf;
   return s;
 }
+
+void clear_error() { g_last_error.clear(); }
+
+}  // namespace gdn
+
+namespace {
+
+using gdn::fail;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

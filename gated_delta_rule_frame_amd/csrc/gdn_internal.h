@@ -71,6 +71,10 @@ int chunked_segment_tokens(const Problem& p, int direction);
 // taken once per device.
 hipError_t noalloc_scratch(void** ptr);
 
+// The calling thread's error text (gdn_api.cpp): sets it and returns `s`; clears it.
+gdn_status fail(gdn_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+void clear_error();
+
 // Kernel timing hooks (gdn_profile.cpp): no-ops unless profiling is enabled.
 void prof_begin(hipStream_t stream, int kernel);
 void prof_end(hipStream_t stream, int kernel);

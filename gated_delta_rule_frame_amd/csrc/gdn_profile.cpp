@@ -106,6 +106,9 @@ const char* gdn_kernel_name(int32_t kernel) {
     case GDN_KERNEL_PROLOGUE: return "prologue_kernel";
     case GDN_KERNEL_SCAN_PREP: return "scan_prep_kernel";
     case GDN_KERNEL_SCAN: return "scan_kernel";
+    case GDN_KERNEL_DECODE: return "decode_kernel";
+    case GDN_KERNEL_NORM: return "norm_kernels";
+    case GDN_KERNEL_NORM_GRAD: return "norm_grad_kernels";
     default: return "";
   }
 }

@@ -1,0 +1,227 @@
+"""Binding of the sequence operators of libgdn (``include/gdn.h``, "Sequences of tokens").
+
+``decode`` wraps ``gdn_decode``; ``group_norm`` and ``group_norm_backward``
+wrap ``gdn_group_norm`` and its gradients.  As in the rest of the package the functions
+check and marshal their arguments and launch the HIP kernels on the current
+stream of the tensors' device; there is no CPU fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import ABI_VERSION, BF16, F32, _check, lib
+
+ACTIVATION = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
+_CODE = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+class SeqProblem(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("heads_k", ctypes.c_int32), ("heads_v", ctypes.c_int32),
+                ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("qkv_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("state_rows", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("sequences", ctypes.c_int32), ("reserved", ctypes.c_int32 * 5)]
+
+
+class NormProblem(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("dtype", ctypes.c_int32), ("batch", ctypes.c_int64),
+                ("spatial", ctypes.c_int32), ("channels", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("center", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32 * 4)]
+
+
+def declare(L):
+    """Argument types of the sequence entry points of a loaded libgdn."""
+    vp, i32 = ctypes.c_void_p, ctypes.c_int32
+    P = ctypes.POINTER(SeqProblem)
+    L.gdn_decode.restype = i32
+    L.gdn_decode.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    N, sz = ctypes.POINTER(NormProblem), ctypes.c_size_t
+    L.gdn_group_norm_workspace_size.restype = i32
+    L.gdn_group_norm_workspace_size.argtypes = [N, i32, ctypes.POINTER(sz)]
+    L.gdn_group_norm.restype = i32
+    L.gdn_group_norm.argtypes = [N, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.gdn_group_norm_backward.restype = i32
+    L.gdn_group_norm_backward.argtypes = [N, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+
+
+def _on(device, call, *args):
+    """Runs a library call with the tensors' device current, on its current stream."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        _check(call(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args, stream))
+
+
+def _rows(name, t, shape, dtype, device):
+    """A packed [tokens, heads, width] input; returns its stride between tokens (0 = dense)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.is_contiguous():
+        return 0
+    s = t.stride()
+    if (shape[2] > 1 and s[2] != 1) or (shape[1] > 1 and s[1] != shape[2]) or s[0] < shape[1] * shape[2]:
+        raise ValueError(f"the heads and widths of {name} must be dense and its rows must not overlap (strides {s})")
+    return s[0]
+
+
+def _dense(name, t, shape, dtype, device):
+    """A contiguous tensor of this shape, type and device."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _problem(q, k, v, log_gate, beta, out_dtype):
+    """Checks the inputs every sequence operator shares; returns (problem, device, tokens, heads_v, d_k, d_v)."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be a tensor on a GPU")
+    if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("q, k must be [tokens,heads_k,d_k] and v [tokens,heads_v,d_v]")
+    if q.dtype not in _CODE or out_dtype not in _CODE:
+        raise TypeError(f"unsupported dtype {q.dtype} or {out_dtype}")
+    device, (n, hk, dk), (hv, dv) = q.device, q.shape, v.shape[1:]
+    p = SeqProblem(ABI_VERSION, hk, hv, dk, dv, _CODE[q.dtype], _CODE[out_dtype], 0, n)
+    p.q_stride = _rows("q", q, q.shape, q.dtype, device)
+    p.k_stride = _rows("k", k, q.shape, q.dtype, device)
+    p.v_stride = _rows("v", v, (n, hv, dv), q.dtype, device)
+    _dense("log_gate", log_gate, (n, hv), torch.float32, device)
+    _dense("beta", beta, (n, hv), torch.float32, device)
+    return p, device, n, hv, dk, dv
+
+
+def _output(out, out_dtype):
+    if out is None:
+        return torch.float32 if out_dtype is None else out_dtype
+    if not isinstance(out, torch.Tensor):
+        raise ValueError("out must be a tensor")
+    if out_dtype is not None and out_dtype != out.dtype:
+        raise TypeError(f"out_dtype {out_dtype} differs from out's dtype {out.dtype}")
+    return out.dtype
+
+
+def decode(q, k, v, log_gate, beta, state, slots=None, *, out_dtype=None, out=None):
+    """One token of the gated delta rule per row, states updated in place (gdn_decode); returns ``out``.
+
+    q, k: [rows,heads_k,d_k]; v: [rows,heads_v,d_v] (fp32 or bf16, one dtype;
+    heads_v a multiple of heads_k); log_gate, beta: [rows,heads_v] fp32;
+    state: [state rows,heads_v,d_k,d_v] fp32.  ``slots`` ([rows] int32) picks
+    each row's state; without it row i uses state row i.  A row whose slot is
+    outside the pool is padding: its state and output rows stay as they were
+    (a fresh output holds nothing there).  Rows of one slot are applied in row
+    order.  The output is fp32 unless ``out_dtype`` or ``out`` says otherwise.
+    """
+    odt = _output(out, out_dtype)
+    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, beta, odt)
+    rows = n
+    if slots is not None:
+        _dense("slots", slots, (n,), torch.int32, device)
+        rows = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 4 else 0
+        p.state_rows = rows
+    _dense("state", state, (rows, hv, dk, dv), torch.float32, device)
+    if out is None:
+        out = torch.empty((n, hv, dv), dtype=odt, device=device)
+    else:
+        _dense("out", out, (n, hv, dv), odt, device)
+    _on(device, lib().gdn_decode, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), beta.data_ptr(),
+        state.data_ptr(), None if slots is None else slots.data_ptr(), out.data_ptr())
+    return out
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _space(size, problem, mode, workspace, device):
+    """(tensor, bytes) of a call's workspace: the caller's, or a fresh one of the needed size."""
+    need = ctypes.c_size_t(0)
+    _check(size(problem, mode, ctypes.byref(need)))
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return workspace, workspace.numel() * workspace.element_size()
+    if need.value == 0:
+        return None, 0
+    return torch.empty(need.value, dtype=torch.uint8, device=device), need.value
+
+
+def _norm_problem(x, groups, weight, bias, gate, activation, center, eps):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous tensor on a GPU")
+    if x.dim() < 2:
+        raise ValueError("x must be [batch, ..., channels]")
+    if x.dtype not in _CODE:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if activation not in ACTIVATION:
+        raise ValueError(f"unknown activation {activation!r}")
+    C = x.shape[-1]
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _dense(name, t, (C,), torch.float32, x.device)
+    if gate is not None:
+        _dense("gate", gate, x.shape, x.dtype, x.device)
+    spatial = 1
+    for n in x.shape[1:-1]:
+        spatial *= n
+    return NormProblem(ABI_VERSION, _CODE[x.dtype], x.shape[0], spatial, C, groups, ACTIVATION[activation], int(bool(center)), eps)
+
+
+def group_norm(x, groups, weight=None, bias=None, gate=None, *, activation="none", center=True, eps=1e-5, out=None,
+               workspace=None):
+    """Group norm with an activation or an activated gate, channels last (gdn_group_norm); returns (out, mean, rstd).
+
+    x: [batch, ..., channels] (fp32 or bf16), statistics over the middle
+    dimensions and the channels of each of ``groups`` groups; weight, bias:
+    [channels] fp32 or None; gate: like x or None.  With u = weight h + bias
+    the output is act(u), or u act(gate) where a gate is given; ``activation``
+    is "none", "silu", "gelu" or "relu".  ``center=False`` normalises by the
+    root mean square; its mean is None.  ``[tokens, heads * d_v]`` with the
+    heads as groups is the norm of each token's heads.  mean and rstd
+    ([batch, groups] fp32) are what ``group_norm_backward`` needs.
+    """
+    p = _norm_problem(x, groups, weight, bias, gate, activation, center, eps)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _dense("out", out, x.shape, x.dtype, x.device)
+    ws, ws_bytes = _space(lib().gdn_group_norm_workspace_size, p, 0, workspace, x.device)
+    stats = (x.shape[0], groups)
+    mean = torch.empty(stats, dtype=torch.float32, device=x.device) if center else None
+    rstd = torch.empty(stats, dtype=torch.float32, device=x.device)
+    _on(x.device, lib().gdn_group_norm, p, x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(gate), out.data_ptr(), _ptr(mean),
+        rstd.data_ptr(), _ptr(ws), ws_bytes)
+    return out, mean, rstd
+
+
+def group_norm_backward(dout, x, groups, mean, rstd, weight=None, bias=None, gate=None, *, activation="none", center=True,
+                        workspace=None):
+    """Gradients of ``group_norm`` (gdn_group_norm_backward); returns (dx, dweight, dbias, dgate).
+
+    dout: like x; mean (None without ``center``) and rstd: what ``group_norm``
+    returned for x; the other arguments as given there.  dweight, dbias and
+    dgate are None where weight, bias or gate are.
+    """
+    p = _norm_problem(x, groups, weight, bias, gate, activation, center, 0.0)
+    _dense("dout", dout, x.shape, x.dtype, x.device)
+    stats = (x.shape[0], groups)
+    if center:
+        _dense("mean", mean, stats, torch.float32, x.device)
+    elif mean is not None:
+        raise ValueError("mean must be None without center")
+    _dense("rstd", rstd, stats, torch.float32, x.device)
+    ws, ws_bytes = _space(lib().gdn_group_norm_workspace_size, p, 1, workspace, x.device)
+    dx = torch.empty_like(x)
+    dw = None if weight is None else torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    dz = None if gate is None else torch.empty_like(gate)
+    _on(x.device, lib().gdn_group_norm_backward, p, dout.data_ptr(), x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(gate),
+        _ptr(mean), rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(dz), _ptr(ws), ws_bytes)
+    return dx, dw, db, dz

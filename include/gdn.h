@@ -296,7 +296,10 @@ enum {
   GDN_KERNEL_PROLOGUE = 6,    /* feature prologue: per-token key and query factors */
   GDN_KERNEL_SCAN_PREP = 7,   /* strip scan: per-sub-chunk inverses, intra-chunk products, gate factors */
   GDN_KERNEL_SCAN = 8,        /* strip scan: sub-chunks in order per state strip; outputs and final state */
-  GDN_KERNEL_COUNT = 9
+  GDN_KERNEL_DECODE = 9,      /* one token per row over a pool of states */
+  GDN_KERNEL_NORM = 10,       /* group norm (all its launches) */
+  GDN_KERNEL_NORM_GRAD = 11,  /* group norm's gradients (all its launches) */
+  GDN_KERNEL_COUNT = 12
 };
 gdn_status gdn_profile_enable(int32_t on);
 gdn_status gdn_profile_reset(void);
@@ -306,6 +309,92 @@ const char* gdn_kernel_name(int32_t kernel);   /* static text; "" if unknown */
 /* Tokens per segment the chunked path would use for (problem, direction), or
  * 0 when the call would take the token-recurrent path.  Host only. */
 gdn_status gdn_plan_segment_tokens(const gdn_problem* problem, int32_t direction, int32_t* tokens_out);
+
+/* ---------------------------------------------------------------------------
+ * Sequences of tokens: the same recurrence (forward direction, key_scale 1)
+ * for serving and training sequence models.  Tensors are packed along the
+ * token axis, without a batch axis:
+ *   q, k        [tokens, heads_k, d_k]   qkv_dtype
+ *   v, out      [tokens, heads_v, d_v]   qkv_dtype, out_dtype
+ *   log_gate    [tokens, heads_v]        fp32, g <= 0 (-inf resets the state)
+ *   beta        [tokens, heads_v]        fp32
+ *   states      [rows, heads_v, d_k, d_v] fp32
+ * Value head h reads key head h / (heads_v / heads_k).  Rows of q, k and v may
+ * be further apart than their width (slices of one fused projection): *_stride
+ * counts elements between tokens, a multiple of 16 bytes, 0 = dense; the heads
+ * and widths inside a row are dense.  All other tensors are dense.  Every
+ * pointer is 16-byte aligned; pointers to tensors without elements may be
+ * NULL.  Streams, errors and validation are as at the top of this file. */
+typedef struct gdn_seq_problem {
+  int32_t abi_version;        /* must equal GDN_ABI_VERSION */
+  int32_t heads_k;            /* key and query heads >= 1 */
+  int32_t heads_v;            /* value heads, a multiple of heads_k */
+  int32_t d_k;                /* multiple of 16, <= 128 */
+  int32_t d_v;                /* multiple of 16, <= 128 */
+  int32_t qkv_dtype;          /* GDN_F32 or GDN_BF16 */
+  int32_t out_dtype;          /* GDN_F32 or GDN_BF16 */
+  int32_t state_rows;         /* rows of the state tensors where `slots` is given, else ignored */
+  int64_t tokens;             /* rows of q, k, v, log_gate, beta and out, >= 0 */
+  int64_t q_stride, k_stride, v_stride;
+  int32_t sequences;          /* packed calls: sequences >= 0; gdn_decode ignores it */
+  int32_t reserved[5];        /* must be zero */
+} gdn_seq_problem;
+
+/* One token for each row of a serving batch, each with a state of its own:
+ * row i applies its token to state[slots[i]] in place (fp32 throughout) and
+ * writes out[i].  slots [tokens] int32, or NULL for row i on state row i (then
+ * state has `tokens` rows).  A row whose slot is outside [0, state_rows) is
+ * padding: neither its output row nor any state is touched.  Rows that name
+ * the same slot are applied one after another, in row order. */
+gdn_status gdn_decode(const gdn_seq_problem* problem,
+                      const void* q, const void* k, const void* v,
+                      const float* log_gate, const float* beta,
+                      float* state, const int32_t* slots, void* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Group norm with an activation or an activated gate, channels last: the norm
+ * of the layer's outputs.  x [batch, spatial, channels] is dense; channels
+ * are split into `groups` of neighbours, and every (batch row, group) has one
+ * mean and one deviation over its spatial * channels / groups values:
+ *   h = (x - mean) rstd,   rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *   u = weight h + bias,   out = act(u), or u act(gate) where a gate is given
+ * With center = 0 the mean is taken as 0 (an RMS norm).  spatial = 1 with the
+ * heads as groups is the norm of each token's heads.  weight and bias
+ * [channels] fp32 or NULL (1 and 0); gate, out and the gradients of x and gate
+ * have x's type and shape; mean and rstd [batch, groups] fp32.  All
+ * statistics and sums are fp32, with no atomics.  RELU has slope 0 at 0; GELU
+ * is u (1 + erf(u / sqrt 2)) / 2. */
+enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU = 2, GDN_ACT_RELU = 3 };
+typedef struct gdn_norm_problem {
+  int32_t abi_version;        /* must equal GDN_ABI_VERSION */
+  int32_t dtype;              /* GDN_F32 or GDN_BF16: x, gate, out and their gradients */
+  int64_t batch;              /* >= 0 */
+  int32_t spatial;            /* >= 1 */
+  int32_t channels;           /* in [1, 2^24], a multiple of groups */
+  int32_t groups;             /* >= 1 */
+  int32_t activation;         /* GDN_ACT_* */
+  int32_t center;             /* 1 or 0 */
+  float eps;                  /* finite, >= 0 */
+  int32_t reserved[4];        /* must be zero */
+} gdn_norm_problem;
+
+/* Device workspace of gdn_group_norm (gradient = 0) or its gradients (1). */
+gdn_status gdn_group_norm_workspace_size(const gdn_norm_problem* problem, int32_t gradient, size_t* bytes_out);
+
+/* out, and rstd and (with center) mean, which the gradients need.  No aliasing. */
+gdn_status gdn_group_norm(const gdn_norm_problem* problem, const void* x, const float* weight, const float* bias,
+                          const void* gate, void* out, float* mean, float* rstd,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of x, weight, bias and gate from that of out.  mean and rstd are
+ * gdn_group_norm's for the same x; weight and bias as there.  dgate is given
+ * exactly when gate is; dweight and dbias [channels] fp32 may be NULL.  No
+ * aliasing. */
+gdn_status gdn_group_norm_backward(const gdn_norm_problem* problem, const void* dout, const void* x,
+                                   const float* weight, const float* bias, const void* gate,
+                                   const float* mean, const float* rstd,
+                                   void* dx, float* dweight, float* dbias, void* dgate,
+                                   void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

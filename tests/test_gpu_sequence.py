@@ -1,0 +1,321 @@
+"""GPU: the sequence operators against float64 references, at the sizes, masks
+and calls where they can go wrong."""
+import pytest
+import torch
+
+from tests import seq_reference as R
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def G():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import gated_delta_rule_frame_amd as G
+    return G
+
+
+def unit(x):
+    return x / x.square().sum(-1, keepdim=True).sqrt()
+
+
+def rows(n, hk, hv, dk, dv, dtype, seed, gate=(0.001, 0.1)):
+    """q, k, v, log_gate, beta on the GPU."""
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    t = [unit(r(n, hk, dk)).to(dtype), unit(r(n, hk, dk)).to(dtype), r(n, hv, dv).to(dtype),
+         -(gate[0] + (gate[1] - gate[0]) * torch.rand(n, hv, generator=g)), torch.sigmoid(r(n, hv))]
+    return [x.cuda() for x in t]
+
+
+# ------------------------------------------------------------------ decode
+
+def decode_reference(q, k, v, g, b, state, slots):
+    """Rows in order; returns (out with None for padding rows, state, bounds of both by magnitude)."""
+    q, k, v, g, b, state = (R.f64(x) for x in (q, k, v, g, b, state))
+    rep = v.shape[1] // q.shape[1]
+    out, mag = [], []
+    state, smag = state.clone(), state.abs()
+    for i, s in enumerate(slots):
+        if not 0 <= s < state.shape[0]:
+            out.append(None)
+            mag.append(None)
+            continue
+        o, S = R.tokens(q[i:i + 1], k[i:i + 1], v[i:i + 1], g[i:i + 1], b[i:i + 1], state[s])
+        kt, qt = k[i].repeat_interleave(rep, 0).abs(), q[i].repeat_interleave(rep, 0).abs()
+        A = smag[s] * torch.exp(g[i])[:, None, None]
+        U = b[i].abs()[:, None] * (v[i].abs() + (kt[:, :, None] * A).sum(1))
+        smag[s] = A + kt[:, :, None] * U[:, None, :]
+        out.append(o[0])
+        mag.append((qt[:, :, None] * smag[s]).sum(1))
+        state[s] = S
+    return out, state, mag, smag
+
+
+@pytest.mark.parametrize("n,hk,hv,dk,dv,dtype,out_dtype", [
+    (1, 1, 1, 16, 16, F32, F32), (1, 20, 20, 112, 112, BF16, BF16), (5, 2, 6, 48, 80, F32, F32), (7, 4, 4, 128, 16, BF16, F32),
+    (3, 1, 4, 16, 128, BF16, BF16), (33, 2, 4, 128, 128, BF16, BF16), (2, 3, 3, 96, 112, F32, BF16)])
+def test_decode(G, n, hk, hv, dk, dv, dtype, out_dtype):
+    x = rows(n, hk, hv, dk, dv, dtype, n)
+    gen = torch.Generator().manual_seed(n)
+    pool = n + 3
+    state = torch.randn(pool, hv, dk, dv, generator=gen).cuda()
+    slots = torch.randperm(pool, generator=gen)[:n]
+    want, after, mag, smag = decode_reference(*x, state, slots.tolist())
+    got = G.decode(*x, state, slots.to(torch.int32).cuda(), out_dtype=out_dtype)
+    assert got.dtype == out_dtype and got.shape == (n, hv, dv)
+    # every value is at most two sums of d_k products and a few roundings (and exp's two steps) away, each half a step of its
+    # magnitude; a bf16 output half a step more
+    eps = (2 * dk + 16) * R.HALF[F32]
+    assert ((R.f64(state) - after).abs() <= eps * smag).all()
+    want, mag = torch.stack(want), torch.stack(mag)
+    tol = eps * mag + (R.HALF[BF16] * want.abs() if out_dtype == BF16 else 0)
+    assert ((R.f64(got) - want).abs() <= 1.01 * tol).all()
+
+
+def test_decode_without_slots_is_row_order_and_strided_inputs_give_the_same(G):
+    n, hk, hv, dk, dv = 6, 2, 4, 64, 32
+    x = rows(n, hk, hv, dk, dv, BF16, 3)
+    state = torch.randn(n, hv, dk, dv, device="cuda")
+    s1, s2, s3 = state.clone(), state.clone(), state.clone()
+    a = G.decode(*x, s1)
+    b = G.decode(*x, s2, torch.arange(n, dtype=torch.int32, device="cuda"))
+    fused = torch.cat([t.reshape(n, -1) for t in x[:3]] + [torch.full((n, 8), float("nan"), dtype=BF16, device="cuda")], 1)
+    q, k, v = (fused[:, i:i + w].view(n, h, d) for i, w, h, d in
+               ((0, hk * dk, hk, dk), (hk * dk, hk * dk, hk, dk), (2 * hk * dk, hv * dv, hv, dv)))
+    assert not q.is_contiguous()
+    c = G.decode(q, k, v, x[3], x[4], s3)
+    assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(s1, s2) and torch.equal(s1, s3)
+
+
+def test_decode_padding_rows_and_repeated_slots(G):
+    """Padding rows leave output and state alone; rows of one slot run in row order, across workgroups' strides."""
+    n, hk, hv, dk, dv, pool = 300, 1, 2, 32, 48, 40
+    x = rows(n, hk, hv, dk, dv, F32, 11)
+    gen = torch.Generator().manual_seed(5)
+    slots = torch.randint(-2, pool + 3, (n,), generator=gen)
+    slots[7], slots[8], slots[299] = 2 ** 31 - 1, -2 ** 31, 4
+    state = torch.randn(pool, hv, dk, dv, generator=gen).cuda()
+    want, after, mag, smag = decode_reference(*x, state, slots.tolist())
+    out = torch.full((n, hv, dv), 7.0, device="cuda")
+    G.decode(*x, state, slots.to(torch.int32).cuda(), out=out)
+    times = 8 + max(slots.tolist().count(s) for s in range(pool))   # tokens applied to one state
+    eps = times * (2 * dk + 16) * R.HALF[F32]
+    assert ((R.f64(state) - after).abs() <= eps * smag).all()
+    for i in range(n):
+        if want[i] is None:
+            assert (out[i] == 7.0).all()
+        else:
+            assert ((R.f64(out[i]) - want[i]).abs() <= eps * mag[i]).all()
+
+
+def test_decode_gates_at_their_ends(G):
+    """A gate of -inf drops the old state; beta 0 writes nothing; a NaN row stays in its own state."""
+    n, d = 4, 32
+    x = rows(n, 1, 1, d, d, F32, 2)
+    x[3][0] = float("-inf")
+    x[4][1] = 0.0
+    x[2][2] = float("nan")
+    state = torch.randn(n, 1, d, d, device="cuda")
+    before = state.clone()
+    out = G.decode(*x, state)
+    want = x[4][0, 0] * x[1][0, 0][:, None] * x[2][0, 0][None, :]
+    assert torch.allclose(state[0, 0], want, rtol=1e-5, atol=1e-6)
+    assert torch.allclose(state[1], before[1] * torch.exp(x[3][1, 0]), rtol=1e-6)
+    assert torch.isnan(out[2]).all() and torch.isfinite(out[[0, 1, 3]]).all() and torch.isfinite(state[3]).all()
+
+
+def test_decode_on_another_stream_and_in_a_graph(G):
+    n, hk, hv, dk, dv = 9, 2, 2, 64, 64
+    x = rows(n, hk, hv, dk, dv, BF16, 4)
+    slots = torch.randperm(n).to(torch.int32).cuda()
+    state = torch.randn(n, hv, dk, dv, device="cuda")
+    eager, captured = state.clone(), state.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        first = G.decode(*x, eager, slots)
+    torch.cuda.current_stream().wait_stream(side)
+    out = torch.empty(n, hv, dv, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        G.decode(*x, captured, slots, out=out)
+    for i in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        want = first if i == 0 else G.decode(*x, eager, slots)
+        assert torch.equal(out, want) and torch.equal(captured, eager)
+
+
+def test_decode_refuses_what_does_not_fit(G):
+    x = rows(4, 2, 4, 32, 32, BF16, 1)
+    state = torch.zeros(4, 4, 32, 32, device="cuda")
+    slots = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for bad in ((x[0], x[1][:, :1].contiguous(), *x[2:]), (x[0].float(), *x[1:]), (*x[:3], x[3].double(), x[4]),
+                (*x[:2], x[2][:, :3].contiguous(), x[3][:, :3].contiguous(), x[4][:, :3].contiguous()),
+                (*x[:4], x[4][:3]), (x[0].half(), x[1].half(), x[2].half(), *x[3:]),
+                (x[0].transpose(1, 2).contiguous().transpose(1, 2), *x[1:]), (x[0].cpu(), *x[1:])):
+        with pytest.raises((ValueError, TypeError, G.GdnError)):
+            G.decode(*bad, state, slots)
+    for bad in (state.double(), state[:, :2].contiguous(), state[:3].contiguous(), state.transpose(2, 3), state[0]):
+        with pytest.raises(ValueError):
+            G.decode(*x, bad)
+    for bad in (slots.long(), slots[:3], slots.cpu()):
+        with pytest.raises(ValueError):
+            G.decode(*x, state, bad)
+    with pytest.raises((ValueError, TypeError)):
+        G.decode(*x, state, slots, out=torch.zeros(4, 4, 32, device="cuda", dtype=torch.float16))
+    with pytest.raises(TypeError):
+        G.decode(*x, state, slots, out=torch.zeros(4, 4, 32, device="cuda"), out_dtype=BF16)
+
+
+# ------------------------------------------------------------------ group norm
+
+def norm_inputs(n, s, c, dtype, gate, affine, seed, offset=0.5):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *sh: torch.randn(*sh, generator=g)  # noqa: E731
+    x = (r(n, s, c) * (0.5 + r(c).abs()) + offset * (1 + r(c).abs())).to(dtype).cuda()
+    return (x, (1 + 0.2 * r(c)).cuda() if affine else None, (0.2 * r(c)).cuda() if affine else None,
+            r(n, s, c).to(dtype).cuda() if gate else None, r(n, s, c).to(dtype).cuda())
+
+
+NORMS = [  # n, s, c, groups, dtype, gate, affine, activation, center
+    (1, 1, 16, 1, F32, False, True, "none", True), (5, 1, 4096, 32, BF16, True, True, "silu", False),
+    (3, 1, 2240, 20, BF16, True, True, "silu", True), (7, 1, 33, 3, F32, False, False, "relu", True),
+    (2, 1, 5120, 1, BF16, False, True, "none", False), (2, 1, 16384, 1, BF16, False, True, "gelu", True),
+    (2, 1, 16392, 1, BF16, True, True, "silu", True), (300, 1, 258, 2, BF16, True, True, "gelu", True),
+    (4, 1, 8, 8, F32, False, True, "none", False), (2, 880, 224, 2, BF16, False, True, "silu", True),
+    (3, 7, 40, 5, F32, True, True, "gelu", True), (1, 1000, 129, 3, BF16, True, True, "relu", False),
+    (40, 2, 64, 4, BF16, False, False, "silu", True), (2, 33, 2240, 20, F32, False, True, "silu", True),
+    (1, 5, 4104, 1, F32, True, False, "silu", False), (1, 4097, 64, 8, BF16, True, True, "silu", True)]
+
+
+@pytest.mark.parametrize("n,s,c,groups,dtype,gate,affine,activation,center", NORMS)
+def test_group_norm_and_its_gradients(G, n, s, c, groups, dtype, gate, affine, activation, center):
+    x, w, b, z, dy = norm_inputs(n, s, c, dtype, gate, affine, n * s + c)
+    b = b if center else None
+    shape = (n, c) if s == 1 else (n, s, c)
+    view = lambda t: None if t is None else t.view(shape)  # noqa: E731
+    out, mean, rstd = G.group_norm(view(x), groups, w, b, view(z), activation=activation, center=center, eps=1e-5)
+    leaves = [None if t is None else R.f64(t).requires_grad_() for t in (x, w, b, z)]
+    ro, rm, rr = R.group_norm(leaves[0], groups, *leaves[1:], activation, center, 1e-5)
+    # fp32 statistics: a value passes through some 20 roundings and sums whose errors grow like the root of their length;
+    # 2e-6 by 2-norm and 3e-5 at any place leave room for the steep part of the activations.  bf16 adds its half step.
+    half = R.HALF[dtype] if dtype == BF16 else 0.0
+
+    def near(got, ref, rounded):
+        e, m = R.far(got, ref)
+        assert e <= 2e-6 + (half if rounded else 0) and m <= 3e-5 + (half if rounded else 0), (e, m)
+
+    assert out.dtype == dtype and out.shape == shape
+    near(out.view(n, s, c), ro, True)
+    near(rstd, rr, False)
+    if center:
+        near(mean, rm, False)
+    else:
+        assert mean is None
+    have = [t for t in leaves if t is not None]
+    ref = dict(zip([i for i, t in enumerate(leaves) if t is not None], torch.autograd.grad(ro, have, R.f64(dy))))
+    got = G.group_norm_backward(view(dy), view(x), groups, mean, rstd, w, b, view(z), activation=activation, center=center)
+    for i, (t, d) in enumerate(zip(leaves, got)):
+        assert (t is None) == (d is None)
+        if t is not None:
+            near(d.view(t.shape), ref[i], i in (0, 3))
+
+
+@pytest.mark.parametrize("s", [1, 50])
+def test_group_norm_far_mean_and_constant_groups(G, s):
+    """A mean of a thousand deviations does not cancel; a constant group has rstd 1 / sqrt(eps) and output bias."""
+    n, c, groups = 4, 64, 4
+    x = norm_inputs(n, s, c, F32, False, False, 3)[0] * 0.1 + 100.0
+    x[1, :, :16] = 3.25
+    w, b = torch.ones(c, device="cuda"), torch.full((c,), 0.5, device="cuda")
+    out, mean, rstd = G.group_norm(x, groups, w, b, eps=1e-5)
+    ro, rm, rr = R.group_norm(R.f64(x), groups, R.f64(w), R.f64(b), None, "none", True, 1e-5)
+    assert R.far(mean, rm)[1] <= 1e-6
+    # the mean's own rounding (half a step of 100, 3.8e-6) enters x - mean, which is about 0.1: relative 4e-5
+    assert R.far(rstd, rr)[1] <= 1e-4 and R.far(out, ro)[1] <= 2e-4
+    assert (out[1, :, :16] == 0.5).all()
+
+
+def test_group_norm_keeps_nan_and_inf_in_their_group(G):
+    for s in (1, 40):
+        x = norm_inputs(3, s, 64, BF16, False, False, 9)[0]
+        x[1, 0, 3], x[2, s - 1, 40] = float("nan"), float("inf")
+        out, mean, rstd = G.group_norm(x, 4, activation="silu")
+        bad = torch.zeros(3, 4, dtype=torch.bool, device="cuda")
+        bad[1, 0] = bad[2, 2] = True
+        got = torch.isfinite(out.float()).view(3, s, 4, 16)
+        assert (got.all(3).all(1) == ~bad).all()
+        assert not got[1, :, 0].any() and not torch.isfinite(out[2, s - 1, 40])
+
+
+def test_group_norm_gradients_against_differences(G):
+    x, w, b, z, dy = norm_inputs(3, 6, 48, F32, True, True, 21)
+    args = dict(activation="silu", center=True)
+    out, mean, rstd = G.group_norm(x, 4, w, b, z, **args)
+    grads = G.group_norm_backward(dy, x, 4, mean, rstd, w, b, z, **args)
+    g = torch.Generator().manual_seed(1)
+    for i, t in enumerate((x, w, b, z)):
+        d = torch.randn(t.shape, generator=g).cuda()
+        h = 2.0 ** -7
+        at = lambda s: [u + s * h * d if j == i else u for j, u in enumerate((x, w, b, z))]  # noqa: E731
+        up, dn = (G.group_norm(a[0], 4, *a[1:], **args)[0] for a in (at(1), at(-1)))
+        slope = ((up.double() - dn.double()) * dy.double()).sum().item() / (2 * h)
+        want = (grads[i].double() * d.double()).sum().item()
+        size = (grads[i].double() ** 2).sum().sqrt().item() * (d.double() ** 2).sum().sqrt().item()
+        # the third difference: h^2 / 6 times slopes of order one; fp32 steps of the outputs over 2 h
+        assert abs(slope - want) <= 2e-3 * size
+
+
+def test_group_norm_streams_graphs_and_two_calls_with_own_workspaces(G):
+    x, w, b, z, dy = norm_inputs(4, 100, 128, BF16, True, True, 2)
+    args = dict(activation="silu")
+    want = G.group_norm(x, 8, w, b, z, **args)
+    wantg = G.group_norm_backward(dy, x, 8, *want[1:], w, b, z, **args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = G.group_norm(x, 8, w, b, z, **args)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = G.group_norm(x, 8, w, b, z, **args)
+        gotg = G.group_norm_backward(dy, x, 8, *got[1:], w, b, z, **args)
+    for _ in range(3):
+        for t in (*got, *gotg):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip((*got, *gotg), (*want, *wantg)))
+        G.group_norm(x, 8, w, b, z, **args)
+
+
+def test_group_norm_refuses_what_does_not_fit(G):
+    x, w, b, z, dy = norm_inputs(2, 3, 32, BF16, True, True, 1)
+    ok = dict(activation="silu")
+    for call in (lambda: G.group_norm(x, 5, w), lambda: G.group_norm(x, 4, w.bfloat16()), lambda: G.group_norm(x, 4, w[:16]),
+                 lambda: G.group_norm(x, 4, gate=z.float()), lambda: G.group_norm(x, 4, gate=z[:1]),
+                 lambda: G.group_norm(x.half(), 4), lambda: G.group_norm(x.transpose(0, 1), 4), lambda: G.group_norm(x[0, 0], 4),
+                 lambda: G.group_norm(x, 4, activation="tanh"), lambda: G.group_norm(x, 4, eps=-1.0),
+                 lambda: G.group_norm(x, 4, out=torch.empty_like(x.float())), lambda: G.group_norm(x, 0),
+                 lambda: G.group_norm(x, 4, workspace=torch.empty(8, device="cuda")),
+                 lambda: G.group_norm_backward(dy, x, 4, None, torch.ones(2, 4, device="cuda"), **ok),
+                 lambda: G.group_norm_backward(dy, x, 4, torch.ones(2, 4, device="cuda"), torch.ones(2, 4, device="cuda"),
+                                               center=False),
+                 lambda: G.group_norm_backward(dy.float(), x, 4, torch.ones(2, 4, device="cuda"),
+                                               torch.ones(2, 4, device="cuda"))):
+        with pytest.raises((ValueError, TypeError, G.GdnError)):
+            call()
+
+
+def test_group_norm_without_rows(G):
+    x = torch.zeros(0, 32, device="cuda")
+    w = torch.ones(32, device="cuda")
+    out, mean, rstd = G.group_norm(x, 4, w, w)
+    assert out.shape == (0, 32) and rstd.shape == (0, 4)
+    dx, dw, db, _ = G.group_norm_backward(x, x, 4, mean, rstd, w, w)
+    assert dx.shape == (0, 32) and (dw == 0).all() and (db == 0).all()

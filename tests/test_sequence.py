@@ -1,0 +1,127 @@
+"""The sequence operators' host layer: argument checks, workspace sizes and
+calls without work, through the C ABI with pointers that are never used (no
+GPU needed), and the binding's refusals."""
+import ctypes
+import os
+import subprocess
+from concurrent.futures import ThreadPoolExecutor
+
+import pytest
+import torch
+
+import gated_delta_rule_frame_amd as G
+from gated_delta_rule_frame_amd import sequence as Q
+
+FAKE = 0x10000
+
+
+def seq(**kw):
+    base = dict(abi_version=G.ABI_VERSION, heads_k=2, heads_v=4, d_k=64, d_v=64, qkv_dtype=G.BF16, out_dtype=G.BF16,
+                state_rows=8, tokens=10, sequences=2)
+    base.update(kw)
+    p = Q.SeqProblem()
+    for n, v in base.items():
+        setattr(p, n, v)
+    return p
+
+
+def message():
+    return G.lib().gdn_last_error_message().decode()
+
+
+BAD_SEQ = [("abi_version", 1), ("heads_k", 0), ("heads_k", 3), ("heads_v", 0), ("heads_v", 70000), ("d_k", 8), ("d_k", 24),
+           ("d_k", 144), ("d_v", 0), ("d_v", 129), ("qkv_dtype", 5), ("out_dtype", -1), ("tokens", -1), ("tokens", 1 << 31),
+           ("q_stride", 127), ("q_stride", 64), ("k_stride", 132), ("v_stride", 255), ("v_stride", -256)]
+
+
+def call_decode(p, q=FAKE, k=FAKE, v=FAKE, g=FAKE, b=FAKE, state=FAKE, slots=FAKE, out=FAKE):
+    return G.lib().gdn_decode(p, q, k, v, g, b, state, slots, out, None)
+
+
+@pytest.mark.parametrize("field,value", BAD_SEQ + [("state_rows", -1)])
+def test_decode_rejects_bad_problems(field, value):
+    assert call_decode(seq(**{field: value})) == G.ERR_INVALID_ARGUMENT
+    assert message()
+
+
+def test_decode_rejects_bad_pointers():
+    assert G.lib().gdn_decode(None, *[FAKE] * 8, None) == G.ERR_INVALID_ARGUMENT
+    for n in ("q", "k", "v", "g", "b", "state", "out"):
+        assert call_decode(seq(), **{n: None}) == G.ERR_INVALID_ARGUMENT
+        assert call_decode(seq(), **{n: FAKE + 4}) == G.ERR_INVALID_ARGUMENT
+    assert call_decode(seq(), slots=FAKE + 8) == G.ERR_INVALID_ARGUMENT
+    p = seq()
+    p.reserved[4] = 1
+    assert call_decode(p) == G.ERR_INVALID_ARGUMENT
+
+
+def test_decode_without_rows_does_nothing():
+    assert G.lib().gdn_decode(seq(tokens=0), *[None] * 8, None) == G.OK
+    assert G.lib().gdn_decode(seq(state_rows=0), *[None] * 5, None, FAKE, None, None) == G.OK
+
+
+def norm(**kw):
+    base = dict(abi_version=G.ABI_VERSION, dtype=G.BF16, batch=3, spatial=5, channels=64, groups=4, activation=1, center=1,
+                eps=1e-5)
+    base.update(kw)
+    p = Q.NormProblem()
+    for n, v in base.items():
+        setattr(p, n, v)
+    return p
+
+
+@pytest.mark.parametrize("field,value", [
+    ("abi_version", 3), ("dtype", 2), ("batch", -1), ("spatial", 0), ("channels", 0), ("channels", 66), ("channels", 1 << 25),
+    ("groups", 0), ("groups", 5), ("activation", 4), ("activation", -1), ("center", 2), ("eps", float("nan")), ("eps", -1e-5),
+    ("batch", 1 << 41)])
+def test_norm_rejects_bad_problems(field, value):
+    n = ctypes.c_size_t()
+    p = norm(**{field: value})
+    assert G.lib().gdn_group_norm_workspace_size(p, 0, ctypes.byref(n)) == G.ERR_INVALID_ARGUMENT
+    assert message()
+    assert G.lib().gdn_group_norm(p, *[FAKE] * 8, 1 << 30, None) == G.ERR_INVALID_ARGUMENT
+    assert G.lib().gdn_group_norm_backward(p, *[FAKE] * 12, 1 << 30, None) == G.ERR_INVALID_ARGUMENT
+
+
+def test_norm_rejects_bad_pointers_and_workspaces():
+    L, n = G.lib(), ctypes.c_size_t()
+    args = dict(x=FAKE, w=FAKE, b=FAKE, z=FAKE, out=FAKE, mean=FAKE, rstd=FAKE)
+
+    def fwd(p=None, ws=FAKE, ws_bytes=1 << 40, **kw):
+        return L.gdn_group_norm(p or norm(), *{**args, **kw}.values(), ws, ws_bytes, None)
+
+    for name in ("x", "out", "rstd", "mean"):
+        assert fwd(**{name: None}) == G.ERR_INVALID_ARGUMENT
+    for name in args:
+        assert fwd(**{name: FAKE + 2}) == G.ERR_INVALID_ARGUMENT
+    assert L.gdn_group_norm_workspace_size(norm(), 0, ctypes.byref(n)) == G.OK and n.value > 0
+    assert fwd(ws_bytes=n.value - 1) == G.ERR_WORKSPACE_TOO_SMALL
+    assert fwd(ws=None) == G.ERR_WORKSPACE_TOO_SMALL
+    assert L.gdn_group_norm_workspace_size(norm(spatial=1), 0, ctypes.byref(n)) == G.OK and n.value == 0
+    back = dict(dout=FAKE, x=FAKE, w=FAKE, b=FAKE, z=FAKE, mean=FAKE, rstd=FAKE, dx=FAKE, dw=FAKE, db=FAKE, dz=FAKE)
+
+    def bwd(ws_bytes=1 << 40, **kw):
+        return L.gdn_group_norm_backward(norm(), *{**back, **kw}.values(), FAKE, ws_bytes, None)
+
+    for name in ("dout", "x", "mean", "rstd", "dx", "z", "dz"):
+        assert bwd(**{name: None}) == G.ERR_INVALID_ARGUMENT
+    for name in back:
+        assert bwd(**{name: FAKE + 8}) == G.ERR_INVALID_ARGUMENT
+    assert L.gdn_group_norm_workspace_size(norm(), 1, ctypes.byref(n)) == G.OK
+    assert bwd(ws_bytes=n.value - 1) == G.ERR_WORKSPACE_TOO_SMALL
+
+
+def test_norm_without_rows_does_nothing():
+    assert G.lib().gdn_group_norm(norm(batch=0), *[None] * 8, 0, None) == G.OK
+    assert G.lib().gdn_group_norm_backward(norm(batch=0), *[None] * 12, 0, None) == G.OK
+
+
+def test_binding_refuses_tensors_off_the_gpu():
+    x = torch.zeros(4, 2, 16)
+    g = torch.zeros(4, 2)
+    with pytest.raises(ValueError):
+        G.decode(x, x, x, g, g, torch.zeros(4, 2, 16, 16))
+    with pytest.raises(ValueError):
+        G.group_norm(x, 2)
+    with pytest.raises(ValueError):
+        G.group_norm_backward(x, x, 2, g, g)
