@@ -18,7 +18,7 @@ import dataclasses
 import os
 
 __all__ = ["forward", "step", "step_noalloc", "workspace_size", "NOALLOC_SCRATCH_BYTES", "make_problem", "lib", "GdnError", "Tuning", "tuning",
-           "decode", "group_norm", "group_norm_backward",
+           "decode", "packed_forward", "packed_backward", "packed_workspace_size", "group_norm", "group_norm_backward",
            "segment_plan", "profile_enable", "profile_reset", "profile_read",
            "FORWARD", "BACKWARD", "BIDIRECTIONAL", "CHUNK_CAUSAL", "ABI_VERSION", "LIB_PATH"]
 
@@ -168,7 +168,8 @@ def workspace_size(problem: Problem, direction=BIDIRECTIONAL) -> int:
 
 
 KERNELS = ("seg_map_kernel", "seg_chain_kernel", "seg_out_kernel", "recurrent_kernel", "jac_map_kernel",
-           "jac_out_kernel", "prologue_kernel", "scan_prep_kernel", "scan_kernel", "decode_kernel", "norm_kernels", "norm_grad_kernels")
+           "jac_out_kernel", "prologue_kernel", "scan_prep_kernel", "scan_kernel", "decode_kernel", "norm_kernels", "norm_grad_kernels",
+           "packed_prep_kernel", "packed_scan_kernel", "packed_scan_grad_kernel", "packed_grads_kernel")
 
 
 def profile_enable(on: bool = True) -> None:
@@ -372,4 +373,4 @@ def __getattr__(name):
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
-_SEQUENCE = ("decode", "group_norm", "group_norm_backward")
+_SEQUENCE = ("decode", "packed_forward", "packed_backward", "packed_workspace_size", "group_norm", "group_norm_backward")

@@ -1,0 +1,157 @@
+// Shared parts of the packed gated delta rule kernels (gdn_packed.hip,
+// gdn_packed_grad.hip): precision and tile layouts (the workspace: gdn_seq.h).
+//
+// Precision.  Matrix products run on the bf16 MFMA with fp32 accumulation.  An
+// operand that is given in bf16 is one term; an fp32 one (states, residuals,
+// triangular inverses, fp32 inputs) is split into three bf16 terms, x = x0 + x1 +
+// x2 exactly to 24 bits, and a product of two split operands sums the six term
+// products i + j <= 2; what is left out is below 2^-24 of the product.  Two terms
+// would leave 4e-6 to 7e-6 relative error in states and gate gradients (a float64
+// emulation of the kernels); three leave 1e-7, that of fp32 arithmetic, without
+// the range limit of fp16 operands.  The bf16 MFMA with six terms still has 2.7
+// times the rate of the fp32 MFMA.
+//
+// Fragments.  Operand convention as in gdn_mfma.h: for a 16 x 32 tile lane l holds
+// row l % 16, columns 8 (l / 16) .. + 8, as one 16-byte vector.  Matrices that a
+// later kernel multiplies are stored fragment by fragment, 64 x 16 bytes each, so
+// that a load is one contiguous KB.
+#pragma once
+
+#include "gdn_common.h"
+#include "gdn_mfma.h"
+#include "gdn_seq.h"
+
+namespace gdn {
+
+// ---------------------------------------------------------------- device
+
+typedef bf16x8_t frag_t;
+
+template <int N>
+struct Frag {
+  frag_t t[N];
+};
+
+__device__ __forceinline__ frag_t as_frag(uint4 v) { return __builtin_bit_cast(frag_t, v); }
+__device__ __forceinline__ uint4 as_bits(frag_t v) { return __builtin_bit_cast(uint4, v); }
+
+__device__ __forceinline__ f32x4 mfma(frag_t a, frag_t b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// c += a b over the term pairs that matter.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4 c) {
+#pragma unroll
+  for (int s = (NA < 3 ? NA : 3) + (NB < 3 ? NB : 3) - 2; s >= 0; --s) {   // smallest terms first
+    if (s > 2) continue;
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) c = mfma(a.t[i], b.t[s - i], c);
+  }
+  return c;
+}
+
+// x as the sum of N bf16 values, largest first.
+template <int N>
+__device__ __forceinline__ void split(float x, bh (&o)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    o[i] = f2bh(x);
+    x -= bh2f(o[i]);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ Frag<N> split8(const float (&x)[8]) {
+  Frag<N> f;
+  float r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r[j] = x[j];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f.t[i][j] = static_cast<__bf16>(r[j]);
+      if (i + 1 < N) r[j] -= static_cast<float>(f.t[i][j]);
+    }
+  return f;
+}
+
+template <int N>
+__device__ __forceinline__ Frag<N> zero_frag() {
+  Frag<N> f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) f.t[i] = as_frag(make_uint4(0, 0, 0, 0));
+  return f;
+}
+
+// Eight consecutive fp32 values as a fragment.
+template <int N>
+__device__ __forceinline__ Frag<N> frag_f32(const float* p) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  return split8<N>(x);
+}
+
+// Eight consecutive input values (bf16 for one term, fp32 for three).
+template <int NT>
+__device__ __forceinline__ Frag<NT> frag_in(const void* p, size_t i) {
+  if constexpr (NT == 1) {
+    Frag<1> f;
+    f.t[0] = as_frag(*reinterpret_cast<const uint4*>(static_cast<const bh*>(p) + i));
+    return f;
+  } else {
+    return frag_f32<3>(static_cast<const float*>(p) + i);
+  }
+}
+
+template <int NT>
+__device__ __forceinline__ float elem_in(const void* p, size_t i) {
+  return load_scalar<NT == 1>(p, i);
+}
+
+template <int N>
+__device__ __forceinline__ Frag<N> load_frag(const uint4* p, int frag, int lane) {
+  Frag<N> f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) f.t[i] = as_frag(p[((size_t)frag * N + i) * 64 + lane]);
+  return f;
+}
+
+template <int N>
+__device__ __forceinline__ void store_frag(uint4* p, int frag, int lane, const Frag<N>& f) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[((size_t)frag * N + i) * 64 + lane] = as_bits(f.t[i]);
+}
+
+// Tokens [start, end) of sequence s.  Bounds that do not fit the packed rows
+// are clamped to them, so no value of cu reads or writes out of range.
+__device__ __forceinline__ void seq_bounds(const int* cu, int s, long long tokens, int* start, int* end) {
+  const int n = (int)tokens;
+  const int a = min(max(cu[s], 0), n);
+  *start = a;
+  *end = min(max(cu[s + 1], a), n);
+}
+
+// The sequence and chunk of a chunk slot; false for a slot without tokens.
+__device__ __forceinline__ bool find_chunk(const int* cu, int sequences, long long tokens, long long slot, int* seq, int* first,
+                                           int* n) {
+  int lo = 0, hi = sequences - 1;
+  const int t = (int)tokens;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (min(max(cu[mid], 0), t) / kC + (long long)mid <= slot) lo = mid;
+    else hi = mid - 1;
+  }
+  int a, b;
+  seq_bounds(cu, lo, tokens, &a, &b);
+  const long long c = slot - (a / kC + (long long)lo);
+  *seq = lo;
+  if (c < 0 || c * kC >= b - a) return false;
+  *first = a + (int)c * kC;
+  *n = min(kC, b - *first);
+  return true;
+}
+
+}  // namespace gdn

@@ -109,6 +109,10 @@ const char* gdn_kernel_name(int32_t kernel) {
     case GDN_KERNEL_DECODE: return "decode_kernel";
     case GDN_KERNEL_NORM: return "norm_kernels";
     case GDN_KERNEL_NORM_GRAD: return "norm_grad_kernels";
+    case GDN_KERNEL_PACKED_PREP: return "packed_prep_kernel";
+    case GDN_KERNEL_PACKED_SCAN: return "packed_scan_kernel";
+    case GDN_KERNEL_PACKED_SCAN_GRAD: return "packed_scan_grad_kernel";
+    case GDN_KERNEL_PACKED_GRADS: return "packed_grads_kernel";
     default: return "";
   }
 }

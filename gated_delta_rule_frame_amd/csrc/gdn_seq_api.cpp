@@ -53,15 +53,31 @@ gdn_status check_seq(const gdn_seq_problem* pr, bool slots, gdn::SeqProblem* out
   return GDN_OK;
 }
 
-// Pointers that must be there and 16-byte aligned; `optional` ones may be NULL.
-gdn_status check_pointers(std::initializer_list<const void*> needed, std::initializer_list<const void*> optional,
-                          const char* names) {
+gdn_status check_packed(const gdn_seq_problem* pr, bool slots, gdn::SeqProblem* out) {
+  const gdn_status s = check_seq(pr, slots, out);
+  if (s != GDN_OK) return s;
+  // one workgroup for 16 columns of each (sequence, value head)
+  if (pr->sequences < 0 || (long long)pr->sequences * pr->heads_v > (1LL << 20))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "sequences must be >= 0 and sequences * heads_v at most 2^20 (got %d, %d heads)",
+                pr->sequences, pr->heads_v);
+  return GDN_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Pointers that must be there; `wide` ones are read 16 bytes at a time.
+gdn_status check_needed(std::initializer_list<const void*> needed, const char* names) {
   for (const void* p : needed)
     if (!p) return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be non-NULL", names);
-  for (const void* p : needed)
+  return GDN_OK;
+}
+
+gdn_status check_aligned(std::initializer_list<const void*> wide, std::initializer_list<const void*> narrow) {
+  for (const void* p : wide)
     if (!aligned16(p)) return fail(GDN_ERR_INVALID_ARGUMENT, "tensor and workspace pointers must be 16-byte aligned");
-  for (const void* p : optional)
-    if (!aligned16(p)) return fail(GDN_ERR_INVALID_ARGUMENT, "tensor and workspace pointers must be 16-byte aligned");
+  for (const void* p : narrow)
+    if (!aligned4(p))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "log_gate, beta, cu_seqlens and slots pointers must be 4-byte aligned");
   return GDN_OK;
 }
 
@@ -120,9 +136,60 @@ gdn_status gdn_decode(const gdn_seq_problem* pr, const void* q, const void* k, c
     gdn_status s = check_seq(pr, slots != nullptr, &p);
     if (s != GDN_OK) return s;
     if (p.tokens == 0 || (slots && p.state_rows == 0)) return finish(hipSuccess);
-    s = check_pointers({q, k, v, log_gate, beta, state, out}, {slots}, "q, k, v, log_gate, beta, state and out");
+    s = check_needed({q, k, v, log_gate, beta, state, out}, "q, k, v, log_gate, beta, state and out");
+    if (s == GDN_OK) s = check_aligned({q, k, v, state, out}, {log_gate, beta, slots});
     if (s != GDN_OK) return s;
     return finish(gdn::decode_launch(p, q, k, v, log_gate, beta, state, slots, out, reinterpret_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return fail(GDN_ERR_HIP, "internal error while enqueueing");
+  }
+}
+
+gdn_status gdn_packed_workspace_size(const gdn_seq_problem* pr, int32_t gradient, size_t* bytes_out) {
+  try {
+    if (!bytes_out) return fail(GDN_ERR_INVALID_ARGUMENT, "bytes_out is NULL");
+    gdn::SeqProblem p;
+    const gdn_status s = check_packed(pr, false, &p);
+    if (s != GDN_OK) return s;
+    *bytes_out = gdn::packed_space(p, gradient != 0, nullptr, nullptr);
+    return finish(hipSuccess);
+  } catch (...) {
+    return fail(GDN_ERR_INVALID_ARGUMENT, "internal error while sizing the workspace");
+  }
+}
+
+gdn_status gdn_packed_forward(const gdn_seq_problem* pr, const void* q, const void* k, const void* v, const float* log_gate,
+                              const float* beta, const int32_t* cu_seqlens, const int32_t* slots, const float* initial_state,
+                              void* out, float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
+  try {
+    gdn::SeqProblem p;
+    gdn_status s = check_packed(pr, slots != nullptr, &p);
+    if (s != GDN_OK) return s;
+    if (p.sequences == 0) return finish(hipSuccess);
+    s = check_needed({cu_seqlens}, "cu_seqlens");
+    if (s == GDN_OK && p.tokens > 0) s = check_needed({q, k, v, log_gate, beta, out}, "q, k, v, log_gate, beta and out");
+    if (s == GDN_OK)
+      s = check_aligned({q, k, v, initial_state, out, final_state, workspace}, {log_gate, beta, cu_seqlens, slots});
+    if (s != GDN_OK) return s;
+    s = check_workspace(gdn::packed_space(p, false, nullptr, nullptr), workspace, workspace_bytes);
+    if (s != GDN_OK) return s;
+    gdn::PackedTensors t = {};
+    t.q = q;
+    t.k = k;
+    t.v = v;
+    t.g = log_gate;
+    t.beta = beta;
+    t.cu = cu_seqlens;
+    t.slots = slots;
+    t.h0 = initial_state;
+    t.out = out;
+    t.hT = final_state;
+    gdn::PackedSpace ws;
+    gdn::packed_space(p, false, workspace, &ws);
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e = gdn::packed_prep(p, t, ws, false, st);
+    if (e == hipSuccess) e = gdn::packed_scan(p, t, ws, false, st);
+    return finish(e);
   } catch (...) {
     return fail(GDN_ERR_HIP, "internal error while enqueueing");
   }
@@ -148,7 +215,8 @@ gdn_status gdn_group_norm(const gdn_norm_problem* pr, const void* x, const float
     gdn_status s = check_norm(pr, &p);
     if (s != GDN_OK) return s;
     if (p.N == 0) return finish(hipSuccess);
-    s = check_pointers({x, out, rstd}, {weight, bias, gate, mean, workspace}, "x, out and rstd");
+    s = check_needed({x, out, rstd}, "x, out and rstd");
+    if (s == GDN_OK) s = check_aligned({x, out, rstd, weight, bias, gate, mean, workspace}, {});
     if (s != GDN_OK) return s;
     if (p.center && !mean) return fail(GDN_ERR_INVALID_ARGUMENT, "mean must be non-NULL with center = 1");
     s = check_workspace(gdn::norm_workspace(p, false), workspace, workspace_bytes);
@@ -168,13 +236,14 @@ gdn_status gdn_group_norm_backward(const gdn_norm_problem* pr, const void* dout,
     gdn_status s = check_norm(pr, &p);
     if (s != GDN_OK) return s;
     if (p.N > 0) {
-      s = check_pointers({dout, x, rstd, dx}, {weight, bias, gate, mean, dweight, dbias, dgate, workspace},
-                         "dout, x, rstd and dx");
+      s = check_needed({dout, x, rstd, dx}, "dout, x, rstd and dx");
+      if (s == GDN_OK)
+        s = check_aligned({dout, x, rstd, dx, weight, bias, gate, mean, dweight, dbias, dgate, workspace}, {});
       if (s != GDN_OK) return s;
       if (p.center && !mean) return fail(GDN_ERR_INVALID_ARGUMENT, "mean must be non-NULL with center = 1");
       if (!gate != !dgate) return fail(GDN_ERR_INVALID_ARGUMENT, "gate and dgate must be given together");
     } else {
-      s = check_pointers({}, {dweight, dbias}, "");
+      s = check_aligned({dweight, dbias}, {});
       if (s != GDN_OK) return s;
       if (!dweight && !dbias) return finish(hipSuccess);
     }

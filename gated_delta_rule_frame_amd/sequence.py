@@ -1,6 +1,7 @@
 """Binding of the sequence operators of libgdn (``include/gdn.h``, "Sequences of tokens").
 
-``decode`` wraps ``gdn_decode``; ``group_norm`` and ``group_norm_backward``
+``decode`` wraps ``gdn_decode``, ``packed_forward`` wraps
+``gdn_packed_forward``; ``group_norm`` and ``group_norm_backward``
 wrap ``gdn_group_norm`` and its gradients.  As in the rest of the package the functions
 check and marshal their arguments and launch the HIP kernels on the current
 stream of the tensors' device; there is no CPU fallback.
@@ -38,6 +39,10 @@ def declare(L):
     P = ctypes.POINTER(SeqProblem)
     L.gdn_decode.restype = i32
     L.gdn_decode.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.gdn_packed_workspace_size.restype = i32
+    L.gdn_packed_workspace_size.argtypes = [P, i32, ctypes.POINTER(ctypes.c_size_t)]
+    L.gdn_packed_forward.restype = i32
+    L.gdn_packed_forward.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     N, sz = ctypes.POINTER(NormProblem), ctypes.c_size_t
     L.gdn_group_norm_workspace_size.restype = i32
     L.gdn_group_norm_workspace_size.argtypes = [N, i32, ctypes.POINTER(sz)]
@@ -134,6 +139,64 @@ def decode(q, k, v, log_gate, beta, state, slots=None, *, out_dtype=None, out=No
     _on(device, lib().gdn_decode, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), beta.data_ptr(),
         state.data_ptr(), None if slots is None else slots.data_ptr(), out.data_ptr())
     return out
+
+
+def packed_forward(q, k, v, log_gate, beta, cu_seqlens, initial_state=None, *, slots=None, out_dtype=None, out=None,
+                   final_state=None, want_state=True, workspace=None):
+    """The gated delta rule over packed sequences (gdn_packed_forward); returns (out, final_state).
+
+    q, k: [tokens,heads_k,d_k]; v: [tokens,heads_v,d_v] (fp32 or bf16, one
+    dtype; heads_v a multiple of heads_k); log_gate, beta: [tokens,heads_v]
+    fp32.  ``cu_seqlens`` ([sequences + 1] int32 on the GPU, not decreasing):
+    sequence s is rows cu_seqlens[s] to cu_seqlens[s + 1]; output rows behind
+    the last one stay as they were (a fresh output holds nothing there).
+    initial_state, final_state: [sequences,heads_v,d_k,d_v] fp32, or with
+    ``slots`` ([sequences] int32) pools of which each sequence uses one row; the
+    final state of a call with ``slots`` goes into ``final_state``, by default
+    into initial_state, in place.  The output is fp32 unless ``out_dtype`` or
+    ``out`` says otherwise.
+    """
+    odt = _output(out, out_dtype)
+    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, beta, odt)
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be a tensor of sequences + 1 values")
+    _dense("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
+    seqs = p.sequences = cu_seqlens.shape[0] - 1
+    states = seqs
+    if slots is not None:
+        _dense("slots", slots, (seqs,), torch.int32, device)
+        if final_state is None:
+            if initial_state is None:
+                raise ValueError("a call with slots needs initial_state or final_state, the pool")
+            if want_state:
+                final_state = initial_state
+        pool = initial_state if final_state is None else final_state
+        states = p.state_rows = pool.shape[0] if isinstance(pool, torch.Tensor) and pool.dim() == 4 else 0
+    shape = (states, hv, dk, dv)
+    if initial_state is not None:
+        _dense("initial_state", initial_state, shape, torch.float32, device)
+    if final_state is not None:
+        _dense("final_state", final_state, shape, torch.float32, device)
+    elif want_state and slots is None:
+        final_state = torch.empty(shape, dtype=torch.float32, device=device)
+    if out is None:
+        out = torch.empty((n, hv, dv), dtype=odt, device=device)
+    else:
+        _dense("out", out, (n, hv, dv), odt, device)
+    L = lib()
+    ws, ws_bytes = _space(L.gdn_packed_workspace_size, p, 0, workspace, device)
+    _on(device, L.gdn_packed_forward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), beta.data_ptr(),
+        cu_seqlens.data_ptr(), _ptr(slots), _ptr(initial_state), out.data_ptr(), _ptr(final_state), _ptr(ws), ws_bytes)
+    return out, final_state
+
+
+def packed_workspace_size(q, v, sequences, *, gradient=False):
+    """Bytes of workspace of ``packed_forward`` (or ``packed_backward``) for inputs like q and v."""
+    p = SeqProblem(ABI_VERSION, q.shape[1], v.shape[1], q.shape[2], v.shape[2], _CODE[q.dtype], F32, 0, q.shape[0])
+    p.sequences = sequences
+    need = ctypes.c_size_t(0)
+    _check(lib().gdn_packed_workspace_size(p, int(gradient), ctypes.byref(need)))
+    return need.value
 
 
 def _ptr(t):

@@ -299,7 +299,11 @@ enum {
   GDN_KERNEL_DECODE = 9,      /* one token per row over a pool of states */
   GDN_KERNEL_NORM = 10,       /* group norm (all its launches) */
   GDN_KERNEL_NORM_GRAD = 11,  /* group norm's gradients (all its launches) */
-  GDN_KERNEL_COUNT = 12
+  GDN_KERNEL_PACKED_PREP = 12,      /* packed sequences: per-chunk inverses, gated products, gate factors */
+  GDN_KERNEL_PACKED_SCAN = 13,      /* packed sequences: chunks in order; outputs and final states */
+  GDN_KERNEL_PACKED_SCAN_GRAD = 14, /* packed gradients: chunks in reverse order */
+  GDN_KERNEL_PACKED_GRADS = 15,     /* packed gradients: every chunk's gradients of its inputs */
+  GDN_KERNEL_COUNT = 16
 };
 gdn_status gdn_profile_enable(int32_t on);
 gdn_status gdn_profile_reset(void);
@@ -322,9 +326,9 @@ gdn_status gdn_plan_segment_tokens(const gdn_problem* problem, int32_t direction
  * Value head h reads key head h / (heads_v / heads_k).  Rows of q, k and v may
  * be further apart than their width (slices of one fused projection): *_stride
  * counts elements between tokens, a multiple of 16 bytes, 0 = dense; the heads
- * and widths inside a row are dense.  All other tensors are dense.  Every
- * pointer is 16-byte aligned; pointers to tensors without elements may be
- * NULL.  Streams, errors and validation are as at the top of this file. */
+ * and widths inside a row are dense.  All other tensors are dense.
+ * Pointers are 16-byte aligned, those of log_gate, beta, cu_seqlens and slots
+ * 4-byte; pointers to tensors without elements may be NULL.  Streams, errors and validation are as at the top of this file. */
 typedef struct gdn_seq_problem {
   int32_t abi_version;        /* must equal GDN_ABI_VERSION */
   int32_t heads_k;            /* key and query heads >= 1 */
@@ -350,6 +354,38 @@ gdn_status gdn_decode(const gdn_seq_problem* problem,
                       const void* q, const void* k, const void* v,
                       const float* log_gate, const float* beta,
                       float* state, const int32_t* slots, void* out, void* stream);
+
+/* Sequences of different lengths in one call.  cu_seqlens [sequences + 1]
+ * int32, device memory, not decreasing: sequence s holds the packed rows
+ * [cu_seqlens[s], cu_seqlens[s + 1]) (none is allowed).  Rows behind the last
+ * sequence are neither read nor written.  Values outside [0, tokens] and
+ * decreasing ones are clamped when they are used, so no value reads or writes
+ * out of range; results are then unspecified.  Chunks of 64 tokens on the
+ * matrix cores for every width and both types; the accuracy is that of fp32
+ * arithmetic and the range that of bf16 (no fp16 domain as GDN_ALGO_AUTO's). */
+
+/* Bytes of device workspace of gdn_packed_forward (gradient = 0) or
+ * gdn_packed_backward (1).  Forward: about 50 KB for each 64 tokens and value
+ * head; gradients: about 270 KB at d_k = d_v = 128. */
+gdn_status gdn_packed_workspace_size(const gdn_seq_problem* problem, int32_t gradient, size_t* bytes_out);
+
+/* out and the state after each sequence's last token.
+ *   slots          [sequences] int32 or NULL: the state row of each sequence, in
+ *                  initial_state and final_state, which then have state_rows
+ *                  rows (a pool as gdn_decode's); NULL: sequence s uses row s.
+ *                  A sequence whose slot is outside the pool starts from zero
+ *                  and its final state is dropped.  Sequences that name the
+ *                  same slot run one after another, in order.
+ *   initial_state  or NULL (zeros)
+ *   final_state    or NULL; may be initial_state (in place).  An empty
+ *                  sequence's is its initial state.
+ * No other aliasing.  The workspace is as gdn_forward's. */
+gdn_status gdn_packed_forward(const gdn_seq_problem* problem,
+                              const void* q, const void* k, const void* v,
+                              const float* log_gate, const float* beta,
+                              const int32_t* cu_seqlens, const int32_t* slots,
+                              const float* initial_state, void* out, float* final_state,
+                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Group norm with an activation or an activated gate, channels last: the norm

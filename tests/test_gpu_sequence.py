@@ -319,3 +319,174 @@ def test_group_norm_without_rows(G):
     assert out.shape == (0, 32) and rstd.shape == (0, 4)
     dx, dw, db, _ = G.group_norm_backward(x, x, 4, mean, rstd, w, w)
     assert dx.shape == (0, 32) and (dw == 0).all() and (db == 0).all()
+
+
+# ------------------------------------------------------------------ packed sequences
+
+def near32(got, ref, out_dtype=F32, times=1.0):
+    """fp32 products and sums through a chunk: the largest of them sum 128 products, in matrix steps of 32 (errors grow
+    like the root: some 12 half steps of the sum of magnitudes), five such products follow one another, and a state passes
+    through all chunks, damped by its gates: 64 half steps by 2-norm (4e-6), ten times that at one place.  A bf16 result
+    adds its half step."""
+    half = R.HALF[out_dtype] if out_dtype == BF16 else 0.0
+    e, m = R.far(got, ref)
+    assert e <= 64 * R.HALF[F32] * times + half and m <= 640 * R.HALF[F32] * times + half, (e, m)
+
+
+def cu_of(lengths, device="cuda"):
+    cu = [0]
+    for n in lengths:
+        cu.append(cu[-1] + n)
+    return torch.tensor(cu, dtype=torch.int32, device=device)
+
+
+PACKED = [  # lengths, hk, hv, dk, dv, dtype, gate range, state
+    ([1], 1, 1, 16, 16, BF16, (0.001, 0.1), False), ([64], 2, 2, 64, 64, BF16, (0.001, 0.1), True),
+    ([0, 1, 63, 0, 65, 2, 0], 2, 4, 112, 112, BF16, (0.001, 0.1), True), ([200, 3], 1, 3, 128, 128, BF16, (0.0005, 0.02), True),
+    ([129], 1, 1, 32, 48, F32, (0.001, 0.1), True), ([70, 130], 2, 2, 128, 96, F32, (0.001, 0.1), True),
+    ([257], 1, 2, 80, 16, F32, (0.1, 6.0), False), ([300, 1, 20], 3, 3, 48, 128, BF16, (0.0, 30.0), True),
+    ([1000], 1, 1, 64, 32, F32, (0.0, 0.0005), True)]
+
+
+@pytest.mark.parametrize("lengths,hk,hv,dk,dv,dtype,gate,with_state", PACKED)
+def test_packed_forward(G, lengths, hk, hv, dk, dv, dtype, gate, with_state):
+    n, pad = sum(lengths), 5
+    x = rows(n + pad, hk, hv, dk, dv, dtype, n, gate)
+    for t in x:
+        t[n:] = float("nan")                     # rows behind the last sequence are not read
+    S0 = torch.randn(len(lengths), hv, dk, dv, device="cuda") if with_state else None
+    cu = cu_of(lengths)
+    ro, rS = R.packed(*(R.f64(t) for t in x), cu.tolist(), R.f64(S0))
+    for odt in (F32, BF16):
+        out = torch.full((n + pad, hv, dv), 3.0, device="cuda", dtype=odt)
+        _, S = G.packed_forward(*x, cu, S0, out=out)
+        assert (out[n:] == 3.0).all()
+        near32(out[:n], ro[:n], odt)
+        near32(S, rS)
+
+
+def test_packed_forward_equals_decode_and_the_dense_forward(G):
+    """Token after token through decode, the packed call, and the layer's own forward scan agree."""
+    n, h, d = 150, 2, 64
+    x = rows(n, h, h, d, d, F32, 8)
+    cu = cu_of([n])
+    S0 = torch.randn(1, h, d, d, device="cuda")
+    out, S = G.packed_forward(*x, cu, S0)
+    state, outs = S0.clone(), []
+    for t in range(n):
+        outs.append(G.decode(*(y[t:t + 1] for y in x), state))
+    near32(out, R.f64(torch.cat(outs)))
+    near32(S, R.f64(state))
+    dense, dS = G.forward(*(y.unsqueeze(0) for y in x), S0, "fwd")
+    near32(out, R.f64(dense[0]))
+    near32(S, R.f64(dS))
+
+
+def test_packed_forward_strides_pools_and_repeated_slots(G):
+    lengths, hk, hv, dk, dv, pool = [5, 70, 0, 64, 3, 90, 1], 1, 2, 48, 32, 6
+    n = sum(lengths)
+    x = rows(n, hk, hv, dk, dv, BF16, 6)
+    fused = torch.cat([t.reshape(n, -1) for t in x[:3]], 1)
+    q, k, v = fused[:, :48].view(n, 1, 48), fused[:, 48:96].view(n, 1, 48), fused[:, 96:].view(n, 2, 32)
+    cu = cu_of(lengths)
+    slots = [4, 1, 0, 4, -1, 4, 9]
+    state = torch.randn(pool, hv, dk, dv, device="cuda")
+    before = state.clone()
+    ref = R.f64(state)
+    outs, c = [], cu.tolist()
+    for i, s in enumerate(slots):
+        S = ref[s] if 0 <= s < pool else torch.zeros(hv, dk, dv, dtype=torch.float64)
+        o, S = R.tokens(*(R.f64(t[c[i]:c[i + 1]]) for t in x), S)
+        outs.append(o)
+        if 0 <= s < pool:
+            ref[s] = S
+    st = torch.tensor(slots, dtype=torch.int32, device="cuda")
+    out, final = G.packed_forward(q, k, v, x[3], x[4], cu, state, slots=st)
+    assert final is state
+    near32(out, torch.cat(outs))
+    near32(state, ref)
+    assert torch.equal(state[[0, 2, 3, 5]], before[[0, 2, 3, 5]])
+    other = torch.full_like(state, 2.0)      # from zeros into a pool: the last sequence of a slot stays
+    G.packed_forward(q, k, v, x[3], x[4], cu, None, slots=st, final_state=other)
+    near32(other[4], R.tokens(*(R.f64(t[c[5]:c[6]]) for t in x), torch.zeros(hv, dk, dv, dtype=torch.float64))[1])
+    assert (other[[2, 3, 5]] == 2.0).all() and (other[0] == 0).all()
+
+
+def test_packed_forward_hard_inputs(G):
+    """-inf gates, beta 0, repeated keys and a NaN token: the first two exactly as the recurrence, NaN from its token on."""
+    n, d = 140, 32
+    x = rows(n, 1, 1, d, d, F32, 14)
+    x[3][70], x[3][3] = float("-inf"), float("-inf")
+    x[4][10:20] = 0.0
+    x[1][30:60] = x[1][30]
+    x[4][30:60] = 1.0
+    cu = cu_of([n])
+    ref = R.packed(*(R.f64(t) for t in x), cu.tolist(), None)
+    out, S = G.packed_forward(*x, cu)
+    near32(out, ref[0], times=4)       # thirty equal keys: the inverse's entries reach 1 at every distance
+    near32(S, ref[1])
+    y = [t.clone() for t in x]
+    y[2][100] = float("nan")
+    out2, S2 = G.packed_forward(*y, cu_of([90, 50]))
+    near32(out2[:90], ref[0][:90], times=4)
+    assert torch.isnan(out2[100:]).all() and torch.isnan(S2[1]).all()
+
+
+def test_packed_forward_bad_offsets_stay_in_range(G):
+    x = rows(130, 1, 1, 16, 16, BF16, 1)
+    out = torch.zeros(130, 1, 16, device="cuda")
+    for cu in ([0, 500, 130], [-9, 70, 130], [100, 20, 130], [0, 130, -5], [2 ** 31 - 1, -2 ** 31, 64]):
+        G.packed_forward(*x, torch.tensor(cu, dtype=torch.int32, device="cuda"), out=out)
+    torch.cuda.synchronize()
+    ref = R.packed(*(R.f64(t) for t in x), [0, 64, 130], None)
+    near32(G.packed_forward(*x, cu_of([64, 66]))[0], ref[0])
+
+
+def test_packed_forward_streams_and_graph(G):
+    x = rows(333, 2, 4, 64, 64, BF16, 5)
+    cu = cu_of([100, 133, 100])
+    S0 = torch.randn(3, 4, 64, 64, device="cuda")
+    want, wantS = G.packed_forward(*x, cu, S0)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in sides:                               # two calls at once, each with a workspace of its own
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(G.packed_forward(*x, cu, S0))
+    for s in sides:
+        torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(o, want) and torch.equal(S, wantS) for o, S in got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, S = G.packed_forward(*x, cu, S0)
+    for _ in range(3):
+        out.zero_(), S.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(S, wantS)
+        G.packed_forward(*x, cu, S0)
+
+
+def test_packed_forward_without_tokens_or_sequences(G):
+    x = [t[:0] for t in rows(1, 1, 2, 32, 32, BF16, 1)]
+    S0 = torch.randn(3, 2, 32, 32, device="cuda")
+    out, S = G.packed_forward(*x, cu_of([0, 0, 0]), S0)
+    assert out.shape == (0, 2, 32) and torch.equal(S, S0)
+    assert (G.packed_forward(*x, cu_of([0]))[1] == 0).all()
+    out, S = G.packed_forward(*x, cu_of([]))
+    assert S.shape == (0, 2, 32, 32)
+
+
+def test_packed_forward_refuses_what_does_not_fit(G):
+    x = rows(10, 2, 4, 32, 32, BF16, 1)
+    cu, S0 = cu_of([4, 6]), torch.zeros(2, 4, 32, 32, device="cuda")
+    slots = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for call in (lambda: G.packed_forward(*x, cu.long(), S0), lambda: G.packed_forward(*x, cu.cpu(), S0),
+                 lambda: G.packed_forward(*x, [0, 4, 10], S0), lambda: G.packed_forward(*x, cu[:0], S0),
+                 lambda: G.packed_forward(*x, cu, S0[:1].contiguous()), lambda: G.packed_forward(*x, cu, S0.bfloat16()),
+                 lambda: G.packed_forward(*x, cu, slots=slots), lambda: G.packed_forward(*x, cu, S0, slots=slots[:1]),
+                 lambda: G.packed_forward(*x, cu, S0, slots=slots, final_state=torch.zeros(3, 4, 32, 32, device="cuda")),
+                 lambda: G.packed_forward(*x, cu, S0, workspace=torch.empty(64, device="cuda")),
+                 lambda: G.packed_forward(*(t.half() if i < 3 else t for i, t in enumerate(x)), cu, S0)):
+        with pytest.raises((ValueError, TypeError, G.GdnError)):
+            call()

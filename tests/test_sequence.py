@@ -48,8 +48,10 @@ def test_decode_rejects_bad_pointers():
     assert G.lib().gdn_decode(None, *[FAKE] * 8, None) == G.ERR_INVALID_ARGUMENT
     for n in ("q", "k", "v", "g", "b", "state", "out"):
         assert call_decode(seq(), **{n: None}) == G.ERR_INVALID_ARGUMENT
-        assert call_decode(seq(), **{n: FAKE + 4}) == G.ERR_INVALID_ARGUMENT
-    assert call_decode(seq(), slots=FAKE + 8) == G.ERR_INVALID_ARGUMENT
+        assert call_decode(seq(), **{n: FAKE + 2}) == G.ERR_INVALID_ARGUMENT
+    for n in ("q", "k", "v", "state", "out"):
+        assert call_decode(seq(), **{n: FAKE + 8}) == G.ERR_INVALID_ARGUMENT
+    assert call_decode(seq(), slots=FAKE + 1) == G.ERR_INVALID_ARGUMENT
     p = seq()
     p.reserved[4] = 1
     assert call_decode(p) == G.ERR_INVALID_ARGUMENT
@@ -58,6 +60,35 @@ def test_decode_rejects_bad_pointers():
 def test_decode_without_rows_does_nothing():
     assert G.lib().gdn_decode(seq(tokens=0), *[None] * 8, None) == G.OK
     assert G.lib().gdn_decode(seq(state_rows=0), *[None] * 5, None, FAKE, None, None) == G.OK
+
+
+def call_packed(p, ws=FAKE, ws_bytes=1 << 40, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, g=FAKE, b=FAKE, cu=FAKE, slots=FAKE, h0=FAKE, out=FAKE, hT=FAKE)
+    a.update(kw)
+    return G.lib().gdn_packed_forward(p, *a.values(), ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("field,value", BAD_SEQ + [("state_rows", -1), ("sequences", -1), ("sequences", 1 << 20)])
+def test_packed_rejects_bad_problems(field, value):
+    assert call_packed(seq(**{field: value})) == G.ERR_INVALID_ARGUMENT
+    n = ctypes.c_size_t()
+    assert field == "state_rows" or \
+        G.lib().gdn_packed_workspace_size(seq(**{field: value}), 0, ctypes.byref(n)) == G.ERR_INVALID_ARGUMENT
+
+
+def test_packed_rejects_bad_pointers_and_workspaces():
+    for n in ("q", "k", "v", "g", "b", "cu", "out"):
+        assert call_packed(seq(), **{n: None}) == G.ERR_INVALID_ARGUMENT
+    for n in ("q", "k", "v", "h0", "out", "hT", "ws"):
+        assert call_packed(seq(), **{n: FAKE + 8}) == G.ERR_INVALID_ARGUMENT
+    for n in ("g", "b", "cu", "slots"):
+        assert call_packed(seq(), **{n: FAKE + 2}) == G.ERR_INVALID_ARGUMENT
+    n = ctypes.c_size_t()
+    assert G.lib().gdn_packed_workspace_size(seq(), 0, None) == G.ERR_INVALID_ARGUMENT
+    assert G.lib().gdn_packed_workspace_size(seq(), 0, ctypes.byref(n)) == G.OK and n.value > 0
+    assert call_packed(seq(), ws_bytes=n.value - 1) == G.ERR_WORKSPACE_TOO_SMALL
+    assert call_packed(seq(), ws=None) == G.ERR_WORKSPACE_TOO_SMALL
+    assert call_packed(seq(sequences=0), cu=None) == G.OK
 
 
 def norm(**kw):
