@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libgdn.so")
 BUILD = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
-HIP_SOURCES = ["gdn_recurrent.hip", "gdn_chunked.hip", "gdn_prologue.hip", "gdn_noalloc.hip", "gdn_decode.hip", "gdn_norm.hip", "gdn_packed.hip"]
+HIP_SOURCES = ["gdn_recurrent.hip", "gdn_chunked.hip", "gdn_prologue.hip", "gdn_noalloc.hip", "gdn_decode.hip", "gdn_norm.hip", "gdn_packed.hip", "gdn_packed_grad.hip"]
 HOST_SOURCES = ["gdn_api.cpp", "gdn_profile.cpp", "gdn_seq_api.cpp"]
 
 

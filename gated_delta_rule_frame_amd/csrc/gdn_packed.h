@@ -125,6 +125,36 @@ __device__ __forceinline__ void store_frag(uint4* p, int frag, int lane, const F
   for (int i = 0; i < N; ++i) p[((size_t)frag * N + i) * 64 + lane] = as_bits(f.t[i]);
 }
 
+constexpr int kTok = 72;    // row stride (bf16) of a 16 x 64 operand tile in LDS
+
+// Writes four consecutive rows of a column as N terms: tile[term][column][row].
+template <int N, int LD>
+__device__ __forceinline__ void put(bh* tile, int plane, int column, int row, const float (&x)[4]) {
+  bh b[4][N];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) split<N>(x[r], b[r]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint2 v;
+    v.x = b[0][i] | (uint32_t)b[1][i] << 16;
+    v.y = b[2][i] | (uint32_t)b[3][i] << 16;
+    *reinterpret_cast<uint2*>(tile + i * plane + column * LD + row) = v;
+  }
+}
+
+template <int LD>
+__device__ __forceinline__ void put3(bh* tile, int plane, int column, int row, const float (&x)[4]) {
+  put<3, LD>(tile, plane, column, row, x);
+}
+
+template <int N, int LD>
+__device__ __forceinline__ Frag<N> get(const bh* tile, int plane, int column, int row) {
+  Frag<N> f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) f.t[i] = as_frag(*reinterpret_cast<const uint4*>(tile + i * plane + column * LD + row));
+  return f;
+}
+
 // Tokens [start, end) of sequence s.  Bounds that do not fit the packed rows
 // are clamped to them, so no value of cu reads or writes out of range.
 __device__ __forceinline__ void seq_bounds(const int* cu, int s, long long tokens, int* start, int* end) {

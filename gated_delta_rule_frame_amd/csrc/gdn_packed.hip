@@ -16,7 +16,6 @@ namespace gdn {
 namespace {
 
 constexpr int kLd = 68;     // row stride (floats) of a 64 x 64 fp32 tile in LDS
-constexpr int kTok = 72;    // row stride (bf16) of a 16 x 64 operand tile in LDS
 
 // Gates below this are this: e^-10000 is 0 in fp32, and G stays finite for -inf.
 constexpr float kLowestGate = -10000.f;
@@ -183,29 +182,6 @@ __global__ __launch_bounds__(256) void packed_prep_kernel(SeqProblem p, PackedTe
   }
 }
 
-// Writes four consecutive rows of a column as three terms: tile[term][column][row].
-template <int LD>
-__device__ __forceinline__ void put3(bh* tile, int plane, int column, int row, const float (&x)[4]) {
-  bh b[4][3];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) split<3>(x[r], b[r]);
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    uint2 v;
-    v.x = b[0][i] | (uint32_t)b[1][i] << 16;
-    v.y = b[2][i] | (uint32_t)b[3][i] << 16;
-    *reinterpret_cast<uint2*>(tile + i * plane + column * LD + row) = v;
-  }
-}
-
-template <int LD>
-__device__ __forceinline__ Frag<3> get3(const bh* tile, int plane, int column, int row) {
-  Frag<3> f;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) f.t[i] = as_frag(*reinterpret_cast<const uint4*>(tile + i * plane + column * LD + row));
-  return f;
-}
-
 template <int NT, int DKP, bool SAVE>
 __global__ __launch_bounds__(256, 1) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, int heads_padded) {
   constexpr int KS = DKP / 32;                        // steps over d_k
@@ -281,7 +257,7 @@ __global__ __launch_bounds__(256, 1) void packed_scan_kernel(SeqProblem p, Packe
       for (int ks = 0; ks < KS; ++ks) {
         const int kc = ks * 32 + lg * 8;
         const bool in = krow < n && kc < p.dk;
-        const Frag<3> b = get3<SLD>(Sl, SP, lr, kc);
+        const Frag<3> b = get<3, SLD>(Sl, SP, lr, kc);
         const Frag<NT> ak = in ? frag_in<NT>(t.k, (size_t)(first + krow) * p.ks + kh * p.dk + kc) : zero_frag<NT>();
         ks_ = mma<NT, 3>(ak, b, ks_);
         if constexpr (!SAVE) {
@@ -302,7 +278,7 @@ __global__ __launch_bounds__(256, 1) void packed_scan_kernel(SeqProblem p, Packe
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
         if (ks <= w / 2)
-          e = mma<3, 3>(load_frag<3>(ws.t1 + cell * kTri * 3 * 64, w * 2 + ks, lane), get3<kTok>(Nl, TP, lr, ks * 32 + lg * 8), e);
+          e = mma<3, 3>(load_frag<3>(ws.t1 + cell * kTri * 3 * 64, w * 2 + ks, lane), get<3, kTok>(Nl, TP, lr, ks * 32 + lg * 8), e);
       float u[4], ud[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -330,7 +306,7 @@ __global__ __launch_bounds__(256, 1) void packed_scan_kernel(SeqProblem p, Packe
           S[m] = S[m] * eGn;
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks)
-            S[m] = mma<NT, 3>(load_frag<NT>(kt, (w * MT + m) * 2 + ks, lane), get3<kTok>(Dl, TP, lr, ks * 32 + lg * 8), S[m]);
+            S[m] = mma<NT, 3>(load_frag<NT>(kt, (w * MT + m) * 2 + ks, lane), get<3, kTok>(Dl, TP, lr, ks * 32 + lg * 8), S[m]);
         }
       }
       put_state();
@@ -338,7 +314,7 @@ __global__ __launch_bounds__(256, 1) void packed_scan_kernel(SeqProblem p, Packe
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
           if (ks <= w / 2)
-            qs_ = mma<3, 3>(load_frag<3>(ws.p + cell * kTri * 3 * 64, w * 2 + ks, lane), get3<kTok>(Ul, TP, lr, ks * 32 + lg * 8), qs_);
+            qs_ = mma<3, 3>(load_frag<3>(ws.p + cell * kTri * 3 * 64, w * 2 + ks, lane), get<3, kTok>(Ul, TP, lr, ks * 32 + lg * 8), qs_);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (row0 + r < n) store_scalar(t.out, ((size_t)(first + row0 + r) * p.hv + h) * p.dv + col, qs_[r], p.out_bf16);

@@ -81,5 +81,7 @@ struct PackedTensors {
 
 hipError_t packed_prep(const SeqProblem& p, const PackedTensors& t, const PackedSpace& s, bool grad, hipStream_t stream);
 hipError_t packed_scan(const SeqProblem& p, const PackedTensors& t, const PackedSpace& s, bool grad, hipStream_t stream);
+hipError_t packed_scan_grad(const SeqProblem& p, const PackedTensors& t, const PackedSpace& s, hipStream_t stream);
+hipError_t packed_grads(const SeqProblem& p, const PackedTensors& t, const PackedSpace& s, hipStream_t stream);
 
 }  // namespace gdn

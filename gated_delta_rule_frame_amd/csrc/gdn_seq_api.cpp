@@ -195,6 +195,39 @@ gdn_status gdn_packed_forward(const gdn_seq_problem* pr, const void* q, const vo
   }
 }
 
+gdn_status gdn_packed_backward(const gdn_seq_problem* pr, const void* q, const void* k, const void* v, const float* log_gate,
+                               const float* beta, const int32_t* cu_seqlens, const float* initial_state, const void* dout,
+                               const float* dfinal_state, void* dq, void* dk, void* dv, float* dlog_gate, float* dbeta,
+                               float* dinitial_state, void* workspace, size_t workspace_bytes, void* stream) {
+  try {
+    gdn::SeqProblem p;
+    gdn_status s = check_packed(pr, false, &p);
+    if (s != GDN_OK) return s;
+    if (p.sequences == 0) return finish(hipSuccess);
+    s = check_needed({cu_seqlens}, "cu_seqlens");
+    if (s == GDN_OK && p.tokens > 0)
+      s = check_needed({q, k, v, log_gate, beta, dout, dq, dk, dv, dlog_gate, dbeta},
+                       "q, k, v, log_gate, beta, dout, dq, dk, dv, dlog_gate and dbeta");
+    if (s == GDN_OK)
+      s = check_aligned({q, k, v, initial_state, dout, dfinal_state, dq, dk, dv, dinitial_state, workspace},
+                        {log_gate, beta, cu_seqlens, dlog_gate, dbeta});
+    if (s == GDN_OK) s = check_workspace(gdn::packed_space(p, true, nullptr, nullptr), workspace, workspace_bytes);
+    if (s != GDN_OK) return s;
+    const gdn::PackedTensors t = {q, k, v, log_gate, beta, cu_seqlens, nullptr, initial_state, nullptr, nullptr,
+                                  dout, dfinal_state, dq, dk, dv, dlog_gate, dbeta, dinitial_state};
+    gdn::PackedSpace ws;
+    gdn::packed_space(p, true, workspace, &ws);
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e = gdn::packed_prep(p, t, ws, true, st);
+    if (e == hipSuccess) e = gdn::packed_scan(p, t, ws, true, st);
+    if (e == hipSuccess) e = gdn::packed_scan_grad(p, t, ws, st);
+    if (e == hipSuccess) e = gdn::packed_grads(p, t, ws, st);
+    return finish(e);
+  } catch (...) {
+    return fail(GDN_ERR_HIP, "internal error while enqueueing");
+  }
+}
+
 gdn_status gdn_group_norm_workspace_size(const gdn_norm_problem* pr, int32_t gradient, size_t* bytes_out) {
   try {
     if (!bytes_out) return fail(GDN_ERR_INVALID_ARGUMENT, "bytes_out is NULL");

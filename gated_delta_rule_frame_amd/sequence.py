@@ -1,7 +1,7 @@
 """Binding of the sequence operators of libgdn (``include/gdn.h``, "Sequences of tokens").
 
-``decode`` wraps ``gdn_decode``, ``packed_forward`` wraps
-``gdn_packed_forward``; ``group_norm`` and ``group_norm_backward``
+``decode`` wraps ``gdn_decode``; ``packed_forward`` and ``packed_backward``
+wrap ``gdn_packed_forward`` and its gradients; ``group_norm`` and ``group_norm_backward``
 wrap ``gdn_group_norm`` and its gradients.  As in the rest of the package the functions
 check and marshal their arguments and launch the HIP kernels on the current
 stream of the tensors' device; there is no CPU fallback.
@@ -43,6 +43,8 @@ def declare(L):
     L.gdn_packed_workspace_size.argtypes = [P, i32, ctypes.POINTER(ctypes.c_size_t)]
     L.gdn_packed_forward.restype = i32
     L.gdn_packed_forward.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    L.gdn_packed_backward.restype = i32
+    L.gdn_packed_backward.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     N, sz = ctypes.POINTER(NormProblem), ctypes.c_size_t
     L.gdn_group_norm_workspace_size.restype = i32
     L.gdn_group_norm_workspace_size.argtypes = [N, i32, ctypes.POINTER(sz)]
@@ -141,6 +143,13 @@ def decode(q, k, v, log_gate, beta, state, slots=None, *, out_dtype=None, out=No
     return out
 
 
+def _sequences(cu_seqlens, device):
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be a tensor of sequences + 1 values")
+    _dense("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
+    return cu_seqlens.shape[0] - 1
+
+
 def packed_forward(q, k, v, log_gate, beta, cu_seqlens, initial_state=None, *, slots=None, out_dtype=None, out=None,
                    final_state=None, want_state=True, workspace=None):
     """The gated delta rule over packed sequences (gdn_packed_forward); returns (out, final_state).
@@ -158,10 +167,7 @@ def packed_forward(q, k, v, log_gate, beta, cu_seqlens, initial_state=None, *, s
     """
     odt = _output(out, out_dtype)
     p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, beta, odt)
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise ValueError("cu_seqlens must be a tensor of sequences + 1 values")
-    _dense("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
-    seqs = p.sequences = cu_seqlens.shape[0] - 1
+    seqs = p.sequences = _sequences(cu_seqlens, device)
     states = seqs
     if slots is not None:
         _dense("slots", slots, (seqs,), torch.int32, device)
@@ -188,6 +194,31 @@ def packed_forward(q, k, v, log_gate, beta, cu_seqlens, initial_state=None, *, s
     _on(device, L.gdn_packed_forward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), beta.data_ptr(),
         cu_seqlens.data_ptr(), _ptr(slots), _ptr(initial_state), out.data_ptr(), _ptr(final_state), _ptr(ws), ws_bytes)
     return out, final_state
+
+
+def packed_backward(q, k, v, log_gate, beta, cu_seqlens, dout, initial_state=None, dfinal_state=None, *, workspace=None):
+    """Gradients of ``packed_forward`` (gdn_packed_backward); returns (dq, dk, dv, dlog_gate, dbeta, dinitial_state).
+
+    The inputs are packed_forward's (without slots); dout: like v;
+    dfinal_state: like the final state, or None (zeros).  dq, dk and dv have
+    q's dtype and are dense, the others are fp32; dinitial_state is None
+    where initial_state is.  Rows behind the last sequence are not written.
+    """
+    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, beta, torch.float32)
+    seqs = p.sequences = _sequences(cu_seqlens, device)
+    _dense("dout", dout, v.shape, q.dtype, device)
+    shape = (seqs, hv, dk, dv)
+    for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
+        if t is not None:
+            _dense(name, t, shape, torch.float32, device)
+    L = lib()
+    ws, ws_bytes = _space(L.gdn_packed_workspace_size, p, 1, workspace, device)
+    grads = [torch.empty(t.shape, dtype=t.dtype, device=device) for t in (q, k, v, log_gate, beta)]
+    dstate = None if initial_state is None else torch.empty_like(initial_state)
+    _on(device, L.gdn_packed_backward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), beta.data_ptr(),
+        cu_seqlens.data_ptr(), _ptr(initial_state), dout.data_ptr(), _ptr(dfinal_state), *(t.data_ptr() for t in grads),
+        _ptr(dstate), _ptr(ws), ws_bytes)
+    return (*grads, dstate)
 
 
 def packed_workspace_size(q, v, sequences, *, gradient=False):

@@ -387,6 +387,25 @@ gdn_status gdn_packed_forward(const gdn_seq_problem* problem,
                               const float* initial_state, void* out, float* final_state,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/* Gradients of sum(out dout) + sum(final_state dfinal_state) for every input,
+ * computed from the inputs alone (nothing is kept from the forward call).
+ *   dout            [tokens, heads_v, d_v]  qkv_dtype
+ *   dfinal_state    [sequences, heads_v, d_k, d_v] fp32 or NULL (zeros)
+ *   dq, dk, dv      shapes of q, k, v, dense, qkv_dtype; dq and dk sum over
+ *                   the value heads of a key head before they are rounded
+ *   dlog_gate, dbeta [tokens, heads_v] fp32
+ *   dinitial_state  [sequences, heads_v, d_k, d_v] fp32 or NULL
+ * initial_state as in gdn_packed_forward without slots.  out_dtype and
+ * state_rows are ignored; rows behind the last sequence are not written; no
+ * aliasing. */
+gdn_status gdn_packed_backward(const gdn_seq_problem* problem,
+                               const void* q, const void* k, const void* v,
+                               const float* log_gate, const float* beta,
+                               const int32_t* cu_seqlens, const float* initial_state,
+                               const void* dout, const float* dfinal_state,
+                               void* dq, void* dk, void* dv, float* dlog_gate, float* dbeta, float* dinitial_state,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Group norm with an activation or an activated gate, channels last: the norm
  * of the layer's outputs.  x [batch, spatial, channels] is dense; channels

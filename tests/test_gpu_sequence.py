@@ -490,3 +490,126 @@ def test_packed_forward_refuses_what_does_not_fit(G):
                  lambda: G.packed_forward(*(t.half() if i < 3 else t for i, t in enumerate(x)), cu, S0)):
         with pytest.raises((ValueError, TypeError, G.GdnError)):
             call()
+
+
+# ------------------------------------------------------------------ packed gradients
+
+NAMES = ("dq", "dk", "dv", "dlog_gate", "dbeta", "dinitial_state")
+
+
+def check_grads(got, ref, n, dtype, times=1.0):
+    for name, x, r in zip(NAMES, got, ref):
+        if x is None:
+            continue
+        if name != "dinitial_state":
+            x, r = x[:n], r[:n]
+        try:
+            near32(x, r, dtype if name in ("dq", "dk", "dv") else F32, times)
+        except AssertionError as e:
+            raise AssertionError(f"{name}: {e}") from None
+
+
+@pytest.mark.parametrize("lengths,hk,hv,dk,dv,dtype,gate,with_state", PACKED)
+def test_packed_backward(G, lengths, hk, hv, dk, dv, dtype, gate, with_state):
+    n, pad = sum(lengths), 3
+    x = rows(n + pad, hk, hv, dk, dv, dtype, n + 1, gate)
+    gen = torch.Generator().manual_seed(n)
+    x[4][n // 2] = 0.0
+    dout = torch.randn(n + pad, hv, dv, generator=gen).to(dtype).cuda()
+    for t in (*x, dout):
+        t[n:] = float("nan")
+    S0 = torch.randn(len(lengths), hv, dk, dv, generator=gen).cuda() if with_state else None
+    dS = torch.randn(len(lengths), hv, dk, dv, generator=gen).cuda() if with_state else None
+    cu = cu_of(lengths)
+    ref = R.packed_grads(*(R.f64(t) for t in x), cu.tolist(), R.f64(S0), R.f64(dout).nan_to_num(), R.f64(dS))
+    got = G.packed_backward(*x, cu, dout, S0, dS)
+    assert (got[5] is None) == (S0 is None)
+    assert [t.dtype for t in got[:5]] == [dtype] * 3 + [F32] * 2
+    # a gate's gradient is the difference of sums over its chunk's tokens: some eight times its own size
+    check_grads(got, ref, n, dtype, 8.0)
+
+
+def test_packed_backward_hard_inputs(G):
+    """-inf gates (gradient 0), beta 0 and equal keys."""
+    n, d = 140, 32
+    x = rows(n, 1, 1, d, d, F32, 14)
+    x[3][70], x[3][3] = float("-inf"), float("-inf")
+    x[4][10:20] = 0.0
+    x[1][30:60] = x[1][30]
+    x[4][30:60] = 1.0
+    cu, dout = cu_of([n]), torch.randn(n, 1, d, device="cuda")
+    finite = [t.clone() for t in x]
+    finite[3][finite[3] < -1e4] = -1e4         # exp is 0 either way; automatic differentiation needs a finite gate
+    ref = R.packed_grads(*(R.f64(t) for t in finite), cu.tolist(), None, R.f64(dout), None)
+    got = G.packed_backward(*x, cu, dout)
+    check_grads(got, ref, n, F32, 32.0)
+    # sums that cancel to zero: within their terms' roundings
+    assert got[3][[3, 70]].abs().max() <= 1e-4 * got[3].abs().max()
+
+
+def test_packed_gradients_against_differences(G):
+    """Directional differences of the forward call, with shared heads and states."""
+    lengths, hk, hv, dk, dv = [70, 5, 90], 2, 4, 32, 48
+    n = sum(lengths)
+    x = rows(n, hk, hv, dk, dv, F32, 31)
+    gen = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    S0, dS, dout, cu = r(3, hv, dk, dv), r(3, hv, dk, dv), r(n, hv, dv), cu_of(lengths)
+    grads = G.packed_backward(*x, cu, dout, S0, dS)
+    leaves = [*x, S0]
+    for i, t in enumerate(leaves):
+        d = r(*t.shape) * (0.05 if i in (3, 4) else 1.0)
+        h = 2.0 ** -8
+
+        def loss(s):
+            y = [u + s * h * d if j == i else u for j, u in enumerate(leaves)]
+            out, S = G.packed_forward(*y[:5], cu, y[5])
+            return (out.double() * dout).sum().item() + (S.double() * dS).sum().item()
+
+        slope = (loss(1) - loss(-1)) / (2 * h)
+        want = (grads[i].double() * d).sum().item()
+        size = grads[i].double().norm().item() * d.double().norm().item()
+        # the third difference, h^2 / 6 of slopes that grow with the norms, and fp32 steps of the losses over 2 h
+        assert abs(slope - want) <= 2e-3 * size, (NAMES[i], slope, want, size)
+
+
+def test_packed_backward_streams_graph_and_repeats(G):
+    x = rows(333, 2, 4, 64, 64, BF16, 5)
+    cu = cu_of([100, 133, 100])
+    S0, dS = torch.randn(3, 4, 64, 64, device="cuda"), torch.randn(3, 4, 64, 64, device="cuda")
+    dout = torch.randn(333, 4, 64, device="cuda").bfloat16()
+    want = G.packed_backward(*x, cu, dout, S0, dS)
+    same = lambda a: all(torch.equal(i, j) for i, j in zip(a, want))  # noqa: E731
+    sides, got = [torch.cuda.Stream() for _ in range(2)], []
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(G.packed_backward(*x, cu, dout, S0, dS))
+    for s in sides:
+        torch.cuda.current_stream().wait_stream(s)
+    assert all(same(g) for g in got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = G.packed_backward(*x, cu, dout, S0, dS)
+    for _ in range(3):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out)
+        G.packed_backward(*x, cu, dout, S0, dS)
+
+
+def test_packed_backward_without_tokens_and_refusals(G):
+    x = [t[:0] for t in rows(1, 1, 2, 32, 32, BF16, 1)]
+    S0 = torch.randn(2, 2, 32, 32, device="cuda")
+    got = G.packed_backward(*x, cu_of([0, 0]), x[2], S0, S0)
+    assert torch.equal(got[5], S0) and got[0].shape == (0, 1, 32)
+    x = rows(10, 2, 4, 32, 32, BF16, 1)
+    cu, S0, dout = cu_of([4, 6]), torch.zeros(2, 4, 32, 32, device="cuda"), torch.zeros(10, 4, 32, device="cuda", dtype=BF16)
+    for call in (lambda: G.packed_backward(*x, cu, dout.float()), lambda: G.packed_backward(*x, cu, dout[:9]),
+                 lambda: G.packed_backward(*x, cu, dout, S0[:1].contiguous()), lambda: G.packed_backward(*x, cu, dout, S0, S0.bfloat16()),
+                 lambda: G.packed_backward(*x, cu.cpu(), dout),
+                 lambda: G.packed_backward(*x, cu, dout, workspace=torch.empty(64, device="cuda"))):
+        with pytest.raises((ValueError, TypeError, G.GdnError)):
+            call()
