@@ -52,6 +52,25 @@ __device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4
   return c;
 }
 
+// c[s] += the products of terms i + j = s, for s = 0, 1, 2: three chains of
+// dependent MFMAs instead of one.
+template <int NA, int NB>
+__device__ __forceinline__ void mma_by_term(const Frag<NA>& a, const Frag<NB>& b, f32x4 (&c)[3]) {
+#pragma unroll
+  for (int s = 0; s < 3; ++s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) c[s] = mfma(a.t[i], b.t[s - i], c[s]);
+}
+
+template <int N, int M>
+__device__ __forceinline__ Frag<N> first_terms(const Frag<M>& f) {
+  Frag<N> o;
+#pragma unroll
+  for (int i = 0; i < N; ++i) o.t[i] = f.t[i];
+  return o;
+}
+
 // x as the sum of N bf16 values, largest first.
 template <int N>
 __device__ __forceinline__ void split(float x, bh (&o)[N]) {
@@ -106,16 +125,75 @@ __device__ __forceinline__ Frag<NT> frag_in(const void* p, size_t i) {
   }
 }
 
+// Element at a 32-bit byte offset from a uniform base (one scalar pair and one
+// vector register of address).
+template <typename T>
+__device__ __forceinline__ T at_byte(const void* base, uint32_t off) {
+  return *reinterpret_cast<const T*>(static_cast<const char*>(base) + off);
+}
+
+// One input value as it lies in memory, and its value.
+template <int NT>
+struct RawIn {
+  using type = uint16_t;
+};
+template <>
+struct RawIn<3> {
+  using type = float;
+};
+__device__ __forceinline__ float raw_value(uint16_t x) { return bf16_bits_to_f32(x); }
+__device__ __forceinline__ float raw_value(float x) { return x; }
+
+// Eight consecutive input values as they lie in memory, split where they are used.
+template <int NT>
+struct RawFrag {
+  uint4 a, b;                       // fp32: two vectors
+};
+template <>
+struct RawFrag<1> {
+  uint4 a;
+};
+
+template <int NT>
+__device__ __forceinline__ RawFrag<NT> zero_raw() {
+  RawFrag<NT> r;
+  r.a = make_uint4(0, 0, 0, 0);
+  if constexpr (NT == 3) r.b = r.a;
+  return r;
+}
+
+template <int NT>
+__device__ __forceinline__ RawFrag<NT> raw_at(const void* base, uint32_t off) {
+  RawFrag<NT> r;
+  r.a = at_byte<uint4>(base, off);
+  if constexpr (NT == 3) r.b = at_byte<uint4>(base, off + 16);
+  return r;
+}
+
+template <int NT>
+__device__ __forceinline__ Frag<NT> frag_of(const RawFrag<NT>& r) {
+  if constexpr (NT == 1) {
+    Frag<1> f;
+    f.t[0] = as_frag(r.a);
+    return f;
+  } else {
+    const float x[8] = {__uint_as_float(r.a.x), __uint_as_float(r.a.y), __uint_as_float(r.a.z), __uint_as_float(r.a.w),
+                        __uint_as_float(r.b.x), __uint_as_float(r.b.y), __uint_as_float(r.b.z), __uint_as_float(r.b.w)};
+    return split8<3>(x);
+  }
+}
+
 template <int NT>
 __device__ __forceinline__ float elem_in(const void* p, size_t i) {
   return load_scalar<NT == 1>(p, i);
 }
 
-template <int N>
+// The first N of a stored fragment's LD terms.
+template <int N, int LD = N>
 __device__ __forceinline__ Frag<N> load_frag(const uint4* p, int frag, int lane) {
   Frag<N> f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) f.t[i] = as_frag(p[((size_t)frag * N + i) * 64 + lane]);
+  for (int i = 0; i < N; ++i) f.t[i] = as_frag(p[((size_t)frag * LD + i) * 64 + lane]);
   return f;
 }
 
@@ -162,6 +240,17 @@ __device__ __forceinline__ void seq_bounds(const int* cu, int s, long long token
   const int a = min(max(cu[s], 0), n);
   *start = a;
   *end = min(max(cu[s + 1], a), n);
+}
+
+// The (sequence, head) and strip of a scan's workgroup.  Workgroups go to the
+// eight XCDs in turn, so the strips of one (sequence, head), which read the same
+// operands, get ids of equal remainder mod 8 that follow one another: they run
+// at the same time on one XCD and share its L2.  The grid has the number of
+// (sequence, head) pairs rounded up to 8, times the strips.
+__device__ __forceinline__ void strip_of(int block, int strips, int* sh, int* strip) {
+  const int i = block / 8;
+  *sh = i / strips * 8 + block % 8;
+  *strip = i % strips;
 }
 
 // The sequence and chunk of a chunk slot; false for a slot without tokens.

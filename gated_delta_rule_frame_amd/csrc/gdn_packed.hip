@@ -182,20 +182,40 @@ __global__ __launch_bounds__(256) void packed_prep_kernel(SeqProblem p, PackedTe
   }
 }
 
-template <int NT, int DKP, bool SAVE>
-__global__ __launch_bounds__(256, 1) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, int heads_padded) {
-  constexpr int KS = DKP / 32;                        // steps over d_k
-  constexpr int MT = DKP >= 64 ? DKP / 64 : 1;        // state row tiles of a wavefront
+// What a chunk's step reads from memory, as each phase of the step needs it.
+// A phase's registers are loaded for the next chunk as soon as the phase has
+// used them, so every load has a whole step to arrive.
+template <int NT, int DKP, int PT>
+struct ChunkIn {
+  static constexpr int KS = DKP / 32, MT = DKP >= 64 ? DKP / 64 : 1;
+  RawFrag<NT> k[KS], q[PT ? KS : 1];   // rows of K and Q
+  typename RawIn<NT>::type v[4];
+  float4 eG;
+  Frag<3> t1[2];                    // T' and the gates of the rows
+  float4 eD, beta;
+  Frag<NT> kt[MT][2];               // K^T
+  float eGn;
+  Frag<PT ? PT : 1> p[2];           // P
+};
+
+// PT: terms of the output products (2 for a bf16 output, whose rounding is 2^9
+// times the third term; 3 for fp32), or 0: no outputs, but e and the state
+// before each chunk are left in the workspace for the gradients.
+template <int NT, int DKP, int PT>
+__global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
+  using In = ChunkIn<NT, DKP, PT>;
+  constexpr int KS = In::KS;                          // steps over d_k
+  constexpr int MT = In::MT;                          // state row tiles of a wavefront
   constexpr int SLD = DKP + 8, SP = 16 * SLD, TP = 16 * kTok;
   __shared__ __align__(16) bh Sl[3 * SP];
   __shared__ __align__(16) bh Nl[3 * TP];
-  __shared__ __align__(16) bh Ul[3 * TP];
+  __shared__ __align__(16) bh Ul[(PT ? PT : 1) * TP];
   __shared__ __align__(16) bh Dl[3 * TP];
   __shared__ int earlier, next;
   const int tid = threadIdx.x, lane = tid % 64, w = tid / 64;
   const int lr = lane % 16, lg = lane / 16;
-  // strips of one (sequence, head) share an XCD and its L2: block ids of equal remainder mod 8
-  const int sh = blockIdx.x % heads_padded, strip = blockIdx.x / heads_padded;
+  int sh, strip;
+  strip_of(blockIdx.x, p.dv / 16, &sh, &strip);
   if (sh >= p.sequences * p.hv) return;
   const int h = sh % p.hv, kh = h / (p.hv / p.hk);
   const int col = strip * 16 + lr;
@@ -217,10 +237,14 @@ __global__ __launch_bounds__(256, 1) void packed_scan_kernel(SeqProblem p, Packe
     if (earlier) return;
   }
   const size_t state = ((size_t)slot_of * p.hv + h) * p.dk * p.dv;
+  const int row0 = 16 * w + 4 * lg;                   // of this lane's four accumulator rows
+  const int krow = 16 * w + lr;                       // of its operand rows
 
   for (;;) {
     int start, end;
     seq_bounds(t.cu, seq, p.tokens, &start, &end);
+    start = __builtin_amdgcn_readfirstlane(start);
+    end = __builtin_amdgcn_readfirstlane(end);
     const long long slot0 = start / kC + (long long)seq;
     f32x4 S[MT];
 #pragma unroll
@@ -238,56 +262,111 @@ __global__ __launch_bounds__(256, 1) void packed_scan_kernel(SeqProblem p, Packe
           put3<SLD>(Sl, SP, lr, (w * MT + m) * 16 + 4 * lg, x);
         }
     };
-    put_state();
-    __syncthreads();
-    for (int first = start, c = 0; first < end; first += kC, ++c) {
-      const int n = min(kC, end - first);
-      const long long slot = slot0 + c;
-      const size_t cell = (size_t)slot * p.hv + h;
-      const float* gates = ws.gates + cell * 3 * kC;
-      const int row0 = 16 * w + 4 * lg;               // of this lane's four accumulator rows
-      const float4 eG = *reinterpret_cast<const float4*>(gates + row0);
-      const float4 eD = *reinterpret_cast<const float4*>(gates + kC + row0);
-      const float4 be = *reinterpret_cast<const float4*>(gates + 2 * kC + row0);
-      const float eGn = gates[kC - 1];
-      const float eg[4] = {eG.x, eG.y, eG.z, eG.w}, ed[4] = {eD.x, eD.y, eD.z, eD.w}, bt[4] = {be.x, be.y, be.z, be.w};
-      const int krow = 16 * w + lr;
-      f32x4 ks_ = zero4(), qs_ = zero4();
+    In in;
+    // columns behind d_k are never loaded and stay zero
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const int kc = ks * 32 + lg * 8;
-        const bool in = krow < n && kc < p.dk;
-        const Frag<3> b = get<3, SLD>(Sl, SP, lr, kc);
-        const Frag<NT> ak = in ? frag_in<NT>(t.k, (size_t)(first + krow) * p.ks + kh * p.dk + kc) : zero_frag<NT>();
-        ks_ = mma<NT, 3>(ak, b, ks_);
-        if constexpr (!SAVE) {
-          const Frag<NT> aq = in ? frag_in<NT>(t.q, (size_t)(first + krow) * p.qs + kh * p.dk + kc) : zero_frag<NT>();
-          qs_ = mma<NT, 3>(aq, b, qs_);
+    for (int ks = 0; ks < KS; ++ks) {
+      in.k[ks] = zero_raw<NT>();
+      if constexpr (PT > 0) in.q[ks] = zero_raw<NT>();
+    }
+    constexpr uint32_t es = NT == 1 ? 2 : 4;          // bytes of an input element
+    // Rows behind the sequence's end take its last row instead: their beta is 0 and their outputs are not stored.
+    auto load_rows = [&](int first, size_t cell) {
+      const int n = end - first;
+      const char* kb = static_cast<const char*>(t.k) + ((size_t)first * p.ks + kh * p.dk) * es;
+      const char* qb = static_cast<const char*>(t.q) + ((size_t)first * p.qs + kh * p.dk) * es;
+      const char* vb = static_cast<const char*>(t.v) + ((size_t)first * p.vs + h * p.dv) * es;
+      const uint32_t row = min(krow, n - 1);
+      const uint32_t ko = row * ((uint32_t)p.ks * es) + lg * 8 * es, qo = row * ((uint32_t)p.qs * es) + lg * 8 * es;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        if (ks * 32 + lg * 8 < p.dk) {
+          in.k[ks] = raw_at<NT>(kb, ko + ks * 32 * es);
+          if constexpr (PT > 0) in.q[ks] = raw_at<NT>(qb, qo + ks * 32 * es);
         }
-      }
-      float x[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float v = row0 + r < n ? elem_in<NT>(t.v, (size_t)(first + row0 + r) * p.vs + h * p.dv + col) : 0.f;
-        x[r] = fmaf(-eg[r], ks_[r], v);
-        qs_[r] *= eg[r];
-      }
-      put3<kTok>(Nl, TP, lr, row0, x);
-      __syncthreads();
-      f32x4 e = zero4();
+      for (int r = 0; r < 4; ++r)
+        in.v[r] = at_byte<typename RawIn<NT>::type>(vb, (uint32_t)min(row0 + r, n - 1) * ((uint32_t)p.vs * es) + col * es);
+      in.eG = *reinterpret_cast<const float4*>(ws.gates + cell * 3 * kC + row0);
+    };
+    auto load_inverse = [&](size_t cell) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        if (ks <= w / 2)
-          e = mma<3, 3>(load_frag<3>(ws.t1 + cell * kTri * 3 * 64, w * 2 + ks, lane), get<3, kTok>(Nl, TP, lr, ks * 32 + lg * 8), e);
+        if (ks <= w / 2) in.t1[ks] = load_frag<3>(ws.t1 + cell * kTri * 3 * 64, w * 2 + ks, lane);
+      in.eD = *reinterpret_cast<const float4*>(ws.gates + cell * 3 * kC + kC + row0);
+      in.beta = *reinterpret_cast<const float4*>(ws.gates + cell * 3 * kC + 2 * kC + row0);
+    };
+    int vector_zero = 0;
+    asm volatile("" : "+v"(vector_zero));             // a scalar load would be waited for with the LDS traffic
+    auto load_state = [&](size_t cell, long long slot) {
+      if (srows) {
+        const uint4* kt = ws.kt + ((size_t)slot * p.hk + kh) * (DKP / 16) * 2 * NT * 64;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) in.kt[m][ks] = load_frag<NT>(kt, (w * MT + m) * 2 + ks, lane);
+      }
+      in.eGn = ws.gates[cell * 3 * kC + kC - 1 + vector_zero];
+      if constexpr (PT > 0)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          if (ks <= w / 2) in.p[ks] = load_frag<PT, 3>(ws.p + cell * kTri * 3 * 64, w * 2 + ks, lane);
+    };
+    put_state();
+    if (start < end) {
+      const size_t cell = (size_t)slot0 * p.hv + h;
+      load_rows(start, cell);
+      load_inverse(cell);
+      load_state(cell, slot0);
+    }
+    __syncthreads();
+    long long slot = slot0;
+    for (int first = start; first < end; first += kC) {
+      const int n = min(kC, end - first);
+      const bool more = first + kC < end;
+      const size_t cell = (size_t)slot * p.hv + h;
+      if (more) ++slot;                               // the last chunk's loads are repeated instead
+      const int nfirst = more ? first + kC : first;
+      const size_t ncell = (size_t)slot * p.hv + h;
+      f32x4 kS[3], qS = zero4();
+#pragma unroll
+      for (int i = 0; i < 3; ++i) kS[i] = zero4();
+      Frag<3> b[KS];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) b[ks] = get<3, SLD>(Sl, SP, lr, ks * 32 + lg * 8);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) mma_by_term<NT, 3>(frag_of<NT>(in.k[ks]), b[ks], kS);
+      float x[4];
+      const float eg[4] = {in.eG.x, in.eG.y, in.eG.z, in.eG.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = fmaf(-eg[r], (kS[2][r] + kS[1][r]) + kS[0][r], row0 + r < n ? raw_value(in.v[r]) : 0.f);
+      put3<kTok>(Nl, TP, lr, row0, x);
+      if constexpr (PT > 0) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) qS = mma<NT, PT>(frag_of<NT>(in.q[ks]), first_terms<PT>(b[ks]), qS);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) qS[r] *= eg[r];
+      }
+      load_rows(nfirst, ncell);
+      __syncthreads();
+      f32x4 eT[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) eT[i] = zero4();
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+        if (ks <= w / 2) mma_by_term<3, 3>(in.t1[ks], get<3, kTok>(Nl, TP, lr, ks * 32 + lg * 8), eT);
+      const f32x4 e = (eT[2] + eT[1]) + eT[0];
+      const float ed[4] = {in.eD.x, in.eD.y, in.eD.z, in.eD.w}, bt[4] = {in.beta.x, in.beta.y, in.beta.z, in.beta.w};
       float u[4], ud[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         u[r] = bt[r] * e[r];
         ud[r] = ed[r] * u[r];
       }
-      if constexpr (!SAVE) put3<kTok>(Ul, TP, lr, row0, u);
       put3<kTok>(Dl, TP, lr, row0, ud);
-      if constexpr (SAVE) {
+      if constexpr (PT > 0) put<PT, kTok>(Ul, TP, lr, row0, u);
+      load_inverse(ncell);
+      if constexpr (PT == 0) {
         float* eo = ws.e + (cell * strips + strip) * kC * 16;
         float* so = ws.s0 + (cell * strips + strip) * DKP * 16;
 #pragma unroll
@@ -300,25 +379,35 @@ __global__ __launch_bounds__(256, 1) void packed_scan_kernel(SeqProblem p, Packe
       }
       __syncthreads();
       if (srows) {
-        const uint4* kt = ws.kt + ((size_t)slot * p.hk + kh) * (DKP / 16) * 2 * NT * 64;
+        Frag<3> d[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) d[ks] = get<3, kTok>(Dl, TP, lr, ks * 32 + lg * 8);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          S[m] = S[m] * eGn;
+          f32x4 a[3];
+          a[0] = S[m] * in.eGn;
+          a[1] = a[2] = zero4();
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-            S[m] = mma<NT, 3>(load_frag<NT>(kt, (w * MT + m) * 2 + ks, lane), get<3, kTok>(Dl, TP, lr, ks * 32 + lg * 8), S[m]);
+          for (int ks = 0; ks < 2; ++ks) mma_by_term<NT, 3>(in.kt[m][ks], d[ks], a);
+          S[m] = a[0] + (a[1] + a[2]);
         }
       }
       put_state();
-      if constexpr (!SAVE) {
+      if constexpr (PT > 0) {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          if (ks <= w / 2)
-            qs_ = mma<3, 3>(load_frag<3>(ws.p + cell * kTri * 3 * 64, w * 2 + ks, lane), get<3, kTok>(Ul, TP, lr, ks * 32 + lg * 8), qs_);
+          if (ks <= w / 2) qS = mma<PT, PT>(in.p[ks], get<PT, kTok>(Ul, TP, lr, ks * 32 + lg * 8), qS);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (row0 + r < n) store_scalar(t.out, ((size_t)(first + row0 + r) * p.hv + h) * p.dv + col, qs_[r], p.out_bf16);
+          if (row0 + r < n) {
+            constexpr uint32_t os = PT == 2 ? 2 : 4;
+            char* ob = static_cast<char*>(t.out) + ((size_t)first * p.hv + h) * p.dv * os;
+            const uint32_t oo = (uint32_t)(row0 + r) * ((uint32_t)(p.hv * p.dv) * os) + col * os;
+            if constexpr (PT == 2) *reinterpret_cast<bh*>(ob + oo) = f2bh(qS[r]);
+            else *reinterpret_cast<float*>(ob + oo) = qS[r];
+          }
       }
+      load_state(ncell, slot);
       __syncthreads();
     }
     if (t.hT && kept && srows)
@@ -405,8 +494,9 @@ hipError_t packed_scan(const SeqProblem& p, const PackedTensors& t, const Packed
   prof_begin(stream, GDN_KERNEL_PACKED_SCAN);
 #define GDN_SCAN(NT, D)                                                                                                          \
   if (f.terms == NT && f.dkp == D) {                                                                                             \
-    if (grad) hipLaunchKernelGGL((packed_scan_kernel<NT, D, true>), grid, dim3(256), 0, stream, p, t, s, padded);                \
-    else hipLaunchKernelGGL((packed_scan_kernel<NT, D, false>), grid, dim3(256), 0, stream, p, t, s, padded);                    \
+    if (grad) hipLaunchKernelGGL((packed_scan_kernel<NT, D, 0>), grid, dim3(256), 0, stream, p, t, s);                   \
+    else if (p.out_bf16) hipLaunchKernelGGL((packed_scan_kernel<NT, D, 2>), grid, dim3(256), 0, stream, p, t, s);        \
+    else hipLaunchKernelGGL((packed_scan_kernel<NT, D, 3>), grid, dim3(256), 0, stream, p, t, s);                        \
   }
   GDN_SCAN(1, 32) GDN_SCAN(1, 64) GDN_SCAN(1, 128) GDN_SCAN(3, 32) GDN_SCAN(3, 64) GDN_SCAN(3, 128)
 #undef GDN_SCAN

@@ -26,11 +26,28 @@ namespace {
 
 constexpr int kLd = 68;     // row stride (floats) of a 64 x 64 fp32 tile in LDS
 
+// What a chunk's step reads, by phase; loaded for the next chunk as soon as a
+// phase has used it, as in the forward scan.
 template <int NT, int DKP>
-__global__ __launch_bounds__(256, 1) void packed_scan_grad_kernel(SeqProblem p, PackedTensors t, PackedSpace ws,
-                                                                 int heads_padded) {
-  constexpr int KS = DKP / 32;
-  constexpr int MT = DKP >= 64 ? DKP / 64 : 1;
+struct GradIn {
+  static constexpr int KS = DKP / 32, MT = DKP >= 64 ? DKP / 64 : 1;
+  typename RawIn<NT>::type dout[4]; // of the chunk after the one whose step runs
+  float4 deG;
+  RawFrag<NT> k[KS];                // rows of K
+  Frag<3> p[2];                     // P^T
+  Frag<NT> qt[MT][2];               // Q^T
+  float4 eD;
+  float eGn;
+  Frag<3> t2[2];                    // T^T
+  float4 eG, beta;
+  Frag<NT> kt[MT][2];               // K^T
+};
+
+template <int NT, int DKP>
+__global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
+  using In = GradIn<NT, DKP>;
+  constexpr int KS = In::KS;
+  constexpr int MT = In::MT;
   constexpr int SLD = DKP + 8, SP = 16 * SLD, TP = 16 * kTok;
   __shared__ __align__(16) bh Sl[3 * SP];           // dS
   __shared__ __align__(16) bh Ol[NT * TP];          // dO
@@ -39,7 +56,8 @@ __global__ __launch_bounds__(256, 1) void packed_scan_grad_kernel(SeqProblem p, 
   __shared__ __align__(16) bh Yl[3 * TP];           // -e^G dN
   const int tid = threadIdx.x, lane = tid % 64, w = tid / 64;
   const int lr = lane % 16, lg = lane / 16;
-  const int sh = blockIdx.x % heads_padded, strip = blockIdx.x / heads_padded;
+  int sh, strip;
+  strip_of(blockIdx.x, p.dv / 16, &sh, &strip);
   if (sh >= p.sequences * p.hv) return;
   const int h = sh % p.hv, kh = h / (p.hv / p.hk), seq = sh / p.hv;
   const int col = strip * 16 + lr;
@@ -48,7 +66,11 @@ __global__ __launch_bounds__(256, 1) void packed_scan_grad_kernel(SeqProblem p, 
   const size_t state = ((size_t)seq * p.hv + h) * p.dk * p.dv;
   int start, end;
   seq_bounds(t.cu, seq, p.tokens, &start, &end);
+  start = __builtin_amdgcn_readfirstlane(start);
+  end = __builtin_amdgcn_readfirstlane(end);
   const long long slot0 = start / kC + (long long)seq;
+  const int row0 = 16 * w + 4 * lg, krow = 16 * w + lr;
+  auto cell_of = [&](int c) { return (size_t)(slot0 + c) * p.hv + h; };
 
   f32x4 S[MT];
 #pragma unroll
@@ -58,90 +80,173 @@ __global__ __launch_bounds__(256, 1) void packed_scan_grad_kernel(SeqProblem p, 
       const int row = (w * MT + m) * 16 + 4 * lg + r;
       S[m][r] = t.dhT && row < p.dk ? t.dhT[state + (size_t)row * p.dv + col] : 0.f;
     }
-  for (int c = (end - start + kC - 1) / kC - 1; c >= 0; --c) {
-    const int first = start + c * kC, n = min(kC, end - first);
-    const long long slot = slot0 + c;
-    const size_t cell = (size_t)slot * p.hv + h;
-    const float* gates = ws.gates + cell * 3 * kC;
-    const int row0 = 16 * w + 4 * lg;
-    const float4 eG = *reinterpret_cast<const float4*>(gates + row0);
-    const float4 eD = *reinterpret_cast<const float4*>(gates + kC + row0);
-    const float4 be = *reinterpret_cast<const float4*>(gates + 2 * kC + row0);
-    const float eGn = gates[kC - 1];
-    const float eg[4] = {eG.x, eG.y, eG.z, eG.w}, ed[4] = {eD.x, eD.y, eD.z, eD.w}, bt[4] = {be.x, be.y, be.z, be.w};
-    __syncthreads();                                 // the previous chunk's products have read the tiles
-    if (srows) {
-      float* so = ws.ds + (cell * strips + strip) * DKP * 16;
+  auto put_state = [&]() {
+    if (srows)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const float x[4] = {S[m][0], S[m][1], S[m][2], S[m][3]};
         put3<SLD>(Sl, SP, lr, (w * MT + m) * 16 + 4 * lg, x);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) so[((w * MT + m) * 16 + 4 * lg + r) * 16 + lr] = S[m][r];
       }
-    }
-    {
-      // this lane's four tokens of dO, plain and times e^G, as operand columns
-      float x[4], y[4];
+  };
+  In in;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[r] = row0 + r < n ? elem_in<NT>(t.dout, ((size_t)(first + row0 + r) * p.hv + h) * p.dv + col) : 0.f;
-        y[r] = eg[r] * x[r];
-      }
-      put<NT, kTok>(Ol, TP, lr, row0, x);
-      put3<kTok>(Xl, TP, lr, row0, y);
-    }
-    __syncthreads();
-    const int krow = 16 * w + lr;
-    f32x4 u = zero4();
+  for (int ks = 0; ks < KS; ++ks) in.k[ks] = zero_raw<NT>();   // columns behind d_k are never loaded and stay zero
+  constexpr uint32_t es = NT == 1 ? 2 : 4;           // bytes of an input element
+  const uint32_t ostride = (uint32_t)(p.hv * p.dv) * es;
+  // Rows behind the sequence's end take its last row instead, where their beta is 0; dO's are set to 0.
+  auto load_dout = [&](int c) {
+    const int first = start + c * kC, n = end - first;
+    const char* ob = static_cast<const char*>(t.dout) + ((size_t)first * p.hv + h) * p.dv * es;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int kc = ks * 32 + lg * 8;
-      const Frag<NT> ak = krow < n && kc < p.dk ? frag_in<NT>(t.k, (size_t)(first + krow) * p.ks + kh * p.dk + kc) : zero_frag<NT>();
-      u = mma<NT, 3>(ak, get<3, SLD>(Sl, SP, lr, kc), u);
-    }
+    for (int r = 0; r < 4; ++r)
+      in.dout[r] = at_byte<typename RawIn<NT>::type>(ob, (uint32_t)min(row0 + r, n - 1) * ostride + col * es);
+    in.deG = *reinterpret_cast<const float4*>(ws.gates + cell_of(c) * 3 * kC + row0);
+  };
+  // chunk c's four tokens of this lane, plain and times e^G, as operand columns
+  auto put_dout = [&](int c) {
+    const int n = end - (start + c * kC);
+    const float eg[4] = {in.deG.x, in.deG.y, in.deG.z, in.deG.w};
+    float x[4], y[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) u[r] *= ed[r];
+    for (int r = 0; r < 4; ++r) {
+      x[r] = row0 + r < n ? raw_value(in.dout[r]) : 0.f;
+      y[r] = eg[r] * x[r];
+    }
+    put<NT, kTok>(Ol, TP, lr, row0, x);
+    put3<kTok>(Xl, TP, lr, row0, y);
+  };
+  int vector_zero = 0;
+  asm volatile("" : "+v"(vector_zero));             // a scalar load would be waited for with the LDS traffic
+  auto load_first = [&](int c) {
+    const int first = start + c * kC, n = end - first;
+    const size_t cell = cell_of(c);
+    const char* kb = static_cast<const char*>(t.k) + ((size_t)first * p.ks + kh * p.dk) * es;
+    const uint32_t ko = (uint32_t)min(krow, n - 1) * ((uint32_t)p.ks * es) + lg * 8 * es;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+      if (ks * 32 + lg * 8 < p.dk) in.k[ks] = raw_at<NT>(kb, ko + ks * 32 * es);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
-      if (ks >= w / 2)
-        u = mma<3, NT>(load_frag<3>(ws.p + cell * kTri * 3 * 64, w * 2 + ks, lane), get<NT, kTok>(Ol, TP, lr, ks * 32 + lg * 8), u);
+      if (ks >= w / 2) in.p[ks] = load_frag<3>(ws.p + cell * kTri * 3 * 64, w * 2 + ks, lane);
+    if (srows) {
+      const uint4* qt = ws.qt + ((size_t)(slot0 + c) * p.hk + kh) * (DKP / 16) * 2 * NT * 64;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) in.qt[m][ks] = load_frag<NT>(qt, (w * MT + m) * 2 + ks, lane);
+    }
+    in.eD = *reinterpret_cast<const float4*>(ws.gates + cell * 3 * kC + kC + row0);
+    in.eGn = ws.gates[cell * 3 * kC + kC - 1 + vector_zero];
+  };
+  auto load_second = [&](int c) {
+    const size_t cell = cell_of(c);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+      if (ks >= w / 2) in.t2[ks] = load_frag<3>(ws.t2 + cell * kTri * 3 * 64, w * 2 + ks, lane);
+    in.eG = *reinterpret_cast<const float4*>(ws.gates + cell * 3 * kC + row0);
+    in.beta = *reinterpret_cast<const float4*>(ws.gates + cell * 3 * kC + 2 * kC + row0);
+  };
+  auto load_third = [&](int c) {
+    if (srows) {
+      const uint4* kt = ws.kt + ((size_t)(slot0 + c) * p.hk + kh) * (DKP / 16) * 2 * NT * 64;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) in.kt[m][ks] = load_frag<NT>(kt, (w * MT + m) * 2 + ks, lane);
+    }
+  };
+  const int last = (end - start + kC - 1) / kC - 1;
+  if (last >= 0) {
+    load_dout(last);
+    put_dout(last);
+    load_dout(last ? last - 1 : 0);
+    load_first(last);
+    load_second(last);
+    load_third(last);
+  }
+  put_state();
+  __syncthreads();
+  for (int c = last; c >= 0; --c) {
+    const int first = start + c * kC, n = min(kC, end - first);
+    const size_t cell = cell_of(c);
+    const int next = c ? c - 1 : 0, after = c > 1 ? c - 2 : 0;   // the first chunks' loads are repeated instead
+    f32x4 a[3], u = zero4();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) a[i] = zero4();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) mma_by_term<NT, 3>(frag_of<NT>(in.k[ks]), get<3, SLD>(Sl, SP, lr, ks * 32 + lg * 8), a);
+    const float ed[4] = {in.eD.x, in.eD.y, in.eD.z, in.eD.w};
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+      if (ks >= w / 2) u = mma<3, NT>(in.p[ks], get<NT, kTok>(Ol, TP, lr, ks * 32 + lg * 8), u);
     {
-      const float x[4] = {u[0], u[1], u[2], u[3]};
+      float x[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = fmaf(ed[r], (a[2][r] + a[1][r]) + a[0][r], u[r]);
       put3<kTok>(Ul, TP, lr, row0, x);
     }
+    if (srows) {
+      // Q^T (e^G dO) needs nothing of this step: it fills the wait for the barrier
+      float* so = ws.ds + (cell * strips + strip) * DKP * 16;
+      Frag<3> xf[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) xf[ks] = get<3, kTok>(Xl, TP, lr, ks * 32 + lg * 8);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) so[((w * MT + m) * 16 + 4 * lg + r) * 16 + lr] = S[m][r];
+        S[m] = S[m] * in.eGn;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) S[m] = mma<NT, 3>(in.qt[m][ks], xf[ks], S[m]);
+      }
+    }
+    load_first(next);
     __syncthreads();
-    f32x4 W = zero4();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) a[i] = zero4();
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
-      if (ks >= w / 2)
-        W = mma<3, 3>(load_frag<3>(ws.t2 + cell * kTri * 3 * 64, w * 2 + ks, lane), get<3, kTok>(Ul, TP, lr, ks * 32 + lg * 8), W);
+      if (ks >= w / 2) mma_by_term<3, 3>(in.t2[ks], get<3, kTok>(Ul, TP, lr, ks * 32 + lg * 8), a);
     {
+      const f32x4 W = (a[2] + a[1]) + a[0];
+      const float eg[4] = {in.eG.x, in.eG.y, in.eG.z, in.eG.w}, bt[4] = {in.beta.x, in.beta.y, in.beta.z, in.beta.w};
       float* wo = ws.w + (cell * strips + strip) * kC * 16;
       float y[4];
 #pragma unroll
+      for (int r = 0; r < 4; ++r) y[r] = -eg[r] * (bt[r] * W[r]);
+      put3<kTok>(Yl, TP, lr, row0, y);
+#pragma unroll
       for (int r = 0; r < 4; ++r) {
         wo[(row0 + r) * 16 + lr] = W[r];
-        const float dn = bt[r] * W[r];
-        y[r] = -eg[r] * dn;
-        if (row0 + r < n) store_scalar(t.dv, ((size_t)(first + row0 + r) * p.hv + h) * p.dv + col, dn, NT == 1);
-      }
-      put3<kTok>(Yl, TP, lr, row0, y);
-    }
-    __syncthreads();
-    if (srows) {
-      const size_t at = ((size_t)slot * p.hk + kh) * (DKP / 16) * 2 * NT * 64;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        S[m] = S[m] * eGn;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const int f = (w * MT + m) * 2 + ks;
-          S[m] = mma<NT, 3>(load_frag<NT>(ws.qt + at, f, lane), get<3, kTok>(Xl, TP, lr, ks * 32 + lg * 8), S[m]);
-          S[m] = mma<NT, 3>(load_frag<NT>(ws.kt + at, f, lane), get<3, kTok>(Yl, TP, lr, ks * 32 + lg * 8), S[m]);
+        if (row0 + r < n) {
+          char* vb = static_cast<char*>(t.dv) + ((size_t)first * p.hv + h) * p.dv * es;
+          const uint32_t vo = (uint32_t)(row0 + r) * ostride + col * es;
+          if constexpr (NT == 1) *reinterpret_cast<bh*>(vb + vo) = f2bh(bt[r] * W[r]);
+          else *reinterpret_cast<float*>(vb + vo) = bt[r] * W[r];
         }
       }
     }
+    put_dout(next);                                  // the next chunk's: this one's have been read
+    load_dout(after);
+    load_second(next);
+    __syncthreads();
+    if (srows) {
+      Frag<3> yf[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) yf[ks] = get<3, kTok>(Yl, TP, lr, ks * 32 + lg * 8);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x4 b[3];
+        b[0] = S[m];
+        b[1] = b[2] = zero4();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) mma_by_term<NT, 3>(in.kt[m][ks], yf[ks], b);
+        S[m] = b[0] + (b[1] + b[2]);
+      }
+    }
+    put_state();
+    load_third(next);
+    __syncthreads();
   }
   if (t.dh0 && srows)
 #pragma unroll
@@ -358,7 +463,7 @@ hipError_t packed_scan_grad(const SeqProblem& p, const PackedTensors& t, const P
   const dim3 grid((unsigned)padded * f.strips);
   prof_begin(stream, GDN_KERNEL_PACKED_SCAN_GRAD);
 #define GDN_SCAN(NT, D) \
-  if (f.terms == NT && f.dkp == D) hipLaunchKernelGGL((packed_scan_grad_kernel<NT, D>), grid, dim3(256), 0, stream, p, t, s, padded);
+  if (f.terms == NT && f.dkp == D) hipLaunchKernelGGL((packed_scan_grad_kernel<NT, D>), grid, dim3(256), 0, stream, p, t, s);
   GDN_SCAN(1, 32) GDN_SCAN(1, 64) GDN_SCAN(1, 128) GDN_SCAN(3, 32) GDN_SCAN(3, 64) GDN_SCAN(3, 128)
 #undef GDN_SCAN
   const hipError_t e = hipGetLastError();

@@ -35,8 +35,8 @@ gdn_status check_seq(const gdn_seq_problem* pr, bool slots, gdn::SeqProblem* out
   struct { const char* name; long long given, width; } st[] = {
       {"q_stride", pr->q_stride, qk}, {"k_stride", pr->k_stride, qk}, {"v_stride", pr->v_stride, v}};
   for (const auto& s : st)
-    if (s.given != 0 && (s.given < s.width || s.given % unit || s.given > (1LL << 31)))
-      return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 0 or a multiple of 16 bytes in [%lld, 2^31] elements (got %lld)",
+    if (s.given != 0 && (s.given < s.width || s.given % unit || s.given > (1LL << 23)))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 0 or a multiple of 16 bytes in [%lld, 2^23] elements (got %lld)",
                   s.name, s.width, s.given);
   out->hk = pr->heads_k;
   out->hv = pr->heads_v;

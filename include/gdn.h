@@ -325,7 +325,7 @@ gdn_status gdn_plan_segment_tokens(const gdn_problem* problem, int32_t direction
  *   states      [rows, heads_v, d_k, d_v] fp32
  * Value head h reads key head h / (heads_v / heads_k).  Rows of q, k and v may
  * be further apart than their width (slices of one fused projection): *_stride
- * counts elements between tokens, a multiple of 16 bytes, 0 = dense; the heads
+ * counts elements between tokens, a multiple of 16 bytes up to 2^23 elements, 0 = dense; the heads
  * and widths inside a row are dense.  All other tensors are dense.
  * Pointers are 16-byte aligned, those of log_gate, beta, cu_seqlens and slots
  * 4-byte; pointers to tensors without elements may be NULL.  Streams, errors and validation are as at the top of this file. */

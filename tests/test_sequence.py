@@ -31,7 +31,7 @@ def message():
 
 BAD_SEQ = [("abi_version", 1), ("heads_k", 0), ("heads_k", 3), ("heads_v", 0), ("heads_v", 70000), ("d_k", 8), ("d_k", 24),
            ("d_k", 144), ("d_v", 0), ("d_v", 129), ("qkv_dtype", 5), ("out_dtype", -1), ("tokens", -1), ("tokens", 1 << 31),
-           ("q_stride", 127), ("q_stride", 64), ("k_stride", 132), ("v_stride", 255), ("v_stride", -256)]
+           ("q_stride", 127), ("q_stride", 64), ("k_stride", 132), ("v_stride", 255), ("v_stride", -256), ("k_stride", (1 << 23) + 8)]
 
 
 def call_decode(p, q=FAKE, k=FAKE, v=FAKE, g=FAKE, b=FAKE, state=FAKE, slots=FAKE, out=FAKE):
