@@ -71,29 +71,30 @@ __device__ __forceinline__ Frag<N> first_terms(const Frag<M>& f) {
   return o;
 }
 
-// x as the sum of N bf16 values, largest first.
+// Two values as the sums of N bf16 values each, largest first, packed by term:
+// one conversion, two unpackings and two subtractions for a term of a pair.
 template <int N>
-__device__ __forceinline__ void split(float x, bh (&o)[N]) {
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&o)[N]) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    o[i] = f2bh(x);
-    x -= bh2f(o[i]);
+    o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{x, y}, b2));   // round to nearest even
+    if (i + 1 < N) {
+      x -= __uint_as_float(o[i] << 16);
+      y -= __uint_as_float(o[i] & 0xffff0000u);
+    }
   }
 }
 
 template <int N>
 __device__ __forceinline__ Frag<N> split8(const float (&x)[8]) {
+  uint32_t o[4][N];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) split2<N>(x[2 * j], x[2 * j + 1], o[j]);
   Frag<N> f;
-  float r[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = x[j];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      f.t[i][j] = static_cast<__bf16>(r[j]);
-      if (i + 1 < N) r[j] -= static_cast<float>(f.t[i][j]);
-    }
+  for (int i = 0; i < N; ++i) f.t[i] = as_frag(make_uint4(o[0][i], o[1][i], o[2][i], o[3][i]));
   return f;
 }
 
@@ -125,11 +126,25 @@ __device__ __forceinline__ Frag<NT> frag_in(const void* p, size_t i) {
   }
 }
 
-// Element at a 32-bit byte offset from a uniform base (one scalar pair and one
-// vector register of address).
-template <typename T>
-__device__ __forceinline__ T at_byte(const void* base, uint32_t off) {
-  return *reinterpret_cast<const T*>(static_cast<const char*>(base) + off);
+// Buffer addressing: `bytes` from a uniform base, per-lane 32-bit offsets.  The
+// hardware returns 0 for loads and drops stores behind the end, so rows behind a
+// sequence's end and columns behind d_k (their lanes' offsets are kNowhere) need
+// no branches: a branch around a load would make every wait for a younger load
+// wait for it too.
+typedef __amdgpu_buffer_rsrc_t buf_t;
+constexpr uint32_t kNowhere = 0x80000000u;
+
+__device__ __forceinline__ buf_t buf(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+__device__ __forceinline__ uint4 buf_load16(buf_t b, uint32_t off) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+}
+
+// Bytes that a chunk's rows span: min(n, 64) rows of `width`, `stride` apart.
+__device__ __forceinline__ uint32_t span(int n, uint32_t stride, uint32_t width) {
+  return n > 0 ? (uint32_t)(min(n, kC) - 1) * stride + width : 0;
 }
 
 // One input value as it lies in memory, and its value.
@@ -144,6 +159,36 @@ struct RawIn<3> {
 __device__ __forceinline__ float raw_value(uint16_t x) { return bf16_bits_to_f32(x); }
 __device__ __forceinline__ float raw_value(float x) { return x; }
 
+// Four input values to and from LDS.
+template <int NT>
+__device__ __forceinline__ void put_values(typename RawIn<NT>::type* to, const typename RawIn<NT>::type (&x)[4]) {
+  if constexpr (NT == 1)
+    *reinterpret_cast<uint2*>(to) = make_uint2(x[0] | (uint32_t)x[1] << 16, x[2] | (uint32_t)x[3] << 16);
+  else
+    *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+template <int NT>
+__device__ __forceinline__ void get_values(const typename RawIn<NT>::type* from, float (&x)[4]) {
+  if constexpr (NT == 1) {
+    const uint2 v = *reinterpret_cast<const uint2*>(from);
+    x[0] = __uint_as_float(v.x << 16);
+    x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16);
+    x[3] = __uint_as_float(v.y & 0xffff0000u);
+  } else {
+    const float4 v = *reinterpret_cast<const float4*>(from);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  }
+}
+
+__device__ __forceinline__ void floats(uint4 v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x);
+  x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z);
+  x[3] = __uint_as_float(v.w);
+}
+
 // Eight consecutive input values as they lie in memory, split where they are used.
 template <int NT>
 struct RawFrag {
@@ -155,19 +200,33 @@ struct RawFrag<1> {
 };
 
 template <int NT>
-__device__ __forceinline__ RawFrag<NT> zero_raw() {
+__device__ __forceinline__ RawFrag<NT> raw_at(buf_t b, uint32_t off) {
   RawFrag<NT> r;
-  r.a = make_uint4(0, 0, 0, 0);
-  if constexpr (NT == 3) r.b = r.a;
+  r.a = buf_load16(b, off);
+  if constexpr (NT == 3) r.b = buf_load16(b, off + 16);
   return r;
 }
 
 template <int NT>
-__device__ __forceinline__ RawFrag<NT> raw_at(const void* base, uint32_t off) {
-  RawFrag<NT> r;
-  r.a = at_byte<uint4>(base, off);
-  if constexpr (NT == 3) r.b = at_byte<uint4>(base, off + 16);
-  return r;
+__device__ __forceinline__ typename RawIn<NT>::type value_at(buf_t b, uint32_t off) {
+  if constexpr (NT == 1) return __builtin_amdgcn_raw_buffer_load_b16(b, off, 0, 0);
+  else return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0));
+}
+
+// Stores x as bf16 (two bytes) or fp32 (four).
+template <int BYTES>
+__device__ __forceinline__ void store_at(buf_t b, uint32_t off, float x) {
+  if constexpr (BYTES == 2) __builtin_amdgcn_raw_buffer_store_b16(f2bh(x), b, off, 0, 0);
+  else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), b, off, 0, 0);
+}
+
+// The first N of LD terms of a fragment whose lane has its place at `off`.
+template <int N, int LD = N>
+__device__ __forceinline__ Frag<N> frag_at(buf_t b, uint32_t off) {
+  Frag<N> f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) f.t[i] = as_frag(buf_load16(b, off + i * 1024));
+  return f;
 }
 
 template <int NT>
@@ -203,33 +262,34 @@ __device__ __forceinline__ void store_frag(uint4* p, int frag, int lane, const F
   for (int i = 0; i < N; ++i) p[((size_t)frag * N + i) * 64 + lane] = as_bits(f.t[i]);
 }
 
-constexpr int kTok = 72;    // row stride (bf16) of a 16 x 64 operand tile in LDS
+// Operand tiles in LDS: 16 columns of K rows (K a multiple of 32) as N terms, in
+// fragment order, [term][K / 32][lane][8]: a fragment is read as 64 contiguous
+// vectors, and the four rows of a column that an accumulator lane holds are half
+// a vector, so a wavefront's write is contiguous too.  (Row-major tiles with a
+// padded stride lost half of the LDS cycles to bank conflicts.)
 
-// Writes four consecutive rows of a column as N terms: tile[term][column][row].
-template <int N, int LD>
-__device__ __forceinline__ void put(bh* tile, int plane, int column, int row, const float (&x)[4]) {
-  bh b[4][N];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) split<N>(x[r], b[r]);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    uint2 v;
-    v.x = b[0][i] | (uint32_t)b[1][i] << 16;
-    v.y = b[2][i] | (uint32_t)b[3][i] << 16;
-    *reinterpret_cast<uint2*>(tile + i * plane + column * LD + row) = v;
-  }
+// Elements from the tile's start to the lane that holds rows row .. row + 3 of a
+// column (row a multiple of 4).
+__device__ __forceinline__ int put_place(int column, int row) {
+  return ((row / 32 * 4 + row % 32 / 8) * 16 + column) * 8 + row % 8;
 }
 
-template <int LD>
-__device__ __forceinline__ void put3(bh* tile, int plane, int column, int row, const float (&x)[4]) {
-  put<3, LD>(tile, plane, column, row, x);
+// Writes four consecutive rows of a column; `to` points at their place.
+template <int N, int K>
+__device__ __forceinline__ void put(bh* to, const float (&x)[4]) {
+  uint32_t lo[N], hi[N];
+  split2<N>(x[0], x[1], lo);
+  split2<N>(x[2], x[3], hi);
+#pragma unroll
+  for (int i = 0; i < N; ++i) *reinterpret_cast<uint2*>(to + i * K * 16) = make_uint2(lo[i], hi[i]);
 }
 
-template <int N, int LD>
-__device__ __forceinline__ Frag<N> get(const bh* tile, int plane, int column, int row) {
+// Rows 32 ks .. of the tile; `from` points at the lane's vector of its first fragment.
+template <int N, int K>
+__device__ __forceinline__ Frag<N> get(const bh* from, int ks) {
   Frag<N> f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) f.t[i] = as_frag(*reinterpret_cast<const uint4*>(tile + i * plane + column * LD + row));
+  for (int i = 0; i < N; ++i) f.t[i] = as_frag(*reinterpret_cast<const uint4*>(from + i * K * 16 + ks * 512));
   return f;
 }
 

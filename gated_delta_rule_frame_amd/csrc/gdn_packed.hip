@@ -182,37 +182,33 @@ __global__ __launch_bounds__(256) void packed_prep_kernel(SeqProblem p, PackedTe
   }
 }
 
-// What a chunk's step reads from memory, as each phase of the step needs it.
-// A phase's registers are loaded for the next chunk as soon as the phase has
-// used them, so every load has a whole step to arrive.
-template <int NT, int DKP, int PT>
-struct ChunkIn {
-  static constexpr int KS = DKP / 32, MT = DKP >= 64 ? DKP / 64 : 1;
-  RawFrag<NT> k[KS], q[PT ? KS : 1];   // rows of K and Q
-  typename RawIn<NT>::type v[4];
-  float4 eG;
-  Frag<3> t1[2];                    // T' and the gates of the rows
-  float4 eD, beta;
-  Frag<NT> kt[MT][2];               // K^T
-  float eGn;
-  Frag<PT ? PT : 1> p[2];           // P
-};
-
+// The scan.  A step's chain of dependent work is
+//     N = V - e^G K S0   |   e = T' N, U, e^(Gn-G) U   |   S1   |
+// with a barrier (|) wherever a product's result becomes the next one's operand
+// through LDS.  One wavefront issues an instruction every four clocks at best, so
+// a step lasts as long as the instructions on this chain and little else: eight
+// wavefronts share the work such that the chain is short.  Wavefronts 0 - 3 (rows
+// 16 w .. of the chunk) run the first two phases; 4 - 7 have the output's
+// products, which fill the waits, and (all eight at d_k > 64) the rows of the
+// state.  Loads are issued two steps ahead into one of two sets of registers,
+// when the set has just been used: a step is shorter than a load from HBM.
+//
 // PT: terms of the output products (2 for a bf16 output, whose rounding is 2^9
 // times the third term; 3 for fp32), or 0: no outputs, but e and the state
 // before each chunk are left in the workspace for the gradients.
 template <int NT, int DKP, int PT>
-__global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
-  using In = ChunkIn<NT, DKP, PT>;
-  constexpr int KS = In::KS;                          // steps over d_k
-  constexpr int MT = In::MT;                          // state row tiles of a wavefront
-  constexpr int SLD = DKP + 8, SP = 16 * SLD, TP = 16 * kTok;
+__global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
+  constexpr int KS = DKP / 32;                        // steps over d_k
+  constexpr int SP = 16 * DKP, TP = 16 * kC;   // elements of a term's tile
+  constexpr uint32_t es = NT == 1 ? 2 : 4;            // bytes of an input element
+  constexpr uint32_t os = PT == 2 ? 2 : 4;            // of an output element
   __shared__ __align__(16) bh Sl[3 * SP];
   __shared__ __align__(16) bh Nl[3 * TP];
   __shared__ __align__(16) bh Ul[(PT ? PT : 1) * TP];
   __shared__ __align__(16) bh Dl[3 * TP];
+  __shared__ __align__(16) typename RawIn<NT>::type Vl[TP];
   __shared__ int earlier, next;
-  const int tid = threadIdx.x, lane = tid % 64, w = tid / 64;
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int lr = lane % 16, lg = lane / 16;
   int sh, strip;
   strip_of(blockIdx.x, p.dv / 16, &sh, &strip);
@@ -220,7 +216,10 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_kernel(SeqPr
   const int h = sh % p.hv, kh = h / (p.hv / p.hk);
   const int col = strip * 16 + lr;
   const int strips = p.dv / 16;
-  const bool srows = DKP >= 64 || w < DKP / 16;
+  const int w = wave & 3;                             // row tile of the chunk
+  const bool first_half = wave < 4;
+  const int srow = DKP > 64 ? wave : wave - 4;        // row tile of the state, if it has one
+  const bool has_state = srow >= 0 && srow < DKP / 16;
   int seq = sh / p.hv;
   const int slot_of = t.slots ? t.slots[seq] : seq;
   const bool kept = !t.slots || (slot_of >= 0 && slot_of < p.state_rows);
@@ -228,7 +227,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_kernel(SeqPr
     // sequences of the same state row belong to the workgroup of the first of them
     if (tid == 0) { earlier = 0; next = 0x7fffffff; }
     __syncthreads();
-    for (int i = tid; i < p.sequences; i += 256)
+    for (int i = tid; i < p.sequences; i += 512)
       if (t.slots[i] == slot_of) {
         if (i < seq) earlier = 1;
         else if (i > seq) atomicMin(&next, i);
@@ -239,192 +238,227 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_kernel(SeqPr
   const size_t state = ((size_t)slot_of * p.hv + h) * p.dk * p.dv;
   const int row0 = 16 * w + 4 * lg;                   // of this lane's four accumulator rows
   const int krow = 16 * w + lr;                       // of its operand rows
+  const int st0 = srow * 16 + 4 * lg;                 // of its four state rows
+  const int tok_place = put_place(lr, row0), st_place = put_place(lr, has_state ? st0 : 0);
+  int vector_zero = 0;
+  asm volatile("" : "+v"(vector_zero));               // a scalar load would be waited for with the LDS traffic
+  // per chunk, in elements of each workspace array
+  const size_t tri = (size_t)kTri * 3 * 64, tr = (size_t)(DKP / 16) * 2 * NT * 64;
 
   for (;;) {
     int start, end;
     seq_bounds(t.cu, seq, p.tokens, &start, &end);
     start = __builtin_amdgcn_readfirstlane(start);
     end = __builtin_amdgcn_readfirstlane(end);
-    const long long slot0 = start / kC + (long long)seq;
-    f32x4 S[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = (w * MT + m) * 16 + 4 * lg + r;
-        S[m][r] = t.h0 && kept && row < p.dk ? t.h0[state + (size_t)row * p.dv + col] : 0.f;
-      }
-    auto put_state = [&]() {
-      if (srows)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const float x[4] = {S[m][0], S[m][1], S[m][2], S[m][3]};
-          put3<SLD>(Sl, SP, lr, (w * MT + m) * 16 + 4 * lg, x);
-        }
-    };
-    In in;
-    // columns behind d_k are never loaded and stay zero
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      in.k[ks] = zero_raw<NT>();
-      if constexpr (PT > 0) in.q[ks] = zero_raw<NT>();
-    }
-    constexpr uint32_t es = NT == 1 ? 2 : 4;          // bytes of an input element
-    // Rows behind the sequence's end take its last row instead: their beta is 0 and their outputs are not stored.
-    auto load_rows = [&](int first, size_t cell) {
-      const int n = end - first;
-      const char* kb = static_cast<const char*>(t.k) + ((size_t)first * p.ks + kh * p.dk) * es;
-      const char* qb = static_cast<const char*>(t.q) + ((size_t)first * p.qs + kh * p.dk) * es;
-      const char* vb = static_cast<const char*>(t.v) + ((size_t)first * p.vs + h * p.dv) * es;
-      const uint32_t row = min(krow, n - 1);
-      const uint32_t ko = row * ((uint32_t)p.ks * es) + lg * 8 * es, qo = row * ((uint32_t)p.qs * es) + lg * 8 * es;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        if (ks * 32 + lg * 8 < p.dk) {
-          in.k[ks] = raw_at<NT>(kb, ko + ks * 32 * es);
-          if constexpr (PT > 0) in.q[ks] = raw_at<NT>(qb, qo + ks * 32 * es);
-        }
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        in.v[r] = at_byte<typename RawIn<NT>::type>(vb, (uint32_t)min(row0 + r, n - 1) * ((uint32_t)p.vs * es) + col * es);
-      in.eG = *reinterpret_cast<const float4*>(ws.gates + cell * 3 * kC + row0);
-    };
-    auto load_inverse = [&](size_t cell) {
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-        if (ks <= w / 2) in.t1[ks] = load_frag<3>(ws.t1 + cell * kTri * 3 * 64, w * 2 + ks, lane);
-      in.eD = *reinterpret_cast<const float4*>(ws.gates + cell * 3 * kC + kC + row0);
-      in.beta = *reinterpret_cast<const float4*>(ws.gates + cell * 3 * kC + 2 * kC + row0);
-    };
-    int vector_zero = 0;
-    asm volatile("" : "+v"(vector_zero));             // a scalar load would be waited for with the LDS traffic
-    auto load_state = [&](size_t cell, long long slot) {
-      if (srows) {
-        const uint4* kt = ws.kt + ((size_t)slot * p.hk + kh) * (DKP / 16) * 2 * NT * 64;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) in.kt[m][ks] = load_frag<NT>(kt, (w * MT + m) * 2 + ks, lane);
-      }
-      in.eGn = ws.gates[cell * 3 * kC + kC - 1 + vector_zero];
-      if constexpr (PT > 0)
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-          if (ks <= w / 2) in.p[ks] = load_frag<PT, 3>(ws.p + cell * kTri * 3 * 64, w * 2 + ks, lane);
-    };
-    put_state();
-    if (start < end) {
-      const size_t cell = (size_t)slot0 * p.hv + h;
-      load_rows(start, cell);
-      load_inverse(cell);
-      load_state(cell, slot0);
-    }
-    __syncthreads();
-    long long slot = slot0;
-    for (int first = start; first < end; first += kC) {
-      const int n = min(kC, end - first);
-      const bool more = first + kC < end;
-      const size_t cell = (size_t)slot * p.hv + h;
-      if (more) ++slot;                               // the last chunk's loads are repeated instead
-      const int nfirst = more ? first + kC : first;
-      const size_t ncell = (size_t)slot * p.hv + h;
-      f32x4 kS[3], qS = zero4();
-#pragma unroll
-      for (int i = 0; i < 3; ++i) kS[i] = zero4();
-      Frag<3> b[KS];
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) b[ks] = get<3, SLD>(Sl, SP, lr, ks * 32 + lg * 8);
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) mma_by_term<NT, 3>(frag_of<NT>(in.k[ks]), b[ks], kS);
-      float x[4];
-      const float eg[4] = {in.eG.x, in.eG.y, in.eG.z, in.eG.w};
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = fmaf(-eg[r], (kS[2][r] + kS[1][r]) + kS[0][r], row0 + r < n ? raw_value(in.v[r]) : 0.f);
-      put3<kTok>(Nl, TP, lr, row0, x);
-      if constexpr (PT > 0) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) qS = mma<NT, PT>(frag_of<NT>(in.q[ks]), first_terms<PT>(b[ks]), qS);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) qS[r] *= eg[r];
-      }
-      load_rows(nfirst, ncell);
-      __syncthreads();
-      f32x4 eT[3];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) eT[i] = zero4();
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-        if (ks <= w / 2) mma_by_term<3, 3>(in.t1[ks], get<3, kTok>(Nl, TP, lr, ks * 32 + lg * 8), eT);
-      const f32x4 e = (eT[2] + eT[1]) + eT[0];
-      const float ed[4] = {in.eD.x, in.eD.y, in.eD.z, in.eD.w}, bt[4] = {in.beta.x, in.beta.y, in.beta.z, in.beta.w};
-      float u[4], ud[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        u[r] = bt[r] * e[r];
-        ud[r] = ed[r] * u[r];
-      }
-      put3<kTok>(Dl, TP, lr, row0, ud);
-      if constexpr (PT > 0) put<PT, kTok>(Ul, TP, lr, row0, u);
-      load_inverse(ncell);
-      if constexpr (PT == 0) {
-        float* eo = ws.e + (cell * strips + strip) * kC * 16;
-        float* so = ws.s0 + (cell * strips + strip) * DKP * 16;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) eo[(row0 + r) * 16 + lr] = e[r];
-        if (srows)
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) so[((w * MT + m) * 16 + 4 * lg + r) * 16 + lr] = S[m][r];
-      }
-      __syncthreads();
-      if (srows) {
-        Frag<3> d[2];
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) d[ks] = get<3, kTok>(Dl, TP, lr, ks * 32 + lg * 8);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          f32x4 a[3];
-          a[0] = S[m] * in.eGn;
-          a[1] = a[2] = zero4();
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) mma_by_term<NT, 3>(in.kt[m][ks], d[ks], a);
-          S[m] = a[0] + (a[1] + a[2]);
-        }
-      }
-      put_state();
-      if constexpr (PT > 0) {
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-          if (ks <= w / 2) qS = mma<PT, PT>(in.p[ks], get<PT, kTok>(Ul, TP, lr, ks * 32 + lg * 8), qS);
+    const size_t slot = start / kC + (size_t)seq;
+    f32x4 S = zero4();
+    if (has_state) {
+      if (t.h0 && kept)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (row0 + r < n) {
-            constexpr uint32_t os = PT == 2 ? 2 : 4;
-            char* ob = static_cast<char*>(t.out) + ((size_t)first * p.hv + h) * p.dv * os;
-            const uint32_t oo = (uint32_t)(row0 + r) * ((uint32_t)(p.hv * p.dv) * os) + col * os;
-            if constexpr (PT == 2) *reinterpret_cast<bh*>(ob + oo) = f2bh(qS[r]);
-            else *reinterpret_cast<float*>(ob + oo) = qS[r];
-          }
-      }
-      load_state(ncell, slot);
-      __syncthreads();
+          if (st0 + r < p.dk) S[r] = t.h0[state + (size_t)(st0 + r) * p.dv + col];
+      const float x[4] = {S[0], S[1], S[2], S[3]};
+      put<3, DKP>(Sl + st_place, x);
     }
-    if (t.hT && kept && srows)
+    const int last = (end - start + kC - 1) / kC - 1;
+    // Loads go to the chunk two steps ahead; behind the last one there is nothing, and they return 0.
+    auto rows_of = [&](int c) { return end - start - c * kC; };
+    // The state's share of a step, by the wavefronts that have rows of it:
+    Frag<NT> kt[2][2];
+    float eGn[2];
+    const uint32_t kt_off = ((uint32_t)srow * 2 * NT * 64 + lane) * 16;
+    auto load_state = [&](int c, int set) {
+      const bool is = c <= last;
+      const buf_t kb = buf(ws.kt + ((slot + c) * p.hk + kh) * tr, is && has_state ? (uint32_t)tr * 16 : 0);
+      const buf_t gb = buf(ws.gates + ((slot + c) * p.hv + h) * 3 * kC, is ? kC * 4 : 0);
+      eGn[set] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(gb, (kC - 1) * 4 + vector_zero, 0, 0));
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int ks = 0; ks < 2; ++ks) kt[set][ks] = frag_at<NT>(kb, kt_off + ks * NT * 1024);
+    };
+    auto step_state = [&](int c, int set) {
+      if constexpr (PT == 0) {
+        const buf_t sb = buf(ws.s0 + (((slot + c) * p.hv + h) * strips + strip) * DKP * 16, has_state ? DKP * 16 * 4 : 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) store_at<4>(sb, ((st0 + r) * 16 + lr) * 4, S[r]);
+      }
+      f32x4 a[3];
+      a[0] = S * eGn[set];
+      a[1] = a[2] = zero4();
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) mma_by_term<NT, 3>(kt[set][ks], get<3, kC>(Dl + lane * 8, ks), a);
+      S = a[0] + (a[1] + a[2]);
+      const float x[4] = {S[0], S[1], S[2], S[3]};
+      if (has_state) put<3, DKP>(Sl + st_place, x);
+      load_state(c + 2, set);
+    };
+    uint32_t col_off[KS];                             // of this lane's columns of K and Q
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) col_off[ks] = ks * 32 + lg * 8 < p.dk ? (ks * 32 + lg * 8) * es : kNowhere;
+    const uint32_t dk_b = p.dk * es, dv_b = p.dv * es;
+    // of this lane's fragments in a lower triangle; there are none to the right of the diagonal
+    uint32_t tri_off[2];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) tri_off[ks] = ks <= w / 2 ? ((uint32_t)(w * 2 + ks) * 3 * 64 + lane) * 16 : kNowhere;
+    if (last < 0) {
+      // nothing to scan: the state stays as it is
+    } else if (first_half) {
+      const uint32_t ks_b = (uint32_t)p.ks * es;
+      RawFrag<NT> k[2][KS];
+      uint4 eG[2], eD[2], be[2];
+      Frag<3> t1[2][2];
+      auto load = [&](int c, int set) {
+        const int n = rows_of(c);
+        const buf_t kb = buf(static_cast<const char*>(t.k) + ((size_t)(start + c * kC) * p.ks + kh * p.dk) * es, span(n, ks_b, dk_b));
+        const size_t cl = (slot + c) * p.hv + h;
+        const buf_t tb = buf(ws.t1 + cl * tri, n > 0 ? (uint32_t)tri * 16 : 0);
+        const buf_t gb = buf(ws.gates + cl * 3 * kC, n > 0 ? 3 * kC * 4 : 0);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) k[set][ks] = raw_at<NT>(kb, krow * ks_b + col_off[ks]);
+        eG[set] = buf_load16(gb, row0 * 4);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) t1[set][ks] = frag_at<3>(tb, tri_off[ks]);
+        eD[set] = buf_load16(gb, (kC + row0) * 4);
+        be[set] = buf_load16(gb, (2 * kC + row0) * 4);
+      };
+      load(0, 0);
+      load_state(0, 0);
+      load(1, 1);
+      load_state(1, 1);
+      __syncthreads();
+      auto step = [&](int c, int set) {
+        __builtin_amdgcn_s_setprio(3);
+        f32x4 a[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) a[i] = zero4();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) mma_by_term<NT, 3>(frag_of<NT>(k[set][ks]), get<3, DKP>(Sl + lane * 8, ks), a);
+        float x[4], eg[4], ed[4], bt[4];
+        floats(eG[set], eg);
+        get_values<NT>(Vl + (w * 64 + lane) * 4, x);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = fmaf(-eg[r], (a[2][r] + a[1][r]) + a[0][r], x[r]);
+        put<3, kC>(Nl + tok_place, x);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 3; ++i) a[i] = zero4();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) mma_by_term<3, 3>(t1[set][ks], get<3, kC>(Nl + lane * 8, ks), a);
+        const f32x4 e = (a[2] + a[1]) + a[0];
+        floats(eD[set], ed);
+        floats(be[set], bt);
+        float ud[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = (w * MT + m) * 16 + 4 * lg + r;
-          if (row < p.dk) t.hT[state + (size_t)row * p.dv + col] = S[m][r];
+          x[r] = bt[r] * e[r];
+          ud[r] = ed[r] * x[r];
         }
+        put<3, kC>(Dl + tok_place, ud);
+        if constexpr (PT > 0) put<PT, kC>(Ul + tok_place, x);
+        __syncthreads();
+        if constexpr (DKP > 64) step_state(c, set);
+        __builtin_amdgcn_s_setprio(0);
+        load(c + 2, set);
+        if constexpr (PT == 0) {
+          const buf_t eb = buf(ws.e + (((slot + c) * p.hv + h) * strips + strip) * kC * 16, kC * 16 * 4);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) store_at<4>(eb, ((row0 + r) * 16 + lr) * 4, e[r]);
+        }
+        __syncthreads();
+      };
+      for (int c = 0; c <= last; c += 2) {
+        step(c, 0);
+        if (c < last) step(c + 1, 1);
+      }
+    } else {
+      const uint32_t qs_b = (uint32_t)p.qs * es, vs_b = (uint32_t)p.vs * es, os_b = (uint32_t)(p.hv * p.dv) * os;
+      RawFrag<NT> q[2][KS];
+      typename RawIn<NT>::type v[2][4];
+      uint4 eG[2];
+      Frag<PT ? PT : 1> pf[2][2];
+      auto load = [&](int c, int set) {
+        const int n = rows_of(c);
+        const size_t first = start + (size_t)c * kC;
+        if constexpr (PT > 0) {
+          const buf_t qb = buf(static_cast<const char*>(t.q) + (first * p.qs + kh * p.dk) * es, span(n, qs_b, dk_b));
+          const buf_t gb = buf(ws.gates + ((slot + c) * p.hv + h) * 3 * kC, n > 0 ? kC * 4 : 0);
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) q[set][ks] = raw_at<NT>(qb, krow * qs_b + col_off[ks]);
+          eG[set] = buf_load16(gb, row0 * 4);
+        }
+        const buf_t vb = buf(static_cast<const char*>(t.v) + (first * p.vs + h * p.dv) * es, span(n, vs_b, dv_b));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[set][r] = value_at<NT>(vb, (row0 + r) * vs_b + col * es);
+      };
+      auto load_p = [&](int c, int set) {
+        if constexpr (PT > 0) {
+          const buf_t pb = buf(ws.p + ((slot + c) * p.hv + h) * tri, c <= last ? (uint32_t)tri * 16 : 0);
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) pf[set][ks] = frag_at<PT, 3>(pb, tri_off[ks]);
+        }
+      };
+      // a chunk's V goes into LDS a step ahead, as columns of four rows for the first half
+      load(0, 0);
+      load_p(0, 0);
+      load_state(0, 0);
+      put_values<NT>(Vl + (w * 64 + lane) * 4, v[0]);
+      load(1, 1);
+      load_p(1, 1);
+      load_state(1, 1);
+      __syncthreads();
+      f32x4 o = zero4();
+      // P U of chunk c and its store, beside the next step's first phase
+      auto finish = [&](int c, int set) {
+        if constexpr (PT > 0) {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) o = mma<PT, PT>(pf[set][ks], get<PT, kC>(Ul + lane * 8, ks), o);
+          const buf_t ob = buf(static_cast<char*>(t.out) + ((start + (size_t)c * kC) * p.hv + h) * p.dv * os,
+                               span(rows_of(c), os_b, p.dv * os));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) store_at<os>(ob, (row0 + r) * os_b + col * os, o[r]);
+          load_p(c + 2, set);
+        }
+      };
+      auto step = [&](int c, int set) {
+        if constexpr (PT > 0)
+          if (c > 0) finish(c - 1, set ^ 1);
+        __syncthreads();
+        put_values<NT>(Vl + (w * 64 + lane) * 4, v[set ^ 1]);
+        if constexpr (PT > 0) {
+          float eg[4];
+          floats(eG[set], eg);
+          o = zero4();
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) o = mma<NT, PT>(frag_of<NT>(q[set][ks]), get<PT, DKP>(Sl + lane * 8, ks), o);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[r] *= eg[r];
+        }
+        load(c + 2, set);
+        __syncthreads();
+        __builtin_amdgcn_s_setprio(3);
+        step_state(c, set);
+        __builtin_amdgcn_s_setprio(0);
+        __syncthreads();
+      };
+      step(0, 0);
+      for (int c = 1; c <= last; c += 2) {
+        step(c, 1);
+        if (c < last) step(c + 1, 0);
+      }
+      if (last & 1) finish(last, 1);
+      else finish(last, 0);
+    }
+    if (t.hT && kept && has_state)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (st0 + r < p.dk) t.hT[state + (size_t)(st0 + r) * p.dv + col] = S[r];
     if (!t.slots || !kept || next == 0x7fffffff) break;
     // the next sequence of this state row (rare)
+    __syncthreads();
     seq = next;
     __syncthreads();
     if (tid == 0) next = 0x7fffffff;
     __syncthreads();
-    for (int i = seq + 1 + tid; i < p.sequences; i += 256)
+    for (int i = seq + 1 + tid; i < p.sequences; i += 512)
       if (t.slots[i] == slot_of) atomicMin(&next, i);
     __syncthreads();
   }
@@ -494,9 +528,9 @@ hipError_t packed_scan(const SeqProblem& p, const PackedTensors& t, const Packed
   prof_begin(stream, GDN_KERNEL_PACKED_SCAN);
 #define GDN_SCAN(NT, D)                                                                                                          \
   if (f.terms == NT && f.dkp == D) {                                                                                             \
-    if (grad) hipLaunchKernelGGL((packed_scan_kernel<NT, D, 0>), grid, dim3(256), 0, stream, p, t, s);                   \
-    else if (p.out_bf16) hipLaunchKernelGGL((packed_scan_kernel<NT, D, 2>), grid, dim3(256), 0, stream, p, t, s);        \
-    else hipLaunchKernelGGL((packed_scan_kernel<NT, D, 3>), grid, dim3(256), 0, stream, p, t, s);                        \
+    if (grad) hipLaunchKernelGGL((packed_scan_kernel<NT, D, 0>), grid, dim3(512), 0, stream, p, t, s);                   \
+    else if (p.out_bf16) hipLaunchKernelGGL((packed_scan_kernel<NT, D, 2>), grid, dim3(512), 0, stream, p, t, s);        \
+    else hipLaunchKernelGGL((packed_scan_kernel<NT, D, 3>), grid, dim3(512), 0, stream, p, t, s);                        \
   }
   GDN_SCAN(1, 32) GDN_SCAN(1, 64) GDN_SCAN(1, 128) GDN_SCAN(3, 32) GDN_SCAN(3, 64) GDN_SCAN(3, 128)
 #undef GDN_SCAN

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(
   using In = GradIn<NT, DKP>;
   constexpr int KS = In::KS;
   constexpr int MT = In::MT;
-  constexpr int SLD = DKP + 8, SP = 16 * SLD, TP = 16 * kTok;
+  constexpr int SP = 16 * DKP, TP = 16 * kC;   // elements of a term's tile
   __shared__ __align__(16) bh Sl[3 * SP];           // dS
   __shared__ __align__(16) bh Ol[NT * TP];          // dO
   __shared__ __align__(16) bh Xl[3 * TP];           // e^G dO
@@ -70,6 +70,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(
   end = __builtin_amdgcn_readfirstlane(end);
   const long long slot0 = start / kC + (long long)seq;
   const int row0 = 16 * w + 4 * lg, krow = 16 * w + lr;
+  const int tok_place = put_place(lr, row0);
   auto cell_of = [&](int c) { return (size_t)(slot0 + c) * p.hv + h; };
 
   f32x4 S[MT];
@@ -85,46 +86,41 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const float x[4] = {S[m][0], S[m][1], S[m][2], S[m][3]};
-        put3<SLD>(Sl, SP, lr, (w * MT + m) * 16 + 4 * lg, x);
+        put<3, DKP>(Sl + put_place(lr, (w * MT + m) * 16 + 4 * lg), x);
       }
   };
   In in;
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks) in.k[ks] = zero_raw<NT>();   // columns behind d_k are never loaded and stay zero
   constexpr uint32_t es = NT == 1 ? 2 : 4;           // bytes of an input element
   const uint32_t ostride = (uint32_t)(p.hv * p.dv) * es;
-  // Rows behind the sequence's end take its last row instead, where their beta is 0; dO's are set to 0.
   auto load_dout = [&](int c) {
     const int first = start + c * kC, n = end - first;
-    const char* ob = static_cast<const char*>(t.dout) + ((size_t)first * p.hv + h) * p.dv * es;
+    const buf_t ob = buf(static_cast<const char*>(t.dout) + ((size_t)first * p.hv + h) * p.dv * es, span(n, ostride, p.dv * es));
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      in.dout[r] = at_byte<typename RawIn<NT>::type>(ob, (uint32_t)min(row0 + r, n - 1) * ostride + col * es);
+    for (int r = 0; r < 4; ++r) in.dout[r] = value_at<NT>(ob, (row0 + r) * ostride + col * es);
     in.deG = *reinterpret_cast<const float4*>(ws.gates + cell_of(c) * 3 * kC + row0);
   };
   // chunk c's four tokens of this lane, plain and times e^G, as operand columns
-  auto put_dout = [&](int c) {
-    const int n = end - (start + c * kC);
+  auto put_dout = [&]() {
     const float eg[4] = {in.deG.x, in.deG.y, in.deG.z, in.deG.w};
     float x[4], y[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      x[r] = row0 + r < n ? raw_value(in.dout[r]) : 0.f;
+      x[r] = raw_value(in.dout[r]);
       y[r] = eg[r] * x[r];
     }
-    put<NT, kTok>(Ol, TP, lr, row0, x);
-    put3<kTok>(Xl, TP, lr, row0, y);
+    put<NT, kC>(Ol + tok_place, x);
+    put<3, kC>(Xl + tok_place, y);
   };
   int vector_zero = 0;
   asm volatile("" : "+v"(vector_zero));             // a scalar load would be waited for with the LDS traffic
   auto load_first = [&](int c) {
     const int first = start + c * kC, n = end - first;
     const size_t cell = cell_of(c);
-    const char* kb = static_cast<const char*>(t.k) + ((size_t)first * p.ks + kh * p.dk) * es;
-    const uint32_t ko = (uint32_t)min(krow, n - 1) * ((uint32_t)p.ks * es) + lg * 8 * es;
+    const uint32_t ks_b = (uint32_t)p.ks * es;
+    const buf_t kb = buf(static_cast<const char*>(t.k) + ((size_t)first * p.ks + kh * p.dk) * es, span(n, ks_b, p.dk * es));
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
-      if (ks * 32 + lg * 8 < p.dk) in.k[ks] = raw_at<NT>(kb, ko + ks * 32 * es);
+      in.k[ks] = raw_at<NT>(kb, ks * 32 + lg * 8 < p.dk ? krow * ks_b + (ks * 32 + lg * 8) * es : kNowhere);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
       if (ks >= w / 2) in.p[ks] = load_frag<3>(ws.p + cell * kTri * 3 * 64, w * 2 + ks, lane);
@@ -158,7 +154,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(
   const int last = (end - start + kC - 1) / kC - 1;
   if (last >= 0) {
     load_dout(last);
-    put_dout(last);
+    put_dout();
     load_dout(last ? last - 1 : 0);
     load_first(last);
     load_second(last);
@@ -174,23 +170,23 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(
 #pragma unroll
     for (int i = 0; i < 3; ++i) a[i] = zero4();
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) mma_by_term<NT, 3>(frag_of<NT>(in.k[ks]), get<3, SLD>(Sl, SP, lr, ks * 32 + lg * 8), a);
+    for (int ks = 0; ks < KS; ++ks) mma_by_term<NT, 3>(frag_of<NT>(in.k[ks]), get<3, DKP>(Sl + lane * 8, ks), a);
     const float ed[4] = {in.eD.x, in.eD.y, in.eD.z, in.eD.w};
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
-      if (ks >= w / 2) u = mma<3, NT>(in.p[ks], get<NT, kTok>(Ol, TP, lr, ks * 32 + lg * 8), u);
+      if (ks >= w / 2) u = mma<3, NT>(in.p[ks], get<NT, kC>(Ol + lane * 8, ks), u);
     {
       float x[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[r] = fmaf(ed[r], (a[2][r] + a[1][r]) + a[0][r], u[r]);
-      put3<kTok>(Ul, TP, lr, row0, x);
+      put<3, kC>(Ul + tok_place, x);
     }
     if (srows) {
       // Q^T (e^G dO) needs nothing of this step: it fills the wait for the barrier
       float* so = ws.ds + (cell * strips + strip) * DKP * 16;
       Frag<3> xf[2];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) xf[ks] = get<3, kTok>(Xl, TP, lr, ks * 32 + lg * 8);
+      for (int ks = 0; ks < 2; ++ks) xf[ks] = get<3, kC>(Xl + lane * 8, ks);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -206,34 +202,30 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(
     for (int i = 0; i < 3; ++i) a[i] = zero4();
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
-      if (ks >= w / 2) mma_by_term<3, 3>(in.t2[ks], get<3, kTok>(Ul, TP, lr, ks * 32 + lg * 8), a);
+      if (ks >= w / 2) mma_by_term<3, 3>(in.t2[ks], get<3, kC>(Ul + lane * 8, ks), a);
     {
       const f32x4 W = (a[2] + a[1]) + a[0];
       const float eg[4] = {in.eG.x, in.eG.y, in.eG.z, in.eG.w}, bt[4] = {in.beta.x, in.beta.y, in.beta.z, in.beta.w};
       float* wo = ws.w + (cell * strips + strip) * kC * 16;
+      const buf_t vb = buf(static_cast<char*>(t.dv) + ((size_t)first * p.hv + h) * p.dv * es, span(n, ostride, p.dv * es));
       float y[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) y[r] = -eg[r] * (bt[r] * W[r]);
-      put3<kTok>(Yl, TP, lr, row0, y);
+      put<3, kC>(Yl + tok_place, y);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         wo[(row0 + r) * 16 + lr] = W[r];
-        if (row0 + r < n) {
-          char* vb = static_cast<char*>(t.dv) + ((size_t)first * p.hv + h) * p.dv * es;
-          const uint32_t vo = (uint32_t)(row0 + r) * ostride + col * es;
-          if constexpr (NT == 1) *reinterpret_cast<bh*>(vb + vo) = f2bh(bt[r] * W[r]);
-          else *reinterpret_cast<float*>(vb + vo) = bt[r] * W[r];
-        }
+        store_at<es>(vb, (row0 + r) * ostride + col * es, bt[r] * W[r]);
       }
     }
-    put_dout(next);                                  // the next chunk's: this one's have been read
+    put_dout();                                      // the next chunk's: this one's have been read
     load_dout(after);
     load_second(next);
     __syncthreads();
     if (srows) {
       Frag<3> yf[2];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) yf[ks] = get<3, kTok>(Yl, TP, lr, ks * 32 + lg * 8);
+      for (int ks = 0; ks < 2; ++ks) yf[ks] = get<3, kC>(Yl + lane * 8, ks);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         f32x4 b[3];
