@@ -39,6 +39,9 @@ __device__ __forceinline__ f32x4 mfma(frag_t a, frag_t b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// 2^x in one instruction (1 ulp; results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
 // c += a b over the term pairs that matter.
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4 c) {

@@ -20,30 +20,55 @@ constexpr int kLd = 68;     // row stride (floats) of a 64 x 64 fp32 tile in LDS
 // Gates below this are this: e^-10000 is 0 in fp32, and G stays finite for -inf.
 constexpr float kLowestGate = -10000.f;
 
+// Four accumulator values of rows (k) row0 .. row0 + 3 of a column, as N terms
+// into stored fragments [column tile][row half]: the same places as in an LDS tile.
+template <int N, int LD>
+__device__ __forceinline__ void store_quad(uint4* frags, int tile, int column, int row, const float (&x)[4]) {
+  uint32_t lo[N], hi[N];
+  split2<N>(x[0], x[1], lo);
+  split2<N>(x[2], x[3], hi);
+  bh* to = reinterpret_cast<bh*>(frags + (size_t)(tile * 2 + row / 32) * LD * 64) + put_place(column, row % 32);
+#pragma unroll
+  for (int i = 0; i < N; ++i) *reinterpret_cast<uint2*>(to + i * 512) = make_uint2(lo[i], hi[i]);
+}
+
+// One workgroup per cell; wavefront w has rows (tokens) 16 w .. of the 64 x 64
+// matrices.  Accumulators hold four rows of a column, which is half a vector of
+// the transposed matrix's fragment; so the products are taken in the order that
+// makes each result leave its registers as it is stored.
 template <int NT, int DKP, bool GRAD>
-__global__ __launch_bounds__(256) void packed_prep_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, long long slots) {
-  constexpr int NM = GRAD ? 2 : 1;
+__global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, long long slots) {
+  constexpr int NM = GRAD ? 2 : 1, KS = DKP / 32;
+  constexpr uint32_t es = NT == 1 ? 2 : 4;
   __shared__ double Gs[kC];
   __shared__ float bs[kC];
   __shared__ __align__(16) float A[NM][kC][kLd];
   __shared__ __align__(16) float T[NM][kC][kLd];
-  __shared__ __align__(16) float P[kC][kLd];
-  const int tid = threadIdx.x, lane = tid % 64, w = tid / 64;
+  const int tid = threadIdx.x, lane = tid % 64, w = __builtin_amdgcn_readfirstlane(tid / 64);
   const int lr = lane % 16, lg = lane / 16;
   const int rep = p.hv / p.hk;
   const long long cells = slots * p.hv;
+  const uint32_t ks_b = (uint32_t)p.ks * es, qs_b = (uint32_t)p.qs * es;
 
   for (long long cell = blockIdx.x; cell < cells; cell += gridDim.x) {
     const int h = (int)(cell % p.hv), kh = h / rep;
     const long long slot = cell / p.hv;
     int seq, first, n;
     if (!find_chunk(t.cu, p.sequences, p.tokens, slot, &seq, &first, &n)) continue;   // uniform over the workgroup
-    __syncthreads();
+    first = __builtin_amdgcn_readfirstlane(first);
+    n = __builtin_amdgcn_readfirstlane(n);
+    const buf_t kb = buf(static_cast<const char*>(t.k) + ((size_t)first * p.ks + kh * p.dk) * es, span(n, ks_b, p.dk * es));
+    const buf_t qb = buf(static_cast<const char*>(t.q) + ((size_t)first * p.qs + kh * p.dk) * es, span(n, qs_b, p.dk * es));
+    auto row_frag = [&](buf_t base, uint32_t stride, int tile, int ks) {
+      const int c = ks * 32 + lg * 8;
+      return frag_of<NT>(raw_at<NT>(base, c < p.dk ? (tile * 16 + lr) * stride + c * es : kNowhere));
+    };
+    __syncthreads();                                  // the previous cell's tiles have been read
     if (w == 0) {
       const size_t at = (size_t)(first + lane) * p.hv + h;
       float g = lane < n ? t.g[at] : 0.f;
       g = g < kLowestGate ? kLowestGate : g;
-      double G = g;
+      double G = g * 1.4426950408889634;              // in units of log 2: exp2 of the differences
 #pragma unroll
       for (int m = 1; m < 64; m <<= 1) {
         const double o = __shfl_up(G, m);
@@ -52,44 +77,97 @@ __global__ __launch_bounds__(256) void packed_prep_kernel(SeqProblem p, PackedTe
       Gs[lane] = G;
       bs[lane] = lane < n ? t.beta[at] : 0.f;
     }
-    // Gram tiles: wavefront w has rows 16 w .. + 16
+    // K K^T as (rows w, columns j); Q K^T the same way for P^T, or as (rows j, columns w) for P
     f32x4 kk[4], qk[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) kk[j] = qk[j] = zero4();
-    const char* kbase = static_cast<const char*>(t.k);
-    const char* qbase = static_cast<const char*>(t.q);
-    auto row_frag = [&](const char* base, long long stride, int tile, int ks) {
-      const int row = tile * 16 + lr, c = ks * 32 + lg * 8;
-      if (row < n && c < p.dk) return frag_in<NT>(base, (size_t)(first + row) * stride + kh * p.dk + c);
-      return zero_frag<NT>();
+    uint4* ktp = ws.kt + ((size_t)slot * p.hk + kh) * (DKP / 16) * 2 * NT * 64;
+    uint4* qtp = ws.qt + ((size_t)slot * p.hk + kh) * (DKP / 16) * 2 * NT * 64;
+    // Rows of an operand fragment to fragments of its transpose: a product with the identity, exact for each bf16 term.
+    auto transpose = [&](const Frag<NT>& f, uint4* to, int ks) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = lg * 8 + j == half * 16 + lr ? 1.f : 0.f;
+        const Frag<1> one = split8<1>(e);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const f32x4 d = mfma(f.t[i], one.t[0], zero4());
+          uint32_t v[2][1];
+          split2<1>(d[0], d[1], v[0]);
+          split2<1>(d[2], d[3], v[1]);
+          const int row = 16 * w + 4 * lg;
+          bh* o = reinterpret_cast<bh*>(to + ((size_t)((ks * 2 + half) * 2 + row / 32) * NT + i) * 64) + put_place(lr, row % 32);
+          *reinterpret_cast<uint2*>(o) = make_uint2(v[0][0], v[1][0]);
+        }
+      }
     };
 #pragma unroll
-    for (int ks = 0; ks < DKP / 32; ++ks) {
-      const Frag<NT> ak = row_frag(kbase, p.ks, w, ks), aq = row_frag(qbase, p.qs, w, ks);
+    for (int ks = 0; ks < KS; ++ks) {
+      const Frag<NT> ak = row_frag(kb, ks_b, w, ks), aq = row_frag(qb, qs_b, w, ks);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j <= w) {
-          const Frag<NT> b = j == w ? ak : row_frag(kbase, p.ks, j, ks);
+          const Frag<NT> b = j == w ? ak : row_frag(kb, ks_b, j, ks);
           kk[j] = mma<NT, NT>(ak, b, kk[j]);
-          qk[j] = mma<NT, NT>(aq, b, qk[j]);
+          qk[j] = GRAD ? mma<NT, NT>(aq, b, qk[j]) : mma<NT, NT>(b, aq, qk[j]);
         }
+      if (h % rep == 0) {
+        transpose(ak, ktp, ks);
+        if constexpr (GRAD) transpose(aq, qtp, ks);
+      }
     }
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
+    {
+      uint4* pp = ws.p + (size_t)cell * kTri * 3 * 64;
+      double Gr[4];
+      float br[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * w + 4 * lg + r, c = 16 * j + lr;
-        const float E = i >= c ? expf((float)(Gs[i] - Gs[c])) : 0.f;
-        const float b = i > c ? E * kk[j][r] : 0.f;
-        A[0][i][c] = b * bs[c];
-        if constexpr (GRAD) A[NM - 1][i][c] = b * bs[i];
-        P[i][c] = i >= c ? E * qk[j][r] : 0.f;
-        if (j > w) {
-          T[0][i][c] = 0.f;
-          if constexpr (GRAD) T[NM - 1][i][c] = 0.f;
+        Gr[r] = Gs[16 * w + 4 * lg + r];
+        br[r] = bs[16 * w + 4 * lg + r];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j <= w) {
+          const int c = 16 * j + lr;
+          const double Gc = Gs[c];
+          const float bc = bs[c];
+          float x[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * w + 4 * lg + r;
+            const float E = i >= c ? exp2_of((float)(Gr[r] - Gc)) : 0.f;
+            const float b = i > c ? E * kk[j][r] : 0.f;
+            A[0][i][c] = b * bc;
+            if constexpr (GRAD) {
+              A[NM - 1][i][c] = b * br[r];
+              x[r] = E * qk[j][r];
+            } else {
+              // qk[j] holds rows 16 j + 4 lg + r of K and the row 16 w + lr of Q
+              const int pi = 16 * w + lr, pj = 16 * j + 4 * lg + r;
+              x[r] = pi >= pj ? exp2_of((float)(Gs[pi] - Gs[pj])) * qk[j][r] : 0.f;
+            }
+          }
+          if constexpr (GRAD) store_quad<3, 3>(pp, j, lr, 16 * w + 4 * lg, x);          // P^T: row tile j, rows i
+          else if (p.out_bf16) store_quad<2, 3>(pp, w, lr, 16 * j + 4 * lg, x);         // P: row tile w, columns j
+          else store_quad<3, 3>(pp, w, lr, 16 * j + 4 * lg, x);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            T[0][16 * w + 4 * lg + r][16 * j + lr] = 0.f;
+            if constexpr (GRAD) T[NM - 1][16 * w + 4 * lg + r][16 * j + lr] = 0.f;
+          }
+          // the fragments on the diagonal's block row hold a block above it
+          const float z[4] = {0.f, 0.f, 0.f, 0.f};
+          if (j / 2 == w / 2) {
+            if constexpr (GRAD) store_quad<3, 3>(pp, j, lr, 16 * w + 4 * lg, z);
+            else store_quad<3, 3>(pp, w, lr, 16 * j + 4 * lg, z);
+          }
         }
       }
+    }
     __syncthreads();
     // (I + A)^-1: the 16 x 16 diagonal blocks by substitution, lane c a column
     {
@@ -99,7 +177,13 @@ __global__ __launch_bounds__(256) void packed_prep_kernel(SeqProblem p, PackedTe
       for (int i = 0; i < 16; ++i) {
         float s = i == lr ? 1.f : 0.f;
 #pragma unroll
-        for (int j = 0; j < i; ++j) s = fmaf(-A[m][o + i][o + j], x[j], s);
+        for (int j4 = 0; j4 < i; j4 += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(&A[m][o + i][o + j4]);
+          s = fmaf(-a.x, x[j4], s);
+          if (j4 + 1 < i) s = fmaf(-a.y, x[j4 + 1], s);
+          if (j4 + 2 < i) s = fmaf(-a.z, x[j4 + 2], s);
+          if (j4 + 3 < i) s = fmaf(-a.w, x[j4 + 3], s);
+        }
         x[i] = s;
       }
       if (lg < NM) {
@@ -116,68 +200,46 @@ __global__ __launch_bounds__(256) void packed_prep_kernel(SeqProblem p, PackedTe
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
           f32x4 x = zero4(), y = zero4();
-          for (int k = bj; k < bi; ++k)
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              x = __builtin_amdgcn_mfma_f32_16x16x4f32(A[m][16 * bi + lr][16 * k + 4 * s + lg],
-                                                       T[m][16 * k + 4 * s + lg][16 * bj + lr], x, 0, 0, 0);
-          // x holds rows 4 lg + r: any order of k that both operands share gives the product
+          for (int k = 0; k < d; ++k) {
+            // any order of k that both operands share gives the product: 4 lg + s
+            const float4 a = *reinterpret_cast<const float4*>(&A[m][16 * bi + lr][16 * (bj + k) + 4 * lg]);
+            const float* b = &T[m][16 * (bj + k) + 4 * lg][16 * bj + lr];
+            x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b[0], x, 0, 0, 0);
+            x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b[kLd], x, 0, 0, 0);
+            x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b[2 * kLd], x, 0, 0, 0);
+            x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b[3 * kLd], x, 0, 0, 0);
+          }
+          const float4 a = *reinterpret_cast<const float4*>(&T[m][16 * bi + lr][16 * bi + 4 * lg]);
+          const float at[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            y = __builtin_amdgcn_mfma_f32_16x16x4f32(T[m][16 * bi + lr][16 * bi + 4 * lg + r], x[r], y, 0, 0, 0);
+          for (int r = 0; r < 4; ++r) y = __builtin_amdgcn_mfma_f32_16x16x4f32(at[r], x[r], y, 0, 0, 0);
 #pragma unroll
           for (int r = 0; r < 4; ++r) T[m][16 * bi + 4 * lg + r][16 * bj + lr] = -y[r];
         }
       }
     }
     __syncthreads();
-    // out as fragments: row tile w; of the lower triangles only the column halves that hold any of it, of the transposed ones
-    // likewise
+    // out as fragments: of T' the column halves up to the diagonal, of T^T those from it on
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const int f = w * 2 + ks;
-      if (ks <= w / 2) {
+      if (ks <= w / 2)
         store_frag<3>(ws.t1 + (size_t)cell * kTri * 3 * 64, f, lane, frag_f32<3>(&T[0][16 * w + lr][32 * ks + 8 * lg]));
-        if constexpr (!GRAD)
-          store_frag<3>(ws.p + (size_t)cell * kTri * 3 * 64, f, lane, frag_f32<3>(&P[16 * w + lr][32 * ks + 8 * lg]));
-      }
       if constexpr (GRAD)
         if (ks >= w / 2) {
-          float x[8], y[8];
+          float x[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            x[j] = T[NM - 1][32 * ks + 8 * lg + j][16 * w + lr];
-            y[j] = P[32 * ks + 8 * lg + j][16 * w + lr];
-          }
+          for (int j = 0; j < 8; ++j) x[j] = T[NM - 1][32 * ks + 8 * lg + j][16 * w + lr];
           store_frag<3>(ws.t2 + (size_t)cell * kTri * 3 * 64, f, lane, split8<3>(x));
-          store_frag<3>(ws.p + (size_t)cell * kTri * 3 * 64, f, lane, split8<3>(y));
         }
     }
     if (tid < kC) {
       float* o = ws.gates + (size_t)cell * 3 * kC;
-      o[tid] = expf((float)Gs[tid]);
-      o[kC + tid] = expf((float)(Gs[kC - 1] - Gs[tid]));
+      o[tid] = exp2_of((float)Gs[tid]);
+      o[kC + tid] = exp2_of((float)(Gs[kC - 1] - Gs[tid]));
       o[2 * kC + tid] = bs[tid];
       if constexpr (GRAD) ws.g[(size_t)cell * kC + tid] = Gs[tid];
-    }
-    if (h % rep == 0) {
-      const size_t at = ((size_t)slot * p.hk + kh) * (DKP / 16) * 2 * NT * 64;
-      auto column_frag = [&](const void* base, long long stride, int mt, int ks) {
-        const int c = mt * 16 + lr;
-        Frag<NT> f;
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int row = ks * 32 + lg * 8 + j;
-          x[j] = c < p.dk && row < n ? elem_in<NT>(base, (size_t)(first + row) * stride + kh * p.dk + c) : 0.f;
-        }
-        f = split8<NT>(x);
-        return f;
-      };
-      for (int f = w; f < DKP / 16 * 2; f += 4) {
-        store_frag<NT>(ws.kt + at, f, lane, column_frag(t.k, p.ks, f / 2, f % 2));
-        if constexpr (GRAD) store_frag<NT>(ws.qt + at, f, lane, column_frag(t.q, p.qs, f / 2, f % 2));
-      }
     }
   }
 }
@@ -190,14 +252,18 @@ __global__ __launch_bounds__(256) void packed_prep_kernel(SeqProblem p, PackedTe
 // wavefronts share the work such that the chain is short.  Wavefronts 0 - 3 (rows
 // 16 w .. of the chunk) run the first two phases; 4 - 7 have the output's
 // products, which fill the waits, and (all eight at d_k > 64) the rows of the
-// state.  Loads are issued two steps ahead into one of two sets of registers,
-// when the set has just been used: a step is shorter than a load from HBM.
+// state.  Loads are issued SETS steps ahead, into registers that have just been
+// used.
 //
 // PT: terms of the output products (2 for a bf16 output, whose rounding is 2^9
 // times the third term; 3 for fp32), or 0: no outputs, but e and the state
 // before each chunk are left in the workspace for the gradients.
-template <int NT, int DKP, int PT>
-__global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
+//
+// SETS: 2 where few workgroups leave a CU to each, so only the step's own length
+// counts; 1 where there are enough of them for two on a CU: half the operand
+// registers, loads one step ahead, and the other workgroup fills the waits.
+template <int NT, int DKP, int PT, int SETS>
+__global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
   constexpr int KS = DKP / 32;                        // steps over d_k
   constexpr int SP = 16 * DKP, TP = 16 * kC;   // elements of a term's tile
   constexpr uint32_t es = NT == 1 ? 2 : 4;            // bytes of an input element
@@ -261,11 +327,11 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
       put<3, DKP>(Sl + st_place, x);
     }
     const int last = (end - start + kC - 1) / kC - 1;
-    // Loads go to the chunk two steps ahead; behind the last one there is nothing, and they return 0.
+    // Loads behind the last chunk return 0.
     auto rows_of = [&](int c) { return end - start - c * kC; };
     // The state's share of a step, by the wavefronts that have rows of it:
-    Frag<NT> kt[2][2];
-    float eGn[2];
+    Frag<NT> kt[SETS][2];
+    float eGn[SETS];
     const uint32_t kt_off = ((uint32_t)srow * 2 * NT * 64 + lane) * 16;
     auto load_state = [&](int c, int set) {
       const bool is = c <= last;
@@ -289,7 +355,7 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
       S = a[0] + (a[1] + a[2]);
       const float x[4] = {S[0], S[1], S[2], S[3]};
       if (has_state) put<3, DKP>(Sl + st_place, x);
-      load_state(c + 2, set);
+      load_state(c + SETS, set);
     };
     uint32_t col_off[KS];                             // of this lane's columns of K and Q
 #pragma unroll
@@ -303,9 +369,9 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
       // nothing to scan: the state stays as it is
     } else if (first_half) {
       const uint32_t ks_b = (uint32_t)p.ks * es;
-      RawFrag<NT> k[2][KS];
-      uint4 eG[2], eD[2], be[2];
-      Frag<3> t1[2][2];
+      RawFrag<NT> k[SETS][KS];
+      uint4 eG[SETS], eD[SETS], be[SETS];
+      Frag<3> t1[SETS][2];
       auto load = [&](int c, int set) {
         const int n = rows_of(c);
         const buf_t kb = buf(static_cast<const char*>(t.k) + ((size_t)(start + c * kC) * p.ks + kh * p.dk) * es, span(n, ks_b, dk_b));
@@ -322,11 +388,13 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
       };
       load(0, 0);
       load_state(0, 0);
-      load(1, 1);
-      load_state(1, 1);
+      if constexpr (SETS == 2) {
+        load(1, 1);
+        load_state(1, 1);
+      }
       __syncthreads();
       auto step = [&](int c, int set) {
-        __builtin_amdgcn_s_setprio(3);
+        if constexpr (SETS == 2) __builtin_amdgcn_s_setprio(3);
         f32x4 a[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) a[i] = zero4();
@@ -356,8 +424,8 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
         if constexpr (PT > 0) put<PT, kC>(Ul + tok_place, x);
         __syncthreads();
         if constexpr (DKP > 64) step_state(c, set);
-        __builtin_amdgcn_s_setprio(0);
-        load(c + 2, set);
+        if constexpr (SETS == 2) __builtin_amdgcn_s_setprio(0);
+        load(c + SETS, set);
         if constexpr (PT == 0) {
           const buf_t eb = buf(ws.e + (((slot + c) * p.hv + h) * strips + strip) * kC * 16, kC * 16 * 4);
 #pragma unroll
@@ -365,29 +433,33 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
         }
         __syncthreads();
       };
-      for (int c = 0; c <= last; c += 2) {
+      for (int c = 0; c <= last; c += SETS) {
         step(c, 0);
-        if (c < last) step(c + 1, 1);
+        if constexpr (SETS == 2)
+          if (c < last) step(c + 1, 1);
       }
     } else {
       const uint32_t qs_b = (uint32_t)p.qs * es, vs_b = (uint32_t)p.vs * es, os_b = (uint32_t)(p.hv * p.dv) * os;
-      RawFrag<NT> q[2][KS];
-      typename RawIn<NT>::type v[2][4];
-      uint4 eG[2];
-      Frag<PT ? PT : 1> pf[2][2];
+      RawFrag<NT> q[SETS][KS];
+      typename RawIn<NT>::type v[4];
+      uint4 eG[SETS];
+      Frag<PT ? PT : 1> pf[SETS][2];
       auto load = [&](int c, int set) {
-        const int n = rows_of(c);
-        const size_t first = start + (size_t)c * kC;
         if constexpr (PT > 0) {
+          const int n = rows_of(c);
+          const size_t first = start + (size_t)c * kC;
           const buf_t qb = buf(static_cast<const char*>(t.q) + (first * p.qs + kh * p.dk) * es, span(n, qs_b, dk_b));
           const buf_t gb = buf(ws.gates + ((slot + c) * p.hv + h) * 3 * kC, n > 0 ? kC * 4 : 0);
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) q[set][ks] = raw_at<NT>(qb, krow * qs_b + col_off[ks]);
           eG[set] = buf_load16(gb, row0 * 4);
         }
-        const buf_t vb = buf(static_cast<const char*>(t.v) + (first * p.vs + h * p.dv) * es, span(n, vs_b, dv_b));
+      };
+      auto load_v = [&](int c) {
+        const buf_t vb = buf(static_cast<const char*>(t.v) + ((start + (size_t)c * kC) * p.vs + h * p.dv) * es,
+                             span(rows_of(c), vs_b, dv_b));
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[set][r] = value_at<NT>(vb, (row0 + r) * vs_b + col * es);
+        for (int r = 0; r < 4; ++r) v[r] = value_at<NT>(vb, (row0 + r) * vs_b + col * es);
       };
       auto load_p = [&](int c, int set) {
         if constexpr (PT > 0) {
@@ -397,13 +469,17 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
         }
       };
       // a chunk's V goes into LDS a step ahead, as columns of four rows for the first half
+      load_v(0);
       load(0, 0);
       load_p(0, 0);
       load_state(0, 0);
-      put_values<NT>(Vl + (w * 64 + lane) * 4, v[0]);
-      load(1, 1);
-      load_p(1, 1);
-      load_state(1, 1);
+      put_values<NT>(Vl + (w * 64 + lane) * 4, v);
+      load_v(1);
+      if constexpr (SETS == 2) {
+        load(1, 1);
+        load_p(1, 1);
+        load_state(1, 1);
+      }
       __syncthreads();
       f32x4 o = zero4();
       // P U of chunk c and its store, beside the next step's first phase
@@ -415,14 +491,15 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
                                span(rows_of(c), os_b, p.dv * os));
 #pragma unroll
           for (int r = 0; r < 4; ++r) store_at<os>(ob, (row0 + r) * os_b + col * os, o[r]);
-          load_p(c + 2, set);
+          load_p(c + SETS, set);
         }
       };
       auto step = [&](int c, int set) {
         if constexpr (PT > 0)
-          if (c > 0) finish(c - 1, set ^ 1);
+          if (c > 0) finish(c - 1, SETS == 2 ? set ^ 1 : 0);
         __syncthreads();
-        put_values<NT>(Vl + (w * 64 + lane) * 4, v[set ^ 1]);
+        put_values<NT>(Vl + (w * 64 + lane) * 4, v);
+        load_v(c + 2);
         if constexpr (PT > 0) {
           float eg[4];
           floats(eG[set], eg);
@@ -432,19 +509,20 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
 #pragma unroll
           for (int r = 0; r < 4; ++r) o[r] *= eg[r];
         }
-        load(c + 2, set);
+        load(c + SETS, set);
         __syncthreads();
-        __builtin_amdgcn_s_setprio(3);
+        if constexpr (SETS == 2) __builtin_amdgcn_s_setprio(3);
         step_state(c, set);
-        __builtin_amdgcn_s_setprio(0);
+        if constexpr (SETS == 2) __builtin_amdgcn_s_setprio(0);
         __syncthreads();
       };
       step(0, 0);
-      for (int c = 1; c <= last; c += 2) {
-        step(c, 1);
-        if (c < last) step(c + 1, 0);
+      for (int c = 1; c <= last; c += SETS) {
+        step(c, SETS - 1);
+        if constexpr (SETS == 2)
+          if (c < last) step(c + 1, 0);
       }
-      if (last & 1) finish(last, 1);
+      if (SETS == 2 && (last & 1)) finish(last, SETS - 1);
       else finish(last, 0);
     }
     if (t.hT && kept && has_state)
@@ -525,15 +603,20 @@ hipError_t packed_scan(const SeqProblem& p, const PackedTensors& t, const Packed
   const PackedPlan f = packed_plan(p);
   const int padded = (p.sequences * p.hv + 7) / 8 * 8;
   const dim3 grid((unsigned)padded * f.strips);
+  const bool two = grid.x > 256;   // more workgroups than CUs
   prof_begin(stream, GDN_KERNEL_PACKED_SCAN);
-#define GDN_SCAN(NT, D)                                                                                                          \
-  if (f.terms == NT && f.dkp == D) {                                                                                             \
-    if (grad) hipLaunchKernelGGL((packed_scan_kernel<NT, D, 0>), grid, dim3(512), 0, stream, p, t, s);                   \
-    else if (p.out_bf16) hipLaunchKernelGGL((packed_scan_kernel<NT, D, 2>), grid, dim3(512), 0, stream, p, t, s);        \
-    else hipLaunchKernelGGL((packed_scan_kernel<NT, D, 3>), grid, dim3(512), 0, stream, p, t, s);                        \
+#define GDN_SCAN2(NT, D, PT)                                                                                          \
+  if (two) hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 1>), grid, dim3(512), 0, stream, p, t, s);               \
+  else hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 2>), grid, dim3(512), 0, stream, p, t, s);
+#define GDN_SCAN(NT, D)                      \
+  if (f.terms == NT && f.dkp == D) {         \
+    if (grad) { GDN_SCAN2(NT, D, 0) }        \
+    else if (p.out_bf16) { GDN_SCAN2(NT, D, 2) } \
+    else { GDN_SCAN2(NT, D, 3) }             \
   }
   GDN_SCAN(1, 32) GDN_SCAN(1, 64) GDN_SCAN(1, 128) GDN_SCAN(3, 32) GDN_SCAN(3, 64) GDN_SCAN(3, 128)
 #undef GDN_SCAN
+#undef GDN_SCAN2
   const hipError_t e = hipGetLastError();
   prof_end(stream, GDN_KERNEL_PACKED_SCAN);
   return e;

@@ -352,7 +352,7 @@ __global__ __launch_bounds__(256, 1) void packed_grads_kernel(SeqProblem p, Pack
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = 16 * j + lr;
-          const float E = i >= c ? expf((float)(Gs[i] - Gs[c])) * bs[c] : 0.f;
+          const float E = i >= c ? exp2_of((float)(Gs[i] - Gs[c])) * bs[c] : 0.f;
           Dl[i][c] = E * D[j][r];
           Ml[i][c] = i > c ? -E * b * X[j][r] : 0.f;
         }

@@ -39,7 +39,7 @@ struct PackedSpace {
   // gradients only
   uint4* t2;      // cells: T^T with T = (I + diag(beta) B)^-1
   uint4* qt;      // as kt, of Q
-  double* g;      // cells: G, 64
+  double* g;      // cells: G in units of log 2, 64
   float* e;       // cells: residuals e [strip][64 tokens][16 columns]
   float* w;       // cells: W = T^T dU, laid out like e
   float* s0;      // cells: state before the chunk [strip][d_k padded][16 columns]
