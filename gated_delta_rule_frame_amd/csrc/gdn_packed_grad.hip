@@ -257,126 +257,216 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 
+// One workgroup per chunk and key head.  Nearly all of it is products over d_v
+// (dO, W and e with S0 and dS1) on split operands, 690 MFMAs a row tile at 128 x
+// 128, so the work is to keep those fed: 32 columns of d_v at a time, every
+// operand that several wavefronts read is split once, by one wavefront, into an
+// LDS buffer (two in turn, one barrier a step), its fp32 values fetched a step
+// ahead.  Wavefronts w and w + 4 have row tile w and each half of the columns of
+// d_k; the second four also have the 64 x 64 products D and M.
 template <int NT, int DKP>
-__global__ __launch_bounds__(256, 1) void packed_grads_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, long long slots) {
-  constexpr int NTI = DKP / 16;                      // column tiles of d_k
-  __shared__ __align__(16) float Dl[kC][kLd];        // D = E o (dO U^T)
-  __shared__ __align__(16) float Ml[kC][kLd];        // M
+__global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, long long slots) {
+  constexpr int NTI = DKP / 16, HT = NTI / 2;        // column tiles of d_k, and of a wavefront
+  constexpr uint32_t es = NT == 1 ? 2 : 4;
+  constexpr int kFrag = 3 * 512;                     // bf16 values of a split fragment
+  constexpr int kBuf = (8 + 2 * NTI) * kFrag;        // W, e: four tiles each; S0, dS1: NTI each
+  __shared__ __align__(16) bh lds[2 * kBuf];
   __shared__ double Gs[kC];
-  __shared__ float bs[kC], dGs[kC], part[8];
-  const int tid = threadIdx.x, lane = tid % 64, w = tid / 64;
-  const int lr = lane % 16, lg = lane / 16;
+  __shared__ float bs[kC], dGs[2][kC], part[16];
+  float (*Dl)[kLd] = reinterpret_cast<float (*)[kLd]>(lds);            // D and M, when the buffers are done with
+  float (*Ml)[kLd] = reinterpret_cast<float (*)[kLd]>(lds) + kC;
+  static_assert(2 * kBuf * sizeof(bh) >= 2 * kC * kLd * sizeof(float), "D and M fit");
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  const int lr = lane % 16, lg = lane / 16, w = wave & 3, half = wave >> 2;
   const int rep = p.hv / p.hk, strips = p.dv / 16, VS = (strips + 1) / 2;
   const long long items = slots * p.hk;
+  const int row0 = 16 * w + 4 * lg, arow = 16 * w + lr;
+  const uint32_t ks_b = (uint32_t)p.ks * es, qs_b = (uint32_t)p.qs * es, os_b = (uint32_t)(p.hv * p.dv) * es;
+  const uint32_t dk_b = (uint32_t)p.dk * es, gs_b = (uint32_t)(p.hk * p.dk) * es;
 
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
     const int kh = (int)(item % p.hk);
     const long long slot = item / p.hk;
     int seq, first, n;
     if (!find_chunk(t.cu, p.sequences, p.tokens, slot, &seq, &first, &n)) continue;   // uniform over the workgroup
-    const int row0 = 16 * w + 4 * lg, arow = 16 * w + lr;
-    const size_t at = ((size_t)slot * p.hk + kh) * NTI * 2 * NT * 64;
-    const uint4* kt = ws.kt + at;
-    const uint4* qt = ws.qt + at;
-    f32x4 gq[NTI], gk[NTI];
+    first = __builtin_amdgcn_readfirstlane(first);
+    n = __builtin_amdgcn_readfirstlane(n);
+    const buf_t kb = buf(static_cast<const char*>(t.k) + ((size_t)first * p.ks + kh * p.dk) * es, span(n, ks_b, dk_b));
+    const buf_t qb = buf(static_cast<const char*>(t.q) + ((size_t)first * p.qs + kh * p.dk) * es, span(n, qs_b, dk_b));
+    const uint32_t tr = NTI * 2 * NT * 64;
+    const buf_t ktb = buf(ws.kt + ((size_t)slot * p.hk + kh) * tr, tr * 16);
+    const buf_t qtb = buf(ws.qt + ((size_t)slot * p.hk + kh) * tr, tr * 16);
+    f32x4 gq[HT], gk[HT];
 #pragma unroll
-    for (int j = 0; j < NTI; ++j) gq[j] = gk[j] = zero4();
+    for (int j = 0; j < HT; ++j) gq[j] = gk[j] = zero4();
 
     for (int h = kh * rep; h < (kh + 1) * rep; ++h) {
       const size_t cell = (size_t)slot * p.hv + h;
       const float* gates = ws.gates + cell * 3 * kC;
-      const float* ec = ws.e + cell * strips * kC * 16;
-      const float* wc = ws.w + cell * strips * kC * 16;
-      const float* sc = ws.s0 + cell * strips * DKP * 16;
-      const float* dc = ws.ds + cell * strips * DKP * 16;
-      __syncthreads();                               // the previous head has read the tiles
+      const uint32_t tok_b = strips * kC * 16 * 4, st_b = strips * DKP * 16 * 4;
+      const buf_t eb = buf(ws.e + cell * strips * kC * 16, tok_b), wb = buf(ws.w + cell * strips * kC * 16, tok_b);
+      const buf_t sb = buf(ws.s0 + cell * strips * DKP * 16, st_b), db = buf(ws.ds + cell * strips * DKP * 16, st_b);
+      const buf_t ob = buf(static_cast<const char*>(t.dout) + ((size_t)first * p.hv + h) * p.dv * es, span(n, os_b, p.dv * es));
+      // this lane's eight values of columns 32 vs .. of a row of e, W (64 rows) or S0, dS1 (DKP rows); behind the last strip
+      // there is nothing
+      uint4 we[2][2], sd[2][2];
+      RawFrag<NT> dof;
+      auto fetch = [&](int vs) {
+        const int strip = vs * 2 + lg / 2, c8 = lg % 2 * 8;
+        const uint32_t nowhere = strip < strips ? 0 : kNowhere;
+        if (half == 0) {
+          const uint32_t o = ((strip * kC + arow) * 16 + c8) * 4 | nowhere;
+          we[0][0] = buf_load16(wb, o);
+          we[0][1] = buf_load16(wb, o + 16);
+          we[1][0] = buf_load16(eb, o);
+          we[1][1] = buf_load16(eb, o + 16);
+        }
+        if (NTI == 8 || wave < NTI) {
+          const uint32_t o = ((strip * DKP + wave * 16 + lr) * 16 + c8) * 4 | nowhere;
+          sd[0][0] = buf_load16(sb, o);
+          sd[0][1] = buf_load16(sb, o + 16);
+          sd[1][0] = buf_load16(db, o);
+          sd[1][1] = buf_load16(db, o + 16);
+        }
+        dof = raw_at<NT>(ob, arow * os_b + (strip * 16 + c8) * es | nowhere);
+      };
+      auto eight = [&](const uint4 (&v)[2], float (&x)[8]) {
+        const uint32_t a[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(a[j]);
+      };
+      auto put_frag = [&](bh* to, const float (&x)[8]) {
+        const Frag<3> f = split8<3>(x);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(to + i * 512 + lane * 8) = as_bits(f.t[i]);
+      };
+      auto get_frag = [&](const bh* from) {
+        Frag<3> f;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) f.t[i] = as_frag(*reinterpret_cast<const uint4*>(from + i * 512 + lane * 8));
+        return f;
+      };
+      fetch(0);
+      __syncthreads();                               // the previous head has read the tiles and gates
       if (tid < kC) {
         Gs[tid] = ws.g[cell * kC + tid];
         bs[tid] = gates[2 * kC + tid];
       }
-      f32x4 dq[NTI], rw[NTI], cl[NTI], D[4], X[4];
+      f32x4 dq[HT], rw[HT], cl[HT], D[4], X[4];
 #pragma unroll
-      for (int j = 0; j < NTI; ++j) dq[j] = rw[j] = cl[j] = zero4();
+      for (int j = 0; j < HT; ++j) dq[j] = rw[j] = cl[j] = zero4();
 #pragma unroll
       for (int j = 0; j < 4; ++j) D[j] = X[j] = zero4();
-      float dbeta = 0.f;                             // of token arow, this lane's columns
-      // products over d_v, 32 columns (two strips) at a time
+      float dbeta = 0.f, dot = 0.f;                  // of token arow over this lane's columns; of <S0, dS1>
       for (int vs = 0; vs < VS; ++vs) {
-        const int strip = vs * 2 + lg / 2, c8 = lg % 2 * 8;
-        const bool in = strip < strips;
-        auto tile = [&](const float* base, int rows, int row) {   // [strip][rows][16]
-          return in ? frag_f32<3>(base + ((size_t)strip * rows + row) * 16 + c8) : zero_frag<3>();
-        };
-        const Frag<NT> ao = in && arow < n
-            ? frag_in<NT>(t.dout, ((size_t)(first + arow) * p.hv + h) * p.dv + strip * 16 + c8) : zero_frag<NT>();
-        const Frag<3> aw = tile(wc, kC, arow), ae = tile(ec, kC, arow);
-        if (in) {
-          const float* a = wc + ((size_t)strip * kC + arow) * 16 + c8;
-          const float* b = ec + ((size_t)strip * kC + arow) * 16 + c8;
+        bh* buf0 = lds + (vs & 1) * kBuf;
+        if (half == 0) {
+          float x[8], y[8];
+          eight(we[0], x);
+          eight(we[1], y);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dbeta = fmaf(a[j], b[j], dbeta);
+          for (int j = 0; j < 8; ++j) dbeta = fmaf(x[j], y[j], dbeta);
+          put_frag(buf0 + w * kFrag, x);
+          put_frag(buf0 + (4 + w) * kFrag, y);
         }
+        if (NTI == 8 || wave < NTI) {
+          float x[8], y[8];
+          eight(sd[0], x);
+          eight(sd[1], y);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j <= w) {
-            const Frag<3> b = j == w ? ae : tile(ec, kC, 16 * j + lr);
-            D[j] = mma<NT, 3>(ao, b, D[j]);
-            X[j] = mma<3, 3>(aw, b, X[j]);
-          }
+          for (int j = 0; j < 8; ++j) dot = fmaf(x[j], y[j], dot);
+          put_frag(buf0 + (8 + wave) * kFrag, x);
+          put_frag(buf0 + (8 + NTI + wave) * kFrag, y);
+        }
+        const Frag<NT> ao = frag_of<NT>(dof);
+        if (vs + 1 < VS) fetch(vs + 1);
+        __syncthreads();
+        const Frag<3> aw = get_frag(buf0 + w * kFrag), ae = get_frag(buf0 + (4 + w) * kFrag);
 #pragma unroll
-        for (int j = 0; j < NTI; ++j) {
-          const Frag<3> s = tile(sc, DKP, 16 * j + lr);
+        for (int j = 0; j < HT; ++j) {
+          const int tile = half * HT + j;
+          const Frag<3> s = get_frag(buf0 + (8 + tile) * kFrag), d = get_frag(buf0 + (8 + NTI + tile) * kFrag);
           dq[j] = mma<NT, 3>(ao, s, dq[j]);
           rw[j] = mma<3, 3>(aw, s, rw[j]);
-          cl[j] = mma<3, 3>(ae, tile(dc, DKP, 16 * j + lr), cl[j]);
+          cl[j] = mma<3, 3>(ae, d, cl[j]);
         }
+        if (half == 1)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j <= w) {
+              const Frag<3> b = get_frag(buf0 + (4 + j) * kFrag);
+              D[j] = mma<NT, 3>(ao, b, D[j]);
+              X[j] = mma<3, 3>(aw, b, X[j]);
+            }
       }
-      dbeta += __shfl_xor(dbeta, 16);
-      dbeta += __shfl_xor(dbeta, 32);
-      if (lg == 0 && arow < n) t.dbeta[(size_t)(first + arow) * p.hv + h] = dbeta;
-      __syncthreads();                               // Gs, bs
+      if (half == 0) {
+        dbeta += __shfl_xor(dbeta, 16);
+        dbeta += __shfl_xor(dbeta, 32);
+        if (lg == 0 && arow < n) t.dbeta[(size_t)(first + arow) * p.hv + h] = dbeta;
+      }
+      // K and Q of this wavefront's rows and columns as accumulators hold them: a product with the identity, exact
+      f32x4 kd[HT], qd[HT];
+#pragma unroll
+      for (int j = 0; j < HT; ++j) {
+        const int tile = half * HT + j, c = tile / 2 * 32 + lg * 8;
+        float one[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) one[i] = lg * 8 + i == tile % 2 * 16 + lr ? 1.f : 0.f;
+        const Frag<1> id = split8<1>(one);
+        const uint32_t nowhere = c < p.dk ? 0 : kNowhere;
+        kd[j] = mma<NT, 1>(frag_of<NT>(raw_at<NT>(kb, arow * ks_b + c * es | nowhere)), id, zero4());
+        qd[j] = mma<NT, 1>(frag_of<NT>(raw_at<NT>(qb, arow * qs_b + c * es | nowhere)), id, zero4());
+      }
       float tails = 0.f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = row0 + r;
         const float eg = gates[i], ed = gates[kC + i], b = bs[i];
-        const bool in = i < n;
 #pragma unroll
-        for (int j = 0; j < NTI; ++j) {
+        for (int j = 0; j < HT; ++j) {
           dq[j][r] *= eg;
           rw[j][r] *= -b * eg;
           cl[j][r] *= b * ed;
-          const int c = 16 * j + lr;
-          if (in && c < p.dk) tails = fmaf(elem_in<NT>(t.k, (size_t)(first + i) * p.ks + kh * p.dk + c), cl[j][r], tails);
+          tails = fmaf(kd[j][r], cl[j][r], tails);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = 16 * j + lr;
-          const float E = i >= c ? exp2_of((float)(Gs[i] - Gs[c])) * bs[c] : 0.f;
-          Dl[i][c] = E * D[j][r];
-          Ml[i][c] = i > c ? -E * b * X[j][r] : 0.f;
-        }
-      }
-      // <S0, dS1>: the workgroup's threads over the cell
-      float dot = 0.f;
-      for (int i = tid; i < strips * DKP * 4; i += 256) {
-        const float4 a = reinterpret_cast<const float4*>(sc)[i], b = reinterpret_cast<const float4*>(dc)[i];
-        dot += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
       }
       tails = wave_sum(tails);
       dot = wave_sum(dot);
+      __syncthreads();                               // the last buffers have been read
       if (lane == 0) {
-        part[w] = tails;
-        part[4 + w] = dot;
+        part[wave] = tails;
+        part[8 + wave] = dot;
       }
+      if (half == 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = 16 * j + lr;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = row0 + r;
+            const float E = i >= c ? exp2_of((float)(Gs[i] - Gs[c])) * bs[c] : 0.f;
+            Dl[i][c] = j <= w ? E * D[j][r] : 0.f;
+            Ml[i][c] = j <= w && i > c ? -E * bs[i] * X[j][r] : 0.f;
+          }
+        }
       __syncthreads();
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int k8 = ks * 32 + lg * 8;
-        Frag<3> ad, am, bd, bm;
+        Frag<NT> kf[HT], qf[HT];
+#pragma unroll
+        for (int j = 0; j < HT; ++j) {
+          const uint32_t o = (((half * HT + j) * 2 + ks) * NT * 64 + lane) * 16;
+          kf[j] = frag_at<NT>(ktb, o);
+          qf[j] = frag_at<NT>(qtb, o);
+        }
         if (ks <= w / 2) {
-          ad = frag_f32<3>(&Dl[arow][k8]);
-          am = frag_f32<3>(&Ml[arow][k8]);
+          const Frag<3> ad = frag_f32<3>(&Dl[arow][k8]), am = frag_f32<3>(&Ml[arow][k8]);
+#pragma unroll
+          for (int j = 0; j < HT; ++j) {
+            dq[j] = mma<3, NT>(ad, kf[j], dq[j]);
+            rw[j] = mma<3, NT>(am, kf[j], rw[j]);
+          }
         }
         if (ks >= w / 2) {
           float x[8], y[8];
@@ -385,46 +475,40 @@ __global__ __launch_bounds__(256, 1) void packed_grads_kernel(SeqProblem p, Pack
             x[j] = Dl[k8 + j][arow];
             y[j] = Ml[k8 + j][arow];
           }
-          bd = split8<3>(x);
-          bm = split8<3>(y);
-        }
+          const Frag<3> bd = split8<3>(x), bm = split8<3>(y);
 #pragma unroll
-        for (int j = 0; j < NTI; ++j) {
-          const Frag<NT> kf = load_frag<NT>(kt, j * 2 + ks, lane);
-          if (ks <= w / 2) {
-            dq[j] = mma<3, NT>(ad, kf, dq[j]);
-            rw[j] = mma<3, NT>(am, kf, rw[j]);
-          }
-          if (ks >= w / 2) {
-            cl[j] = mma<3, NT>(bd, load_frag<NT>(qt, j * 2 + ks, lane), cl[j]);
-            cl[j] = mma<3, NT>(bm, kf, cl[j]);
+          for (int j = 0; j < HT; ++j) {
+            cl[j] = mma<3, NT>(bd, qf[j], cl[j]);
+            cl[j] = mma<3, NT>(bm, kf[j], cl[j]);
           }
         }
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = row0 + r;
         float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < NTI; ++j) {
-          const int c = 16 * j + lr;
-          const bool in = i < n && c < p.dk;
-          const float q = in ? elem_in<NT>(t.q, (size_t)(first + i) * p.qs + kh * p.dk + c) : 0.f;
-          const float k = in ? elem_in<NT>(t.k, (size_t)(first + i) * p.ks + kh * p.dk + c) : 0.f;
-          s += q * dq[j][r] + k * (rw[j][r] - cl[j][r]);
+        for (int j = 0; j < HT; ++j) {
+          s += qd[j][r] * dq[j][r] + kd[j][r] * (rw[j][r] - cl[j][r]);
           gq[j][r] += dq[j][r];
           gk[j][r] += rw[j][r] + cl[j][r];
         }
 #pragma unroll
         for (int m = 1; m < 16; m <<= 1) s += __shfl_xor(s, m);
-        if (lr == 0) dGs[i] = s;
+        if (lr == 0) dGs[half][row0 + r] = s;
       }
       __syncthreads();
-      if (w == 0) {
+      if (wave == 0) {
         // the chunk's last G is every padded row's too, so its share can sit in row 63
-        double s = dGs[lane];
-        if (lane == kC - 1)
-          s += (double)(part[0] + part[1] + part[2] + part[3]) + (double)gates[kC - 1] * (part[4] + part[5] + part[6] + part[7]);
+        double s = (double)dGs[0][lane] + dGs[1][lane];
+        if (lane == kC - 1) {
+          double tail = 0.0, states = 0.0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            tail += part[i];
+            states += part[8 + i];
+          }
+          s += tail + (double)gates[kC - 1] * states;
+        }
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
           const double o = __shfl_down(s, m);
@@ -433,17 +517,18 @@ __global__ __launch_bounds__(256, 1) void packed_grads_kernel(SeqProblem p, Pack
         if (lane < n) t.dg[(size_t)(first + lane) * p.hv + h] = (float)s;
       }
     }
+    const buf_t dqb = buf(static_cast<char*>(t.dq) + ((size_t)first * p.hk + kh) * p.dk * es, span(n, gs_b, dk_b));
+    const buf_t dkb = buf(static_cast<char*>(t.dk) + ((size_t)first * p.hk + kh) * p.dk * es, span(n, gs_b, dk_b));
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int j = 0; j < HT; ++j) {
+      const int c = (half * HT + j) * 16 + lr;
+      const uint32_t nowhere = c < p.dk ? 0 : kNowhere;
 #pragma unroll
-      for (int j = 0; j < NTI; ++j) {
-        const int c = 16 * j + lr;
-        if (row0 + r < n && c < p.dk) {
-          const size_t o = ((size_t)(first + row0 + r) * p.hk + kh) * p.dk + c;
-          store_scalar(t.dq, o, gq[j][r], NT == 1);
-          store_scalar(t.dk, o, gk[j][r], NT == 1);
-        }
+      for (int r = 0; r < 4; ++r) {
+        store_at<es>(dqb, (row0 + r) * gs_b + c * es | nowhere, gq[j][r]);
+        store_at<es>(dkb, (row0 + r) * gs_b + c * es | nowhere, gk[j][r]);
       }
+    }
   }
 }
 
@@ -469,7 +554,7 @@ hipError_t packed_grads(const SeqProblem& p, const PackedTensors& t, const Packe
   const dim3 grid((unsigned)(items < kMaxBlocks ? items : kMaxBlocks));
   prof_begin(stream, GDN_KERNEL_PACKED_GRADS);
 #define GDN_GRADS(NT, D) \
-  if (f.terms == NT && f.dkp == D) hipLaunchKernelGGL((packed_grads_kernel<NT, D>), grid, dim3(256), 0, stream, p, t, s, f.slots);
+  if (f.terms == NT && f.dkp == D) hipLaunchKernelGGL((packed_grads_kernel<NT, D>), grid, dim3(512), 0, stream, p, t, s, f.slots);
   GDN_GRADS(1, 32) GDN_GRADS(1, 64) GDN_GRADS(1, 128) GDN_GRADS(3, 32) GDN_GRADS(3, 64) GDN_GRADS(3, 128)
 #undef GDN_GRADS
   const hipError_t e = hipGetLastError();
