@@ -14,10 +14,12 @@ struct NormProblem {
   float eps;
 };
 
-// How the S > 1 kernels cut the rows of one n: `splits` workgroups of `rows`
-// rows, each with `rpb` rows at a time; a thread leaves one of `parts` sums.
+// How the S > 1 kernels cut the work.  A group has `per` channel vectors; a
+// workgroup has `tile` of them (whole groups, or one of `pieces` of a group), in
+// `tiles` along the channels, and one of `splits` ranges of `rows` rows, `rpb`
+// at a time; z workgroups walk over n.  A (n, group) has `parts` partial sums.
 struct NormPlan {
-  int cvs, tile, tiles, rpb, rows, splits, parts, threads;
+  int per, tile, tiles, pieces, rpb, rows, splits, parts, threads, z;
 };
 
 // Device pointers of a gradient call (bias, gate, dgate, dweight, dbias and,

@@ -17,9 +17,8 @@
 //     dbias over its rows need no exchange.
 //   S > 1: the S x C values of one n are contiguous and a group is a column
 //     band of them.  A first kernel walks over the rows with one thread per
-//     channel vector and leaves sums for each (n, part, channel vector or
-//     channel); a small kernel joins them; a last one reads the inputs again and
-//     writes the result.
+//     channel vector and leaves each workgroup's sums for its groups; a small
+//     kernel joins them; a last one reads the inputs again and writes the result.
 // Sums are fp32: a group's second moment is taken about its mean (S = 1) or
 // about each thread's first value and joined pairwise with counts, so a mean
 // far from zero does not cancel.  No atomics: results are the same every run.
@@ -32,22 +31,49 @@ namespace {
 constexpr int kT = 256;       // threads of the S = 1 kernels
 constexpr int kTF = 512;      // most threads of the S > 1 kernels
 
+// A vector as it lies in memory, so that one can be fetched ahead in few registers.
 template <bool BF16, int VEC>
-__device__ __forceinline__ void load_vec(const void* p, size_t i, float (&x)[VEC]) {
+struct RawVec {
+  uint4 v;
+};
+template <>
+struct RawVec<true, 1> {
+  uint16_t v;
+};
+template <>
+struct RawVec<false, 1> {
+  float v;
+};
+
+template <bool BF16, int VEC>
+__device__ __forceinline__ RawVec<BF16, VEC> fetch_vec(const void* p, size_t i) {
+  RawVec<BF16, VEC> r;
+  r.v = *reinterpret_cast<const decltype(r.v)*>(static_cast<const char*>(p) + i * (BF16 ? 2 : 4));
+  return r;
+}
+
+template <bool BF16, int VEC>
+__device__ __forceinline__ void unpack(const RawVec<BF16, VEC>& r, float (&x)[VEC]) {
   if constexpr (VEC == 1) {
-    x[0] = load_scalar<BF16>(p, i);
-  } else if constexpr (BF16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (BF16) x[0] = bf16_bits_to_f32(r.v);
+    else x[0] = r.v;
+  } else {
+    const uint32_t a[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      x[2 * j] = __uint_as_float(a[j] << 16);
-      x[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
+      if constexpr (BF16) {
+        x[2 * j] = __uint_as_float(a[j] << 16);
+        x[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
+      } else {
+        x[j] = __uint_as_float(a[j]);
+      }
     }
-  } else {
-    const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
   }
+}
+
+template <bool BF16, int VEC>
+__device__ __forceinline__ void load_vec(const void* p, size_t i, float (&x)[VEC]) {
+  unpack<BF16, VEC>(fetch_vec<BF16, VEC>(p, i), x);
 }
 
 template <bool BF16, int VEC>
@@ -129,16 +155,43 @@ __device__ __forceinline__ float lane_sum(float x, int L, float* lds) {
 
 // ---------------------------------------------------------------- S = 1
 
+// Where a thread of the S = 1 kernels works: one group, and rows first, first +
+// step, ...  A workgroup holds kT / L groups: of one row, or all groups of
+// several rows where a row has fewer.
+struct RowPlace {
+  int grp;
+  bool on;
+  long long first, step;
+};
+
+__device__ __forceinline__ RowPlace row_place(const NormProblem& p, int L) {
+  const int slots = kT / L, slot = threadIdx.x / L;
+  RowPlace t;
+  if (p.G >= slots) {
+    t.grp = blockIdx.x * slots + slot;
+    t.on = t.grp < p.G;
+    t.first = blockIdx.y;
+    t.step = gridDim.y;
+  } else {
+    const int rows = slots / p.G, r = slot / p.G;
+    t.grp = slot % p.G;
+    t.on = r < rows;
+    t.first = t.on ? (long long)blockIdx.y * rows + r : p.N;
+    t.step = (long long)gridDim.y * rows;
+  }
+  return t;
+}
+
 template <bool BF16, int VEC, int NV, bool GATE>
 __global__ __launch_bounds__(kT) void norm_rows_kernel(
     const void* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
     const void* __restrict__ gate, void* __restrict__ out, float* __restrict__ mean, float* __restrict__ rstd,
     NormProblem p, int L) {
   __shared__ float lds[4];
-  const int per = kT / L, lane = threadIdx.x % L;
-  const int grp = blockIdx.x * per + threadIdx.x / L;
-  const int cvs = p.cg / VEC;
-  const bool on = grp < p.G;
+  const int lane = threadIdx.x % L;
+  const RowPlace t = row_place(p, L);
+  const int grp = t.grp, cvs = p.cg / VEC;
+  const bool on = t.on;
   float w[NV][VEC], b[NV][VEC];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -151,17 +204,34 @@ __global__ __launch_bounds__(kT) void norm_rows_kernel(
       b[j][e] = in && bias ? bias[c] : 0.f;
     }
   const float inv = 1.f / (float)p.cg;
-  for (long long n = blockIdx.y; n < p.N; n += gridDim.y) {
-    float v[NV][VEC], s = 0.f;
-    const size_t base = (size_t)n * p.C + (size_t)grp * p.cg;
+  // the next row's values are fetched before this one's sums
+  RawVec<BF16, VEC> rx[NV], rz[GATE ? NV : 1];
+  auto fetch = [&](long long n) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int cv = lane + L * j;
-      if (on && cv < cvs) {
-        load_vec<BF16, VEC>(x, base + (size_t)cv * VEC, v[j]);
+      if (!(on && cv < cvs)) continue;
+      const size_t at = (size_t)n * p.C + (size_t)grp * p.cg + (size_t)cv * VEC;
+      rx[j] = fetch_vec<BF16, VEC>(x, at);
+      if constexpr (GATE) rz[j] = fetch_vec<BF16, VEC>(gate, at);
+    }
+  };
+  if (t.first < p.N) fetch(t.first);
+  for (long long n = t.first; n < p.N; n += t.step) {
+    float v[NV][VEC], z[GATE ? NV : 1][VEC], s = 0.f;
+    const size_t base = (size_t)n * p.C + (size_t)grp * p.cg;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += v[j][e];
-      }
+    for (int j = 0; j < NV; ++j) {
+      unpack<BF16, VEC>(rx[j], v[j]);
+      if constexpr (GATE) unpack<BF16, VEC>(rz[j], z[j]);
+    }
+    if (n + t.step < p.N) fetch(n + t.step);
+    if (p.center) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (on && lane + L * j < cvs)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) s += v[j][e];
     }
     float m = 0.f;
     if (p.center) m = lane_sum(s, L, lds) * inv;
@@ -176,12 +246,10 @@ __global__ __launch_bounds__(kT) void norm_rows_kernel(
     for (int j = 0; j < NV; ++j) {
       const int cv = lane + L * j;
       if (!(on && cv < cvs)) continue;
-      float z[VEC];
-      if constexpr (GATE) load_vec<BF16, VEC>(gate, base + (size_t)cv * VEC, z);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float u = fmaf((v[j][e] - m) * r, w[j][e], b[j][e]);
-        v[j][e] = GATE ? u * act(p.act, z[e]) : act(p.act, u);
+        v[j][e] = GATE ? u * act(p.act, z[GATE ? j : 0][e]) : act(p.act, u);
       }
       store_vec<BF16, VEC>(out, base + (size_t)cv * VEC, v[j]);
     }
@@ -192,8 +260,8 @@ __global__ __launch_bounds__(kT) void norm_rows_kernel(
   }
 }
 
-// dx, dgate, and for each workgroup row block the sums of du h and du per channel:
-// part [gridDim.y][2][C].
+// dx, dgate, and for each of the rows walked at once the sums of du h and du per
+// channel: part [rows at once][2][C].
 template <bool BF16, int VEC, int NV, bool GATE>
 __global__ __launch_bounds__(kT) void norm_rows_grad_kernel(
     const void* __restrict__ dout, const void* __restrict__ x, const float* __restrict__ weight,
@@ -201,10 +269,10 @@ __global__ __launch_bounds__(kT) void norm_rows_grad_kernel(
     const float* __restrict__ rstd, void* __restrict__ dx, void* __restrict__ dgate, float* __restrict__ part,
     NormProblem p, int L) {
   __shared__ float lds[4];
-  const int per = kT / L, lane = threadIdx.x % L;
-  const int grp = blockIdx.x * per + threadIdx.x / L;
-  const int cvs = p.cg / VEC;
-  const bool on = grp < p.G;
+  const int lane = threadIdx.x % L;
+  const RowPlace t = row_place(p, L);
+  const int grp = t.grp, cvs = p.cg / VEC;
+  const bool on = t.on;
   float w[NV][VEC], b[NV][VEC], sw[NV][VEC], sb[NV][VEC];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -218,23 +286,44 @@ __global__ __launch_bounds__(kT) void norm_rows_grad_kernel(
       sw[j][e] = sb[j][e] = 0.f;
     }
   const float inv = 1.f / (float)p.cg;
-  for (long long n = blockIdx.y; n < p.N; n += gridDim.y) {
-    const size_t base = (size_t)n * p.C + (size_t)grp * p.cg;
-    const float m = on && p.center ? mean[(size_t)n * p.G + grp] : 0.f;
-    const float r = on ? rstd[(size_t)n * p.G + grp] : 0.f;
-    float h[NV][VEC], d[NV][VEC], s1 = 0.f, s2 = 0.f;
+  // the next row's values are fetched before this one's sums
+  RawVec<BF16, VEC> rx[NV], rd[NV], rz[GATE ? NV : 1];
+  float nm = 0.f, nr = 0.f;
+  auto fetch = [&](long long n) {
+    nm = on && p.center ? mean[(size_t)n * p.G + grp] : 0.f;
+    nr = on ? rstd[(size_t)n * p.G + grp] : 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int cv = lane + L * j;
       if (!(on && cv < cvs)) continue;
-      float z[VEC], dz[VEC];
-      load_vec<BF16, VEC>(x, base + (size_t)cv * VEC, h[j]);
-      load_vec<BF16, VEC>(dout, base + (size_t)cv * VEC, d[j]);
-      if constexpr (GATE) load_vec<BF16, VEC>(gate, base + (size_t)cv * VEC, z);
+      const size_t at = (size_t)n * p.C + (size_t)grp * p.cg + (size_t)cv * VEC;
+      rx[j] = fetch_vec<BF16, VEC>(x, at);
+      rd[j] = fetch_vec<BF16, VEC>(dout, at);
+      if constexpr (GATE) rz[j] = fetch_vec<BF16, VEC>(gate, at);
+    }
+  };
+  if (t.first < p.N) fetch(t.first);
+  for (long long n = t.first; n < p.N; n += t.step) {
+    const size_t base = (size_t)n * p.C + (size_t)grp * p.cg;
+    const float m = nm, r = nr;
+    float h[NV][VEC], d[NV][VEC], zz[GATE ? NV : 1][VEC], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      unpack<BF16, VEC>(rx[j], h[j]);
+      unpack<BF16, VEC>(rd[j], d[j]);
+      if constexpr (GATE) unpack<BF16, VEC>(rz[j], zz[j]);
+    }
+    if (n + t.step < p.N) fetch(n + t.step);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int cv = lane + L * j;
+      if (!(on && cv < cvs)) continue;
+      float dz[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         h[j][e] = (h[j][e] - m) * r;
-        const float du = grad_u<GATE>(p.act, d[j][e], fmaf(h[j][e], w[j][e], b[j][e]), GATE ? z[e] : 0.f, &dz[e]);
+        const float du =
+            grad_u<GATE>(p.act, d[j][e], fmaf(h[j][e], w[j][e], b[j][e]), GATE ? zz[GATE ? j : 0][e] : 0.f, &dz[e]);
         sw[j][e] = fmaf(du, h[j][e], sw[j][e]);
         sb[j][e] += du;
         d[j][e] = du * w[j][e];
@@ -260,7 +349,7 @@ __global__ __launch_bounds__(kT) void norm_rows_grad_kernel(
     for (int e = 0; e < VEC; ++e) {
       const int cv = lane + L * j;
       if (!(on && cv < cvs)) continue;
-      float* o = part + (size_t)blockIdx.y * 2 * p.C + grp * p.cg + cv * VEC + e;
+      float* o = part + (size_t)t.first * 2 * p.C + grp * p.cg + cv * VEC + e;
       o[0] = sw[j][e];
       o[p.C] = sb[j][e];
     }
@@ -268,59 +357,31 @@ __global__ __launch_bounds__(kT) void norm_rows_grad_kernel(
 
 // ---------------------------------------------------------------- S > 1
 
-// The place of a thread of the S > 1 kernels: one channel vector, every
-// rpb-th row of the part's rows.
+// The place of a thread of the S > 1 kernels: one channel vector, every rpb-th
+// row of the part's rows.  A workgroup has whole groups, or a piece of one.
 struct Place {
-  int cv, first, last, step, part;
+  int cv, grp, first, last, step, off;
   bool on;
 };
 
 __device__ __forceinline__ Place place(const NormProblem& p, const NormPlan& f) {
   Place t;
-  const int tid = threadIdx.x, off = tid / f.tile;
-  t.cv = blockIdx.x * f.tile + tid % f.tile;
-  t.on = off < f.rpb && t.cv < f.cvs;
-  t.first = blockIdx.y * f.rows + off;
+  const int tid = threadIdx.x, c = tid % f.tile;
+  t.off = tid / f.tile;
+  if (f.pieces == 1) {
+    t.cv = blockIdx.x * f.tile + c;
+    t.grp = t.cv / f.per;
+    t.on = t.off < f.rpb && t.grp < p.G;
+  } else {
+    const int in = blockIdx.x % f.pieces * f.tile + c;
+    t.grp = blockIdx.x / f.pieces;
+    t.cv = t.grp * f.per + in;
+    t.on = t.off < f.rpb && in < f.per;
+  }
+  t.first = blockIdx.y * f.rows + t.off;
   t.last = min((blockIdx.y + 1) * f.rows, p.S);
   t.step = f.rpb;
-  t.part = blockIdx.y * f.rpb + off;
   return t;
-}
-
-// Sum and second moment about the mean of each thread's values:
-// part [N][parts][cvs] pairs.
-template <bool BF16, int VEC>
-__global__ __launch_bounds__(kTF) void norm_stats_kernel(const void* __restrict__ x, float2* __restrict__ part, NormProblem p,
-                                                         NormPlan f) {
-  const Place t = place(p, f);
-  if (!t.on) return;
-  for (long long n = blockIdx.z; n < p.N; n += gridDim.z) {
-    const size_t base = (size_t)n * p.S * p.C + (size_t)t.cv * VEC;
-    float s = 0.f, s2 = 0.f, shift = 0.f;
-    int rows = 0;
-    float v[VEC];
-    if (t.first < t.last && p.center) {
-      load_vec<BF16, VEC>(x, base + (size_t)t.first * p.C, v);
-      shift = v[0];
-    }
-#pragma unroll 4
-    for (int i = t.first; i < t.last; i += t.step, ++rows) {
-      load_vec<BF16, VEC>(x, base + (size_t)i * p.C, v);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = v[e] - shift;
-        s += d;
-        s2 = fmaf(d, d, s2);
-      }
-    }
-    float2 r = make_float2(0.f, s2);
-    if (p.center && rows) {
-      const float d = s / (float)(rows * VEC);
-      const float about = s2 - s * d;
-      r = make_float2(shift + d, about < 0.f ? 0.f : about);   // NaN stays NaN
-    }
-    part[((size_t)n * f.parts + t.part) * f.cvs + t.cv] = r;
-  }
 }
 
 // Joins two sets of values given as (count, mean, second moment about it).
@@ -334,29 +395,110 @@ __device__ __forceinline__ void join(float& n, float& m, float& q, float n2, flo
   n = t;
 }
 
-// One wavefront per (n, group): joins the threads' sums into mean and 1 / deviation.
-__global__ __launch_bounds__(64) void norm_stats_join_kernel(const float2* __restrict__ part, float* __restrict__ mean,
-                                                             float* __restrict__ rstd, NormProblem p, NormPlan f, int vec) {
-  const int per = f.cvs / p.G, grp = blockIdx.x;
-  const long long items = (long long)f.parts * per;
-  for (long long n = blockIdx.y; n < p.N; n += gridDim.y) {
+// The groups of a workgroup and its threads of one: a wavefront sums each group's
+// values, left by thread in LDS.  `each(entry)` adds a thread's, `done(group)`
+// is called with the wavefront's lanes' sums.
+template <typename Each, typename Done>
+__device__ __forceinline__ void by_group(const NormProblem& p, const NormPlan& f, Each each, Done done) {
+  const int groups = f.pieces == 1 ? f.tile / f.per : 1, wide = f.pieces == 1 ? f.per : f.tile;
+  const int first = f.pieces == 1 ? blockIdx.x * groups : blockIdx.x / f.pieces;
+  for (int g = threadIdx.x / 64; g < groups && first + g < p.G; g += blockDim.x / 64) {
+    for (int i = threadIdx.x % 64; i < wide * f.rpb; i += 64) each(i / wide * f.tile + g * wide + i % wide);
+    done(first + g);
+  }
+}
+
+// Count, sum and second moment of a workgroup's values of each group:
+// part [N][splits * pieces][G].
+template <bool BF16, int VEC>
+__global__ __launch_bounds__(kTF) void norm_stats_kernel(const void* __restrict__ x, float4* __restrict__ part, NormProblem p,
+                                                         NormPlan f) {
+  __shared__ float lds[3][kTF];
+  const Place t = place(p, f);
+  for (long long n = blockIdx.z; n < p.N; n += gridDim.z) {
+    const size_t base = (size_t)n * p.S * p.C + (size_t)t.cv * VEC;
+    float s = 0.f, s2 = 0.f, shift = 0.f;
+    int rows = 0;
+    float v[VEC];
+    if (t.on && t.first < t.last && p.center) {
+      load_vec<BF16, VEC>(x, base + (size_t)t.first * p.C, v);
+      shift = v[0];
+    }
+    if (t.on)
+#pragma unroll 4
+      for (int i = t.first; i < t.last; i += t.step, ++rows) {
+        load_vec<BF16, VEC>(x, base + (size_t)i * p.C, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = v[e] - shift;
+          s += d;
+          s2 = fmaf(d, d, s2);
+        }
+      }
+    float c = (float)(rows * VEC), m = 0.f, q = s2;
+    if (p.center && rows) {
+      const float d = s / c, about = s2 - s * d;
+      m = shift + d;
+      q = about < 0.f ? 0.f : about;                   // NaN stays NaN
+    }
+    __syncthreads();                                   // the previous n has been summed
+    lds[0][threadIdx.x] = c;
+    lds[1][threadIdx.x] = m;
+    lds[2][threadIdx.x] = q;
+    __syncthreads();
+    c = m = q = 0.f;
+    by_group(p, f,
+             [&](int i) {
+               if (p.center) join(c, m, q, lds[0][i], lds[1][i], lds[2][i]);
+               else q += lds[2][i];
+             },
+             [&](int grp) {
+               for (int k = 32; k; k >>= 1) {
+                 const float c2 = __shfl_down(c, k), m2 = __shfl_down(m, k), q2 = __shfl_down(q, k);
+                 if (p.center) join(c, m, q, c2, m2, q2);
+                 else q += q2;
+               }
+               const int piece = f.pieces == 1 ? 0 : blockIdx.x % f.pieces;
+               if (threadIdx.x % 64 == 0)
+                 part[((size_t)n * f.parts + blockIdx.y * f.pieces + piece) * p.G + grp] = make_float4(c, m, q, 0.f);
+               c = m = q = 0.f;
+             });
+  }
+}
+
+// The parts of each (n, group) joined into mean and 1 / deviation, by `lanes`
+// neighbouring lanes (a power of two).
+__global__ __launch_bounds__(256) void norm_stats_join_kernel(const float4* __restrict__ part, float* __restrict__ mean,
+                                                              float* __restrict__ rstd, NormProblem p, NormPlan f, int lanes) {
+  const int lane = threadIdx.x % lanes, per = 256 / lanes;
+  const long long pairs = p.N * p.G;
+  for (long long i = blockIdx.x * (long long)per + threadIdx.x / lanes; i < pairs; i += (long long)gridDim.x * per) {
+    const long long n = i / p.G;
+    const int grp = (int)(i % p.G);
     float c = 0.f, m = 0.f, q = 0.f;
-    for (long long i = threadIdx.x; i < items; i += 64) {
-      const int k = (int)(i / per), split = k / f.rpb;
-      const int first = split * f.rows + k % f.rpb, last = min((split + 1) * f.rows, p.S);
-      const float cnt = first < last ? (float)(((last - first + f.rpb - 1) / f.rpb) * vec) : 0.f;
-      const float2 a = part[((size_t)n * f.parts + k) * f.cvs + (size_t)grp * per + i % per];
-      if (p.center) join(c, m, q, cnt, a.x, a.y);
-      else q += a.y;
+    for (int k = lane; k < f.parts; k += lanes) {
+      const float4 a = part[((size_t)n * f.parts + k) * p.G + grp];
+      if (p.center) join(c, m, q, a.x, a.y, a.z);
+      else q += a.z;
     }
-    for (int s = 32; s; s >>= 1) {
-      const float c2 = __shfl_down(c, s), m2 = __shfl_down(m, s), q2 = __shfl_down(q, s);
-      if (p.center) join(c, m, q, c2, m2, q2);
-      else q += q2;
+    for (int k = lanes / 2; k; k >>= 1) {
+      const float c2 = __shfl_xor(c, k), m2 = __shfl_xor(m, k), q2 = __shfl_xor(q, k);
+      if (p.center) {
+        // both sides of an exchange join in the same order
+        if (lane & k) {
+          float a = c2, b = m2, d = q2;
+          join(a, b, d, c, m, q);
+          c = a; m = b; q = d;
+        } else {
+          join(c, m, q, c2, m2, q2);
+        }
+      } else {
+        q += q2;
+      }
     }
-    if (threadIdx.x == 0) {
-      if (mean) mean[(size_t)n * p.G + grp] = m;
-      rstd[(size_t)n * p.G + grp] = 1.f / sqrtf(q / ((float)p.S * (float)p.cg) + p.eps);
+    if (lane == 0) {
+      if (mean) mean[i] = m;
+      rstd[i] = 1.f / sqrtf(q / ((float)p.S * (float)p.cg) + p.eps);
     }
   }
 }
@@ -374,7 +516,7 @@ __global__ __launch_bounds__(kTF) void norm_apply_kernel(const void* __restrict_
     w[e] = weight ? weight[t.cv * VEC + e] : 1.f;
     b[e] = bias ? bias[t.cv * VEC + e] : 0.f;
   }
-  const int grp = t.cv * VEC / p.cg;
+  const int grp = t.grp;
   // from the last n to the first: the pass before went upwards, and its last rows are still in the cache
   for (long long n = p.N - 1 - blockIdx.z; n >= 0; n -= gridDim.z) {
     const size_t base = (size_t)n * p.S * p.C + (size_t)t.cv * VEC;
@@ -394,103 +536,120 @@ __global__ __launch_bounds__(kTF) void norm_apply_kernel(const void* __restrict_
   }
 }
 
-// FINAL false: dgate, and sums over each thread's rows of du h and du per
-// channel, part [N][parts][2][C].  FINAL true: dx, with the group's sums of
-// dh and dh h in sums [N][G].
+// FINAL false: dgate, the workgroup's sums of dh and dh h of each group, psum
+// [N][splits * pieces][G], and its sums over all its rows of du h and du per
+// channel, part [gridDim.z][splits][2][C].  FINAL true: dx, with the
+// group's sums in sums [N][G].
 template <bool BF16, int VEC, bool GATE, bool FINAL>
-__global__ __launch_bounds__(kTF) void norm_grad_kernel(
+__global__ __launch_bounds__(kTF, 4) void norm_grad_kernel(
     const void* __restrict__ dout, const void* __restrict__ x, const float* __restrict__ weight,
     const float* __restrict__ bias, const void* __restrict__ gate, const float* __restrict__ mean,
     const float* __restrict__ rstd, void* __restrict__ dx, void* __restrict__ dgate, float* __restrict__ part,
-    const float2* __restrict__ sums, NormProblem p, NormPlan f) {
+    float2* __restrict__ psum, const float2* __restrict__ sums, NormProblem p, NormPlan f) {
+  constexpr int kUnroll = FINAL ? 4 : 2;            // rows in flight: the sums take registers too
+  __shared__ float2 lds[FINAL ? 1 : kTF];
   const Place t = place(p, f);
-  if (!t.on) return;
-  float w[VEC], b[VEC];
+  if (FINAL && !t.on) return;
+  float w[VEC], b[VEC], sw[VEC] = {}, sb[VEC] = {};
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    w[e] = weight ? weight[t.cv * VEC + e] : 1.f;
-    b[e] = bias ? bias[t.cv * VEC + e] : 0.f;
+    w[e] = weight && t.on ? weight[t.cv * VEC + e] : 1.f;
+    b[e] = bias && t.on ? bias[t.cv * VEC + e] : 0.f;
   }
-  const int grp = t.cv * VEC / p.cg;
   const float inv = 1.f / ((float)p.S * (float)p.cg);
   for (long long z = blockIdx.z; z < p.N; z += gridDim.z) {
     const long long n = FINAL ? p.N - 1 - z : z;   // the second pass backwards, as in norm_apply_kernel
     const size_t base = (size_t)n * p.S * p.C + (size_t)t.cv * VEC;
-    const float m = p.center ? mean[(size_t)n * p.G + grp] : 0.f, r = rstd[(size_t)n * p.G + grp];
-    float sw[VEC] = {}, sb[VEC] = {};
+    const float m = t.on && p.center ? mean[(size_t)n * p.G + t.grp] : 0.f, r = t.on ? rstd[(size_t)n * p.G + t.grp] : 0.f;
     float s1 = 0.f, s2 = 0.f;
     if constexpr (FINAL) {
-      const float2 s = sums[(size_t)n * p.G + grp];
+      const float2 s = sums[(size_t)n * p.G + t.grp];
       s1 = p.center ? s.x * inv : 0.f;
       s2 = s.y * inv;
     }
-#pragma unroll 4
-    for (int i = t.first; i < t.last; i += t.step) {
-      float v[VEC], d[VEC], z[VEC], dz[VEC];
-      load_vec<BF16, VEC>(x, base + (size_t)i * p.C, v);
-      load_vec<BF16, VEC>(dout, base + (size_t)i * p.C, d);
-      if constexpr (GATE) load_vec<BF16, VEC>(gate, base + (size_t)i * p.C, z);
+    if (t.on)
+#pragma unroll kUnroll
+      for (int i = t.first; i < t.last; i += t.step) {
+        float v[VEC], d[VEC], z4[VEC], dz[VEC];
+        load_vec<BF16, VEC>(x, base + (size_t)i * p.C, v);
+        load_vec<BF16, VEC>(dout, base + (size_t)i * p.C, d);
+        if constexpr (GATE) load_vec<BF16, VEC>(gate, base + (size_t)i * p.C, z4);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float h = (v[e] - m) * r;
-        const float du = grad_u<GATE>(p.act, d[e], fmaf(h, w[e], b[e]), GATE ? z[e] : 0.f, &dz[e]);
-        if constexpr (FINAL) {
-          v[e] = r * (du * w[e] - s1 - h * s2);
-        } else {
-          sw[e] = fmaf(du, h, sw[e]);
-          sb[e] += du;
+        for (int e = 0; e < VEC; ++e) {
+          const float h = (v[e] - m) * r;
+          const float du = grad_u<GATE>(p.act, d[e], fmaf(h, w[e], b[e]), GATE ? z4[e] : 0.f, &dz[e]);
+          if constexpr (FINAL) {
+            v[e] = r * (du * w[e] - s1 - h * s2);
+          } else {
+            sw[e] = fmaf(du, h, sw[e]);
+            sb[e] += du;
+            s1 = fmaf(du, w[e], s1);
+            s2 = fmaf(du * w[e], h, s2);
+          }
         }
+        if constexpr (FINAL) store_vec<BF16, VEC>(dx, base + (size_t)i * p.C, v);
+        else if constexpr (GATE) store_vec<BF16, VEC>(dgate, base + (size_t)i * p.C, dz);
       }
-      if constexpr (FINAL) store_vec<BF16, VEC>(dx, base + (size_t)i * p.C, v);
-      else if constexpr (GATE) store_vec<BF16, VEC>(dgate, base + (size_t)i * p.C, dz);
-    }
     if constexpr (!FINAL) {
-      float* o = part + ((size_t)n * f.parts + t.part) * 2 * p.C + (size_t)t.cv * VEC;
+      __syncthreads();                                 // the previous n has been summed
+      lds[threadIdx.x] = make_float2(s1, s2);
+      __syncthreads();
+      s1 = s2 = 0.f;
+      by_group(p, f,
+               [&](int i) {
+                 s1 += lds[i].x;
+                 s2 += lds[i].y;
+               },
+               [&](int grp) {
+                 for (int k = 32; k; k >>= 1) {
+                   s1 += __shfl_xor(s1, k);
+                   s2 += __shfl_xor(s2, k);
+                 }
+                 const int piece = f.pieces == 1 ? 0 : blockIdx.x % f.pieces;
+                 if (threadIdx.x % 64 == 0)
+                   psum[((size_t)n * f.parts + blockIdx.y * f.pieces + piece) * p.G + grp] = make_float2(s1, s2);
+                 s1 = s2 = 0.f;
+               });
+    }
+  }
+  if constexpr (!FINAL) {
+    // over the rpb rows at a time, through LDS
+    float* o = part + ((size_t)blockIdx.z * f.splits + blockIdx.y) * 2 * p.C + (size_t)t.cv * VEC;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        o[e] = sw[e];
-        o[p.C + e] = sb[e];
+    for (int e = 0; e < VEC; ++e) {
+      __syncthreads();
+      lds[threadIdx.x] = make_float2(sw[e], sb[e]);
+      __syncthreads();
+      if (t.on && t.off == 0) {
+        float a = sw[e], c = sb[e];
+        for (int k = 1; k < f.rpb; ++k) {
+          a += lds[threadIdx.x + k * f.tile].x;
+          c += lds[threadIdx.x + k * f.tile].y;
+        }
+        o[e] = a;
+        o[p.C + e] = c;
       }
     }
   }
 }
 
-// One workgroup per (n, group): sums of dh = weight du and of dh h.
-__global__ __launch_bounds__(256) void norm_grad_join_kernel(const float* __restrict__ part, const float* __restrict__ weight,
-                                                             float2* __restrict__ sums, NormProblem p, NormPlan f) {
-  __shared__ float lds[2][4];
-  const int grp = blockIdx.x;
-  // a thread stays on one channel and walks over the parts
-  const int wide = p.cg < 256 ? p.cg : 256, rows = 256 / wide;
-  const int c0 = threadIdx.x % wide, r0 = threadIdx.x / wide;
-  for (long long n = blockIdx.y; n < p.N; n += gridDim.y) {
+// The parts of each (n, group)'s sums added up, by `lanes` neighbouring lanes.
+__global__ __launch_bounds__(256) void norm_grad_join_kernel(const float2* __restrict__ psum, float2* __restrict__ sums,
+                                                             NormProblem p, NormPlan f, int lanes) {
+  const int lane = threadIdx.x % lanes, per = 256 / lanes;
+  const long long pairs = p.N * p.G;
+  for (long long i = blockIdx.x * (long long)per + threadIdx.x / lanes; i < pairs; i += (long long)gridDim.x * per) {
+    const float2* at = psum + (size_t)(i / p.G) * f.parts * p.G + i % p.G;
     float s1 = 0.f, s2 = 0.f;
-    if (r0 < rows)
-      for (int c = c0; c < p.cg; c += wide) {
-        const float w = weight ? weight[grp * p.cg + c] : 1.f;
-        const float* o = part + (size_t)n * f.parts * 2 * p.C + grp * p.cg + c;
-        float a = 0.f, b = 0.f;
-#pragma unroll 8
-        for (int k = r0; k < f.parts; k += rows) {
-          a += o[(size_t)k * 2 * p.C + p.C];
-          b += o[(size_t)k * 2 * p.C];
-        }
-        s1 = fmaf(w, a, s1);
-        s2 = fmaf(w, b, s2);
-      }
-    for (int s = 32; s; s >>= 1) {
-      s1 += __shfl_xor(s1, s);
-      s2 += __shfl_xor(s2, s);
+    for (int k = lane; k < f.parts; k += lanes) {
+      s1 += at[(size_t)k * p.G].x;
+      s2 += at[(size_t)k * p.G].y;
     }
-    __syncthreads();
-    if (threadIdx.x % 64 == 0) {
-      lds[0][threadIdx.x / 64] = s1;
-      lds[1][threadIdx.x / 64] = s2;
+    for (int k = lanes / 2; k; k >>= 1) {
+      s1 += __shfl_xor(s1, k);
+      s2 += __shfl_xor(s2, k);
     }
-    __syncthreads();
-    if (threadIdx.x == 0)
-      sums[(size_t)n * p.G + grp] = make_float2(lds[0][0] + lds[0][1] + lds[0][2] + lds[0][3],
-                                                lds[1][0] + lds[1][1] + lds[1][2] + lds[1][3]);
+    if (lane == 0) sums[i] = make_float2(s1, s2);
   }
 }
 
@@ -523,12 +682,15 @@ int vec_of(const NormProblem& p) {
 }
 
 // Lanes of a group on the S = 1 way and vectors per lane (0: the group is too
-// wide for the registers of one workgroup).
+// wide for the registers of one workgroup).  A wavefront has a group alone,
+// without an exchange through LDS, up to 16 values a lane (32 take the
+// gradient kernel's registers to one wavefront a SIMD: 16384 rows of one group
+// of 2048 bf16 278 us against 76 by a workgroup).
 void rows_shape(const NormProblem& p, int* L, int* NV) {
-  const int cvs = p.cg / vec_of(p);
+  const int vec = vec_of(p), cvs = p.cg / vec;
   int l = 1;
   while (l < 64 && l < cvs) l *= 2;
-  if (cvs > 64) l = kT;
+  if (cvs > 64 * (vec == 1 ? 8 : 16 / vec)) l = kT;
   const int need = (cvs + l - 1) / l;
   *L = l;
   *NV = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : 0;
@@ -540,41 +702,57 @@ bool by_rows(const NormProblem& p) {
   return p.S == 1 && NV > 0;
 }
 
-dim3 rows_grid(const NormProblem& p, int L, bool gradient) {
-  const int per = kT / L, x = (p.G + per - 1) / per;
-  // the gradient leaves one row of sums per workgroup row: a few rounds over the 256 CUs; the forward
-  // kernel only amortises its weights
-  long long y = ((gradient ? 2048 : 8192) + x - 1) / x;
-  y = y < 1 ? 1 : y > 65535 ? 65535 : y;
-  if (y > p.N) y = p.N;
+// About 2048 workgroups, a few rounds over the 256 CUs: each loads its weights
+// once, and in the gradient leaves its rows' sums.  *rows: rows walked at once.
+dim3 rows_grid(const NormProblem& p, int L, long long* rows) {
+  const int slots = kT / L, x = p.G >= slots ? (p.G + slots - 1) / slots : 1, at_once = p.G >= slots ? 1 : slots / p.G;
+  long long y = (2048 + x - 1) / x;
+  const long long most = (p.N + at_once - 1) / at_once;
+  if (y > most) y = most;
+  if (rows) *rows = y * at_once;
   return dim3(x, (unsigned)y);
 }
 
 NormPlan plan(const NormProblem& p) {
   NormPlan f;
-  f.cvs = p.C / vec_of(p);
-  const int tiles = (f.cvs + kTF - 1) / kTF;
-  f.tile = (f.cvs + tiles - 1) / tiles;
-  f.tiles = tiles;
+  f.per = p.cg / vec_of(p);
+  if (f.per <= kTF) {
+    int groups = kTF / f.per < p.G ? kTF / f.per : p.G;
+    f.tiles = (p.G + groups - 1) / groups;
+    groups = (p.G + f.tiles - 1) / f.tiles;
+    f.tile = groups * f.per;
+    f.pieces = 1;
+  } else {
+    f.pieces = (f.per + kTF - 1) / kTF;
+    f.tile = (f.per + f.pieces - 1) / f.pieces;
+    f.tiles = p.G * f.pieces;
+  }
   f.rpb = kTF / f.tile;
   if (f.rpb > p.S) f.rpb = p.S;
-  // parts of the rows: about 2048 workgroups in all, at least 8 rows a thread
-  long long want = 2048 / ((long long)tiles * (p.N < 2048 ? p.N : 2048));
-  long long most = p.S / (8LL * f.rpb);
+  // splits of the rows: about 2048 workgroups in all, at least 4 rows a thread
+  const long long want = 2048 / ((long long)f.tiles * (p.N < 2048 ? p.N : 2048)), most = p.S / (4LL * f.rpb);
   long long splits = want < most ? want : most;
   if (splits < 1) splits = 1;
-  if (splits > 4096) splits = 4096;
   f.rows = (int)((p.S + splits - 1) / splits);
   f.splits = (p.S + f.rows - 1) / f.rows;
-  f.parts = f.splits * f.rpb;
+  f.parts = f.splits * f.pieces;
   f.threads = (f.tile * f.rpb + 63) / 64 * 64;
+  // workgroups over n: all of them, or about 2048 in all that walk over n
+  long long z = 2048 / ((long long)f.tiles * f.splits);
+  f.z = (int)(z < 1 ? 1 : z < p.N ? z : p.N);
   return f;
 }
 
-int loop_dim(long long n, long long others) {
-  long long y = kMaxBlocks / 4 / others;   // up to 512 threads a workgroup
-  y = y < 1 ? 1 : y > 65535 ? 65535 : y;
-  return (int)(n < y ? n : y);
+// Lanes that join a (n, group)'s parts, and the workgroups of that.
+int join_lanes(const NormPlan& f) {
+  int l = 1;
+  while (l < 64 && l < f.parts) l *= 2;
+  return l;
+}
+
+unsigned join_grid(const NormProblem& p, int lanes) {
+  const long long b = (p.N * p.G + 256 / lanes - 1) / (256 / lanes);
+  return (unsigned)(b < kMaxBlocks ? b : kMaxBlocks);
 }
 
 template <bool BF16, int VEC, bool GATE>
@@ -583,7 +761,7 @@ hipError_t forward_v(const NormProblem& p, const void* x, const float* weight, c
   if (by_rows(p)) {
     int L, NV;
     rows_shape(p, &L, &NV);
-    const dim3 grid = rows_grid(p, L, false);
+    const dim3 grid = rows_grid(p, L, nullptr);
 #define GDN_ROWS(V)                                                                                                      \
   case V:                                                                                                                \
     hipLaunchKernelGGL((norm_rows_kernel<BF16, VEC, V, GATE>), grid, dim3(kT), 0, st, x, weight, bias, gate, out, mean, \
@@ -594,11 +772,11 @@ hipError_t forward_v(const NormProblem& p, const void* x, const float* weight, c
     return hipGetLastError();
   }
   const NormPlan f = plan(p);
-  float2* part = static_cast<float2*>(ws);
-  const long long xy = (long long)f.tiles * f.splits;
-  const dim3 grid(f.tiles, f.splits, loop_dim(p.N, xy)), small(p.G, loop_dim(p.N, p.G));
+  float4* part = static_cast<float4*>(ws);
+  const dim3 grid(f.tiles, f.splits, f.z);
+  const int lanes = join_lanes(f);
   hipLaunchKernelGGL((norm_stats_kernel<BF16, VEC>), grid, dim3(f.threads), 0, st, x, part, p, f);
-  hipLaunchKernelGGL(norm_stats_join_kernel, small, dim3(64), 0, st, part, mean, rstd, p, f, VEC);
+  hipLaunchKernelGGL(norm_stats_join_kernel, dim3(join_grid(p, lanes)), dim3(256), 0, st, part, mean, rstd, p, f, lanes);
   hipLaunchKernelGGL((norm_apply_kernel<BF16, VEC, GATE>), grid, dim3(f.threads), 0, st, x, weight, bias, gate, out, mean, rstd,
                      p, f);
   return hipGetLastError();
@@ -611,8 +789,7 @@ hipError_t backward_v(const NormProblem& p, const NormGrad& t, void* ws, hipStre
   if (p.N > 0 && by_rows(p)) {
     int L, NV;
     rows_shape(p, &L, &NV);
-    const dim3 grid = rows_grid(p, L, true);
-    rows = grid.y;
+    const dim3 grid = rows_grid(p, L, &rows);
 #define GDN_ROWS(V)                                                                                                       \
   case V:                                                                                                                 \
     hipLaunchKernelGGL((norm_rows_grad_kernel<BF16, VEC, V, GATE>), grid, dim3(kT), 0, st, t.dout, t.x, t.weight, t.bias, \
@@ -622,15 +799,16 @@ hipError_t backward_v(const NormProblem& p, const NormGrad& t, void* ws, hipStre
 #undef GDN_ROWS
   } else if (p.N > 0) {
     const NormPlan f = plan(p);
-    rows = p.N * f.parts;
-    float2* sums = reinterpret_cast<float2*>(part + (size_t)rows * 2 * p.C);
-    const long long xy = (long long)f.tiles * f.splits;
-    const dim3 grid(f.tiles, f.splits, loop_dim(p.N, xy)), small(p.G, loop_dim(p.N, p.G));
+    rows = (long long)f.z * f.splits;
+    float2* psum = reinterpret_cast<float2*>(part + (size_t)rows * 2 * p.C);
+    float2* sums = psum + (size_t)p.N * f.parts * p.G;
+    const dim3 grid(f.tiles, f.splits, f.z);
+    const int lanes = join_lanes(f);
     hipLaunchKernelGGL((norm_grad_kernel<BF16, VEC, GATE, false>), grid, dim3(f.threads), 0, st, t.dout, t.x, t.weight, t.bias,
-                       t.gate, t.mean, t.rstd, t.dx, t.dgate, part, sums, p, f);
-    hipLaunchKernelGGL(norm_grad_join_kernel, small, dim3(256), 0, st, part, t.weight, sums, p, f);
+                       t.gate, t.mean, t.rstd, t.dx, t.dgate, part, psum, sums, p, f);
+    hipLaunchKernelGGL(norm_grad_join_kernel, dim3(join_grid(p, lanes)), dim3(256), 0, st, psum, sums, p, f, lanes);
     hipLaunchKernelGGL((norm_grad_kernel<BF16, VEC, GATE, true>), grid, dim3(f.threads), 0, st, t.dout, t.x, t.weight, t.bias,
-                       t.gate, t.mean, t.rstd, t.dx, t.dgate, part, sums, p, f);
+                       t.gate, t.mean, t.rstd, t.dx, t.dgate, part, psum, sums, p, f);
   }
   if (t.dweight || t.dbias)
     hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((p.C + 15) / 16, 2), dim3(256), 0, st, part, t.dweight, t.dbias, rows, p.C);
@@ -643,12 +821,15 @@ size_t norm_workspace(const NormProblem& p, bool gradient) {
   if (p.N == 0) return 0;
   if (by_rows(p)) {
     int L, NV;
+    long long rows;
     rows_shape(p, &L, &NV);
-    return gradient ? (size_t)rows_grid(p, L, true).y * 2 * p.C * sizeof(float) : 0;
+    rows_grid(p, L, &rows);
+    return gradient ? (size_t)rows * 2 * p.C * sizeof(float) : 0;
   }
   const NormPlan f = plan(p);
-  const size_t rows = (size_t)p.N * f.parts;
-  return gradient ? (rows * 2 * p.C + (size_t)p.N * p.G * 2) * sizeof(float) : rows * f.cvs * sizeof(float2);
+  const size_t sums = (size_t)p.N * f.parts * p.G;
+  return gradient ? (size_t)f.z * f.splits * 2 * p.C * sizeof(float) + (sums + (size_t)p.N * p.G) * sizeof(float2)
+                  : sums * sizeof(float4);
 }
 
 hipError_t norm_launch(const NormProblem& p, const void* x, const float* weight, const float* bias, const void* gate, void* out,
