@@ -259,29 +259,36 @@ __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_ker
 // times the third term; 3 for fp32), or 0: no outputs, but e and the state
 // before each chunk are left in the workspace for the gradients.
 //
-// SETS: 2 where few workgroups leave a CU to each, so only the step's own length
-// counts; 1 where there are enough of them for two on a CU: half the operand
-// registers, loads one step ahead, and the other workgroup fills the waits.
-template <int NT, int DKP, int PT, int SETS>
-__global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
+// NS: strips of 16 columns of a workgroup.  One where every strip can have a CU
+// to itself (d_k = d_v = 128, 16 chunks, 256 strips: 37 us against 46 in pairs):
+// only the step's own length counts, loads run two steps ahead.  Two where there
+// are more: the operands come through a CU's L1 once for both, which is what
+// bounds a full CU, and a step's waits have twice the products to fill them;
+// loads run one step ahead (384 strips 47 us against 69, 2048 strips 208 against
+// 315; single strips with two workgroups on a CU: 62 and 282).
+template <int NT, int DKP, int PT, int NS>
+__global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
+  constexpr int SETS = NS == 1 ? 2 : 1;               // operand sets in registers: steps that loads run ahead
   constexpr int KS = DKP / 32;                        // steps over d_k
   constexpr int SP = 16 * DKP, TP = 16 * kC;   // elements of a term's tile
   constexpr uint32_t es = NT == 1 ? 2 : 4;            // bytes of an input element
   constexpr uint32_t os = PT == 2 ? 2 : 4;            // of an output element
-  __shared__ __align__(16) bh Sl[3 * SP];
-  __shared__ __align__(16) bh Nl[3 * TP];
-  __shared__ __align__(16) bh Ul[(PT ? PT : 1) * TP];
-  __shared__ __align__(16) bh Dl[3 * TP];
-  __shared__ __align__(16) typename RawIn<NT>::type Vl[TP];
+  __shared__ __align__(16) bh Sl[NS][3 * SP];
+  __shared__ __align__(16) bh Nl[NS][3 * TP];
+  __shared__ __align__(16) bh Ul[NS][(PT ? PT : 1) * TP];
+  __shared__ __align__(16) bh Dl[NS][3 * TP];
+  __shared__ __align__(16) typename RawIn<NT>::type Vl[NS][TP];
   __shared__ int earlier, next;
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int lr = lane % 16, lg = lane / 16;
-  int sh, strip;
-  strip_of(blockIdx.x, p.dv / 16, &sh, &strip);
+  const int strips = p.dv / 16;
+  int sh, strip;                                      // strips strip .. + NS; the last one of the last workgroup may not exist
+  strip_of(blockIdx.x, (strips + NS - 1) / NS, &sh, &strip);
+  strip *= NS;
   if (sh >= p.sequences * p.hv) return;
   const int h = sh % p.hv, kh = h / (p.hv / p.hk);
   const int col = strip * 16 + lr;
-  const int strips = p.dv / 16;
+  const auto there = [&](int i) { return NS == 1 || strip + i < strips; };
   const int w = wave & 3;                             // row tile of the chunk
   const bool first_half = wave < 4;
   const int srow = DKP > 64 ? wave : wave - 4;        // row tile of the state, if it has one
@@ -317,14 +324,18 @@ __global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(Seq
     start = __builtin_amdgcn_readfirstlane(start);
     end = __builtin_amdgcn_readfirstlane(end);
     const size_t slot = start / kC + (size_t)seq;
-    f32x4 S = zero4();
-    if (has_state) {
-      if (t.h0 && kept)
+    f32x4 S[NS];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (st0 + r < p.dk) S[r] = t.h0[state + (size_t)(st0 + r) * p.dv + col];
-      const float x[4] = {S[0], S[1], S[2], S[3]};
-      put<3, DKP>(Sl + st_place, x);
+    for (int i = 0; i < NS; ++i) {
+      S[i] = zero4();
+      if (has_state) {
+        if (t.h0 && kept && there(i))
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (st0 + r < p.dk) S[i][r] = t.h0[state + (size_t)(st0 + r) * p.dv + col + 16 * i];
+        const float x[4] = {S[i][0], S[i][1], S[i][2], S[i][3]};
+        put<3, DKP>(Sl[i] + st_place, x);
+      }
     }
     const int last = (end - start + kC - 1) / kC - 1;
     // Loads behind the last chunk return 0.
@@ -342,19 +353,23 @@ __global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(Seq
       for (int ks = 0; ks < 2; ++ks) kt[set][ks] = frag_at<NT>(kb, kt_off + ks * NT * 1024);
     };
     auto step_state = [&](int c, int set) {
-      if constexpr (PT == 0) {
-        const buf_t sb = buf(ws.s0 + (((slot + c) * p.hv + h) * strips + strip) * DKP * 16, has_state ? DKP * 16 * 4 : 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) store_at<4>(sb, ((st0 + r) * 16 + lr) * 4, S[r]);
+      for (int i = 0; i < NS; ++i) {
+        if constexpr (PT == 0) {
+          const buf_t sb = buf(ws.s0 + (((slot + c) * p.hv + h) * strips + strip + i) * DKP * 16,
+                               has_state && there(i) ? DKP * 16 * 4 : 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) store_at<4>(sb, ((st0 + r) * 16 + lr) * 4, S[i][r]);
+        }
+        f32x4 a[3];
+        a[0] = S[i] * eGn[set];
+        a[1] = a[2] = zero4();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) mma_by_term<NT, 3>(kt[set][ks], get<3, kC>(Dl[i] + lane * 8, ks), a);
+        S[i] = a[0] + (a[1] + a[2]);
+        const float x[4] = {S[i][0], S[i][1], S[i][2], S[i][3]};
+        if (has_state) put<3, DKP>(Sl[i] + st_place, x);
       }
-      f32x4 a[3];
-      a[0] = S * eGn[set];
-      a[1] = a[2] = zero4();
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) mma_by_term<NT, 3>(kt[set][ks], get<3, kC>(Dl + lane * 8, ks), a);
-      S = a[0] + (a[1] + a[2]);
-      const float x[4] = {S[0], S[1], S[2], S[3]};
-      if (has_state) put<3, DKP>(Sl + st_place, x);
       load_state(c + SETS, set);
     };
     uint32_t col_off[KS];                             // of this lane's columns of K and Q
@@ -395,42 +410,53 @@ __global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(Seq
       __syncthreads();
       auto step = [&](int c, int set) {
         if constexpr (SETS == 2) __builtin_amdgcn_s_setprio(3);
-        f32x4 a[3];
-#pragma unroll
-        for (int i = 0; i < 3; ++i) a[i] = zero4();
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) mma_by_term<NT, 3>(frag_of<NT>(k[set][ks]), get<3, DKP>(Sl + lane * 8, ks), a);
-        float x[4], eg[4], ed[4], bt[4];
+        float eg[4], ed[4], bt[4];
+        f32x4 e[NS];
         floats(eG[set], eg);
-        get_values<NT>(Vl + (w * 64 + lane) * 4, x);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = fmaf(-eg[r], (a[2][r] + a[1][r]) + a[0][r], x[r]);
-        put<3, kC>(Nl + tok_place, x);
+        for (int i = 0; i < NS; ++i) {
+          f32x4 a[3];
+#pragma unroll
+          for (int j = 0; j < 3; ++j) a[j] = zero4();
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) mma_by_term<NT, 3>(frag_of<NT>(k[set][ks]), get<3, DKP>(Sl[i] + lane * 8, ks), a);
+          float x[4];
+          get_values<NT>(Vl[i] + (w * 64 + lane) * 4, x);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[r] = fmaf(-eg[r], (a[2][r] + a[1][r]) + a[0][r], x[r]);
+          put<3, kC>(Nl[i] + tok_place, x);
+        }
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 3; ++i) a[i] = zero4();
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) mma_by_term<3, 3>(t1[set][ks], get<3, kC>(Nl + lane * 8, ks), a);
-        const f32x4 e = (a[2] + a[1]) + a[0];
         floats(eD[set], ed);
         floats(be[set], bt);
-        float ud[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          x[r] = bt[r] * e[r];
-          ud[r] = ed[r] * x[r];
+        for (int i = 0; i < NS; ++i) {
+          f32x4 a[3];
+#pragma unroll
+          for (int j = 0; j < 3; ++j) a[j] = zero4();
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) mma_by_term<3, 3>(t1[set][ks], get<3, kC>(Nl[i] + lane * 8, ks), a);
+          e[i] = (a[2] + a[1]) + a[0];
+          float x[4], ud[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            x[r] = bt[r] * e[i][r];
+            ud[r] = ed[r] * x[r];
+          }
+          put<3, kC>(Dl[i] + tok_place, ud);
+          if constexpr (PT > 0) put<PT, kC>(Ul[i] + tok_place, x);
         }
-        put<3, kC>(Dl + tok_place, ud);
-        if constexpr (PT > 0) put<PT, kC>(Ul + tok_place, x);
         __syncthreads();
         if constexpr (DKP > 64) step_state(c, set);
         if constexpr (SETS == 2) __builtin_amdgcn_s_setprio(0);
         load(c + SETS, set);
-        if constexpr (PT == 0) {
-          const buf_t eb = buf(ws.e + (((slot + c) * p.hv + h) * strips + strip) * kC * 16, kC * 16 * 4);
+        if constexpr (PT == 0)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) store_at<4>(eb, ((row0 + r) * 16 + lr) * 4, e[r]);
-        }
+          for (int i = 0; i < NS; ++i) {
+            const buf_t eb = buf(ws.e + (((slot + c) * p.hv + h) * strips + strip + i) * kC * 16, there(i) ? kC * 16 * 4 : 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) store_at<4>(eb, ((row0 + r) * 16 + lr) * 4, e[i][r]);
+          }
         __syncthreads();
       };
       for (int c = 0; c <= last; c += SETS) {
@@ -441,7 +467,7 @@ __global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(Seq
     } else {
       const uint32_t qs_b = (uint32_t)p.qs * es, vs_b = (uint32_t)p.vs * es, os_b = (uint32_t)(p.hv * p.dv) * os;
       RawFrag<NT> q[SETS][KS];
-      typename RawIn<NT>::type v[4];
+      typename RawIn<NT>::type v[NS][4];
       uint4 eG[SETS];
       Frag<PT ? PT : 1> pf[SETS][2];
       auto load = [&](int c, int set) {
@@ -459,7 +485,10 @@ __global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(Seq
         const buf_t vb = buf(static_cast<const char*>(t.v) + ((start + (size_t)c * kC) * p.vs + h * p.dv) * es,
                              span(rows_of(c), vs_b, dv_b));
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = value_at<NT>(vb, (row0 + r) * vs_b + col * es);
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            v[i][r] = value_at<NT>(vb, there(i) ? (row0 + r) * vs_b + (col + 16 * i) * es : kNowhere);
       };
       auto load_p = [&](int c, int set) {
         if constexpr (PT > 0) {
@@ -473,7 +502,11 @@ __global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(Seq
       load(0, 0);
       load_p(0, 0);
       load_state(0, 0);
-      put_values<NT>(Vl + (w * 64 + lane) * 4, v);
+      auto put_v = [&]() {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) put_values<NT>(Vl[i] + (w * 64 + lane) * 4, v[i]);
+      };
+      put_v();
       load_v(1);
       if constexpr (SETS == 2) {
         load(1, 1);
@@ -481,16 +514,20 @@ __global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(Seq
         load_state(1, 1);
       }
       __syncthreads();
-      f32x4 o = zero4();
+      f32x4 o[NS];
       // P U of chunk c and its store, beside the next step's first phase
       auto finish = [&](int c, int set) {
         if constexpr (PT > 0) {
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) o = mma<PT, PT>(pf[set][ks], get<PT, kC>(Ul + lane * 8, ks), o);
           const buf_t ob = buf(static_cast<char*>(t.out) + ((start + (size_t)c * kC) * p.hv + h) * p.dv * os,
                                span(rows_of(c), os_b, p.dv * os));
 #pragma unroll
-          for (int r = 0; r < 4; ++r) store_at<os>(ob, (row0 + r) * os_b + col * os, o[r]);
+          for (int i = 0; i < NS; ++i) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) o[i] = mma<PT, PT>(pf[set][ks], get<PT, kC>(Ul[i] + lane * 8, ks), o[i]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              store_at<os>(ob, there(i) ? (row0 + r) * os_b + (col + 16 * i) * os : kNowhere, o[i][r]);
+          }
           load_p(c + SETS, set);
         }
       };
@@ -498,16 +535,20 @@ __global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(Seq
         if constexpr (PT > 0)
           if (c > 0) finish(c - 1, SETS == 2 ? set ^ 1 : 0);
         __syncthreads();
-        put_values<NT>(Vl + (w * 64 + lane) * 4, v);
+        put_v();
         load_v(c + 2);
         if constexpr (PT > 0) {
           float eg[4];
           floats(eG[set], eg);
-          o = zero4();
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) o = mma<NT, PT>(frag_of<NT>(q[set][ks]), get<PT, DKP>(Sl + lane * 8, ks), o);
+          for (int i = 0; i < NS; ++i) {
+            o[i] = zero4();
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[r] *= eg[r];
+            for (int ks = 0; ks < KS; ++ks)
+              o[i] = mma<NT, PT>(frag_of<NT>(q[set][ks]), get<PT, DKP>(Sl[i] + lane * 8, ks), o[i]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[i][r] *= eg[r];
+          }
         }
         load(c + SETS, set);
         __syncthreads();
@@ -527,8 +568,10 @@ __global__ __launch_bounds__(512, SETS == 1 ? 4 : 2) void packed_scan_kernel(Seq
     }
     if (t.hT && kept && has_state)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (st0 + r < p.dk) t.hT[state + (size_t)(st0 + r) * p.dv + col] = S[r];
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (st0 + r < p.dk && there(i)) t.hT[state + (size_t)(st0 + r) * p.dv + col + 16 * i] = S[i][r];
     if (!t.slots || !kept || next == 0x7fffffff) break;
     // the next sequence of this state row (rare)
     __syncthreads();
@@ -601,13 +644,13 @@ hipError_t packed_prep(const SeqProblem& p, const PackedTensors& t, const Packed
 
 hipError_t packed_scan(const SeqProblem& p, const PackedTensors& t, const PackedSpace& s, bool grad, hipStream_t stream) {
   const PackedPlan f = packed_plan(p);
-  const int padded = (p.sequences * p.hv + 7) / 8 * 8;
-  const dim3 grid((unsigned)padded * f.strips);
-  const bool two = grid.x > 256;   // more workgroups than CUs
+  const unsigned heads = (p.sequences * p.hv + 7) / 8 * 8;
+  const bool pairs = f.strips > 1 && (long long)p.sequences * p.hv * f.strips > 256;   // more strips than CUs
+  const dim3 grid(heads * (pairs ? (f.strips + 1) / 2 : f.strips));
   prof_begin(stream, GDN_KERNEL_PACKED_SCAN);
-#define GDN_SCAN2(NT, D, PT)                                                                                          \
-  if (two) hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 1>), grid, dim3(512), 0, stream, p, t, s);               \
-  else hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 2>), grid, dim3(512), 0, stream, p, t, s);
+#define GDN_SCAN2(NT, D, PT)                                                                                         \
+  if (pairs) hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 2>), grid, dim3(512), 0, stream, p, t, s);            \
+  else hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 1>), grid, dim3(512), 0, stream, p, t, s);
 #define GDN_SCAN(NT, D)                      \
   if (f.terms == NT && f.dkp == D) {         \
     if (grad) { GDN_SCAN2(NT, D, 0) }        \

@@ -28,10 +28,10 @@ constexpr int kLd = 68;     // row stride (floats) of a 64 x 64 fp32 tile in LDS
 
 // What a chunk's step reads, by phase; loaded for the next chunk as soon as a
 // phase has used it, as in the forward scan.
-template <int NT, int DKP>
+template <int NT, int DKP, int NS>
 struct GradIn {
   static constexpr int KS = DKP / 32, MT = DKP >= 64 ? DKP / 64 : 1;
-  typename RawIn<NT>::type dout[4]; // of the chunk after the one whose step runs
+  typename RawIn<NT>::type dout[NS][4]; // of the chunk after the one whose step runs
   float4 deG;
   RawFrag<NT> k[KS];                // rows of K
   Frag<3> p[2];                     // P^T
@@ -43,25 +43,33 @@ struct GradIn {
   Frag<NT> kt[MT][2];               // K^T
 };
 
-template <int NT, int DKP>
+// NS: strips of 16 columns of a workgroup.  One where all of them are resident at
+// once, two to a CU; two where there are more: operands are fetched once for both
+// (d_k = d_v = 128, bf16, 16 chunks: 2048 strips 245 us against 353; 512 strips
+// of equal lengths 71 against 87, but 420 of three unequal sequences 32 against
+// 27, since the longest sequence's steps are what lasts).  Eight wavefronts in two
+// roles as in the forward scan gave 305 and 79.
+template <int NT, int DKP, int NS>
 __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
-  using In = GradIn<NT, DKP>;
+  using In = GradIn<NT, DKP, NS>;
   constexpr int KS = In::KS;
   constexpr int MT = In::MT;
   constexpr int SP = 16 * DKP, TP = 16 * kC;   // elements of a term's tile
-  __shared__ __align__(16) bh Sl[3 * SP];           // dS
-  __shared__ __align__(16) bh Ol[NT * TP];          // dO
-  __shared__ __align__(16) bh Xl[3 * TP];           // e^G dO
-  __shared__ __align__(16) bh Ul[3 * TP];           // dU
-  __shared__ __align__(16) bh Yl[3 * TP];           // -e^G dN
+  __shared__ __align__(16) bh Sl[NS][3 * SP];           // dS
+  __shared__ __align__(16) bh Ol[NS][NT * TP];          // dO
+  __shared__ __align__(16) bh Xl[NS][3 * TP];           // e^G dO
+  __shared__ __align__(16) bh Ul[NS][3 * TP];           // dU
+  __shared__ __align__(16) bh Yl[NS][3 * TP];           // -e^G dN
   const int tid = threadIdx.x, lane = tid % 64, w = tid / 64;
   const int lr = lane % 16, lg = lane / 16;
   int sh, strip;
-  strip_of(blockIdx.x, p.dv / 16, &sh, &strip);
+  strip_of(blockIdx.x, (p.dv / 16 + NS - 1) / NS, &sh, &strip);
+  strip *= NS;                                      // strips strip .. + NS; the last one of the last workgroup may not exist
   if (sh >= p.sequences * p.hv) return;
   const int h = sh % p.hv, kh = h / (p.hv / p.hk), seq = sh / p.hv;
   const int col = strip * 16 + lr;
   const int strips = p.dv / 16;
+  const auto there = [&](int i) { return NS == 1 || strip + i < strips; };
   const bool srows = DKP >= 64 || w < DKP / 16;
   const size_t state = ((size_t)seq * p.hv + h) * p.dk * p.dv;
   int start, end;
@@ -73,20 +81,22 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(
   const int tok_place = put_place(lr, row0);
   auto cell_of = [&](int c) { return (size_t)(slot0 + c) * p.hv + h; };
 
-  f32x4 S[MT];
+  f32x4 S[NS][MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int i = 0; i < NS; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = (w * MT + m) * 16 + 4 * lg + r;
-      S[m][r] = t.dhT && row < p.dk ? t.dhT[state + (size_t)row * p.dv + col] : 0.f;
-    }
-  auto put_state = [&]() {
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = (w * MT + m) * 16 + 4 * lg + r;
+        S[i][m][r] = t.dhT && row < p.dk && there(i) ? t.dhT[state + (size_t)row * p.dv + col + 16 * i] : 0.f;
+      }
+  auto put_state = [&](int i) {
     if (srows)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const float x[4] = {S[m][0], S[m][1], S[m][2], S[m][3]};
-        put<3, DKP>(Sl + put_place(lr, (w * MT + m) * 16 + 4 * lg), x);
+        const float x[4] = {S[i][m][0], S[i][m][1], S[i][m][2], S[i][m][3]};
+        put<3, DKP>(Sl[i] + put_place(lr, (w * MT + m) * 16 + 4 * lg), x);
       }
   };
   In in;
@@ -96,20 +106,26 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(
     const int first = start + c * kC, n = end - first;
     const buf_t ob = buf(static_cast<const char*>(t.dout) + ((size_t)first * p.hv + h) * p.dv * es, span(n, ostride, p.dv * es));
 #pragma unroll
-    for (int r = 0; r < 4; ++r) in.dout[r] = value_at<NT>(ob, (row0 + r) * ostride + col * es);
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        in.dout[i][r] = value_at<NT>(ob, there(i) ? (row0 + r) * ostride + (col + 16 * i) * es : kNowhere);
     in.deG = *reinterpret_cast<const float4*>(ws.gates + cell_of(c) * 3 * kC + row0);
   };
   // chunk c's four tokens of this lane, plain and times e^G, as operand columns
   auto put_dout = [&]() {
     const float eg[4] = {in.deG.x, in.deG.y, in.deG.z, in.deG.w};
-    float x[4], y[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      x[r] = raw_value(in.dout[r]);
-      y[r] = eg[r] * x[r];
+    for (int i = 0; i < NS; ++i) {
+      float x[4], y[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        x[r] = raw_value(in.dout[i][r]);
+        y[r] = eg[r] * x[r];
+      }
+      put<NT, kC>(Ol[i] + tok_place, x);
+      put<3, kC>(Xl[i] + tok_place, y);
     }
-    put<NT, kC>(Ol + tok_place, x);
-    put<3, kC>(Xl + tok_place, y);
   };
   int vector_zero = 0;
   asm volatile("" : "+v"(vector_zero));             // a scalar load would be waited for with the LDS traffic
@@ -160,94 +176,110 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(
     load_second(last);
     load_third(last);
   }
-  put_state();
+#pragma unroll
+  for (int i = 0; i < NS; ++i) put_state(i);
   __syncthreads();
   for (int c = last; c >= 0; --c) {
     const int first = start + c * kC, n = min(kC, end - first);
     const size_t cell = cell_of(c);
     const int next = c ? c - 1 : 0, after = c > 1 ? c - 2 : 0;   // the first chunks' loads are repeated instead
-    f32x4 a[3], u = zero4();
-#pragma unroll
-    for (int i = 0; i < 3; ++i) a[i] = zero4();
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) mma_by_term<NT, 3>(frag_of<NT>(in.k[ks]), get<3, DKP>(Sl + lane * 8, ks), a);
-    const float ed[4] = {in.eD.x, in.eD.y, in.eD.z, in.eD.w};
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-      if (ks >= w / 2) u = mma<3, NT>(in.p[ks], get<NT, kC>(Ol + lane * 8, ks), u);
     {
-      float x[4];
+      const float ed[4] = {in.eD.x, in.eD.y, in.eD.z, in.eD.w};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = fmaf(ed[r], (a[2][r] + a[1][r]) + a[0][r], u[r]);
-      put<3, kC>(Ul + tok_place, x);
+      for (int i = 0; i < NS; ++i) {
+        f32x4 a[3], u = zero4();
+#pragma unroll
+        for (int j = 0; j < 3; ++j) a[j] = zero4();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) mma_by_term<NT, 3>(frag_of<NT>(in.k[ks]), get<3, DKP>(Sl[i] + lane * 8, ks), a);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          if (ks >= w / 2) u = mma<3, NT>(in.p[ks], get<NT, kC>(Ol[i] + lane * 8, ks), u);
+        float x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = fmaf(ed[r], (a[2][r] + a[1][r]) + a[0][r], u[r]);
+        put<3, kC>(Ul[i] + tok_place, x);
+      }
     }
     if (srows) {
       // Q^T (e^G dO) needs nothing of this step: it fills the wait for the barrier
-      float* so = ws.ds + (cell * strips + strip) * DKP * 16;
-      Frag<3> xf[2];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) xf[ks] = get<3, kC>(Xl + lane * 8, ks);
+      for (int i = 0; i < NS; ++i) {
+        const buf_t sb = buf(ws.ds + (cell * strips + strip + i) * DKP * 16, there(i) ? DKP * 16 * 4 : 0);
+        Frag<3> xf[2];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+        for (int ks = 0; ks < 2; ++ks) xf[ks] = get<3, kC>(Xl[i] + lane * 8, ks);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) so[((w * MT + m) * 16 + 4 * lg + r) * 16 + lr] = S[m][r];
-        S[m] = S[m] * in.eGn;
+        for (int m = 0; m < MT; ++m) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) S[m] = mma<NT, 3>(in.qt[m][ks], xf[ks], S[m]);
+          for (int r = 0; r < 4; ++r) store_at<4>(sb, (((w * MT + m) * 16 + 4 * lg + r) * 16 + lr) * 4, S[i][m][r]);
+          S[i][m] = S[i][m] * in.eGn;
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) S[i][m] = mma<NT, 3>(in.qt[m][ks], xf[ks], S[i][m]);
+        }
       }
     }
     load_first(next);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 3; ++i) a[i] = zero4();
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-      if (ks >= w / 2) mma_by_term<3, 3>(in.t2[ks], get<3, kC>(Ul + lane * 8, ks), a);
     {
-      const f32x4 W = (a[2] + a[1]) + a[0];
       const float eg[4] = {in.eG.x, in.eG.y, in.eG.z, in.eG.w}, bt[4] = {in.beta.x, in.beta.y, in.beta.z, in.beta.w};
-      float* wo = ws.w + (cell * strips + strip) * kC * 16;
       const buf_t vb = buf(static_cast<char*>(t.dv) + ((size_t)first * p.hv + h) * p.dv * es, span(n, ostride, p.dv * es));
-      float y[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) y[r] = -eg[r] * (bt[r] * W[r]);
-      put<3, kC>(Yl + tok_place, y);
+      for (int i = 0; i < NS; ++i) {
+        f32x4 a[3];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        wo[(row0 + r) * 16 + lr] = W[r];
-        store_at<es>(vb, (row0 + r) * ostride + col * es, bt[r] * W[r]);
+        for (int j = 0; j < 3; ++j) a[j] = zero4();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          if (ks >= w / 2) mma_by_term<3, 3>(in.t2[ks], get<3, kC>(Ul[i] + lane * 8, ks), a);
+        const f32x4 W = (a[2] + a[1]) + a[0];
+        const buf_t wb = buf(ws.w + (cell * strips + strip + i) * kC * 16, there(i) ? kC * 16 * 4 : 0);
+        float y[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = -eg[r] * (bt[r] * W[r]);
+        put<3, kC>(Yl[i] + tok_place, y);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          store_at<4>(wb, ((row0 + r) * 16 + lr) * 4, W[r]);
+          store_at<es>(vb, there(i) ? (row0 + r) * ostride + (col + 16 * i) * es : kNowhere, bt[r] * W[r]);
+        }
       }
     }
     put_dout();                                      // the next chunk's: this one's have been read
     load_dout(after);
     load_second(next);
     __syncthreads();
-    if (srows) {
-      Frag<3> yf[2];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) yf[ks] = get<3, kC>(Yl + lane * 8, ks);
+    for (int i = 0; i < NS; ++i) {
+      if (srows) {
+        Frag<3> yf[2];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        f32x4 b[3];
-        b[0] = S[m];
-        b[1] = b[2] = zero4();
+        for (int ks = 0; ks < 2; ++ks) yf[ks] = get<3, kC>(Yl[i] + lane * 8, ks);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) mma_by_term<NT, 3>(in.kt[m][ks], yf[ks], b);
-        S[m] = b[0] + (b[1] + b[2]);
+        for (int m = 0; m < MT; ++m) {
+          f32x4 b[3];
+          b[0] = S[i][m];
+          b[1] = b[2] = zero4();
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) mma_by_term<NT, 3>(in.kt[m][ks], yf[ks], b);
+          S[i][m] = b[0] + (b[1] + b[2]);
+        }
       }
+      put_state(i);
     }
-    put_state();
     load_third(next);
     __syncthreads();
   }
   if (t.dh0 && srows)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < NS; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = (w * MT + m) * 16 + 4 * lg + r;
-        if (row < p.dk) t.dh0[state + (size_t)row * p.dv + col] = S[m][r];
-      }
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = (w * MT + m) * 16 + 4 * lg + r;
+          if (row < p.dk && there(i)) t.dh0[state + (size_t)row * p.dv + col + 16 * i] = S[i][m][r];
+        }
 }
 
 // Sum over a wavefront's 64 lanes.
@@ -536,11 +568,15 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
 
 hipError_t packed_scan_grad(const SeqProblem& p, const PackedTensors& t, const PackedSpace& s, hipStream_t stream) {
   const PackedPlan f = packed_plan(p);
-  const int padded = (p.sequences * p.hv + 7) / 8 * 8;
-  const dim3 grid((unsigned)padded * f.strips);
+  const unsigned heads = (p.sequences * p.hv + 7) / 8 * 8;
+  const bool pairs = f.strips > 1 && (long long)p.sequences * p.hv * f.strips > 512;   // more than two strips a CU
+  const dim3 grid(heads * (pairs ? (f.strips + 1) / 2 : f.strips));
   prof_begin(stream, GDN_KERNEL_PACKED_SCAN_GRAD);
-#define GDN_SCAN(NT, D) \
-  if (f.terms == NT && f.dkp == D) hipLaunchKernelGGL((packed_scan_grad_kernel<NT, D>), grid, dim3(256), 0, stream, p, t, s);
+#define GDN_SCAN(NT, D)                                                                                            \
+  if (f.terms == NT && f.dkp == D) {                                                                               \
+    if (pairs) hipLaunchKernelGGL((packed_scan_grad_kernel<NT, D, 2>), grid, dim3(256), 0, stream, p, t, s);       \
+    else hipLaunchKernelGGL((packed_scan_grad_kernel<NT, D, 1>), grid, dim3(256), 0, stream, p, t, s);             \
+  }
   GDN_SCAN(1, 32) GDN_SCAN(1, 64) GDN_SCAN(1, 128) GDN_SCAN(3, 32) GDN_SCAN(3, 64) GDN_SCAN(3, 128)
 #undef GDN_SCAN
   const hipError_t e = hipGetLastError();

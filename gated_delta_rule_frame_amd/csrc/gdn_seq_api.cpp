@@ -26,8 +26,8 @@ gdn_status check_seq(const gdn_seq_problem* pr, bool slots, gdn::SeqProblem* out
     return fail(GDN_ERR_INVALID_ARGUMENT, "d_k and d_v must be multiples of 16 in [16, 128] (got %d, %d)", pr->d_k, pr->d_v);
   if ((pr->qkv_dtype != GDN_F32 && pr->qkv_dtype != GDN_BF16) || (pr->out_dtype != GDN_F32 && pr->out_dtype != GDN_BF16))
     return fail(GDN_ERR_INVALID_ARGUMENT, "qkv_dtype/out_dtype must be GDN_F32 or GDN_BF16");
-  if (pr->tokens < 0 || pr->tokens > (1LL << 31) - 65)
-    return fail(GDN_ERR_INVALID_ARGUMENT, "tokens must be in [0, 2^31 - 65] (got %lld)", (long long)pr->tokens);
+  if (pr->tokens < 0 || pr->tokens > (1LL << 31) - 256)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "tokens must be in [0, 2^31 - 256] (got %lld)", (long long)pr->tokens);
   if (slots && pr->state_rows < 0)
     return fail(GDN_ERR_INVALID_ARGUMENT, "state_rows must be >= 0 (got %d)", pr->state_rows);
   const long long qk = (long long)pr->heads_k * pr->d_k, v = (long long)pr->heads_v * pr->d_v;

@@ -345,7 +345,9 @@ PACKED = [  # lengths, hk, hv, dk, dv, dtype, gate range, state
     ([0, 1, 63, 0, 65, 2, 0], 2, 4, 112, 112, BF16, (0.001, 0.1), True), ([200, 3], 1, 3, 128, 128, BF16, (0.0005, 0.02), True),
     ([129], 1, 1, 32, 48, F32, (0.001, 0.1), True), ([70, 130], 2, 2, 128, 96, F32, (0.001, 0.1), True),
     ([257], 1, 2, 80, 16, F32, (0.1, 6.0), False), ([300, 1, 20], 3, 3, 48, 128, BF16, (0.0, 30.0), True),
-    ([1000], 1, 1, 64, 32, F32, (0.0, 0.0005), True)]
+    ([1000], 1, 1, 64, 32, F32, (0.0, 0.0005), True),
+    # more column strips than CUs, an odd number of them in a head: pairs of strips, the last one alone
+    ([7, 0, 65, 130, 1] * 9, 2, 4, 48, 48, F32, (0.001, 0.1), True), ([70, 64, 1] * 8, 3, 6, 128, 80, BF16, (0.001, 0.1), True)]
 
 
 @pytest.mark.parametrize("lengths,hk,hv,dk,dv,dtype,gate,with_state", PACKED)
