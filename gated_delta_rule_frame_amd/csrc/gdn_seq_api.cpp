@@ -89,8 +89,8 @@ gdn_status check_norm(const gdn_norm_problem* pr, gdn::NormProblem* out) {
     if (pr->reserved[i] != 0) return fail(GDN_ERR_INVALID_ARGUMENT, "reserved[%d] is not zero", i);
   if (pr->dtype != GDN_F32 && pr->dtype != GDN_BF16)
     return fail(GDN_ERR_INVALID_ARGUMENT, "dtype must be GDN_F32 or GDN_BF16");
-  if (pr->batch < 0 || pr->spatial < 1 || pr->channels < 1 || pr->channels > (1 << 24))
-    return fail(GDN_ERR_INVALID_ARGUMENT, "batch must be >= 0, spatial >= 1, channels in [1, 2^24] (got %lld, %d, %d)",
+  if (pr->batch < 0 || pr->spatial < 1 || pr->spatial > (1 << 30) || pr->channels < 1 || pr->channels > (1 << 24))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "batch must be >= 0, spatial in [1, 2^30], channels in [1, 2^24] (got %lld, %d, %d)",
                 (long long)pr->batch, pr->spatial, pr->channels);
   if (pr->groups < 1 || pr->channels % pr->groups)
     return fail(GDN_ERR_INVALID_ARGUMENT, "channels (%d) must be a multiple of groups (%d)", pr->channels, pr->groups);

@@ -424,7 +424,7 @@ typedef struct gdn_norm_problem {
   int32_t abi_version;        /* must equal GDN_ABI_VERSION */
   int32_t dtype;              /* GDN_F32 or GDN_BF16: x, gate, out and their gradients */
   int64_t batch;              /* >= 0 */
-  int32_t spatial;            /* >= 1 */
+  int32_t spatial;            /* in [1, 2^30] */
   int32_t channels;           /* in [1, 2^24], a multiple of groups */
   int32_t groups;             /* >= 1 */
   int32_t activation;         /* GDN_ACT_* */

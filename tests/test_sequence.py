@@ -2,9 +2,6 @@
 calls without work, through the C ABI with pointers that are never used (no
 GPU needed), and the binding's refusals."""
 import ctypes
-import os
-import subprocess
-from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -102,7 +99,7 @@ def norm(**kw):
 
 
 @pytest.mark.parametrize("field,value", [
-    ("abi_version", 3), ("dtype", 2), ("batch", -1), ("spatial", 0), ("channels", 0), ("channels", 66), ("channels", 1 << 25),
+    ("abi_version", 3), ("dtype", 2), ("batch", -1), ("spatial", 0), ("spatial", (1 << 30) + 1), ("channels", 0), ("channels", 66), ("channels", 1 << 25),
     ("groups", 0), ("groups", 5), ("activation", 4), ("activation", -1), ("center", 2), ("eps", float("nan")), ("eps", -1e-5),
     ("batch", 1 << 41)])
 def test_norm_rejects_bad_problems(field, value):
