@@ -202,13 +202,16 @@ def packed_forward(q, k, v, log_gate, beta, cu_seqlens, initial_state=None, *, s
     return out, final_state
 
 
-def packed_backward(q, k, v, log_gate, beta, cu_seqlens, dout, initial_state=None, dfinal_state=None, *, workspace=None):
+def packed_backward(q, k, v, log_gate, beta, cu_seqlens, dout, initial_state=None, dfinal_state=None, *, grads=None,
+                    workspace=None):
     """Gradients of ``packed_forward`` (gdn_packed_backward); returns (dq, dk, dv, dlog_gate, dbeta, dinitial_state).
 
     The inputs are packed_forward's (without slots); dout: like v;
     dfinal_state: like the final state, or None (zeros).  dq, dk and dv have
     q's dtype and are dense, the others are fp32; dinitial_state is None
-    where initial_state is.  Rows behind the last sequence are not written.
+    where initial_state is.  Rows behind the last sequence are not written, so
+    that in fresh tensors they hold nothing: for a padded batch give ``grads``,
+    five zeroed tensors (dq, dk, dv, dlog_gate, dbeta) to write into.
     """
     p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, beta, torch.float32)
     seqs = p.sequences = _sequences(cu_seqlens, device)
@@ -217,9 +220,16 @@ def packed_backward(q, k, v, log_gate, beta, cu_seqlens, dout, initial_state=Non
     for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
         if t is not None:
             _dense(name, t, shape, torch.float32, device)
+    inputs = {"dq": q, "dk": k, "dv": v, "dlog_gate": log_gate, "dbeta": beta}
+    if grads is None:
+        grads = [torch.empty(t.shape, dtype=t.dtype, device=device) for t in inputs.values()]
+    else:
+        if len(grads) != 5:
+            raise ValueError(f"grads must be five tensors (got {len(grads)})")
+        for (name, t), d in zip(inputs.items(), grads):
+            _dense(name, d, t.shape, t.dtype, device)
     L = lib()
     ws, ws_bytes = _space(L.gdn_packed_workspace_size, p, 1, workspace, device)
-    grads = [torch.empty(t.shape, dtype=t.dtype, device=device) for t in (q, k, v, log_gate, beta)]
     dstate = None if initial_state is None else torch.empty_like(initial_state)
     _on(device, L.gdn_packed_backward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), beta.data_ptr(),
         cu_seqlens.data_ptr(), _ptr(initial_state), dout.data_ptr(), _ptr(dfinal_state), *(t.data_ptr() for t in grads),

@@ -615,3 +615,150 @@ def test_packed_backward_without_tokens_and_refusals(G):
                  lambda: G.packed_backward(*x, cu, dout, workspace=torch.empty(64, device="cuda"))):
         with pytest.raises((ValueError, TypeError, G.GdnError)):
             call()
+
+
+def test_packed_backward_writes_into_given_tensors(G):
+    """A padded batch: given zeroed tensors keep the rows behind the last sequence at zero."""
+    x, cu = rows(140, 1, 2, 32, 48, BF16, 9), cu_of([30, 70])
+    dout = torch.randn(140, 2, 48, device="cuda").bfloat16()
+    want = G.packed_backward(*x, cu, dout)
+    mine = [torch.zeros_like(t) for t in x]
+    got = G.packed_backward(*x, cu, dout, grads=mine)
+    for m, a, b in zip(mine, got, want):
+        assert a is m and torch.equal(a[:100], b[:100]) and not a[100:].any()
+    for bad in (mine[:4], [*mine[:4], mine[4].bfloat16()], [mine[0][:, :, :16], *mine[1:]], [mine[0].float(), *mine[1:]]):
+        with pytest.raises(ValueError):
+            G.packed_backward(*x, cu, dout, grads=bad)
+
+
+def test_packed_backward_strided_inputs(G):
+    """q, k and v as slices of one fused projection: the gradients of dense copies, bit for bit."""
+    x, cu = rows(150, 2, 4, 48, 64, F32, 10), cu_of([1, 80, 69])
+    fused = torch.cat([t.reshape(150, -1) for t in x[:3]], 1)
+    q, k, v = fused[:, :96].view(150, 2, 48), fused[:, 96:192].view(150, 2, 48), fused[:, 192:].view(150, 4, 64)
+    dout = torch.randn(150, 4, 64, device="cuda")
+    for a, b in zip(G.packed_backward(q, k, v, *x[3:], cu, dout)[:5], G.packed_backward(*x, cu, dout)):
+        assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ together
+
+def test_serving_prompts_then_tokens(G):
+    """Prompts into a pool of states, their gated norm, then decoding steps with padding rows and their norm."""
+    lengths, hk, hv, d, pool, steps = [70, 1, 130], 2, 4, 64, 5, 3
+    n, C = sum(lengths), 4 * 64
+    x, cu = rows(n, hk, hv, d, d, BF16, 21), cu_of(lengths)
+    gen = torch.Generator().manual_seed(22)
+    z = torch.randn(n, C, generator=gen).bfloat16().cuda()
+    weight = (1 + 0.1 * torch.randn(C, generator=gen)).cuda()
+    state = torch.zeros(pool, hv, d, d, device="cuda")
+    slots = [3, 0, 4]
+    norm = dict(activation="silu", center=False, eps=1e-6)
+
+    def check(got, o, gate):
+        # the output is rounded to bf16 before the norm and after it, and its group's rms moves by at most as much:
+        # three half steps; and near32's bound of fp32 errors, 4e-5 of the rms, times weight and gate up to 5
+        ref = R.group_norm(o.reshape(-1, 1, C), hv, R.f64(weight), None, R.f64(gate).reshape(-1, 1, C), "silu", False, 1e-6)[0]
+        err = (R.f64(got) - ref[:, 0]).abs()
+        assert (err <= 3.1 * 2.0 ** -8 * ref[:, 0].abs() + 2e-4).all(), err.max()
+
+    out, _ = G.packed_forward(*x, cu, state, slots=torch.tensor(slots, dtype=torch.int32, device="cuda"), out_dtype=BF16)
+    y, _, _ = G.group_norm(out.view(n, C), hv, weight, None, z, **norm)
+    ref, S = R.packed(*(R.f64(t) for t in x), cu.tolist(), None)
+    check(y, ref, z)
+    for i in range(steps):
+        t = rows(4, hk, hv, d, d, BF16, 30 + i)
+        gate = torch.randn(4, C, generator=gen).bfloat16().cuda()
+        order = torch.tensor([4, -1, 3, 0], dtype=torch.int32, device="cuda")
+        out = G.decode(*t, state, order, out=torch.zeros(4, hv, d, device="cuda", dtype=BF16))
+        y, _, _ = G.group_norm(out.view(4, C), hv, weight, None, gate, **norm)
+        want = torch.zeros(4, hv, d, dtype=torch.float64)
+        for row, seq in ((0, 2), (2, 0), (3, 1)):
+            o, S[seq] = R.tokens(*(R.f64(a[row:row + 1]) for a in t), S[seq])
+            want[row] = o[0]
+        check(y, want, gate)
+    near32(state[slots], S, times=2)
+    assert not state[[1, 2]].any()
+
+
+def test_training_through_the_norm(G):
+    """Gradients of sum(norm(rule(inputs)) w) through both backward calls, against differentiation in float64."""
+    lengths, hk, hv, d = [33, 90], 1, 2, 32
+    n, C = sum(lengths), 2 * 32
+    x, cu = rows(n, hk, hv, d, d, F32, 41), cu_of(lengths)
+    gen = torch.Generator().manual_seed(42)
+    r = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    z, w, S0, weight = r(n, C), r(n, C), r(2, hv, d, d), 1 + 0.1 * r(C)
+    out, _ = G.packed_forward(*x, cu, S0)
+    y, mean, rstd = G.group_norm(out.view(n, C), hv, weight, None, z, activation="silu", center=False)
+    dout, dw, _, dz = G.group_norm_backward(w, out.view(n, C), hv, None, rstd, weight, None, z, activation="silu", center=False)
+    got = G.packed_backward(*x, cu, dout.view(n, hv, d), S0)
+    leaves = [R.f64(t).requires_grad_() for t in (*x, S0, weight, z)]
+    o, _ = R.packed(*leaves[:5], cu.tolist(), leaves[5])
+    f = R.group_norm(o.reshape(n, 1, C), hv, leaves[6], None, leaves[7].reshape(n, 1, C), "silu", False, 1e-5)[0][:, 0]
+    near32(y, f.detach())
+    want = torch.autograd.grad((f * R.f64(w)).sum(), leaves)
+    # the norm's rstd scales the rule's output up by 1 / rms of it: its errors count relative to small outputs
+    check_grads(got, want[:6], n, F32, 32.0)
+    near32(dw, want[6], times=8)
+    near32(dz, want[7], times=8)
+
+
+# ------------------------------------------------------------------ large tensors
+
+def test_pools_past_32_bits(G):
+    """State rows whose offsets pass 2^31 elements (8.8 GB): as in a small pool."""
+    hv, d, pool = 32, 128, 4200
+    assert (pool - 2) * hv * d * d > 2 ** 31
+    state = torch.zeros(pool, hv, d, d, device="cuda")
+    small = torch.randn(3, hv, d, d, device="cuda")
+    far = [pool - 1, 5, pool - 2]
+    state[far] = small
+    x = rows(3, 16, hv, d, d, BF16, 51)
+    at = lambda s: torch.tensor(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    assert torch.equal(G.decode(*x, state, at(far)), G.decode(*x, small, at([0, 1, 2])))
+    assert torch.equal(state[far], small)
+    x, cu = rows(100, 16, hv, d, d, BF16, 52), cu_of([64, 1, 35])
+    a, b = (G.packed_forward(*x, cu, s, slots=at(i))[0] for s, i in ((state, far), (small, [0, 1, 2])))
+    assert torch.equal(a, b) and torch.equal(state[far], small)
+    assert not state[[0, 4, 6, pool - 3]].any()
+
+
+def test_packed_rows_past_32_bits(G):
+    """Rows whose offsets pass 2^31 elements: the last sequence as in a call of its own, forward and backward."""
+    hv, d, each, count = 16, 128, 2048, 520
+    n = each * count
+    assert (n - each) * hv * d > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=BF16)  # noqa: E731
+    x = [r(n, 1, 16), r(n, 1, 16), r(n, hv, d), torch.full((n, hv), -0.01, device="cuda"), torch.full((n, hv), 0.1, device="cuda")]
+    cu, tail = cu_of([each] * count), slice(n - each, n)
+    y, one = [t[tail].contiguous() for t in x], cu_of([each])
+    out, S = G.packed_forward(*x, cu, out_dtype=BF16)
+    want, wantS = G.packed_forward(*y, one, out_dtype=BF16)
+    assert torch.equal(out[tail], want) and torch.equal(S[-1:], wantS)
+    dout = out
+    got = G.packed_backward(*x, cu, dout)
+    for a, b in zip(got[:5], G.packed_backward(*y, one, dout[tail].contiguous())):
+        assert torch.equal(a[tail], b)
+
+
+@pytest.mark.parametrize("n,s,c,groups", [(530000, 1, 4096, 32), (300, 8000, 1024, 8)])
+def test_group_norm_past_32_bits(G, n, s, c, groups):
+    """The last item of more than 2^31 elements as in a call of its own."""
+    assert (n - 1) * s * c > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(n, s, c, generator=gen, device="cuda", dtype=BF16)
+    y = x[-1:].clone()
+    out, mean, rstd = G.group_norm(x, groups)
+    ref = R.group_norm(R.f64(y), groups, None, None, None, "none", True, 1e-5)
+    near32(mean[-1:], ref[1], times=4)
+    near32(rstd[-1:], ref[2], times=4)
+    near32(out[-1:], ref[0], BF16)
+    dx = G.group_norm_backward(out, x, groups, mean, rstd)[0]
+    one = G.group_norm_backward(out[-1:].contiguous(), y, groups, mean[-1:].contiguous(), rstd[-1:].contiguous())[0]
+    # both results are rounded to bf16, each by up to half a step of its own value.  Before that, dx cancels (dout is the
+    # normalised x itself) and leaves the errors of the mean of dout x^, which is 1: fp32 sums over a million values, in
+    # chains of some 1000 additions whose errors grow like the root, 32 half steps, in each call; times x^ up to 6
+    a, b = dx[-1:].float(), one.float()
+    assert ((a - b).abs() <= 2.0 ** -8 * (a.abs() + b.abs()) + 2 * 32 * 6 * 2.0 ** -24).all()
