@@ -9,17 +9,21 @@
 // (without centring: mean = 0, no mean(dh) term).  All of it is a few flops
 // per element, so HBM bounds it: the floor is each tensor read or written once.
 //
-// Two ways, by S:
+// Three ways, by the size of a group:
 //   S = 1 (the norm of each token's heads): a group is cg neighbouring values.
 //     L lanes (a power of two, or a whole workgroup) keep a group in registers,
 //     so everything is read once; a workgroup stays on its channels and walks
 //     over the rows, so weights stay in registers and the sums of dweight and
 //     dbias over its rows need no exchange.
-//   S > 1: the S x C values of one n are contiguous and a group is a column
-//     band of them.  A first kernel walks over the rows with one thread per
-//     channel vector and leaves each workgroup's sums for its groups; a small
-//     kernel joins them; a last one reads the inputs again and writes the result.
-// Sums are fp32: a group's second moment is taken about its mean (S = 1) or
+//   S > 1, and the S x cg values (a band of the S x C of one n) fit the registers
+//     of at most 512 lanes: the same, with lanes over rows and channels.  One
+//     launch, one read (20000 x 4 x 512 bf16 in 32 groups 69 us against 233 the
+//     third way, 8 x 64 x 512 in 8: 6.8 against 16, their gradients 96 against 211
+//     and 13 against 26).
+//   Otherwise a first kernel walks over the rows with one thread per channel
+//     vector and leaves each workgroup's sums for its groups; a small kernel
+//     joins them; a last one reads the inputs again and writes the result.
+// Sums are fp32: a group's second moment is taken about its mean (in registers) or
 // about each thread's first value and joined pairwise with counts, so a mean
 // far from zero does not cancel.  No atomics: results are the same every run.
 #include "gdn_common.h"
@@ -114,6 +118,25 @@ __device__ __forceinline__ float act(int a, float u) {
   }
 }
 
+template <int VEC>
+__device__ __forceinline__ void act_all(int a, float (&u)[VEC]) {
+  switch (a) {
+    case GDN_ACT_SILU:
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) u[e] = act(GDN_ACT_SILU, u[e]);
+      break;
+    case GDN_ACT_GELU:
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) u[e] = act(GDN_ACT_GELU, u[e]);
+      break;
+    case GDN_ACT_RELU:
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) u[e] = act(GDN_ACT_RELU, u[e]);
+      break;
+    default: break;
+  }
+}
+
 // Value and slope of the activation.
 __device__ __forceinline__ float2 act_slope(int a, float u) {
   switch (a) {
@@ -139,6 +162,21 @@ __device__ __forceinline__ float grad_u(int a, float dy, float u, float z, float
     return dy * f.x;
   }
   return dy * f.y;
+}
+
+// The same for a vector of them, dy in place.
+template <bool GATE, int VEC>
+__device__ __forceinline__ void grad_all(int a, float (&dy)[VEC], const float (&u)[VEC], const float (&z)[VEC], float (&dz)[VEC]) {
+  const auto each = [&](int act) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) dy[e] = grad_u<GATE>(act, dy[e], u[e], z[e], &dz[e]);
+  };
+  switch (a) {
+    case GDN_ACT_SILU: each(GDN_ACT_SILU); break;
+    case GDN_ACT_GELU: each(GDN_ACT_GELU); break;
+    case GDN_ACT_RELU: each(GDN_ACT_RELU); break;
+    default: each(GDN_ACT_NONE); break;
+  }
 }
 
 // Sum over the L lanes of a group; L a power of two up to 64, or kT.
@@ -674,6 +712,310 @@ __global__ __launch_bounds__(256) void norm_weight_grad_kernel(const float* __re
   }
 }
 
+// ---------------------------------------------------------------- S > 1, bands
+
+// Where a thread of the band kernels works.  L lanes (a power of two up to 64, or
+// all T of a workgroup) hold the S x cg values of an (n, group): rpb rows at
+// once, one vector a lane, rows row0, row0 + rpb, ...  A workgroup holds T / L
+// groups of one n, or all groups of several n where there are fewer, and walks
+// over n.  Workgroups go to the eight XCDs in turn: neighbouring bands, which
+// share cache lines, get ids of equal remainder, so that one L2 serves them.
+struct Band {
+  int grp, cv, row0, rpb;
+  bool on, valid;                   // has a group; the workgroup has work
+  long long first, step;
+};
+
+template <int T>
+__device__ __forceinline__ Band band_place(const NormProblem& p, int L, int vec, int X, int Y) {
+  const int slots = T / L, slot = threadIdx.x / L, l = threadIdx.x % L, cvs = p.cg / vec;
+  const unsigned total = (unsigned)X * Y, share = (total + 7) / 8, at = blockIdx.x % 8 * share + blockIdx.x / 8;
+  const int bx = at % X, by = at / X;
+  Band t;
+  t.valid = at < total && blockIdx.x / 8 < share;
+  t.rpb = L / cvs;
+  t.row0 = l / cvs;
+  t.cv = l % cvs;
+  if (p.G >= slots) {
+    t.grp = bx * slots + slot;
+    t.on = t.grp < p.G;
+    t.first = by;
+    t.step = Y;
+  } else {
+    const int rows = slots / p.G, r = slot / p.G;
+    t.grp = slot % p.G;
+    t.on = r < rows;
+    t.first = (long long)by * rows + r;
+    t.step = (long long)Y * rows;
+  }
+  t.on = t.on && t.row0 < t.rpb;
+  return t;
+}
+
+// Sums of two values over a band's lanes.
+template <int T>
+__device__ __forceinline__ float2 band_sum(float a, float b, int L, float2* lds) {
+  for (int m = L < 64 ? L >> 1 : 32; m; m >>= 1) {
+    a += __shfl_xor(a, m);
+    b += __shfl_xor(b, m);
+  }
+  if (L > 64) {
+    __syncthreads();
+    if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) {
+      a += lds[i].x;
+      b += lds[i].y;
+    }
+  }
+  return make_float2(a, b);
+}
+
+// Hides where a fetched vector came from: the values unpacked from it are not
+// kept in registers from one use to the next.
+template <bool BF16, int VEC>
+__device__ __forceinline__ void forget(RawVec<BF16, VEC>& v) {
+  if constexpr (VEC == 1) asm volatile("" : "+v"(v.v));
+  else asm volatile("" : "+v"(v.v.x), "+v"(v.v.y), "+v"(v.v.z), "+v"(v.v.w));
+}
+
+constexpr int kTurn = 5;            // passes (vectors of a lane) of one turn of the output loop
+
+// The activation is a switch over some code for each, of which a copy for every
+// pass would take registers and instruction cache: the output loop handles kTurn
+// passes a turn and moves the next ones' vectors down.  NV = 10 leaves two
+// workgroups of 512 on a CU.  More does not pay: a 121 x 880 x 2240 frame norm in
+// 20 groups, a band in 15 passes of 1024 lanes, 390 us (in 25 of 512, with
+// spills, 482) against 324 by reading twice, because loads, sums and stores of
+// the one band that a CU holds follow one another.
+template <bool BF16, int VEC, int NV, bool GATE, int T>
+__global__ __launch_bounds__(T, 4) void norm_band_kernel(
+    const void* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias, const void* __restrict__ gate,
+    void* __restrict__ out, float* __restrict__ mean, float* __restrict__ rstd, NormProblem p, int L, int X, int Y) {
+  constexpr uint32_t es = BF16 ? 2 : 4;
+  __shared__ float2 lds[T / 64];
+  const Band t = band_place<T>(p, L, VEC, X, Y);
+  if (!t.valid) return;
+  const float inv = 1.f / ((float)p.S * (float)p.cg);
+  int full = p.S / t.rpb;                              // passes in which every lane has a row; one more has some
+  const int passes = (p.S + t.rpb - 1) / t.rpb;
+  const bool part = t.on && t.row0 + full * t.rpb < p.S;
+  const auto has = [&](int j) { return j < full ? t.on : j == full && part; };
+  // bytes from the first value of an n; lanes without a row read one that exists, and add nothing
+  const uint32_t off0 = t.on ? (uint32_t)(min(t.row0, p.S - 1) * p.C + t.grp * p.cg + t.cv * VEC) * es : 0;
+  const uint32_t step = (uint32_t)(t.rpb * p.C) * es;
+  for (long long n = t.first; n < p.N; n += t.step) {
+    const size_t base = (size_t)n * p.S * p.C * es;
+    const char* xn = static_cast<const char*>(x) + base;
+    RawVec<BF16, VEC> v[NV];
+    float s = 0.f, q = 0.f;
+#pragma unroll
+    for (int j0 = 0; j0 < NV; j0 += kTurn)
+      if (j0 < passes)
+#pragma unroll
+        for (int j = j0; j < j0 + kTurn; ++j)
+          if (NV > kTurn || j < passes) v[j] = fetch_vec<BF16, VEC>(xn + (has(j) ? off0 + j * step : off0), 0);
+    float m = 0.f;
+    if (p.center) {
+      asm volatile("" : "+s"(full));                   // the passes' masks are made anew, not kept in registers
+#pragma unroll
+      for (int j0 = 0; j0 < NV; j0 += kTurn)
+        if (j0 < passes)
+#pragma unroll
+          for (int j = j0; j < j0 + kTurn; ++j) {
+            if (NV == kTurn && j >= passes) continue;
+            float a[VEC], y = 0.f;
+            unpack<BF16, VEC>(v[j], a);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) y += a[e];
+            s += has(j) ? y : 0.f;
+          }
+      m = band_sum<T>(s, 0.f, L, lds).x * inv;
+      s = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) forget(v[j]);
+    }
+    asm volatile("" : "+s"(full));
+#pragma unroll
+    for (int j0 = 0; j0 < NV; j0 += kTurn)
+      if (j0 < passes)
+#pragma unroll
+        for (int j = j0; j < j0 + kTurn; ++j) {
+          if (NV == kTurn && j >= passes) continue;
+          float a[VEC], y = 0.f, y2 = 0.f;
+          unpack<BF16, VEC>(v[j], a);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float d = a[e] - m;
+            y += d;
+            y2 = fmaf(d, d, y2);
+          }
+          s += has(j) ? y : 0.f;
+          q += has(j) ? y2 : 0.f;
+        }
+    asm volatile("" : "+s"(full));
+    const float2 sums = band_sum<T>(s, q, L, lds);
+    q = sums.y;
+    if (p.center) {
+      // what the mean's rounding left
+      const float d = sums.x * inv;
+      m += d;
+      q = fmaf(-d, sums.x, q);
+    }
+    const float r = 1.f / sqrtf(q * inv + p.eps);
+    if (!t.on) continue;
+    if (t.row0 == 0 && t.cv == 0) {
+      const size_t i = (size_t)n * p.G + t.grp;
+      if (mean) mean[i] = m;
+      rstd[i] = r;
+    }
+    float w[VEC], b[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      w[e] = weight ? weight[t.grp * p.cg + t.cv * VEC + e] : 1.f;
+      b[e] = bias ? bias[t.grp * p.cg + t.cv * VEC + e] : 0.f;
+    }
+    char* on = static_cast<char*>(out) + base;
+    const char* zn = static_cast<const char*>(gate) + base;
+    uint32_t off = off0;
+#pragma unroll 1
+    for (int j0 = 0; j0 < passes; j0 += kTurn) {
+#pragma unroll
+      for (int j = 0; j < kTurn; ++j) {
+        if (j0 + j >= passes) continue;
+        const bool is = has(j0 + j);
+        float a[VEC], z[VEC];
+        forget(v[j]);
+        unpack<BF16, VEC>(v[j], a);
+        if constexpr (GATE) load_vec<BF16, VEC>(zn + (is ? off : off0), 0, z);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) a[e] = fmaf((a[e] - m) * r, w[e], b[e]);
+        if constexpr (GATE) {
+          act_all<VEC>(p.act, z);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) a[e] *= z[e];
+        } else {
+          act_all<VEC>(p.act, a);
+        }
+        if (is) store_vec<BF16, VEC>(on + off, 0, a);
+        off += step;
+        __builtin_amdgcn_sched_barrier(0);             // one pass's temporaries at a time
+      }
+#pragma unroll
+      for (int j = 0; j + kTurn < NV; ++j) v[j] = v[j + kTurn];
+    }
+  }
+}
+
+// Gradients: x and dout in registers.  dweight and dbias: the sums of a lane over
+// its n, joined over the lanes of the same channels, part [n held at once by all
+// workgroups][2][C].
+template <bool BF16, int VEC, bool GATE, int T>
+__global__ __launch_bounds__(T, T == kT ? 3 : 2) void norm_band_grad_kernel(
+    const void* __restrict__ dout, const void* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
+    const void* __restrict__ gate, const float* __restrict__ mean, const float* __restrict__ rstd, void* __restrict__ dx,
+    void* __restrict__ dgate, float* __restrict__ parts, NormProblem p, int L, int X, int Y) {
+  constexpr uint32_t es = BF16 ? 2 : 4;
+  __shared__ float2 lds[T];
+  const Band t = band_place<T>(p, L, VEC, X, Y);
+  if (!t.valid) return;
+  const float inv = 1.f / ((float)p.S * (float)p.cg);
+  const int full = p.S / t.rpb, passes = (p.S + t.rpb - 1) / t.rpb;
+  const bool part = t.on && t.row0 + full * t.rpb < p.S;
+  const auto has = [&](int j) { return j < full ? t.on : j == full && part; };
+  const int c0 = t.on ? t.grp * p.cg + t.cv * VEC : 0;
+  const uint32_t off0 = t.on ? (uint32_t)(min(t.row0, p.S - 1) * p.C + c0) * es : 0;
+  const uint32_t step = (uint32_t)(t.rpb * p.C) * es;
+  float w[VEC], b[VEC], sw[VEC], sb[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    w[e] = weight ? weight[c0 + e] : 1.f;
+    b[e] = bias ? bias[c0 + e] : 0.f;
+    sw[e] = sb[e] = 0.f;
+  }
+  for (long long n = t.first; n < p.N; n += t.step) {
+    const size_t base = (size_t)n * p.S * p.C * es, at = (size_t)n * p.G + (t.on ? t.grp : 0);
+    const char *xn = static_cast<const char*>(x) + base, *yn = static_cast<const char*>(dout) + base;
+    const char* zn = static_cast<const char*>(gate) + base;
+    RawVec<BF16, VEC> v[kTurn], g[kTurn];
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j)
+      if (j < passes) {
+        const uint32_t off = has(j) ? off0 + j * step : off0;
+        v[j] = fetch_vec<BF16, VEC>(xn + off, 0);
+        g[j] = fetch_vec<BF16, VEC>(yn + off, 0);
+      }
+    const float m = p.center ? mean[at] : 0.f, r = rstd[at];
+    float s1 = 0.f, s2 = 0.f;
+    // h, du and dz of a pass
+    const auto pass = [&](int j, float (&h)[VEC], float (&du)[VEC], float (&dz)[VEC]) {
+      float u[VEC], z[VEC] = {};
+      forget(v[j]);
+      forget(g[j]);
+      unpack<BF16, VEC>(v[j], h);
+      unpack<BF16, VEC>(g[j], du);
+      if constexpr (GATE) load_vec<BF16, VEC>(zn + (has(j) ? off0 + j * step : off0), 0, z);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        h[e] = (h[e] - m) * r;
+        u[e] = fmaf(h[e], w[e], b[e]);
+      }
+      grad_all<GATE, VEC>(p.act, du, u, z, dz);
+    };
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      if (j >= passes) continue;
+      float h[VEC], du[VEC], dz[VEC];
+      pass(j, h, du, dz);
+      const bool is = has(j);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float y = is ? du[e] : 0.f, k = is ? h[e] : 0.f;   // of another row: NaN there stays there
+        sw[e] = fmaf(y, k, sw[e]);
+        sb[e] += y;
+        s1 = fmaf(y, w[e], s1);
+        s2 = fmaf(y * w[e], k, s2);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const float2 sums = band_sum<T>(s1, s2, L, lds);
+    s1 = p.center ? sums.x * inv : 0.f;
+    s2 = sums.y * inv;
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      if (j >= passes) continue;
+      float h[VEC], du[VEC], dz[VEC];
+      pass(j, h, du, dz);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) h[e] = r * (du[e] * w[e] - s1 - h[e] * s2);
+      if (has(j)) {
+        const size_t off = base + off0 + j * step;
+        store_vec<BF16, VEC>(static_cast<char*>(dx) + off, 0, h);
+        if constexpr (GATE) store_vec<BF16, VEC>(static_cast<char*>(dgate) + off, 0, dz);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  float* o = parts + (size_t)t.first * 2 * p.C + c0;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    __syncthreads();
+    lds[threadIdx.x] = make_float2(sw[e], sb[e]);
+    __syncthreads();
+    if (t.on && t.row0 == 0) {
+      float a = 0.f, c = 0.f;
+      for (int k = 0; k < t.rpb; ++k) {
+        a += lds[threadIdx.x + k * (p.cg / VEC)].x;
+        c += lds[threadIdx.x + k * (p.cg / VEC)].y;
+      }
+      o[e] = a;
+      o[p.C + e] = c;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- host
 
 int vec_of(const NormProblem& p) {
@@ -743,6 +1085,33 @@ NormPlan plan(const NormProblem& p) {
   return f;
 }
 
+// Lanes of an (n, group) on the band way, the fewest that hold it; returns the
+// passes its kernel has registers for, or 0 where the band does not fit (the
+// gradient keeps two tensors, so half as much).
+int band_shape(const NormProblem& p, bool grad, int* L) {
+  const int cvs = p.cg / vec_of(p);
+  if ((long long)p.S * p.C * (p.bf16 ? 2 : 4) >= 1LL << 31) return 0;     // offsets within an n have 32 bits
+  for (int l = 8; l <= kTF; l *= l == 64 ? 4 : 2) {
+    const int most = l == kTF && !grad ? 2 * kTurn : kTurn, rpb = l / cvs;
+    if (rpb == 0 || (p.S + rpb - 1) / rpb > most) continue;
+    *L = l;
+    return most;
+  }
+  return 0;
+}
+
+// Workgroups: X over the groups, Y over n; the gradient's about 2048 in all, each
+// of which walks over several n and leaves one set of sums.  *rows: n held at once.
+dim3 band_grid(const NormProblem& p, bool grad, int L, int* X, int* Y, long long* rows) {
+  const int slots = (L < kTF ? kT : kTF) / L, at_once = p.G >= slots ? 1 : slots / p.G;
+  *X = p.G >= slots ? (p.G + slots - 1) / slots : 1;
+  const long long all = (p.N + at_once - 1) / at_once, most = (grad ? 2048 : kMaxBlocks) / *X;
+  const long long y = most < 1 ? 1 : most < all ? most : all, walk = (all + y - 1) / y;
+  *Y = (int)((all + walk - 1) / walk);                 // as few as the longest walk allows
+  *rows = (long long)*Y * at_once;
+  return dim3(((unsigned)*X * *Y + 7) / 8 * 8);
+}
+
 // Lanes that join a (n, group)'s parts, and the workgroups of that.
 int join_lanes(const NormPlan& f) {
   int l = 1;
@@ -771,6 +1140,14 @@ hipError_t forward_v(const NormProblem& p, const void* x, const float* weight, c
 #undef GDN_ROWS
     return hipGetLastError();
   }
+  int L, X, Y;
+  if (const int passes = band_shape(p, false, &L)) {
+    long long rows;
+    const dim3 grid = band_grid(p, false, L, &X, &Y, &rows);
+    const auto f = passes == kTurn && L < kTF ? norm_band_kernel<BF16, VEC, kTurn, GATE, kT> : norm_band_kernel<BF16, VEC, 2 * kTurn, GATE, kTF>;
+    hipLaunchKernelGGL(f, grid, dim3(L < kTF ? kT : kTF), 0, st, x, weight, bias, gate, out, mean, rstd, p, L, X, Y);
+    return hipGetLastError();
+  }
   const NormPlan f = plan(p);
   float4* part = static_cast<float4*>(ws);
   const dim3 grid(f.tiles, f.splits, f.z);
@@ -786,6 +1163,7 @@ template <bool BF16, int VEC, bool GATE>
 hipError_t backward_v(const NormProblem& p, const NormGrad& t, void* ws, hipStream_t st) {
   float* part = static_cast<float*>(ws);
   long long rows = 0;
+  int L, X, Y;
   if (p.N > 0 && by_rows(p)) {
     int L, NV;
     rows_shape(p, &L, &NV);
@@ -797,6 +1175,11 @@ hipError_t backward_v(const NormProblem& p, const NormGrad& t, void* ws, hipStre
     break;
     switch (NV) { GDN_ROWS(1) GDN_ROWS(2) GDN_ROWS(4) GDN_ROWS(8) }
 #undef GDN_ROWS
+  } else if (p.N > 0 && band_shape(p, true, &L)) {
+    const dim3 grid = band_grid(p, true, L, &X, &Y, &rows);
+    const auto f = L < kTF ? norm_band_grad_kernel<BF16, VEC, GATE, kT> : norm_band_grad_kernel<BF16, VEC, GATE, kTF>;
+    hipLaunchKernelGGL(f, grid, dim3(L < kTF ? kT : kTF), 0, st, t.dout, t.x, t.weight, t.bias, t.gate, t.mean, t.rstd, t.dx,
+                       t.dgate, part, p, L, X, Y);
   } else if (p.N > 0) {
     const NormPlan f = plan(p);
     rows = (long long)f.z * f.splits;
@@ -824,6 +1207,12 @@ size_t norm_workspace(const NormProblem& p, bool gradient) {
     long long rows;
     rows_shape(p, &L, &NV);
     rows_grid(p, L, &rows);
+    return gradient ? (size_t)rows * 2 * p.C * sizeof(float) : 0;
+  }
+  int L, X, Y;
+  if (band_shape(p, gradient, &L)) {
+    long long rows;
+    band_grid(p, gradient, L, &X, &Y, &rows);
     return gradient ? (size_t)rows * 2 * p.C * sizeof(float) : 0;
   }
   const NormPlan f = plan(p);

@@ -189,7 +189,11 @@ NORMS = [  # n, s, c, groups, dtype, gate, affine, activation, center
     (4, 1, 8, 8, F32, False, True, "none", False), (2, 880, 224, 2, BF16, False, True, "silu", True),
     (3, 7, 40, 5, F32, True, True, "gelu", True), (1, 1000, 129, 3, BF16, True, True, "relu", False),
     (40, 2, 64, 4, BF16, False, False, "silu", True), (2, 33, 2240, 20, F32, False, True, "silu", True),
-    (1, 5, 4104, 1, F32, True, False, "silu", False), (1, 4097, 64, 8, BF16, True, True, "silu", True)]
+    (1, 5, 4104, 1, F32, True, False, "silu", False), (1, 4097, 64, 8, BF16, True, True, "silu", True),
+    # bands in registers: several n a workgroup, 512 lanes with five passes and with ten, odd widths, walks over n
+    (500, 3, 48, 2, F32, True, True, "silu", True), (37, 130, 256, 2, BF16, True, True, "silu", True),
+    (5, 200, 512, 4, BF16, False, True, "gelu", False), (200, 2, 1290, 10, BF16, True, True, "relu", True),
+    (100, 2, 16384, 2048, BF16, False, True, "silu", True), (4, 64, 32, 4, F32, False, True, "none", False)]
 
 
 @pytest.mark.parametrize("n,s,c,groups,dtype,gate,affine,activation,center", NORMS)
@@ -302,7 +306,7 @@ def test_group_norm_refuses_what_does_not_fit(G):
                  lambda: G.group_norm(x.half(), 4), lambda: G.group_norm(x.transpose(0, 1), 4), lambda: G.group_norm(x[0, 0], 4),
                  lambda: G.group_norm(x, 4, activation="tanh"), lambda: G.group_norm(x, 4, eps=-1.0),
                  lambda: G.group_norm(x, 4, out=torch.empty_like(x.float())), lambda: G.group_norm(x, 0),
-                 lambda: G.group_norm(x, 4, workspace=torch.empty(8, device="cuda")),
+                 lambda: G.group_norm(torch.zeros(1, 6000, 32, device="cuda"), 4, workspace=torch.empty(8, device="cuda")),
                  lambda: G.group_norm_backward(dy, x, 4, None, torch.ones(2, 4, device="cuda"), **ok),
                  lambda: G.group_norm_backward(dy, x, 4, torch.ones(2, 4, device="cuda"), torch.ones(2, 4, device="cuda"),
                                                center=False),

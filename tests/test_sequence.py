@@ -122,10 +122,12 @@ def test_norm_rejects_bad_pointers_and_workspaces():
         assert fwd(**{name: None}) == G.ERR_INVALID_ARGUMENT
     for name in args:
         assert fwd(**{name: FAKE + 2}) == G.ERR_INVALID_ARGUMENT
-    assert L.gdn_group_norm_workspace_size(norm(), 0, ctypes.byref(n)) == G.OK and n.value > 0
-    assert fwd(ws_bytes=n.value - 1) == G.ERR_WORKSPACE_TOO_SMALL
-    assert fwd(ws=None) == G.ERR_WORKSPACE_TOO_SMALL
-    assert L.gdn_group_norm_workspace_size(norm(spatial=1), 0, ctypes.byref(n)) == G.OK and n.value == 0
+    wide = norm(spatial=5000)            # does not fit registers
+    assert L.gdn_group_norm_workspace_size(wide, 0, ctypes.byref(n)) == G.OK and n.value > 0
+    assert fwd(wide, ws_bytes=n.value - 1) == G.ERR_WORKSPACE_TOO_SMALL
+    assert fwd(wide, ws=None) == G.ERR_WORKSPACE_TOO_SMALL
+    for s in (1, 5):
+        assert L.gdn_group_norm_workspace_size(norm(spatial=s), 0, ctypes.byref(n)) == G.OK and n.value == 0
     back = dict(dout=FAKE, x=FAKE, w=FAKE, b=FAKE, z=FAKE, mean=FAKE, rstd=FAKE, dx=FAKE, dw=FAKE, db=FAKE, dz=FAKE)
 
     def bwd(ws_bytes=1 << 40, **kw):
