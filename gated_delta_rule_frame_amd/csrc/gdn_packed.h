@@ -66,14 +66,6 @@ __device__ __forceinline__ void mma_by_term(const Frag<NA>& a, const Frag<NB>& b
       if (s - i >= 0 && s - i < NB) c[s] = mfma(a.t[i], b.t[s - i], c[s]);
 }
 
-template <int N, int M>
-__device__ __forceinline__ Frag<N> first_terms(const Frag<M>& f) {
-  Frag<N> o;
-#pragma unroll
-  for (int i = 0; i < N; ++i) o.t[i] = f.t[i];
-  return o;
-}
-
 // Two values as the sums of N bf16 values each, largest first, packed by term:
 // one conversion, two unpackings and two subtractions for a term of a pair.
 template <int N>
@@ -101,32 +93,12 @@ __device__ __forceinline__ Frag<N> split8(const float (&x)[8]) {
   return f;
 }
 
-template <int N>
-__device__ __forceinline__ Frag<N> zero_frag() {
-  Frag<N> f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) f.t[i] = as_frag(make_uint4(0, 0, 0, 0));
-  return f;
-}
-
 // Eight consecutive fp32 values as a fragment.
 template <int N>
 __device__ __forceinline__ Frag<N> frag_f32(const float* p) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   return split8<N>(x);
-}
-
-// Eight consecutive input values (bf16 for one term, fp32 for three).
-template <int NT>
-__device__ __forceinline__ Frag<NT> frag_in(const void* p, size_t i) {
-  if constexpr (NT == 1) {
-    Frag<1> f;
-    f.t[0] = as_frag(*reinterpret_cast<const uint4*>(static_cast<const bh*>(p) + i));
-    return f;
-  } else {
-    return frag_f32<3>(static_cast<const float*>(p) + i);
-  }
 }
 
 // Buffer addressing: `bytes` from a uniform base, per-lane 32-bit offsets.  The
@@ -243,11 +215,6 @@ __device__ __forceinline__ Frag<NT> frag_of(const RawFrag<NT>& r) {
                         __uint_as_float(r.b.x), __uint_as_float(r.b.y), __uint_as_float(r.b.z), __uint_as_float(r.b.w)};
     return split8<3>(x);
   }
-}
-
-template <int NT>
-__device__ __forceinline__ float elem_in(const void* p, size_t i) {
-  return load_scalar<NT == 1>(p, i);
 }
 
 // The first N of a stored fragment's LD terms.

@@ -384,11 +384,11 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
         Gs[tid] = ws.g[cell * kC + tid];
         bs[tid] = gates[2 * kC + tid];
       }
-      f32x4 dq[HT], rw[HT], cl[HT], D[4], X[4];
+      f32x4 dq[HT], rw[HT], cl[HT], Z[4];             // Z: dO e^T in the first half, W e^T in the second
 #pragma unroll
       for (int j = 0; j < HT; ++j) dq[j] = rw[j] = cl[j] = zero4();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) D[j] = X[j] = zero4();
+      for (int j = 0; j < 4; ++j) Z[j] = zero4();
       float dbeta = 0.f, dot = 0.f;                  // of token arow over this lane's columns; of <S0, dS1>
       for (int vs = 0; vs < VS; ++vs) {
         bh* buf0 = lds + (vs & 1) * kBuf;
@@ -422,14 +422,13 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
           rw[j] = mma<3, 3>(aw, s, rw[j]);
           cl[j] = mma<3, 3>(ae, d, cl[j]);
         }
-        if (half == 1)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j <= w) {
-              const Frag<3> b = get_frag(buf0 + (4 + j) * kFrag);
-              D[j] = mma<NT, 3>(ao, b, D[j]);
-              X[j] = mma<3, 3>(aw, b, X[j]);
-            }
+        for (int j = 0; j < 4; ++j)
+          if (j <= w) {
+            const Frag<3> b = get_frag(buf0 + (4 + j) * kFrag);
+            if (half == 0) Z[j] = mma<NT, 3>(ao, b, Z[j]);
+            else Z[j] = mma<3, 3>(aw, b, Z[j]);
+          }
       }
       if (half == 0) {
         dbeta += __shfl_xor(dbeta, 16);
@@ -469,18 +468,19 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
         part[wave] = tails;
         part[8 + wave] = dot;
       }
-      if (half == 1)
+      {
+        float (*to)[kLd] = half == 0 ? Dl : Ml;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = 16 * j + lr;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int i = row0 + r;
-            const float E = i >= c ? exp2_of((float)(Gs[i] - Gs[c])) * bs[c] : 0.f;
-            Dl[i][c] = j <= w ? E * D[j][r] : 0.f;
-            Ml[i][c] = j <= w && i > c ? -E * bs[i] * X[j][r] : 0.f;
+            const float E = i >= c + half ? exp2_of((float)(Gs[i] - Gs[c])) * bs[c] : 0.f;   // M: below the diagonal
+            to[i][c] = j <= w ? (half == 0 ? E : -E * bs[i]) * Z[j][r] : 0.f;
           }
         }
+      }
       __syncthreads();
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
