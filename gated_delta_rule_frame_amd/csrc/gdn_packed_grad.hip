@@ -295,16 +295,24 @@ __device__ __forceinline__ float wave_sum(float x) {
 // operand that several wavefronts read is split once, by one wavefront, into an
 // LDS buffer (two in turn, one barrier a step), its fp32 values fetched a step
 // ahead.  Wavefronts w and w + 4 have row tile w and each half of the columns of
-// d_k; the second four also have the 64 x 64 products D and M.
+// d_k; the first four also have the 64 x 64 product D, the second M.
+//
+// Measured (8192 tokens, 16 key and 32 value heads of 128, bf16): 513 us, 31 us a
+// chunk and value head on each CU, of which its 270 KB take 14 at the rate of a
+// large copy and the MFMAs 7: one workgroup has a CU's registers and LDS, so its
+// phases follow one another.  Sixteen wavefronts of 128 registers: 584 us; four
+// of 512: 738; eight that stay and fetch the next chunk's first operands ahead:
+// 590 (their registers spill).
 template <int NT, int DKP>
 __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, long long slots) {
   constexpr int NTI = DKP / 16, HT = NTI / 2;        // column tiles of d_k, and of a wavefront
+  constexpr int KH = (HT + 1) / 2;                   // fragments of 32 columns that cover the latter
   constexpr uint32_t es = NT == 1 ? 2 : 4;
   constexpr int kFrag = 3 * 512;                     // bf16 values of a split fragment
   constexpr int kBuf = (8 + 2 * NTI) * kFrag;        // W, e: four tiles each; S0, dS1: NTI each
   __shared__ __align__(16) bh lds[2 * kBuf];
   __shared__ double Gs[kC];
-  __shared__ float bs[kC], dGs[2][kC], part[16];
+  __shared__ float bs[kC], egs[kC], eds[kC], dGs[2][kC], part[16];   // beta, e^G, e^(Gn - G)
   float (*Dl)[kLd] = reinterpret_cast<float (*)[kLd]>(lds);            // D and M, when the buffers are done with
   float (*Ml)[kLd] = reinterpret_cast<float (*)[kLd]>(lds) + kC;
   static_assert(2 * kBuf * sizeof(bh) >= 2 * kC * kLd * sizeof(float), "D and M fit");
@@ -331,37 +339,45 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
     f32x4 gq[HT], gk[HT];
 #pragma unroll
     for (int j = 0; j < HT; ++j) gq[j] = gk[j] = zero4();
-
-    for (int h = kh * rep; h < (kh + 1) * rep; ++h) {
+    RawFrag<NT> rk[KH], rq[KH];
+    // as accumulators hold them: a product with the identity, exact
+    auto as_rows = [&](const RawFrag<NT> (&f)[KH], int j) {
+      float one[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) one[i] = lg * 8 + i == (half * HT + j) % 2 * 16 + lr ? 1.f : 0.f;
+      return mma<NT, 1>(frag_of<NT>(f[HT == 1 ? 0 : j / 2]), split8<1>(one), zero4());
+    };
+    // this lane's eight values of columns 32 vs .. of a row of e, W (64 rows) or S0, dS1 (DKP rows); behind the last strip
+    // there is nothing
+    uint4 we[2][2], sd[2][2];
+    RawFrag<NT> dof;
+    const uint32_t tok_b = strips * kC * 16 * 4, st_b = strips * DKP * 16 * 4;
+    auto fetch = [&](int h, int vs) {
       const size_t cell = (size_t)slot * p.hv + h;
-      const float* gates = ws.gates + cell * 3 * kC;
-      const uint32_t tok_b = strips * kC * 16 * 4, st_b = strips * DKP * 16 * 4;
       const buf_t eb = buf(ws.e + cell * strips * kC * 16, tok_b), wb = buf(ws.w + cell * strips * kC * 16, tok_b);
       const buf_t sb = buf(ws.s0 + cell * strips * DKP * 16, st_b), db = buf(ws.ds + cell * strips * DKP * 16, st_b);
       const buf_t ob = buf(static_cast<const char*>(t.dout) + ((size_t)first * p.hv + h) * p.dv * es, span(n, os_b, p.dv * es));
-      // this lane's eight values of columns 32 vs .. of a row of e, W (64 rows) or S0, dS1 (DKP rows); behind the last strip
-      // there is nothing
-      uint4 we[2][2], sd[2][2];
-      RawFrag<NT> dof;
-      auto fetch = [&](int vs) {
-        const int strip = vs * 2 + lg / 2, c8 = lg % 2 * 8;
-        const uint32_t nowhere = strip < strips ? 0 : kNowhere;
-        if (half == 0) {
-          const uint32_t o = ((strip * kC + arow) * 16 + c8) * 4 | nowhere;
-          we[0][0] = buf_load16(wb, o);
-          we[0][1] = buf_load16(wb, o + 16);
-          we[1][0] = buf_load16(eb, o);
-          we[1][1] = buf_load16(eb, o + 16);
-        }
-        if (NTI == 8 || wave < NTI) {
-          const uint32_t o = ((strip * DKP + wave * 16 + lr) * 16 + c8) * 4 | nowhere;
-          sd[0][0] = buf_load16(sb, o);
-          sd[0][1] = buf_load16(sb, o + 16);
-          sd[1][0] = buf_load16(db, o);
-          sd[1][1] = buf_load16(db, o + 16);
-        }
-        dof = raw_at<NT>(ob, arow * os_b + (strip * 16 + c8) * es | nowhere);
-      };
+      const int strip = vs * 2 + lg / 2, c8 = lg % 2 * 8;
+      const uint32_t nowhere = strip < strips ? 0 : kNowhere;
+      if (half == 0) {
+        const uint32_t o = ((strip * kC + arow) * 16 + c8) * 4 | nowhere;
+        we[0][0] = buf_load16(wb, o);
+        we[0][1] = buf_load16(wb, o + 16);
+        we[1][0] = buf_load16(eb, o);
+        we[1][1] = buf_load16(eb, o + 16);
+      }
+      if (NTI == 8 || wave < NTI) {
+        const uint32_t o = ((strip * DKP + wave * 16 + lr) * 16 + c8) * 4 | nowhere;
+        sd[0][0] = buf_load16(sb, o);
+        sd[0][1] = buf_load16(sb, o + 16);
+        sd[1][0] = buf_load16(db, o);
+        sd[1][1] = buf_load16(db, o + 16);
+      }
+      dof = raw_at<NT>(ob, arow * os_b + (strip * 16 + c8) * es | nowhere);
+    };
+
+    for (int h = kh * rep; h < (kh + 1) * rep; ++h) {
+      const size_t cell = (size_t)slot * p.hv + h;
       auto eight = [&](const uint4 (&v)[2], float (&x)[8]) {
         const uint32_t a[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
@@ -378,10 +394,13 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
         for (int i = 0; i < 3; ++i) f.t[i] = as_frag(*reinterpret_cast<const uint4*>(from + i * 512 + lane * 8));
         return f;
       };
-      fetch(0);
+      fetch(h, 0);
       __syncthreads();                               // the previous head has read the tiles and gates
       if (tid < kC) {
+        const float* gates = ws.gates + cell * 3 * kC;
         Gs[tid] = ws.g[cell * kC + tid];
+        egs[tid] = gates[tid];
+        eds[tid] = gates[kC + tid];
         bs[tid] = gates[2 * kC + tid];
       }
       f32x4 dq[HT], rw[HT], cl[HT], Z[4];             // Z: dO e^T in the first half, W e^T in the second
@@ -411,7 +430,7 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
           put_frag(buf0 + (8 + NTI + wave) * kFrag, y);
         }
         const Frag<NT> ao = frag_of<NT>(dof);
-        if (vs + 1 < VS) fetch(vs + 1);
+        if (vs + 1 < VS) fetch(h, vs + 1);
         __syncthreads();
         const Frag<3> aw = get_frag(buf0 + w * kFrag), ae = get_frag(buf0 + (4 + w) * kFrag);
 #pragma unroll
@@ -435,30 +454,36 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
         dbeta += __shfl_xor(dbeta, 32);
         if (lg == 0 && arow < n) t.dbeta[(size_t)(first + arow) * p.hv + h] = dbeta;
       }
-      // K and Q of this wavefront's rows and columns as accumulators hold them: a product with the identity, exact
-      f32x4 kd[HT], qd[HT];
+      // rows of K and Q in this wavefront's columns
 #pragma unroll
-      for (int j = 0; j < HT; ++j) {
-        const int tile = half * HT + j, c = tile / 2 * 32 + lg * 8;
-        float one[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) one[i] = lg * 8 + i == tile % 2 * 16 + lr ? 1.f : 0.f;
-        const Frag<1> id = split8<1>(one);
+      for (int j = 0; j < KH; ++j) {
+        const int c = (half * HT / 2 + j) * 32 + lg * 8;
         const uint32_t nowhere = c < p.dk ? 0 : kNowhere;
-        kd[j] = mma<NT, 1>(frag_of<NT>(raw_at<NT>(kb, arow * ks_b + c * es | nowhere)), id, zero4());
-        qd[j] = mma<NT, 1>(frag_of<NT>(raw_at<NT>(qb, arow * qs_b + c * es | nowhere)), id, zero4());
+        rk[j] = raw_at<NT>(kb, arow * ks_b + c * es | nowhere);
+        rq[j] = raw_at<NT>(qb, arow * qs_b + c * es | nowhere);
       }
-      float tails = 0.f;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = row0 + r;
-        const float eg = gates[i], ed = gates[kC + i], b = bs[i];
+      // K^T and Q^T for what follows, on their way over the next barriers
+      Frag<NT> kf[2][HT], qf[2][HT];
+      auto fetch_transposed = [&](int ks) {
 #pragma unroll
         for (int j = 0; j < HT; ++j) {
-          dq[j][r] *= eg;
-          rw[j][r] *= -b * eg;
-          cl[j][r] *= b * ed;
-          tails = fmaf(kd[j][r], cl[j][r], tails);
+          const uint32_t o = (((half * HT + j) * 2 + ks) * NT * 64 + lane) * 16;
+          kf[ks][j] = frag_at<NT>(ktb, o);
+          qf[ks][j] = frag_at<NT>(qtb, o);
+        }
+      };
+      if constexpr (NT == 1) fetch_transposed(0);
+      float tails = 0.f;
+#pragma unroll
+      for (int j = 0; j < HT; ++j) {
+        const f32x4 kd = as_rows(rk, j);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = row0 + r;
+          dq[j][r] *= egs[i];
+          rw[j][r] *= -bs[i] * egs[i];
+          cl[j][r] *= bs[i] * eds[i];
+          tails = fmaf(kd[r], cl[j][r], tails);
         }
       }
       tails = wave_sum(tails);
@@ -485,19 +510,13 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int k8 = ks * 32 + lg * 8;
-        Frag<NT> kf[HT], qf[HT];
-#pragma unroll
-        for (int j = 0; j < HT; ++j) {
-          const uint32_t o = (((half * HT + j) * 2 + ks) * NT * 64 + lane) * 16;
-          kf[j] = frag_at<NT>(ktb, o);
-          qf[j] = frag_at<NT>(qtb, o);
-        }
+        if (NT == 3 || ks == 1) fetch_transposed(ks);
         if (ks <= w / 2) {
           const Frag<3> ad = frag_f32<3>(&Dl[arow][k8]), am = frag_f32<3>(&Ml[arow][k8]);
 #pragma unroll
           for (int j = 0; j < HT; ++j) {
-            dq[j] = mma<3, NT>(ad, kf[j], dq[j]);
-            rw[j] = mma<3, NT>(am, kf[j], rw[j]);
+            dq[j] = mma<3, NT>(ad, kf[ks][j], dq[j]);
+            rw[j] = mma<3, NT>(am, kf[ks][j], rw[j]);
           }
         }
         if (ks >= w / 2) {
@@ -510,23 +529,25 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
           const Frag<3> bd = split8<3>(x), bm = split8<3>(y);
 #pragma unroll
           for (int j = 0; j < HT; ++j) {
-            cl[j] = mma<3, NT>(bd, qf[j], cl[j]);
-            cl[j] = mma<3, NT>(bm, kf[j], cl[j]);
+            cl[j] = mma<3, NT>(bd, qf[ks][j], cl[j]);
+            cl[j] = mma<3, NT>(bm, kf[ks][j], cl[j]);
           }
         }
       }
+      float sum[4] = {};
+#pragma unroll
+      for (int j = 0; j < HT; ++j) {
+        const f32x4 kd = as_rows(rk, j), qd = as_rows(rq, j);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[r] += qd[r] * dq[j][r] + kd[r] * (rw[j][r] - cl[j][r]);
+        gq[j] += dq[j];
+        gk[j] += rw[j] + cl[j];
+      }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < HT; ++j) {
-          s += qd[j][r] * dq[j][r] + kd[j][r] * (rw[j][r] - cl[j][r]);
-          gq[j][r] += dq[j][r];
-          gk[j][r] += rw[j][r] + cl[j][r];
-        }
-#pragma unroll
-        for (int m = 1; m < 16; m <<= 1) s += __shfl_xor(s, m);
-        if (lr == 0) dGs[half][row0 + r] = s;
+        for (int m = 1; m < 16; m <<= 1) sum[r] += __shfl_xor(sum[r], m);
+        if (lr == 0) dGs[half][row0 + r] = sum[r];
       }
       __syncthreads();
       if (wave == 0) {
@@ -539,7 +560,7 @@ __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, Pack
             tail += part[i];
             states += part[8 + i];
           }
-          s += tail + (double)gates[kC - 1] * states;
+          s += tail + (double)egs[kC - 1] * states;
         }
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
