@@ -4,7 +4,9 @@ Argument marshalling only: every step of the computation runs in the HIP
 kernels of ``libgdn.so``.  PyTorch supplies device memory and the current HIP
 stream.  The names mirror the C ABI in ``include/gdn.h``: ``forward`` wraps
 ``gdn_forward``, ``step`` wraps ``gdn_step``, ``workspace_size`` wraps
-``gdn_workspace_size``.
+``gdn_workspace_size``.  The calls on sequences of tokens (``decode``,
+``packed_forward``, ``packed_backward``) and the norm (``group_norm``,
+``group_norm_backward``) are in ``sequence``.
 
 There is no CPU fallback: if the library is not built, or a call is made with
 tensors that are not on a GPU, these functions raise.
