@@ -863,6 +863,7 @@ __global__ __launch_bounds__(T, 4) void norm_band_kernel(
       const float d = sums.x * inv;
       m += d;
       q = fmaf(-d, sums.x, q);
+      q = q < 0.f ? 0.f : q;                           // NaN stays NaN
     }
     const float r = 1.f / sqrtf(q * inv + p.eps);
     if (!t.on) continue;

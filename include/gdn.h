@@ -375,7 +375,9 @@ gdn_status gdn_packed_workspace_size(const gdn_seq_problem* problem, int32_t gra
  *                  rows (a pool as gdn_decode's); NULL: sequence s uses row s.
  *                  A sequence whose slot is outside the pool starts from zero
  *                  and its final state is dropped.  Sequences that name the
- *                  same slot run one after another, in order.
+ *                  same slot run one after another, in order: in place each
+ *                  goes on where the one before ended; otherwise each starts
+ *                  from initial_state's row, and the last one's state stays.
  *   initial_state  or NULL (zeros)
  *   final_state    or NULL; may be initial_state (in place).  An empty
  *                  sequence's is its initial state.

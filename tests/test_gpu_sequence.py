@@ -298,6 +298,34 @@ def test_group_norm_streams_graphs_and_two_calls_with_own_workspaces(G):
         G.group_norm(x, 8, w, b, z, **args)
 
 
+def test_group_norm_in_two_passes_in_a_graph(G):
+    """A group that does not fit registers: several kernels over a workspace, replayed."""
+    x, w, b, z, dy = norm_inputs(2, 6000, 32, BF16, True, True, 3)
+    args = dict(activation="gelu")
+    want = G.group_norm(x, 4, w, b, z, **args)
+    wantg = G.group_norm_backward(dy, x, 4, *want[1:], w, b, z, **args)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = G.group_norm(x, 4, w, b, z, **args)
+        gotg = G.group_norm_backward(dy, x, 4, *got[1:], w, b, z, **args)
+    for _ in range(3):
+        for t in (*got, *gotg):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip((*got, *gotg), (*want, *wantg)))
+        G.group_norm(x, 4, w, b, z, **args)
+
+
+@pytest.mark.parametrize("s", [1, 3, 200, 9000])
+def test_group_norm_constant_groups_without_eps(G, s):
+    """Nothing to divide by: a deviation of 0 or of its roundings, never the root of a negative number."""
+    x = (torch.arange(1, 9, device="cuda").repeat_interleave(16) * 0.37 + 100).repeat(3, s, 1)
+    _, mean, rstd = G.group_norm(x, 8, eps=0.0)
+    assert (rstd >= 1e4).all() and not torch.isnan(rstd).any()      # inf, or 1 / (some half steps of 103)
+    near32(mean, R.f64(x[:, 0].view(3, 8, 16).mean(2)))
+
+
 def test_group_norm_refuses_what_does_not_fit(G):
     x, w, b, z, dy = norm_inputs(2, 3, 32, BF16, True, True, 1)
     ok = dict(activation="silu")
@@ -416,6 +444,27 @@ def test_packed_forward_strides_pools_and_repeated_slots(G):
     G.packed_forward(q, k, v, x[3], x[4], cu, None, slots=st, final_state=other)
     near32(other[4], R.tokens(*(R.f64(t[c[5]:c[6]]) for t in x), torch.zeros(hv, dk, dv, dtype=torch.float64))[1])
     assert (other[[2, 3, 5]] == 2.0).all() and (other[0] == 0).all()
+
+
+def test_packed_forward_many_strips_into_a_pool(G):
+    """More strips than CUs, an odd number a head, repeated and absent slots: as the sequences one after another."""
+    lengths = [65, 3, 0, 128, 20, 1, 70, 64] * 3
+    hk, hv, dk, dv, pool = 4, 8, 64, 48, 16
+    n, c = sum(lengths), cu_of(lengths).tolist()
+    x = rows(n, hk, hv, dk, dv, BF16, 61)
+    slots = [(5 * i) % 18 - 1 for i in range(len(lengths))]
+    state = torch.randn(pool, hv, dk, dv, device="cuda")
+    want, outs = state.clone(), []
+    for i, s in enumerate(slots):
+        at = s if 0 <= s < pool else None
+        S = torch.zeros(1, hv, dk, dv, device="cuda") if at is None else want[at:at + 1].clone()
+        o, S = G.packed_forward(*(t[c[i]:c[i + 1]] for t in x), cu_of(lengths[i:i + 1]), S)
+        outs.append(o)
+        if at is not None:
+            want[at] = S[0]
+    out, _ = G.packed_forward(*x, cu_of(lengths), state, slots=torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    near32(out, R.f64(torch.cat(outs)))
+    near32(state, R.f64(want))
 
 
 def test_packed_forward_hard_inputs(G):
