@@ -9,6 +9,7 @@ stream of the tensors' device; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -58,12 +59,13 @@ def declare(L):
 # (1.8 us of a 12 us single-row decode step) where this torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _on(device, call, *args):
     """Runs a library call with the tensors' device current, on its current stream."""
     stream = _raw_stream(device.index)
-    if device.index == torch.cuda.current_device():
+    if device.index == _current():
         _check(call(*args, stream))
     else:
         with torch.cuda.device(device):
@@ -72,9 +74,9 @@ def _on(device, call, *args):
 
 def _rows(name, t, shape, dtype, device):
     """A packed [tokens, heads, width] input; returns its stride between tokens (0 = dense)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.get_device() != device.index:
         raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)} (got {tuple(t.shape)})")
@@ -88,7 +90,8 @@ def _rows(name, t, shape, dtype, device):
 
 def _dense(name, t, shape, dtype, device):
     """A contiguous tensor of this shape, type and device."""
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if (not isinstance(t, torch.Tensor) or t.get_device() != device.index or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
@@ -196,7 +199,7 @@ def packed_forward(q, k, v, log_gate, beta, cu_seqlens, initial_state=None, *, s
     else:
         _dense("out", out, (n, hv, dv), odt, device)
     L = lib()
-    ws, ws_bytes = _space(L.gdn_packed_workspace_size, p, 0, workspace, device)
+    ws, ws_bytes = _space("gdn_packed_workspace_size", p, 0, workspace, device)
     _on(device, L.gdn_packed_forward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), beta.data_ptr(),
         cu_seqlens.data_ptr(), _ptr(slots), _ptr(initial_state), out.data_ptr(), _ptr(final_state), _ptr(ws), ws_bytes)
     return out, final_state
@@ -229,7 +232,7 @@ def packed_backward(q, k, v, log_gate, beta, cu_seqlens, dout, initial_state=Non
         for (name, t), d in zip(inputs.items(), grads):
             _dense(name, d, t.shape, t.dtype, device)
     L = lib()
-    ws, ws_bytes = _space(L.gdn_packed_workspace_size, p, 1, workspace, device)
+    ws, ws_bytes = _space("gdn_packed_workspace_size", p, 1, workspace, device)
     dstate = None if initial_state is None else torch.empty_like(initial_state)
     _on(device, L.gdn_packed_backward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), beta.data_ptr(),
         cu_seqlens.data_ptr(), _ptr(initial_state), dout.data_ptr(), _ptr(dfinal_state), *(t.data_ptr() for t in grads),
@@ -241,26 +244,31 @@ def packed_workspace_size(q, v, sequences, *, gradient=False):
     """Bytes of workspace of ``packed_forward`` (or ``packed_backward``) for inputs like q and v."""
     p = SeqProblem(ABI_VERSION, q.shape[1], v.shape[1], q.shape[2], v.shape[2], _CODE[q.dtype], F32, 0, q.shape[0])
     p.sequences = sequences
-    need = ctypes.c_size_t(0)
-    _check(lib().gdn_packed_workspace_size(p, int(gradient), ctypes.byref(need)))
-    return need.value
+    return _need("gdn_packed_workspace_size", SeqProblem, bytes(p), int(gradient))
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _space(size, problem, mode, workspace, device):
-    """(tensor, bytes) of a call's workspace: the caller's, or a fresh one of the needed size."""
+@functools.lru_cache(maxsize=1024)
+def _need(call, kind, fields, mode):
+    """Bytes of workspace of the problem of these bytes; it depends on nothing else."""
     need = ctypes.c_size_t(0)
-    _check(size(problem, mode, ctypes.byref(need)))
+    _check(getattr(lib(), call)(kind.from_buffer_copy(fields), mode, ctypes.byref(need)))
+    return need.value
+
+
+def _space(call, problem, mode, workspace, device):
+    """(tensor, bytes) of a call's workspace: the caller's, or a fresh one of the needed size."""
+    need = _need(call, type(problem), bytes(problem), mode)
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {device}")
         return workspace, workspace.numel() * workspace.element_size()
-    if need.value == 0:
+    if need == 0:
         return None, 0
-    return torch.empty(need.value, dtype=torch.uint8, device=device), need.value
+    return torch.empty(need, dtype=torch.uint8, device=device), need
 
 
 def _norm_problem(x, groups, weight, bias, gate, activation, center, eps):
@@ -302,7 +310,7 @@ def group_norm(x, groups, weight=None, bias=None, gate=None, *, activation="none
         out = torch.empty_like(x)
     else:
         _dense("out", out, x.shape, x.dtype, x.device)
-    ws, ws_bytes = _space(lib().gdn_group_norm_workspace_size, p, 0, workspace, x.device)
+    ws, ws_bytes = _space("gdn_group_norm_workspace_size", p, 0, workspace, x.device)
     stats = (x.shape[0], groups)
     mean = torch.empty(stats, dtype=torch.float32, device=x.device) if center else None
     rstd = torch.empty(stats, dtype=torch.float32, device=x.device)
@@ -327,7 +335,7 @@ def group_norm_backward(dout, x, groups, mean, rstd, weight=None, bias=None, gat
     elif mean is not None:
         raise ValueError("mean must be None without center")
     _dense("rstd", rstd, stats, torch.float32, x.device)
-    ws, ws_bytes = _space(lib().gdn_group_norm_workspace_size, p, 1, workspace, x.device)
+    ws, ws_bytes = _space("gdn_group_norm_workspace_size", p, 1, workspace, x.device)
     dx = torch.empty_like(x)
     dw = None if weight is None else torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
