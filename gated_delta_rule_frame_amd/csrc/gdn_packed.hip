@@ -296,7 +296,7 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
   const bool first_half = wave < 4;
   const int srow = DKP > 64 ? wave : wave - 4;        // row tile of the state, if it has one
   const bool has_state = srow >= 0 && srow < DKP / 16;
-  int seq = sh / p.hv;
+  int seq = NS == 1 ? sh / p.hv : by_length(t.cu, p.sequences, p.tokens, sh / p.hv);   // NS = 1: all start at once
   const int slot_of = t.slots ? t.slots[seq] : seq;
   const bool kept = !t.slots || (slot_of >= 0 && slot_of < p.state_rows);
   if (t.slots && kept) {

@@ -66,7 +66,8 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(
   strip_of(blockIdx.x, (p.dv / 16 + NS - 1) / NS, &sh, &strip);
   strip *= NS;                                      // strips strip .. + NS; the last one of the last workgroup may not exist
   if (sh >= p.sequences * p.hv) return;
-  const int h = sh % p.hv, kh = h / (p.hv / p.hk), seq = sh / p.hv;
+  const int h = sh % p.hv, kh = h / (p.hv / p.hk);
+  const int seq = NS == 1 ? sh / p.hv : by_length(t.cu, p.sequences, p.tokens, sh / p.hv);   // NS = 1: all start at once
   const int col = strip * 16 + lr;
   const int strips = p.dv / 16;
   const auto there = [&](int i) { return NS == 1 || strip + i < strips; };

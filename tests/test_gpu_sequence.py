@@ -379,7 +379,9 @@ PACKED = [  # lengths, hk, hv, dk, dv, dtype, gate range, state
     ([257], 1, 2, 80, 16, F32, (0.1, 6.0), False), ([300, 1, 20], 3, 3, 48, 128, BF16, (0.0, 30.0), True),
     ([1000], 1, 1, 64, 32, F32, (0.0, 0.0005), True),
     # more column strips than CUs, an odd number of them in a head: pairs of strips, the last one alone
-    ([7, 0, 65, 130, 1] * 9, 2, 4, 48, 48, F32, (0.001, 0.1), True), ([70, 64, 1] * 8, 3, 6, 128, 80, BF16, (0.001, 0.1), True)]
+    ([7, 0, 65, 130, 1] * 9, 2, 4, 48, 48, F32, (0.001, 0.1), True), ([70, 64, 1] * 8, 3, 6, 128, 80, BF16, (0.001, 0.1), True),
+    # more sequences than are ordered by length
+    ([1, 20, 66] * 23, 1, 4, 32, 32, BF16, (0.001, 0.1), True)]
 
 
 @pytest.mark.parametrize("lengths,hk,hv,dk,dv,dtype,gate,with_state", PACKED)
