@@ -66,6 +66,14 @@ __device__ __forceinline__ void mma_by_term(const Frag<NA>& a, const Frag<NB>& b
       if (s - i >= 0 && s - i < NB) c[s] = mfma(a.t[i], b.t[s - i], c[s]);
 }
 
+template <int N, int M>
+__device__ __forceinline__ Frag<N> first_terms(const Frag<M>& f) {
+  Frag<N> o;
+#pragma unroll
+  for (int i = 0; i < N; ++i) o.t[i] = f.t[i];
+  return o;
+}
+
 // Two values as the sums of N bf16 values each, largest first, packed by term:
 // one conversion, two unpackings and two subtractions for a term of a pair.
 template <int N>

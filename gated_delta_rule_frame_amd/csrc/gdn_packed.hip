@@ -245,6 +245,38 @@ __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_ker
   }
 }
 
+// Sequences of one state row belong to the workgroup (of T threads) of the first of
+// them: whether seq is that one, and in *next the one after it, or 2^31 - 1.
+template <int T>
+__device__ __forceinline__ bool first_of_slot(const int* slots, int sequences, int seq, int slot, int* earlier, int* next) {
+  if (threadIdx.x == 0) {
+    *earlier = 0;
+    *next = 0x7fffffff;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < sequences; i += T)
+    if (slots[i] == slot) {
+      if (i < seq) *earlier = 1;
+      else if (i > seq) atomicMin(next, i);
+    }
+  __syncthreads();
+  return !*earlier;
+}
+
+// That next one, and in *next the one after it.
+template <int T>
+__device__ __forceinline__ int next_of_slot(const int* slots, int sequences, int slot, int* next) {
+  __syncthreads();
+  const int seq = *next;
+  __syncthreads();
+  if (threadIdx.x == 0) *next = 0x7fffffff;
+  __syncthreads();
+  for (int i = seq + 1 + threadIdx.x; i < sequences; i += T)
+    if (slots[i] == slot) atomicMin(next, i);
+  __syncthreads();
+  return seq;
+}
+
 // The scan.  A step's chain of dependent work is
 //     N = V - e^G K S0   |   e = T' N, U, e^(Gn-G) U   |   S1   |
 // with a barrier (|) wherever a product's result becomes the next one's operand
@@ -263,12 +295,11 @@ __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_ker
 // before each chunk are left in the workspace for the gradients.
 //
 // NS: strips of 16 columns of a workgroup.  One where every strip can have a CU
-// to itself (d_k = d_v = 128, 16 chunks, 256 strips: 37 us against 46 in pairs):
-// only the step's own length counts, loads run two steps ahead.  Two where there
-// are more: the operands come through a CU's L1 once for both, which is what
-// bounds a full CU, and a step's waits have twice the products to fill them;
-// loads run one step ahead (384 strips 47 us against 69, 2048 strips 208 against
-// 315; single strips with two workgroups on a CU: 62 and 282).
+// to itself (d_k = d_v = 128, bf16, 16 chunks, 256 strips: 37 us against 46 in
+// pairs): only the step's own length counts, loads run two steps ahead.  Two
+// where there are more: the operands come through a CU's L1 once for both, which is
+// what bounds a full CU, and a step's waits have twice the products to fill them;
+// loads run one step ahead (384 strips 47 us against 69).
 template <int NT, int DKP, int PT, int NS>
 __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
   constexpr int SETS = NS == 1 ? 2 : 1;               // operand sets in registers: steps that loads run ahead
@@ -299,18 +330,7 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
   int seq = NS == 1 ? sh / p.hv : by_length(t.cu, p.sequences, p.tokens, sh / p.hv);   // NS = 1: all start at once
   const int slot_of = t.slots ? t.slots[seq] : seq;
   const bool kept = !t.slots || (slot_of >= 0 && slot_of < p.state_rows);
-  if (t.slots && kept) {
-    // sequences of the same state row belong to the workgroup of the first of them
-    if (tid == 0) { earlier = 0; next = 0x7fffffff; }
-    __syncthreads();
-    for (int i = tid; i < p.sequences; i += 512)
-      if (t.slots[i] == slot_of) {
-        if (i < seq) earlier = 1;
-        else if (i > seq) atomicMin(&next, i);
-      }
-    __syncthreads();
-    if (earlier) return;
-  }
+  if (t.slots && kept && !first_of_slot<512>(t.slots, p.sequences, seq, slot_of, &earlier, &next)) return;
   const size_t state = ((size_t)slot_of * p.hv + h) * p.dk * p.dv;
   const int row0 = 16 * w + 4 * lg;                   // of this lane's four accumulator rows
   const int krow = 16 * w + lr;                       // of its operand rows
@@ -576,15 +596,251 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
         for (int r = 0; r < 4; ++r)
           if (st0 + r < p.dk && there(i)) t.hT[state + (size_t)(st0 + r) * p.dv + col + 16 * i] = S[i][r];
     if (!t.slots || !kept || next == 0x7fffffff) break;
-    // the next sequence of this state row (rare)
+    seq = next_of_slot<512>(t.slots, p.sequences, slot_of, &next);
+  }
+}
+
+// The scan where there are more pairs of strips than CUs, bf16: then what counts
+// is the work of all CUs, not the length of a step, and four wavefronts that each
+// do every part of it, for two strips, leave two workgroups on a CU to fill each
+// other's waits.  K and Q share the state's operand reads, a lane's rows of V
+// need no staging.  13 prompts of 8191 tokens, 32 heads of 128: 200 us against
+// 264 by the eight wavefronts above in pairs; 2048 equal strips of 16 chunks 184
+// against 208, but 512 of them 59 against 48.  fp32 operands take the registers
+// of both workgroups (2048 strips 398 against 372), so they stay with those.
+template <int DKP, int PT>
+__global__ __launch_bounds__(256, 2) void packed_scan_pairs_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
+  constexpr int NT = 1, NS = 2, KS = DKP / 32, MT = DKP >= 64 ? DKP / 64 : 1;
+  constexpr int SP = 16 * DKP, TP = 16 * kC;          // elements of a term's tile
+  constexpr uint32_t es = NT == 1 ? 2 : 4;            // bytes of an input element
+  constexpr uint32_t os = PT == 2 ? 2 : 4;            // of an output element
+  __shared__ __align__(16) bh Sl[NS][3 * SP];
+  __shared__ __align__(16) bh Nl[NS][3 * TP];
+  __shared__ __align__(16) bh Ul[NS][(PT ? PT : 1) * TP];
+  __shared__ __align__(16) bh Dl[NS][3 * TP];
+  __shared__ int earlier, next;
+  const int tid = threadIdx.x, lane = tid % 64, w = __builtin_amdgcn_readfirstlane(tid / 64);
+  const int lr = lane % 16, lg = lane / 16;
+  const int strips = p.dv / 16;
+  int sh, strip;                                      // strips strip, strip + 1; the second of the last pair may not exist
+  strip_of(blockIdx.x, (strips + 1) / 2, &sh, &strip);
+  strip *= NS;
+  if (sh >= p.sequences * p.hv) return;
+  const int h = sh % p.hv, kh = h / (p.hv / p.hk);
+  const int col = strip * 16 + lr;
+  const auto there = [&](int i) { return strip + i < strips; };
+  const bool srows = DKP >= 64 || w < DKP / 16;       // has rows of the state
+  int seq = by_length(t.cu, p.sequences, p.tokens, sh / p.hv);
+  const int slot_of = t.slots ? t.slots[seq] : seq;
+  const bool kept = !t.slots || (slot_of >= 0 && slot_of < p.state_rows);
+  if (t.slots && kept && !first_of_slot<256>(t.slots, p.sequences, seq, slot_of, &earlier, &next)) return;
+  const size_t state = ((size_t)slot_of * p.hv + h) * p.dk * p.dv;
+  const int row0 = 16 * w + 4 * lg;                   // of this lane's four accumulator rows
+  const int krow = 16 * w + lr;                       // of its operand rows
+  const int tok_place = put_place(lr, row0);
+  int vector_zero = 0;
+  asm volatile("" : "+v"(vector_zero));               // a scalar load would be waited for with the LDS traffic
+  const size_t tri = (size_t)kTri * 3 * 64, tr = (size_t)(DKP / 16) * 2 * NT * 64;
+  const uint32_t ks_b = (uint32_t)p.ks * es, qs_b = (uint32_t)p.qs * es, vs_b = (uint32_t)p.vs * es;
+  const uint32_t dk_b = p.dk * es, dv_b = p.dv * es, os_b = (uint32_t)(p.hv * p.dv) * os;
+  uint32_t col_off[KS], tri_off[2];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) col_off[ks] = ks * 32 + lg * 8 < p.dk ? (ks * 32 + lg * 8) * es : kNowhere;
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) tri_off[ks] = ks <= w / 2 ? ((uint32_t)(w * 2 + ks) * 3 * 64 + lane) * 16 : kNowhere;
+
+  for (;;) {
+    int start, end;
+    seq_bounds(t.cu, seq, p.tokens, &start, &end);
+    start = __builtin_amdgcn_readfirstlane(start);
+    end = __builtin_amdgcn_readfirstlane(end);
+    const size_t slot = start / kC + (size_t)seq;
+    const int last = (end - start + kC - 1) / kC - 1;
+    f32x4 S[NS][MT];
+    auto put_state = [&](int i) {
+      if (srows)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const float x[4] = {S[i][m][0], S[i][m][1], S[i][m][2], S[i][m][3]};
+          put<3, DKP>(Sl[i] + put_place(lr, (w * MT + m) * 16 + 4 * lg), x);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = (w * MT + m) * 16 + 4 * lg + r;
+          S[i][m][r] = t.h0 && kept && there(i) && row < p.dk ? t.h0[state + (size_t)row * p.dv + col + 16 * i] : 0.f;
+        }
+      put_state(i);
+    }
+    // Loads behind the last chunk return 0.
+    auto rows_of = [&](int c) { return end - start - c * kC; };
+    RawFrag<NT> k[KS], q[KS];
+    typename RawIn<NT>::type v[NS][4];
+    uint4 eG, eD, be;
+    Frag<3> t1[2];
+    Frag<PT ? PT : 1> pf[2];
+    Frag<NT> kt[MT][2];
+    float eGn;
+    auto load_rows = [&](int c) {
+      const int n = rows_of(c);
+      const size_t first = start + (size_t)c * kC;
+      const buf_t kb = buf(static_cast<const char*>(t.k) + (first * p.ks + kh * p.dk) * es, span(n, ks_b, dk_b));
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) k[ks] = raw_at<NT>(kb, krow * ks_b + col_off[ks]);
+      if constexpr (PT > 0) {
+        const buf_t qb = buf(static_cast<const char*>(t.q) + (first * p.qs + kh * p.dk) * es, span(n, qs_b, dk_b));
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[ks] = raw_at<NT>(qb, krow * qs_b + col_off[ks]);
+      }
+      const buf_t vb = buf(static_cast<const char*>(t.v) + (first * p.vs + h * p.dv) * es, span(n, vs_b, dv_b));
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[i][r] = value_at<NT>(vb, there(i) ? (row0 + r) * vs_b + (col + 16 * i) * es : kNowhere);
+      eG = buf_load16(buf(ws.gates + ((slot + c) * p.hv + h) * 3 * kC, n > 0 ? kC * 4 : 0), row0 * 4);
+    };
+    auto load_inverse = [&](int c) {
+      const size_t cl = (slot + c) * p.hv + h;
+      const buf_t tb = buf(ws.t1 + cl * tri, c <= last ? (uint32_t)tri * 16 : 0);
+      const buf_t gb = buf(ws.gates + cl * 3 * kC, c <= last ? 3 * kC * 4 : 0);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) t1[ks] = frag_at<3>(tb, tri_off[ks]);
+      eD = buf_load16(gb, (kC + row0) * 4);
+      be = buf_load16(gb, (2 * kC + row0) * 4);
+      eGn = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(gb, (kC - 1) * 4 + vector_zero, 0, 0));
+    };
+    auto load_state = [&](int c) {
+      const buf_t kb = buf(ws.kt + ((slot + c) * p.hk + kh) * tr, c <= last && srows ? (uint32_t)tr * 16 : 0);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) kt[m][ks] = frag_at<NT>(kb, (((w * MT + m) * 2 + ks) * NT * 64 + lane) * 16);
+      if constexpr (PT > 0) {
+        const buf_t pb = buf(ws.p + ((slot + c) * p.hv + h) * tri, c <= last ? (uint32_t)tri * 16 : 0);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) pf[ks] = frag_at<PT, 3>(pb, tri_off[ks]);
+      }
+    };
+    load_rows(0);
+    load_inverse(0);
+    load_state(0);
     __syncthreads();
-    seq = next;
-    __syncthreads();
-    if (tid == 0) next = 0x7fffffff;
-    __syncthreads();
-    for (int i = seq + 1 + tid; i < p.sequences; i += 512)
-      if (t.slots[i] == slot_of) atomicMin(&next, i);
-    __syncthreads();
+    for (int c = 0; c <= last; ++c) {
+      const size_t cl = (slot + c) * p.hv + h;
+      f32x4 o[NS];
+      {
+        float eg[4];
+        floats(eG, eg);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          f32x4 a[3];
+#pragma unroll
+          for (int j = 0; j < 3; ++j) a[j] = zero4();
+          o[i] = zero4();
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const Frag<3> sf = get<3, DKP>(Sl[i] + lane * 8, ks);
+            mma_by_term<NT, 3>(frag_of<NT>(k[ks]), sf, a);
+            if constexpr (PT > 0) o[i] = mma<NT, PT>(frag_of<NT>(q[ks]), first_terms<PT>(sf), o[i]);
+          }
+          float x[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            x[r] = fmaf(-eg[r], (a[2][r] + a[1][r]) + a[0][r], raw_value(v[i][r]));
+            o[i][r] *= eg[r];
+          }
+          put<3, kC>(Nl[i] + tok_place, x);
+        }
+      }
+      load_rows(c + 1);
+      __syncthreads();
+      {
+        float ed[4], bt[4];
+        floats(eD, ed);
+        floats(be, bt);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          f32x4 a[3];
+#pragma unroll
+          for (int j = 0; j < 3; ++j) a[j] = zero4();
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            if (ks <= w / 2) mma_by_term<3, 3>(t1[ks], get<3, kC>(Nl[i] + lane * 8, ks), a);
+          const f32x4 e = (a[2] + a[1]) + a[0];
+          float x[4], ud[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            x[r] = bt[r] * e[r];
+            ud[r] = ed[r] * x[r];
+          }
+          put<3, kC>(Dl[i] + tok_place, ud);
+          if constexpr (PT > 0) {
+            put<PT, kC>(Ul[i] + tok_place, x);
+          } else {
+            const buf_t eb = buf(ws.e + (cl * strips + strip + i) * kC * 16, there(i) ? kC * 16 * 4 : 0);
+            const buf_t sb = buf(ws.s0 + (cl * strips + strip + i) * DKP * 16, there(i) && srows ? DKP * 16 * 4 : 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) store_at<4>(eb, ((row0 + r) * 16 + lr) * 4, e[r]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) store_at<4>(sb, (((w * MT + m) * 16 + 4 * lg + r) * 16 + lr) * 4, S[i][m][r]);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) S[i][m] = S[i][m] * eGn;
+        }
+      }
+      load_inverse(c + 1);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        if (srows) {
+          Frag<3> df[2];
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) df[ks] = get<3, kC>(Dl[i] + lane * 8, ks);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            f32x4 a[3];
+            a[0] = S[i][m];
+            a[1] = a[2] = zero4();
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) mma_by_term<NT, 3>(kt[m][ks], df[ks], a);
+            S[i][m] = a[0] + (a[1] + a[2]);
+          }
+        }
+        put_state(i);
+      }
+      if constexpr (PT > 0) {
+        const buf_t ob = buf(static_cast<char*>(t.out) + ((start + (size_t)c * kC) * p.hv + h) * p.dv * os,
+                             span(rows_of(c), os_b, p.dv * os));
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            if (ks <= w / 2) o[i] = mma<PT, PT>(pf[ks], get<PT, kC>(Ul[i] + lane * 8, ks), o[i]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) store_at<os>(ob, there(i) ? (row0 + r) * os_b + (col + 16 * i) * os : kNowhere, o[i][r]);
+        }
+      }
+      load_state(c + 1);
+      __syncthreads();
+    }
+    if (t.hT && kept && srows)
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = (w * MT + m) * 16 + 4 * lg + r;
+            if (row < p.dk && there(i)) t.hT[state + (size_t)row * p.dv + col + 16 * i] = S[i][m][r];
+          }
+    if (!t.slots || !kept || next == 0x7fffffff) break;
+    seq = next_of_slot<256>(t.slots, p.sequences, slot_of, &next);
   }
 }
 
@@ -648,11 +904,14 @@ hipError_t packed_prep(const SeqProblem& p, const PackedTensors& t, const Packed
 hipError_t packed_scan(const SeqProblem& p, const PackedTensors& t, const PackedSpace& s, bool grad, hipStream_t stream) {
   const PackedPlan f = packed_plan(p);
   const unsigned heads = (p.sequences * p.hv + 7) / 8 * 8;
-  const bool pairs = f.strips > 1 && (long long)p.sequences * p.hv * f.strips > 256;   // more strips than CUs
+  const long long strips = (long long)p.sequences * p.hv * f.strips;
+  const bool pairs = f.strips > 1 && strips > 256;     // more strips than CUs
+  const bool four = pairs && strips > 512 && f.terms == 1;   // more pairs than CUs
   const dim3 grid(heads * (pairs ? (f.strips + 1) / 2 : f.strips));
   prof_begin(stream, GDN_KERNEL_PACKED_SCAN);
 #define GDN_SCAN2(NT, D, PT)                                                                                         \
-  if (pairs) hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 2>), grid, dim3(512), 0, stream, p, t, s);            \
+  if (four) hipLaunchKernelGGL((packed_scan_pairs_kernel<D, PT>), grid, dim3(256), 0, stream, p, t, s);              \
+  else if (pairs) hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 2>), grid, dim3(512), 0, stream, p, t, s);       \
   else hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 1>), grid, dim3(512), 0, stream, p, t, s);
 #define GDN_SCAN(NT, D)                      \
   if (f.terms == NT && f.dkp == D) {         \

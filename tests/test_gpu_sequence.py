@@ -380,7 +380,8 @@ PACKED = [  # lengths, hk, hv, dk, dv, dtype, gate range, state
     ([1000], 1, 1, 64, 32, F32, (0.0, 0.0005), True),
     # more column strips than CUs, an odd number of them in a head: pairs of strips, the last one alone
     ([7, 0, 65, 130, 1] * 9, 2, 4, 48, 48, F32, (0.001, 0.1), True), ([70, 64, 1] * 8, 3, 6, 128, 80, BF16, (0.001, 0.1), True),
-    # more sequences than are ordered by length
+    # more pairs of strips than CUs; more sequences than are ordered by length
+    ([64, 70, 0, 5, 200] * 6, 2, 4, 112, 112, BF16, (0.001, 0.1), True),
     ([1, 20, 66] * 23, 1, 4, 32, 32, BF16, (0.001, 0.1), True)]
 
 
@@ -448,9 +449,10 @@ def test_packed_forward_strides_pools_and_repeated_slots(G):
     assert (other[[2, 3, 5]] == 2.0).all() and (other[0] == 0).all()
 
 
-def test_packed_forward_many_strips_into_a_pool(G):
+@pytest.mark.parametrize("times", [2, 3])
+def test_packed_forward_many_strips_into_a_pool(G, times):
     """More strips than CUs, an odd number a head, repeated and absent slots: as the sequences one after another."""
-    lengths = [65, 3, 0, 128, 20, 1, 70, 64] * 3
+    lengths = [65, 3, 0, 128, 20, 1, 70, 64] * times
     hk, hv, dk, dv, pool = 4, 8, 64, 48, 16
     n, c = sum(lengths), cu_of(lengths).tolist()
     x = rows(n, hk, hv, dk, dv, BF16, 61)
