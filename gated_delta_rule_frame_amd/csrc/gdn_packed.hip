@@ -38,22 +38,24 @@ __device__ __forceinline__ void store_quad(uint4* frags, int tile, int column, i
 // makes each result leave its registers as it is stored.  What it writes
 // bounds it: 32768 tokens of 35 heads of 64 272 us, some 60 KB a cell, 4 TB/s.
 template <int NT, int DKP, bool GRAD>
-__global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, long long slots) {
+__global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, long long slots, int heads) {
   constexpr int NM = GRAD ? 2 : 1, KS = DKP / 32;
   constexpr uint32_t es = NT == 1 ? 2 : 4;
-  __shared__ double Gs[kC];
-  __shared__ float bs[kC];
+  __shared__ double Gb[2][kC];
+  __shared__ float bb[2][kC];
   __shared__ __align__(16) float A[NM][kC][kLd];
   __shared__ __align__(16) float T[NM][kC][kLd];
   const int tid = threadIdx.x, lane = tid % 64, w = __builtin_amdgcn_readfirstlane(tid / 64);
   const int lr = lane % 16, lg = lane / 16;
   const int rep = p.hv / p.hk;
-  const long long cells = slots * p.hv;
+  const int share = GRAD ? heads : 1;                 // value heads of a workgroup
+  const int parts = p.hv / share;
+  const long long items = slots * parts;
   const uint32_t ks_b = (uint32_t)p.ks * es, qs_b = (uint32_t)p.qs * es;
 
-  for (long long cell = blockIdx.x; cell < cells; cell += gridDim.x) {
-    const int h = (int)(cell % p.hv), kh = h / rep;
-    const long long slot = cell / p.hv;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const int h0 = (int)(item % parts) * share, kh = h0 / rep;
+    const long long slot = item / parts;
     int seq, first, n;
     if (!find_chunk(t.cu, p.sequences, p.tokens, slot, &seq, &first, &n)) continue;   // uniform over the workgroup
     first = __builtin_amdgcn_readfirstlane(first);
@@ -64,8 +66,7 @@ __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_ker
       const int c = ks * 32 + lg * 8;
       return frag_of<NT>(raw_at<NT>(base, c < p.dk ? (tile * 16 + lr) * stride + c * es : kNowhere));
     };
-    __syncthreads();                                  // the previous cell's tiles have been read
-    if (w == 0) {
+    auto gates_of = [&](int h) {                        // by one wavefront, into the buffers of the head's turn
       const size_t at = (size_t)(first + lane) * p.hv + h;
       float g = lane < n ? t.g[at] : 0.f;
       g = g < kLowestGate ? kLowestGate : g;
@@ -75,9 +76,11 @@ __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_ker
         const double o = __shfl_up(G, m);
         if (lane >= m) G += o;
       }
-      Gs[lane] = G;
-      bs[lane] = lane < n ? t.beta[at] : 0.f;
-    }
+      Gb[(h - h0) & 1][lane] = G;
+      bb[(h - h0) & 1][lane] = lane < n ? t.beta[at] : 0.f;
+    };
+    __syncthreads();                                  // the previous cell's tiles have been read
+    if (w == 0) gates_of(h0);
     // K K^T as (rows w, columns j); Q K^T the same way for P^T, or as (rows j, columns w) for P
     f32x4 kk[4], qk[4];
 #pragma unroll
@@ -114,133 +117,139 @@ __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_ker
           kk[j] = mma<NT, NT>(ak, b, kk[j]);
           qk[j] = GRAD ? mma<NT, NT>(aq, b, qk[j]) : mma<NT, NT>(b, aq, qk[j]);
         }
-      if (h % rep == 0) {
+      if (h0 % rep == 0) {
         transpose(ak, ktp, ks);
         if constexpr (GRAD) transpose(aq, qtp, ks);
       }
     }
-    __syncthreads();
-    {
-      uint4* pp = ws.p + (size_t)cell * kTri * 3 * 64;
-      double Gr[4];
-      float br[4];
+    for (int h = h0; h < h0 + share; ++h) {
+      const long long cell = GRAD ? slot * p.hv + h : item;
+      const double* Gs = Gb[(h - h0) & 1];
+      const float* bs = bb[(h - h0) & 1];
+      __syncthreads();                                // the gates are there, the previous head's tiles have been read
+      if (w == 3 && h + 1 < h0 + share) gates_of(h + 1);
+      {
+        uint4* pp = ws.p + (size_t)cell * kTri * 3 * 64;
+        double Gr[4];
+        float br[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        Gr[r] = Gs[16 * w + 4 * lg + r];
-        br[r] = bs[16 * w + 4 * lg + r];
-      }
+        for (int r = 0; r < 4; ++r) {
+          Gr[r] = Gs[16 * w + 4 * lg + r];
+          br[r] = bs[16 * w + 4 * lg + r];
+        }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j <= w) {
-          const int c = 16 * j + lr;
-          const double Gc = Gs[c];
-          const float bc = bs[c];
-          float x[4];
+        for (int j = 0; j < 4; ++j) {
+          if (j <= w) {
+            const int c = 16 * j + lr;
+            const double Gc = Gs[c];
+            const float bc = bs[c];
+            float x[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int i = 16 * w + 4 * lg + r;
-            const float E = i >= c ? exp2_of((float)(Gr[r] - Gc)) : 0.f;
-            const float b = i > c ? E * kk[j][r] : 0.f;
-            A[0][i][c] = b * bc;
-            if constexpr (GRAD) {
-              A[NM - 1][i][c] = b * br[r];
-              x[r] = E * qk[j][r];
-            } else {
-              // qk[j] holds rows 16 j + 4 lg + r of K and the row 16 w + lr of Q
-              const int pi = 16 * w + lr, pj = 16 * j + 4 * lg + r;
-              x[r] = pi >= pj ? exp2_of((float)(Gs[pi] - Gs[pj])) * qk[j][r] : 0.f;
+            for (int r = 0; r < 4; ++r) {
+              const int i = 16 * w + 4 * lg + r;
+              const float E = i >= c ? exp2_of((float)(Gr[r] - Gc)) : 0.f;
+              const float b = i > c ? E * kk[j][r] : 0.f;
+              A[0][i][c] = b * bc;
+              if constexpr (GRAD) {
+                A[NM - 1][i][c] = b * br[r];
+                x[r] = E * qk[j][r];
+              } else {
+                // qk[j] holds rows 16 j + 4 lg + r of K and the row 16 w + lr of Q
+                const int pi = 16 * w + lr, pj = 16 * j + 4 * lg + r;
+                x[r] = pi >= pj ? exp2_of((float)(Gs[pi] - Gs[pj])) * qk[j][r] : 0.f;
+              }
+            }
+            if constexpr (GRAD) store_quad<3, 3>(pp, j, lr, 16 * w + 4 * lg, x);          // P^T: row tile j, rows i
+            else if (p.out_bf16) store_quad<2, 3>(pp, w, lr, 16 * j + 4 * lg, x);         // P: row tile w, columns j
+            else store_quad<3, 3>(pp, w, lr, 16 * j + 4 * lg, x);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              T[0][16 * w + 4 * lg + r][16 * j + lr] = 0.f;
+              if constexpr (GRAD) T[NM - 1][16 * w + 4 * lg + r][16 * j + lr] = 0.f;
+            }
+            // the fragments on the diagonal's block row hold a block above it
+            const float z[4] = {0.f, 0.f, 0.f, 0.f};
+            if (j / 2 == w / 2) {
+              if constexpr (GRAD) store_quad<3, 3>(pp, j, lr, 16 * w + 4 * lg, z);
+              else store_quad<3, 3>(pp, w, lr, 16 * j + 4 * lg, z);
             }
           }
-          if constexpr (GRAD) store_quad<3, 3>(pp, j, lr, 16 * w + 4 * lg, x);          // P^T: row tile j, rows i
-          else if (p.out_bf16) store_quad<2, 3>(pp, w, lr, 16 * j + 4 * lg, x);         // P: row tile w, columns j
-          else store_quad<3, 3>(pp, w, lr, 16 * j + 4 * lg, x);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            T[0][16 * w + 4 * lg + r][16 * j + lr] = 0.f;
-            if constexpr (GRAD) T[NM - 1][16 * w + 4 * lg + r][16 * j + lr] = 0.f;
-          }
-          // the fragments on the diagonal's block row hold a block above it
-          const float z[4] = {0.f, 0.f, 0.f, 0.f};
-          if (j / 2 == w / 2) {
-            if constexpr (GRAD) store_quad<3, 3>(pp, j, lr, 16 * w + 4 * lg, z);
-            else store_quad<3, 3>(pp, w, lr, 16 * j + 4 * lg, z);
-          }
         }
       }
-    }
-    __syncthreads();
-    // (I + A)^-1: the 16 x 16 diagonal blocks by substitution, lane c a column
-    {
-      const int m = GRAD ? lg & 1 : 0, o = 16 * w;
-      float x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float s = i == lr ? 1.f : 0.f;
-#pragma unroll
-        for (int j4 = 0; j4 < i; j4 += 4) {
-          const float4 a = *reinterpret_cast<const float4*>(&A[m][o + i][o + j4]);
-          s = fmaf(-a.x, x[j4], s);
-          if (j4 + 1 < i) s = fmaf(-a.y, x[j4 + 1], s);
-          if (j4 + 2 < i) s = fmaf(-a.z, x[j4 + 2], s);
-          if (j4 + 3 < i) s = fmaf(-a.w, x[j4 + 3], s);
-        }
-        x[i] = s;
-      }
-      if (lg < NM) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) T[m][o + i][o + lr] = x[i];
-      }
-    }
-    // then the blocks below the diagonal, T_ij = -T_ii sum_k A_ik T_kj, by distance from it
-#pragma unroll
-    for (int d = 1; d < 4; ++d) {
       __syncthreads();
-      if (w < 4 - d) {
-        const int bi = w + d, bj = w;
+      // (I + A)^-1: the 16 x 16 diagonal blocks by substitution, lane c a column
+      {
+        const int m = GRAD ? lg & 1 : 0, o = 16 * w;
+        float x[16];
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-          f32x4 x = zero4(), y = zero4();
+        for (int i = 0; i < 16; ++i) {
+          float s = i == lr ? 1.f : 0.f;
 #pragma unroll
-          for (int k = 0; k < d; ++k) {
-            // any order of k that both operands share gives the product: 4 lg + s
-            const float4 a = *reinterpret_cast<const float4*>(&A[m][16 * bi + lr][16 * (bj + k) + 4 * lg]);
-            const float* b = &T[m][16 * (bj + k) + 4 * lg][16 * bj + lr];
-            x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b[0], x, 0, 0, 0);
-            x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b[kLd], x, 0, 0, 0);
-            x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b[2 * kLd], x, 0, 0, 0);
-            x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b[3 * kLd], x, 0, 0, 0);
+          for (int j4 = 0; j4 < i; j4 += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(&A[m][o + i][o + j4]);
+            s = fmaf(-a.x, x[j4], s);
+            if (j4 + 1 < i) s = fmaf(-a.y, x[j4 + 1], s);
+            if (j4 + 2 < i) s = fmaf(-a.z, x[j4 + 2], s);
+            if (j4 + 3 < i) s = fmaf(-a.w, x[j4 + 3], s);
           }
-          const float4 a = *reinterpret_cast<const float4*>(&T[m][16 * bi + lr][16 * bi + 4 * lg]);
-          const float at[4] = {a.x, a.y, a.z, a.w};
+          x[i] = s;
+        }
+        if (lg < NM) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) y = __builtin_amdgcn_mfma_f32_16x16x4f32(at[r], x[r], y, 0, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) T[m][16 * bi + 4 * lg + r][16 * bj + lr] = -y[r];
+          for (int i = 0; i < 16; ++i) T[m][o + i][o + lr] = x[i];
         }
       }
-    }
-    __syncthreads();
-    // out as fragments: of T' the column halves up to the diagonal, of T^T those from it on
+      // then the blocks below the diagonal, T_ij = -T_ii sum_k A_ik T_kj, by distance from it
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const int f = w * 2 + ks;
-      if (ks <= w / 2)
-        store_frag<3>(ws.t1 + (size_t)cell * kTri * 3 * 64, f, lane, frag_f32<3>(&T[0][16 * w + lr][32 * ks + 8 * lg]));
-      if constexpr (GRAD)
-        if (ks >= w / 2) {
-          float x[8];
+      for (int d = 1; d < 4; ++d) {
+        __syncthreads();
+        if (w < 4 - d) {
+          const int bi = w + d, bj = w;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = T[NM - 1][32 * ks + 8 * lg + j][16 * w + lr];
-          store_frag<3>(ws.t2 + (size_t)cell * kTri * 3 * 64, f, lane, split8<3>(x));
+          for (int m = 0; m < NM; ++m) {
+            f32x4 x = zero4(), y = zero4();
+#pragma unroll
+            for (int k = 0; k < d; ++k) {
+              // any order of k that both operands share gives the product: 4 lg + s
+              const float4 a = *reinterpret_cast<const float4*>(&A[m][16 * bi + lr][16 * (bj + k) + 4 * lg]);
+              const float* b = &T[m][16 * (bj + k) + 4 * lg][16 * bj + lr];
+              x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b[0], x, 0, 0, 0);
+              x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b[kLd], x, 0, 0, 0);
+              x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b[2 * kLd], x, 0, 0, 0);
+              x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b[3 * kLd], x, 0, 0, 0);
+            }
+            const float4 a = *reinterpret_cast<const float4*>(&T[m][16 * bi + lr][16 * bi + 4 * lg]);
+            const float at[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y = __builtin_amdgcn_mfma_f32_16x16x4f32(at[r], x[r], y, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) T[m][16 * bi + 4 * lg + r][16 * bj + lr] = -y[r];
+          }
         }
-    }
-    if (tid < kC) {
-      float* o = ws.gates + (size_t)cell * 3 * kC;
-      o[tid] = exp2_of((float)Gs[tid]);
-      o[kC + tid] = exp2_of((float)(Gs[kC - 1] - Gs[tid]));
-      o[2 * kC + tid] = bs[tid];
-      if constexpr (GRAD) ws.g[(size_t)cell * kC + tid] = Gs[tid];
+      }
+      __syncthreads();
+      // out as fragments: of T' the column halves up to the diagonal, of T^T those from it on
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int f = w * 2 + ks;
+        if (ks <= w / 2)
+          store_frag<3>(ws.t1 + (size_t)cell * kTri * 3 * 64, f, lane, frag_f32<3>(&T[0][16 * w + lr][32 * ks + 8 * lg]));
+        if constexpr (GRAD)
+          if (ks >= w / 2) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = T[NM - 1][32 * ks + 8 * lg + j][16 * w + lr];
+            store_frag<3>(ws.t2 + (size_t)cell * kTri * 3 * 64, f, lane, split8<3>(x));
+          }
+      }
+      if (tid < kC) {
+        float* o = ws.gates + (size_t)cell * 3 * kC;
+        o[tid] = exp2_of((float)Gs[tid]);
+        o[kC + tid] = exp2_of((float)(Gs[kC - 1] - Gs[tid]));
+        o[2 * kC + tid] = bs[tid];
+        if constexpr (GRAD) ws.g[(size_t)cell * kC + tid] = Gs[tid];
+      }
     }
   }
 }
@@ -886,13 +895,18 @@ size_t packed_space(const SeqProblem& p, bool grad, void* base, PackedSpace* s) 
 
 hipError_t packed_prep(const SeqProblem& p, const PackedTensors& t, const PackedSpace& s, bool grad, hipStream_t stream) {
   const PackedPlan f = packed_plan(p);
-  const long long cells = f.slots * p.hv;
-  const dim3 grid((unsigned)(cells < kMaxBlocks ? cells : kMaxBlocks));
+  // Value heads of a workgroup: in the gradients all of a key head, whose products
+  // they share, where that leaves each CU four workgroups (8192 tokens, 16 and 32
+  // heads of 128: 116 us against 148).  In the forward call those products' registers
+  // cost half of the wavefronts or spill (122 against 104).
+  const int share = grad && f.slots * p.hk >= 1024 ? p.hv / p.hk : 1;
+  const long long items = f.slots * (p.hv / share);
+  const dim3 grid((unsigned)(items < kMaxBlocks ? items : kMaxBlocks));
   prof_begin(stream, GDN_KERNEL_PACKED_PREP);
 #define GDN_PREP(NT, D)                                                                                                          \
   if (f.terms == NT && f.dkp == D) {                                                                                             \
-    if (grad) hipLaunchKernelGGL((packed_prep_kernel<NT, D, true>), grid, dim3(256), 0, stream, p, t, s, f.slots);               \
-    else hipLaunchKernelGGL((packed_prep_kernel<NT, D, false>), grid, dim3(256), 0, stream, p, t, s, f.slots);                   \
+    if (grad) hipLaunchKernelGGL((packed_prep_kernel<NT, D, true>), grid, dim3(256), 0, stream, p, t, s, f.slots, share);        \
+    else hipLaunchKernelGGL((packed_prep_kernel<NT, D, false>), grid, dim3(256), 0, stream, p, t, s, f.slots, share);            \
   }
   GDN_PREP(1, 32) GDN_PREP(1, 64) GDN_PREP(1, 128) GDN_PREP(3, 32) GDN_PREP(3, 64) GDN_PREP(3, 128)
 #undef GDN_PREP
