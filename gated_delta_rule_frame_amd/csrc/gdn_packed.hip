@@ -160,8 +160,7 @@ __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_ker
               }
             }
             if constexpr (GRAD) store_quad<3, 3>(pp, j, lr, 16 * w + 4 * lg, x);          // P^T: row tile j, rows i
-            else if (p.out_bf16) store_quad<2, 3>(pp, w, lr, 16 * j + 4 * lg, x);         // P: row tile w, columns j
-            else store_quad<3, 3>(pp, w, lr, 16 * j + 4 * lg, x);
+            else store_quad<3, 3>(pp, w, lr, 16 * j + 4 * lg, x);                         // P: row tile w, columns j
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -299,9 +298,12 @@ __device__ __forceinline__ int next_of_slot(const int* slots, int sequences, int
 // a step, on 140 CUs (4009 us with four wavefronts, row-major LDS tiles and loads
 // of the step's own operands).
 //
-// PT: terms of the output products (2 for a bf16 output, whose rounding is 2^9
-// times the third term; 3 for fp32), or 0: no outputs, but e and the state
-// before each chunk are left in the workspace for the gradients.
+// OB: bytes of an output element (2: bf16, 4: fp32), or 0: no outputs, but e and
+// the state before each chunk are left in the workspace for the gradients.  The
+// output's products take three terms whatever its type: with two, 3 to 5% faster
+// (13 prompts of 8191 tokens, 32 heads of 128, the call 289 us against 303; 32768
+// tokens, 35 heads of 64 1088 against 1120), three in a thousand bf16 outputs
+// are the neighbour of what the fp32 result rounds to.
 //
 // NS: strips of 16 columns of a workgroup.  One where every strip can have a CU
 // to itself (d_k = d_v = 128, bf16, 16 chunks, 256 strips: 37 us against 46 in
@@ -309,13 +311,14 @@ __device__ __forceinline__ int next_of_slot(const int* slots, int sequences, int
 // where there are more: the operands come through a CU's L1 once for both, which is
 // what bounds a full CU, and a step's waits have twice the products to fill them;
 // loads run one step ahead (384 strips 47 us against 69).
-template <int NT, int DKP, int PT, int NS>
+template <int NT, int DKP, int OB, int NS>
 __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
+  constexpr int PT = OB ? 3 : 0;                      // terms of the output products
   constexpr int SETS = NS == 1 ? 2 : 1;               // operand sets in registers: steps that loads run ahead
   constexpr int KS = DKP / 32;                        // steps over d_k
   constexpr int SP = 16 * DKP, TP = 16 * kC;   // elements of a term's tile
   constexpr uint32_t es = NT == 1 ? 2 : 4;            // bytes of an input element
-  constexpr uint32_t os = PT == 2 ? 2 : 4;            // of an output element
+  constexpr uint32_t os = OB;                         // of an output element
   __shared__ __align__(16) bh Sl[NS][3 * SP];
   __shared__ __align__(16) bh Nl[NS][3 * TP];
   __shared__ __align__(16) bh Ul[NS][(PT ? PT : 1) * TP];
@@ -617,12 +620,13 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
 // 264 by the eight wavefronts above in pairs; 2048 equal strips of 16 chunks 184
 // against 208, but 512 of them 59 against 48.  fp32 operands take the registers
 // of both workgroups (2048 strips 398 against 372), so they stay with those.
-template <int DKP, int PT>
+template <int DKP, int OB>
 __global__ __launch_bounds__(256, 2) void packed_scan_pairs_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
+  constexpr int PT = OB ? 3 : 0;                      // terms of the output products
   constexpr int NT = 1, NS = 2, KS = DKP / 32, MT = DKP >= 64 ? DKP / 64 : 1;
   constexpr int SP = 16 * DKP, TP = 16 * kC;          // elements of a term's tile
   constexpr uint32_t es = NT == 1 ? 2 : 4;            // bytes of an input element
-  constexpr uint32_t os = PT == 2 ? 2 : 4;            // of an output element
+  constexpr uint32_t os = OB;                         // of an output element
   __shared__ __align__(16) bh Sl[NS][3 * SP];
   __shared__ __align__(16) bh Nl[NS][3 * TP];
   __shared__ __align__(16) bh Ul[NS][(PT ? PT : 1) * TP];
@@ -923,15 +927,15 @@ hipError_t packed_scan(const SeqProblem& p, const PackedTensors& t, const Packed
   const bool four = pairs && strips > 512 && f.terms == 1;   // more pairs than CUs
   const dim3 grid(heads * (pairs ? (f.strips + 1) / 2 : f.strips));
   prof_begin(stream, GDN_KERNEL_PACKED_SCAN);
-#define GDN_SCAN2(NT, D, PT)                                                                                         \
-  if (four) hipLaunchKernelGGL((packed_scan_pairs_kernel<D, PT>), grid, dim3(256), 0, stream, p, t, s);              \
-  else if (pairs) hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 2>), grid, dim3(512), 0, stream, p, t, s);       \
-  else hipLaunchKernelGGL((packed_scan_kernel<NT, D, PT, 1>), grid, dim3(512), 0, stream, p, t, s);
+#define GDN_SCAN2(NT, D, OB)                                                                                         \
+  if (four) hipLaunchKernelGGL((packed_scan_pairs_kernel<D, OB>), grid, dim3(256), 0, stream, p, t, s);              \
+  else if (pairs) hipLaunchKernelGGL((packed_scan_kernel<NT, D, OB, 2>), grid, dim3(512), 0, stream, p, t, s);       \
+  else hipLaunchKernelGGL((packed_scan_kernel<NT, D, OB, 1>), grid, dim3(512), 0, stream, p, t, s);
 #define GDN_SCAN(NT, D)                      \
   if (f.terms == NT && f.dkp == D) {         \
     if (grad) { GDN_SCAN2(NT, D, 0) }        \
     else if (p.out_bf16) { GDN_SCAN2(NT, D, 2) } \
-    else { GDN_SCAN2(NT, D, 3) }             \
+    else { GDN_SCAN2(NT, D, 4) }             \
   }
   GDN_SCAN(1, 32) GDN_SCAN(1, 64) GDN_SCAN(1, 128) GDN_SCAN(3, 32) GDN_SCAN(3, 64) GDN_SCAN(3, 128)
 #undef GDN_SCAN
