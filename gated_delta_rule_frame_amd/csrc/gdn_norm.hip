@@ -26,6 +26,8 @@
 // Sums are fp32: a group's second moment is taken about its mean (in registers) or
 // about each thread's first value and joined pairwise with counts, so a mean
 // far from zero does not cancel.  No atomics: results are the same every run.
+#include <cfloat>
+
 #include "gdn_common.h"
 #include "gdn_norm.h"
 
@@ -100,19 +102,30 @@ __device__ __forceinline__ void store_vec(void* p, size_t i, const float (&x)[VE
 // 1 / (1 + e^-u) with the hardware's 2^x and 1 / x (1 ulp each): with expf and an
 // IEEE division the vector units, not memory, bounded the kernels (a 121 x 880 x
 // 2240 bf16 frame norm with SiLU: 360 us for the pass that writes, 2.7 TB/s).
-// The product -u log2(e) keeps its rounding error as a first-order factor, so
-// the exponent's size costs no accuracy; above 2^126 the result is 0.
+// The product -u log2(e) keeps its rounding error as a factor close to 1, so the
+// exponent's size costs no accuracy; that factor is made from u held to a range
+// where it is finite.  The result is 0 below -89, 1 at the other end and NaN for NaN.
+__device__ __forceinline__ float held(float u) { return __builtin_amdgcn_fmed3f(u, -100.f, 100.f); }
+
 __device__ __forceinline__ float sigmoid(float u) {
-  const float t = fminf(-1.44269504f * u, 126.f);
-  const float lo = fmaf(-1.44269504f, u, -t) - 1.92596299e-8f * u;      // log2(e) = 1.44269504 + 1.926e-8
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_amdgcn_rcpf(1.f + fmaf(e, t < 126.f ? 0.69314718f * lo : 0.f, e));
+  const float c = held(u), t = -1.44269504f * c;
+  const float lo = fmaf(-1.44269504f, c, -t) - 1.92596299e-8f * c;      // log2(e) = 1.44269504 + 1.926e-8
+  const float e = __builtin_amdgcn_exp2f(-1.44269504f * u);
+  return __builtin_amdgcn_rcpf(fmaf(e, fmaf(0.69314718f, lo, 1.f), 1.f));
 }
 
+// u cut off where the normal distribution's density is 0 and its integral 0 or 1,
+// so that 0 times an infinity is not asked for; NaN stays NaN.
+__device__ __forceinline__ float gelu_range(float u) {
+  const float lo = u < -40.f ? -40.f : u;
+  return lo > 40.f ? 40.f : lo;
+}
+
+// At -inf value and slope are their limits 0, at +inf inf and 1.
 __device__ __forceinline__ float act(int a, float u) {
   switch (a) {
-    case GDN_ACT_SILU: return u * sigmoid(u);
-    case GDN_ACT_GELU: return 0.5f * u * (1.f + erff(u * 0.70710678f));
+    case GDN_ACT_SILU: return fmaxf(u, -FLT_MAX) * sigmoid(u);    // -inf 0; NaN is in the second factor
+    case GDN_ACT_GELU: return 0.5f * (u < -40.f ? -40.f : u) * (1.f + erff(u * 0.70710678f));
     case GDN_ACT_RELU: return u < 0.f ? 0.f : u;
     default: return u;
   }
@@ -142,11 +155,11 @@ __device__ __forceinline__ float2 act_slope(int a, float u) {
   switch (a) {
     case GDN_ACT_SILU: {
       const float s = sigmoid(u);
-      return make_float2(u * s, s * (1.f + u * (1.f - s)));
+      return make_float2(fmaxf(u, -FLT_MAX) * s, s * (1.f + held(u) * (1.f - s)));
     }
     case GDN_ACT_GELU: {
-      const float c = 0.5f * (1.f + erff(u * 0.70710678f));
-      return make_float2(u * c, c + u * 0.39894228f * expf(-0.5f * u * u));
+      const float c = 0.5f * (1.f + erff(u * 0.70710678f)), r = gelu_range(u);
+      return make_float2((u < -40.f ? -40.f : u) * c, c + r * 0.39894228f * expf(-0.5f * r * r));
     }
     case GDN_ACT_RELU: return make_float2(u < 0.f ? 0.f : u, u > 0.f ? 1.f : 0.f);
     default: return make_float2(u, 1.f);

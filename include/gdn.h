@@ -420,7 +420,8 @@ gdn_status gdn_packed_backward(const gdn_seq_problem* problem,
  * [channels] fp32 or NULL (1 and 0); gate, out and the gradients of x and gate
  * have x's type and shape; mean and rstd [batch, groups] fp32.  All
  * statistics and sums are fp32, with no atomics.  RELU has slope 0 at 0; GELU
- * is u (1 + erf(u / sqrt 2)) / 2. */
+ * is u (1 + erf(u / sqrt 2)) / 2.  SILU, GELU and RELU and their slopes are 0 at
+ * -inf (a masked gate lets nothing through), inf and 1 at +inf. */
 enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU = 2, GDN_ACT_RELU = 3 };
 typedef struct gdn_norm_problem {
   int32_t abi_version;        /* must equal GDN_ABI_VERSION */

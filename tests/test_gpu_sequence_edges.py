@@ -22,3 +22,99 @@ def test_packed_forward_bf16_output_is_the_fp32_output_rounded(G, lengths, hk, h
     a, Sa = G.packed_forward(*x, cu_of(lengths), S0)
     b, Sb = G.packed_forward(*x, cu_of(lengths), S0, out_dtype=BF16)
     assert torch.equal(a.to(BF16), b) and torch.equal(Sa, Sb)
+
+
+# ------------------------------------------------------------------ activations at the ends of the range
+
+def act_limits(name, u):
+    """Value and slope of the activation in float64, with their limits at +-inf."""
+    big = u.abs() > 40.0                     # there both are their limits to far below fp32, but for SiLU's tail
+    t = torch.where(big, torch.zeros_like(u), u)
+    if name == "silu":
+        big = u.abs() > 600.0
+        t = torch.where(big, torch.zeros_like(u), u)
+        s = 1 / (1 + torch.exp(-t))
+        value, slope = t * s, s * (1 + t * (1 - s))
+    elif name == "gelu":
+        c = 0.5 * (1 + torch.erf(t / 2 ** 0.5))
+        value, slope = t * c, c + t * torch.exp(-0.5 * t * t) / (2 * torch.pi) ** 0.5
+    else:
+        value, slope = torch.relu(t), (t > 0).double()
+    return torch.where(big, torch.relu(u), value), torch.where(big, (u > 0).double(), slope)
+
+
+def ends(dtype):
+    m = torch.finfo(dtype).max
+    return torch.tensor([[-30.0, -88.0, -90.0, -104.0, -1e30, -2.4e38, -m, float("-inf")],
+                         [30.0, 88.0, 90.0, 104.0, 1e30, 2.4e38, m, float("inf")]])
+
+
+def close(got, ref, dtype):
+    """The group norm's bound at one place, 3e-5, of the value and of order one, and the output's own rounding."""
+    got, ref = R.f64(got), ref.to(torch.float64)
+    far = torch.isinf(ref)
+    assert torch.equal(got[far], ref[far])
+    ok = (got - ref)[~far].abs() <= (3e-5 + (R.HALF[dtype] if dtype == BF16 else 0.0)) * ref[~far].abs() + 3e-5
+    assert ok.all(), int((~ok).sum())
+
+
+@pytest.mark.parametrize("s", [1, 3, 6000])          # a row, a band in registers, two passes
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("activation", ["silu", "gelu", "relu"])
+def test_group_norm_activations_at_the_ends_of_the_range(G, s, dtype, activation):  # noqa: F811
+    """Gates and activated values up to the type's largest and lowest values and +-inf: a masked gate lets nothing through,
+    forward or backward, and no value or slope is NaN."""
+    n, c, groups = 2, 32, 4
+    gen = torch.Generator().manual_seed(s)
+    r = lambda *sh: torch.randn(*sh, generator=gen)  # noqa: E731
+    x, dy, gate = r(n, s, c).to(dtype).cuda(), r(n, s, c).to(dtype).cuda(), r(n, s, c).to(dtype)
+    gate[:, :, 8:16], gate[:, :, 24:] = ends(dtype)[0].to(dtype), ends(dtype)[1].to(dtype)
+    gate = gate.cuda()
+    # |x^| < 12 here, weights keep the largest gate's products in range
+    w = torch.full((c,), 0.05).cuda()
+    out, mean, rstd = G.group_norm(x, groups, w, None, gate, activation=activation)
+    dx, dw, _, dz = G.group_norm_backward(dy, x, groups, mean, rstd, w, None, gate, activation=activation)
+    X, Y, W, Z = R.f64(x).view(n, s, groups, 8), R.f64(dy).view(n, s, groups, 8), R.f64(w).view(groups, 8), R.f64(gate).view(n, s, groups, 8)
+    M = X.mean((1, 3), keepdim=True)
+    rs = 1 / torch.sqrt((X - M).square().mean((1, 3), keepdim=True) + 1e-5)
+    h = (X - M) * rs
+    value, slope = act_limits(activation, Z)
+    flat = lambda t: t.reshape(n, s, c)  # noqa: E731
+    close(out, flat(h * W * value), dtype)
+    close(dz, flat(Y * h * W * slope), dtype)
+
+    def inward(du):
+        d = du * W
+        return rs * (d - d.mean((1, 3), keepdim=True) - h * (d * h).mean((1, 3), keepdim=True))
+
+    small = [0, 1, 2]                                  # the last group's gradients overflow with its gates
+    close(dx.view(n, s, groups, 8)[:, :, small], inward(Y * value)[:, :, small], dtype)
+    # ungated, the same values through the bias
+    b = torch.cat([r(8), ends(F32)[0], r(8), ends(F32)[1]]).cuda()
+    out, mean, rstd = G.group_norm(x, groups, w, b, activation=activation)
+    dx, dw, db, _ = G.group_norm_backward(dy, x, groups, mean, rstd, w, b, activation=activation)
+    u = (h * W + R.f64(b).view(groups, 8)).float().double()
+    value, slope = act_limits(activation, u)
+    if dtype == F32:                                   # in bf16 the largest fp32 values round to inf
+        close(out, flat(value), dtype)
+    else:
+        close(out[:, :, :24], flat(value)[:, :, :24], dtype)
+        assert not torch.isnan(out).any()
+    close(dx, flat(inward(Y * slope)), dtype)
+    terms = (Y * slope).abs().sum((0, 1)).reshape(c)
+    assert ((R.f64(db) - (Y * slope).sum((0, 1)).reshape(c)).abs() <= 3e-5 * (1 + terms)).all()
+    assert torch.isfinite(dw).all()
+
+
+@pytest.mark.parametrize("s", [1, 3, 6000])
+@pytest.mark.parametrize("activation", ["none", "silu", "gelu", "relu"])
+def test_group_norm_gate_of_nan(G, s, activation):  # noqa: F811
+    """A gate of NaN is NaN in its own place, forward and in the gate's gradient (ReLU's slope there is 0), and nowhere else."""
+    x, z = torch.randn(2, s, 32).cuda(), torch.randn(2, s, 32).cuda()
+    z[1, s - 1, 7] = float("nan")
+    out, mean, rstd = G.group_norm(x, 4, None, None, z, activation=activation)
+    bad = torch.isnan(z)
+    assert torch.equal(torch.isnan(out), bad)
+    dz = G.group_norm_backward(x, x, 4, mean, rstd, None, None, z, activation=activation)[3]
+    assert not torch.isnan(dz[~bad]).any()
+    assert torch.isnan(dz[bad]).all() == (activation in ("silu", "gelu"))
