@@ -127,8 +127,8 @@ def lib():
         L.gdn_step.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.gdn_step_noalloc.restype = i32
         L.gdn_step_noalloc.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp]
-        from . import sequence
-        sequence.declare(L)
+        from . import sequence_abi
+        sequence_abi.declare(L)
         if L.gdn_abi_version() != ABI_VERSION:
             raise ImportError(f"libgdn ABI {L.gdn_abi_version()} != binding ABI {ABI_VERSION}")
         _lib = L

@@ -2,6 +2,9 @@
 calls without work, through the C ABI with pointers that are never used (no
 GPU needed), and the binding's refusals."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -155,3 +158,14 @@ def test_binding_refuses_tensors_off_the_gpu():
         G.group_norm(x, 2)
     with pytest.raises(ValueError):
         G.group_norm_backward(x, x, 2, g, g)
+
+
+def test_host_calls_need_no_torch():
+    """The library loads, and its host-only calls run, where torch cannot be imported."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import gated_delta_rule_frame_amd as G\n"
+            "p = G.make_problem(1, 2, 64, 64, 2, 880, G.BF16, G.F32)\n"
+            "assert G.lib().gdn_abi_version() == G.ABI_VERSION\n"
+            "print(G.workspace_size(p), G.segment_plan(p))\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=os.path.dirname(os.path.dirname(__file__)))
+    assert r.returncode == 0, r.stderr
