@@ -16,6 +16,7 @@ import torch
 from . import ABI_VERSION, BF16, F32, _check, lib
 from .sequence_abi import NormProblem, SeqProblem
 
+_MAX = 2 ** 31 - 1          # of the ABI's 32-bit sizes, which ctypes would cut off without an error
 ACTIVATION = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
 _CODE = {torch.bfloat16: BF16, torch.float32: F32}
 
@@ -25,6 +26,12 @@ _CODE = {torch.bfloat16: BF16, torch.float32: F32}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _fits(name, n):
+    if n > _MAX:
+        raise ValueError(f"{name} must be below 2^31 (got {n})")
+    return n
 
 
 def _on(device, call, *args):
@@ -70,6 +77,8 @@ def _problem(q, k, v, log_gate, beta, out_dtype):
     if q.dtype not in _CODE or out_dtype not in _CODE:
         raise TypeError(f"unsupported dtype {q.dtype} or {out_dtype}")
     device, (n, hk, dk), (hv, dv) = q.device, q.shape, v.shape[1:]
+    if max(hk, hv, dk, dv) > _MAX:
+        raise ValueError(f"heads and widths must be below 2^31 (got {hk}, {hv}, {dk}, {dv})")
     p = SeqProblem(ABI_VERSION, hk, hv, dk, dv, _CODE[q.dtype], _CODE[out_dtype], 0, n)
     p.q_stride = _rows("q", q, q.shape, q.dtype, device)
     p.k_stride = _rows("k", k, q.shape, q.dtype, device)
@@ -106,7 +115,7 @@ def decode(q, k, v, log_gate, beta, state, slots=None, *, out_dtype=None, out=No
     if slots is not None:
         _dense("slots", slots, (n,), torch.int32, device)
         rows = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 4 else 0
-        p.state_rows = rows
+        p.state_rows = _fits("the pool's rows", rows)
     _dense("state", state, (rows, hv, dk, dv), torch.float32, device)
     if out is None:
         out = torch.empty((n, hv, dv), dtype=odt, device=device)
@@ -121,7 +130,7 @@ def _sequences(cu_seqlens, device):
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be a tensor of sequences + 1 values")
     _dense("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
-    return cu_seqlens.shape[0] - 1
+    return _fits("sequences", cu_seqlens.shape[0] - 1)
 
 
 def packed_forward(q, k, v, log_gate, beta, cu_seqlens, initial_state=None, *, slots=None, out_dtype=None, out=None,
@@ -151,7 +160,8 @@ def packed_forward(q, k, v, log_gate, beta, cu_seqlens, initial_state=None, *, s
             if want_state:
                 final_state = initial_state
         pool = initial_state if final_state is None else final_state
-        states = p.state_rows = pool.shape[0] if isinstance(pool, torch.Tensor) and pool.dim() == 4 else 0
+        states = pool.shape[0] if isinstance(pool, torch.Tensor) and pool.dim() == 4 else 0
+        p.state_rows = _fits("the pool's rows", states)
     shape = (states, hv, dk, dv)
     if initial_state is not None:
         _dense("initial_state", initial_state, shape, torch.float32, device)
@@ -208,7 +218,7 @@ def packed_backward(q, k, v, log_gate, beta, cu_seqlens, dout, initial_state=Non
 def packed_workspace_size(q, v, sequences, *, gradient=False):
     """Bytes of workspace of ``packed_forward`` (or ``packed_backward``) for inputs like q and v."""
     p = SeqProblem(ABI_VERSION, q.shape[1], v.shape[1], q.shape[2], v.shape[2], _CODE[q.dtype], F32, 0, q.shape[0])
-    p.sequences = sequences
+    p.sequences = _fits("sequences", sequences)
     return _need("gdn_packed_workspace_size", SeqProblem, bytes(p), int(gradient))
 
 
@@ -254,6 +264,8 @@ def _norm_problem(x, groups, weight, bias, gate, activation, center, eps):
     spatial = 1
     for n in x.shape[1:-1]:
         spatial *= n
+    for name, n in (("the spatial size", spatial), ("channels", C), ("groups", groups)):
+        _fits(name, n)
     return NormProblem(ABI_VERSION, _CODE[x.dtype], x.shape[0], spatial, C, groups, ACTIVATION[activation], int(bool(center)), eps)
 
 

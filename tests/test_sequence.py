@@ -169,3 +169,32 @@ def test_host_calls_need_no_torch():
             "print(G.workspace_size(p), G.segment_plan(p))\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=os.path.dirname(os.path.dirname(__file__)))
     assert r.returncode == 0, r.stderr
+
+
+def test_binding_refuses_sizes_beyond_the_abis_fields():
+    """Sizes of 2^31 and more are refused, not cut off to 32 bits (tensors without memory: no GPU needed)."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        e = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device="cuda")  # noqa: E731
+        f = lambda *s: e(*s, dtype=torch.float32)  # noqa: E731
+        i = lambda *s: e(*s, dtype=torch.int32)  # noqa: E731
+        big = 2 ** 32 + 16
+        for x, groups in ((e(1, big, 1), 1), (e(1, 2 ** 16, 2 ** 16 + 1, 1), 1), (e(1, big), 1), (e(1, 16), big)):
+            with pytest.raises(ValueError, match="2.31"):
+                G.group_norm(x, groups)
+            with pytest.raises(ValueError, match="2.31"):
+                G.group_norm_backward(x, x, groups, f(1, groups), f(1, groups))
+        q, v, g = e(4, 2, 64), e(4, 2, 64), f(4, 2)
+        for bad in ((e(1, big, 16), e(1, big, 16), f(1, big)), (e(1, 1, big), e(1, 1, 16), f(1, 1)), (e(1, 1, 16), e(1, 1, big), f(1, 1))):
+            with pytest.raises(ValueError, match="2.31"):
+                G.decode(bad[0], bad[0], bad[1], bad[2], bad[2], f(1, 1, 16, 16))
+        with pytest.raises(ValueError, match="2.31"):
+            G.decode(q, q, v, g, g, f(big, 2, 64, 64), i(4))
+        with pytest.raises(ValueError, match="2.31"):
+            G.packed_forward(q, q, v, g, g, i(big))
+        with pytest.raises(ValueError, match="2.31"):
+            G.packed_forward(q, q, v, g, g, i(3), f(big, 2, 64, 64), slots=i(2))
+        with pytest.raises(ValueError, match="2.31"):
+            G.packed_backward(q, q, v, g, g, i(big), v)
+        with pytest.raises(ValueError, match="2.31"):
+            G.packed_workspace_size(q, v, big)
