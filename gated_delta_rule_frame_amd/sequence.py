@@ -146,7 +146,8 @@ def packed_forward(q, k, v, log_gate, beta, cu_seqlens, initial_state=None, *, s
     ``slots`` ([sequences] int32) pools of which each sequence uses one row; the
     final state of a call with ``slots`` goes into ``final_state``, by default
     into initial_state, in place.  The output is fp32 unless ``out_dtype`` or
-    ``out`` says otherwise.
+    ``out`` says otherwise.  A NaN or infinity in a token's row can make outputs
+    of up to 63 earlier tokens of its sequence NaN (those in its chunk of 64).
     """
     odt = _output(out, out_dtype)
     p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, beta, odt)

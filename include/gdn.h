@@ -320,7 +320,7 @@ gdn_status gdn_plan_segment_tokens(const gdn_problem* problem, int32_t direction
  * token axis, without a batch axis:
  *   q, k        [tokens, heads_k, d_k]   qkv_dtype
  *   v, out      [tokens, heads_v, d_v]   qkv_dtype, out_dtype
- *   log_gate    [tokens, heads_v]        fp32, g <= 0 (-inf resets the state)
+ *   log_gate    [tokens, heads_v]        fp32, g <= 0 (-inf drops a finite state)
  *   beta        [tokens, heads_v]        fp32
  *   states      [rows, heads_v, d_k, d_v] fp32
  * Value head h reads key head h / (heads_v / heads_k).  Rows of q, k and v may
@@ -349,7 +349,8 @@ typedef struct gdn_seq_problem {
  * writes out[i].  slots [tokens] int32, or NULL for row i on state row i (then
  * state has `tokens` rows).  A row whose slot is outside [0, state_rows) is
  * padding: neither its output row nor any state is touched.  Rows that name
- * the same slot are applied one after another, in row order. */
+ * the same slot are applied one after another, in row order.  A NaN stays in
+ * its row and state.  No aliasing. */
 gdn_status gdn_decode(const gdn_seq_problem* problem,
                       const void* q, const void* k, const void* v,
                       const float* log_gate, const float* beta,
@@ -362,7 +363,13 @@ gdn_status gdn_decode(const gdn_seq_problem* problem,
  * decreasing ones are clamped when they are used, so no value reads or writes
  * out of range; results are then unspecified.  Chunks of 64 tokens on the
  * matrix cores for every width and both types; the accuracy is that of fp32
- * arithmetic and the range that of bf16 (no fp16 domain as GDN_ALGO_AUTO's). */
+ * arithmetic and the range that of bf16 (no fp16 domain as GDN_ALGO_AUTO's).
+ * A NaN or infinity in a token's q spoils that token's outputs; in its k, v,
+ * log_gate or beta, beside what the recurrence makes of it, also outputs of
+ * earlier tokens in its chunk (0 times it is NaN), at most 63 of them, in the
+ * value heads that read it and, for v, in its column.  Earlier chunks, other
+ * sequences, value heads and columns come out as without it.  Gradients: every
+ * token of the sequence may be NaN, other sequences are as without it. */
 
 /* Bytes of device workspace of gdn_packed_forward (gradient = 0) or
  * gdn_packed_backward (1).  Forward: about 50 KB for each 64 tokens and value

@@ -118,3 +118,54 @@ def test_group_norm_gate_of_nan(G, s, activation):  # noqa: F811
     dz = G.group_norm_backward(x, x, 4, mean, rstd, None, None, z, activation=activation)[3]
     assert not torch.isnan(dz[~bad]).any()
     assert torch.isnan(dz[bad]).all() == (activation in ("silu", "gelu"))
+
+
+# ------------------------------------------------------------------ NaN and infinities in a packed batch
+
+@pytest.mark.parametrize("lengths,hk,hv,dk,dv", STRIPS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("where", ["q", "k", "v", "log_gate", "beta"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_packed_forward_bad_value_stays_in_its_chunk_and_heads(G, lengths, hk, hv, dk, dv, dtype, where, value):  # noqa: F811
+    """Earlier chunks, other sequences, other value heads and (for v) columns come out bit for bit as without it; from its
+    token on it shows as in the recurrence (a q only in its own outputs)."""
+    rep = hv // hk
+    x = rows(sum(lengths), hk, hv, dk, dv, dtype, 81)
+    cu = cu_of(lengths)
+    c = cu.tolist()
+    s = max(range(len(lengths)), key=lambda i: lengths[i])
+    t = c[s] + (lengths[s] - 1) // 64 * 64 + 1                # a token of the last chunk
+    want, wantS = G.packed_forward(*x, cu)
+    i = ["q", "k", "v", "log_gate", "beta"].index(where)
+    bad = [y.clone() for y in x]
+    head = hk - 1 if i < 2 else hv - 1
+    if i < 3:
+        bad[i][t, head, 5] = value
+    else:
+        bad[i][t, head] = value
+    got, gotS = G.packed_forward(*bad, cu)
+    heads = slice(head * rep, (head + 1) * rep) if i < 2 else slice(head, head + 1)
+    cols = slice(5, 6) if where == "v" else slice(0, dv)
+    first = t if where == "q" else c[s] + (t - c[s]) // 64 * 64
+    last = t + 1 if where == "q" else c[s + 1]
+    reach = torch.zeros_like(got, dtype=torch.bool)
+    reach[first:last, heads, cols] = True
+    assert torch.equal(got[~reach], want[~reach])
+    assert not torch.isfinite(got[t:last, heads, cols]).any()
+    states = torch.zeros_like(gotS, dtype=torch.bool)
+    states[s, heads, :, cols] = where != "q"
+    assert torch.equal(gotS[~states], wantS[~states])
+    assert where == "q" or not torch.isfinite(gotS[s, heads, :, cols]).any()
+
+
+def test_packed_backward_bad_value_stays_in_its_sequence(G):  # noqa: F811
+    lengths, hk, hv, dk, dv = [70, 130, 40], 2, 4, 48, 32
+    x, cu = rows(240, hk, hv, dk, dv, BF16, 82), cu_of(lengths)
+    dout = torch.randn(240, hv, dv).to(BF16).cuda()
+    want = G.packed_backward(*x, cu, dout)
+    for i in range(6):
+        bad = [y.clone() for y in (*x, dout)]
+        bad[i][100, 1] = float("nan")
+        got = G.packed_backward(*bad[:5], cu, bad[5])
+        for a, b in zip(got[:5], want[:5]):
+            assert torch.equal(a[:70], b[:70]) and torch.equal(a[200:], b[200:])
