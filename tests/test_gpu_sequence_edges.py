@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import seq_reference as R
-from tests.test_gpu_sequence import BF16, F32, G, cu_of, rows  # noqa: F401  (G: the fixture)
+from tests.test_gpu_sequence import BF16, F32, G, NAMES, PACKED, cu_of, near32, rows  # noqa: F401  (G: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +169,62 @@ def test_packed_backward_bad_value_stays_in_its_sequence(G):  # noqa: F811
         got = G.packed_backward(*bad[:5], cu, bad[5])
         for a, b in zip(got[:5], want[:5]):
             assert torch.equal(a[:70], b[:70]) and torch.equal(a[200:], b[200:])
+
+
+# ------------------------------------------------------------------ every kernel that the dispatch chooses
+
+# 257 to 512 strips (the forward scan's pairs, the reverse scan's single strips) at every padded d_k; then key heads enough
+# for the gradients' preparation by key head (tokens / 64 + sequences times heads_k from 1024 on), at every padded d_k
+CHOSEN = [([1, 20, 66] * 8, 2, 4, 32, 48), ([3, 70, 129] * 3, 4, 8, 64, 64), ([70, 1, 64, 90] * 3, 2, 4, 112, 112),
+          ([65, 30] * 5, 4, 4, 128, 128),
+          ([1] * 1020 + [70, 2, 140], 1, 2, 16, 16), ([1] * 500 + [64, 0, 130] * 5, 2, 4, 64, 32),
+          ([1] * 340 + [70, 3], 3, 6, 112, 48), ([2, 0] * 129 + [65], 4, 16, 128, 16)]
+
+
+def near_grads(got, ref, q):
+    """near32's bound for each gradient but the gates'.  A gate's is the suffix sum over its chunk of q dq + k rows - k cols
+    per token, which cancel (one token without a state: to 0).  Its error is that of its terms, so it is counted against
+    their size: q dq's, |q dq| summed over d_k, at each place that near32's 64 half steps are for; three terms in place of
+    one, and a suffix of up to 64 tokens whose errors grow like the root: 3 sqrt 64 = 24; or, where the gradient is larger,
+    eight times against itself, as everywhere."""
+    for name, x, r in zip(NAMES, got, ref):
+        if x is None:
+            continue
+        try:
+            if name != "dlog_gate":
+                near32(x, r, x.dtype)
+            else:
+                terms = (R.f64(q) * ref[0]).abs().sum(-1).square().mean().sqrt()
+                d, own = (R.f64(x) - r).abs(), r.square().mean().sqrt()
+                bound = 64 * R.HALF[F32] * max(8 * own, 24 * terms)
+                assert d.square().mean().sqrt() <= bound and d.max() <= 10 * bound, (d.max().item(), bound.item())
+        except AssertionError as e:
+            raise AssertionError(f"{name}: {e}") from None
+
+
+@pytest.mark.parametrize("lengths,hk,hv,dk,dv", CHOSEN)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_packed_calls_of_every_chosen_kernel(G, lengths, hk, hv, dk, dv, dtype):  # noqa: F811
+    n, gen = sum(lengths), torch.Generator().manual_seed(91)
+    x, cu = rows(n, hk, hv, dk, dv, dtype, 90), cu_of(lengths)
+    S0, dS = (torch.randn(len(lengths), hv, dk, dv, generator=gen).cuda() for _ in range(2))
+    dout = torch.randn(n, hv, dv, generator=gen).to(dtype).cuda()
+    leaves = [R.f64(t) for t in x]
+    ro, rS = R.packed(*leaves, cu.tolist(), R.f64(S0))
+    for odt in (F32, BF16):
+        out, S = G.packed_forward(*x, cu, S0, out_dtype=odt)
+        near32(out, ro, odt)
+        near32(S, rS)
+    near_grads(G.packed_backward(*x, cu, dout, S0, dS),
+               R.packed_grads(*leaves, cu.tolist(), R.f64(S0), R.f64(dout), R.f64(dS)), x[0])
+
+
+@pytest.mark.parametrize("lengths,hk,hv,dk,dv,dtype,gate,with_state", PACKED)
+def test_packed_backward_to_the_last_term(G, lengths, hk, hv, dk, dv, dtype, gate, with_state):  # noqa: F811
+    """Each gradient but the gates' to near32's own bound, below what a lost third term of the operands would cost."""
+    n, gen = sum(lengths), torch.Generator().manual_seed(sum(lengths))
+    x, cu = rows(n, hk, hv, dk, dv, dtype, n + 7, gate), cu_of(lengths)
+    dout = torch.randn(n, hv, dv, generator=gen).to(dtype).cuda()
+    S0, dS = (torch.randn(len(lengths), hv, dk, dv, generator=gen).cuda() if with_state else None for _ in range(2))
+    ref = R.packed_grads(*(R.f64(t) for t in x), cu.tolist(), R.f64(S0), R.f64(dout), R.f64(dS))
+    near_grads(G.packed_backward(*x, cu, dout, S0, dS), ref, x[0])
