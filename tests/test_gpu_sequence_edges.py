@@ -228,3 +228,67 @@ def test_packed_backward_to_the_last_term(G, lengths, hk, hv, dk, dv, dtype, gat
     S0, dS = (torch.randn(len(lengths), hv, dk, dv, generator=gen).cuda() if with_state else None for _ in range(2))
     ref = R.packed_grads(*(R.f64(t) for t in x), cu.tolist(), R.f64(S0), R.f64(dout), R.f64(dS))
     near_grads(G.packed_backward(*x, cu, dout, S0, dS), ref, x[0])
+
+
+# ------------------------------------------------------------------ bad offsets, between guards
+
+GUARD = 1 << 16
+
+
+class Guarded:
+    """Tensors that lie between bytes of a pattern, and whether those are as they were."""
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, shape, dtype):
+        n = torch.Size(shape).numel() * torch.empty(0, dtype=dtype).element_size()
+        whole = torch.full((2 * GUARD + (n + 255) // 256 * 256,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.all.append((whole, n))
+        return whole[GUARD:GUARD + n].view(dtype).view(shape)
+
+    def intact(self):
+        return all((w[:GUARD] == 0xA5).all() and (w[GUARD + n:] == 0xA5).all() for w, n in self.all)
+
+
+def offset_lists(sequences, n):
+    gen = torch.Generator().manual_seed(sequences)
+    yield torch.randint(-n, 2 * n, (sequences + 1,), generator=gen)
+    yield torch.randint(0, n, (sequences + 1,), generator=gen).sort(descending=True)[0]
+    yield torch.randint(-2 ** 31, 2 ** 31, (sequences + 1,), generator=gen)
+    yield torch.full((sequences + 1,), 2 ** 31 - 1)
+    yield torch.tensor([0, n] * sequences)[:sequences + 1]
+
+
+@pytest.mark.parametrize("sequences,hk,hv,dk,dv", [(3, 1, 2, 16, 48), (40, 2, 4, 48, 64), (70, 2, 4, 112, 128)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_packed_calls_with_bad_offsets_write_nothing_else(G, sequences, hk, hv, dk, dv, dtype):  # noqa: F811
+    """Offsets out of order and out of range, forward (with a pool, slots and final states) and backward: every write lies in
+    its tensor, and a correct call afterwards gives what it gave before."""
+    from gated_delta_rule_frame_amd import sequence as Q
+    n, pool = 300, sequences + 2
+    x = rows(n, hk, hv, dk, dv, dtype, 95)
+    gen = torch.Generator().manual_seed(96)
+    S0 = torch.randn(pool, hv, dk, dv, generator=gen).cuda()
+    dout = torch.randn(n, hv, dv, generator=gen).to(dtype).cuda()
+    slots = torch.randint(-1, pool + 1, (sequences,), generator=gen).to(torch.int32).cuda()
+    good = cu_of([n // sequences] * sequences)
+    want = G.packed_forward(*x, good, S0[:sequences])
+    wantg = G.packed_backward(*x, good, dout, S0[:sequences], S0[:sequences])
+    need = [G.packed_workspace_size(x[0], x[2], sequences, gradient=g) for g in (False, True)]
+    for cu in offset_lists(sequences, n):
+        cu, keep = cu.to(torch.int32).cuda(), Guarded()
+        G.packed_forward(*x, cu, S0, slots=slots, out=keep((n, hv, dv), F32), final_state=keep(S0.shape, F32),
+                         workspace=keep((need[0],), torch.uint8))
+        p, _, _, _, _, _ = Q._problem(*x, F32)
+        p.sequences = sequences
+        grads = [keep(t.shape, t.dtype) for t in x]
+        dS0, ws = keep((sequences, hv, dk, dv), F32), keep((need[1],), torch.uint8)
+        assert G.lib().gdn_packed_backward(p, *(t.data_ptr() for t in (*x, cu, S0, dout, S0, *grads, dS0, ws)), need[1],
+                                           torch.cuda.current_stream().cuda_stream) == G.OK
+        torch.cuda.synchronize()
+        assert keep.intact()
+    again, againg = G.packed_forward(*x, good, S0[:sequences]), G.packed_backward(*x, good, dout, S0[:sequences], S0[:sequences])
+    filled = good[-1].item()
+    assert torch.equal(again[0][:filled], want[0][:filled]) and torch.equal(again[1], want[1])
+    assert all(torch.equal(a[:filled], b[:filled]) for a, b in zip(againg[:5], wantg)) and torch.equal(againg[5], wantg[5])

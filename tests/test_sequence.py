@@ -3,6 +3,7 @@ calls without work, through the C ABI with pointers that are never used (no
 GPU needed), and the binding's refusals."""
 import ctypes
 import os
+import random
 import subprocess
 import sys
 
@@ -198,3 +199,51 @@ def test_binding_refuses_sizes_beyond_the_abis_fields():
             G.packed_backward(q, q, v, g, g, i(big), v)
         with pytest.raises(ValueError, match="2.31"):
             G.packed_workspace_size(q, v, big)
+
+
+def bounds(cu, s, tokens):
+    """seq_bounds of gdn_packed.h."""
+    a = min(max(cu[s], 0), tokens)
+    return a, min(max(cu[s + 1], a), tokens)
+
+
+def chunk_of(cu, sequences, tokens, slot):
+    """find_chunk of gdn_packed.h: (sequence, first row, rows), or None."""
+    lo, hi = 0, sequences - 1
+    while lo < hi:
+        mid = (lo + hi + 1) // 2
+        if min(max(cu[mid], 0), tokens) // 64 + mid <= slot:
+            lo = mid
+        else:
+            hi = mid - 1
+    a, b = bounds(cu, lo, tokens)
+    c = slot - (a // 64 + lo)
+    return None if c < 0 or c * 64 >= b - a else (lo, a + c * 64, min(64, b - a - c * 64))
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_offsets_of_any_value_index_within_rows_and_workspace(seed):
+    """The kernels' index arithmetic on offsets of any value: rows within the packed ones, chunk slots within the workspace's;
+    on offsets in order every chunk has a slot of its own, and it is the one found from there."""
+    r = random.Random(seed)
+    tokens, sequences = r.choice([0, 1, 63, 64, 65, 1000]), r.choice([1, 2, 5, 64, 65, 200])
+    for kind in range(4):
+        cu = [r.choice([r.randint(-5, tokens + 5), r.randint(0, tokens), r.choice([-2 ** 31, 2 ** 31 - 1, -1, 0])])
+              if kind else r.randint(0, tokens) for _ in range(sequences + 1)]
+        if kind < 2:
+            cu.sort()
+        slots, seen = tokens // 64 + sequences, {}
+        for s in range(sequences):
+            a, b = bounds(cu, s, tokens)
+            assert 0 <= a <= b <= tokens
+            for c in range((b - a + 63) // 64):
+                assert 0 <= a // 64 + s + c < slots
+                if kind < 2:
+                    assert (a // 64 + s + c) not in seen
+                    seen[a // 64 + s + c] = (s, a + 64 * c, min(64, b - a - 64 * c))
+        for slot in range(slots):
+            found = chunk_of(cu, sequences, tokens, slot)
+            if found:
+                assert 0 <= found[0] < sequences and 0 <= found[1] and 0 < found[2] <= 64 and found[1] + found[2] <= tokens
+            if kind < 2:
+                assert found == seen.get(slot)
