@@ -372,8 +372,14 @@ gdn_status gdn_decode(const gdn_seq_problem* problem,
  * token of the sequence may be NaN, other sequences are as without it. */
 
 /* Bytes of device workspace of gdn_packed_forward (gradient = 0) or
- * gdn_packed_backward (1).  Forward: about 50 KB for each 64 tokens and value
- * head; gradients: about 270 KB at d_k = d_v = 128. */
+ * gdn_packed_backward (1): (tokens / 64 + sequences) times
+ *   forward    heads_v 49920 + heads_k 128 t D
+ *   gradients  heads_v (75008 + 512 d_v + 8 D d_v) + heads_k 256 t D
+ * with D = d_k padded to 32, 64 or 128 and t = 1 (bf16) or 3 (fp32).  At d_k =
+ * d_v = 128, bf16 and as many key as value heads that is 66 KB and 304 KB for
+ * each 64 tokens and head, and the same again for each sequence: many short
+ * ones (1000 of one token, 16 heads: 1.1 and 4.9 GB) take most of it.  A batch
+ * is split at sequence bounds into several calls where that is too much. */
 gdn_status gdn_packed_workspace_size(const gdn_seq_problem* problem, int32_t gradient, size_t* bytes_out);
 
 /* out and the state after each sequence's last token.

@@ -247,3 +247,13 @@ def test_offsets_of_any_value_index_within_rows_and_workspace(seed):
                 assert 0 <= found[0] < sequences and 0 <= found[1] and 0 < found[2] <= 64 and found[1] + found[2] <= tokens
             if kind < 2:
                 assert found == seen.get(slot)
+
+
+@pytest.mark.parametrize("dtype,t", [(G.BF16, 1), (G.F32, 3)])
+def test_packed_workspace_is_what_the_header_says(dtype, t):
+    n = ctypes.c_size_t()
+    for tokens, sequences, hk, hv, dk, dv in ((1000, 1000, 16, 16, 128, 128), (64, 1, 1, 4, 16, 48), (63, 2, 2, 2, 48, 16), (0, 3, 1, 1, 80, 80)):
+        p = seq(tokens=tokens, sequences=sequences, heads_k=hk, heads_v=hv, d_k=dk, d_v=dv, qkv_dtype=dtype)
+        slots, D = tokens // 64 + sequences, 32 if dk <= 32 else 64 if dk <= 64 else 128
+        for gradient, size in ((0, hv * 49920 + hk * 128 * t * D), (1, hv * (75008 + 512 * dv + 8 * D * dv) + hk * 256 * t * D)):
+            assert G.lib().gdn_packed_workspace_size(p, gradient, ctypes.byref(n)) == G.OK and n.value == slots * size
