@@ -4,7 +4,10 @@
 wrap ``gdn_packed_forward`` and its gradients; ``group_norm`` and ``group_norm_backward``
 wrap ``gdn_group_norm`` and its gradients.  As in the rest of the package the functions
 check and marshal their arguments and launch the HIP kernels on the current
-stream of the tensors' device; there is no CPU fallback.
+stream of the tensors' device; there is no CPU fallback, and results carry no
+autograd graph, whether the inputs require gradients or not: a training step
+calls ``packed_backward`` and ``group_norm_backward`` itself (a
+``torch.autograd.Function`` around a pair of calls, for instance).
 """
 from __future__ import annotations
 
@@ -146,7 +149,8 @@ def packed_forward(q, k, v, log_gate, beta, cu_seqlens, initial_state=None, *, s
     ``slots`` ([sequences] int32) pools of which each sequence uses one row; the
     final state of a call with ``slots`` goes into ``final_state``, by default
     into initial_state, in place.  The output is fp32 unless ``out_dtype`` or
-    ``out`` says otherwise.  A NaN or infinity in a token's row can make outputs
+    ``out`` says otherwise; it carries no autograd graph (``packed_backward``
+    gives the gradients).  A NaN or infinity in a token's row can make outputs
     of up to 63 earlier tokens of its sequence NaN (those in its chunk of 64).
     """
     odt = _output(out, out_dtype)
@@ -281,7 +285,8 @@ def group_norm(x, groups, weight=None, bias=None, gate=None, *, activation="none
     is "none", "silu", "gelu" or "relu".  ``center=False`` normalises by the
     root mean square; its mean is None.  ``[tokens, heads * d_v]`` with the
     heads as groups is the norm of each token's heads.  mean and rstd
-    ([batch, groups] fp32) are what ``group_norm_backward`` needs.
+    ([batch, groups] fp32) are what ``group_norm_backward`` needs; nothing
+    returned carries an autograd graph.
     """
     p = _norm_problem(x, groups, weight, bias, gate, activation, center, eps)
     if out is None:
