@@ -66,14 +66,6 @@ __device__ __forceinline__ void mma_by_term(const Frag<NA>& a, const Frag<NB>& b
       if (s - i >= 0 && s - i < NB) c[s] = mfma(a.t[i], b.t[s - i], c[s]);
 }
 
-template <int N, int M>
-__device__ __forceinline__ Frag<N> first_terms(const Frag<M>& f) {
-  Frag<N> o;
-#pragma unroll
-  for (int i = 0; i < N; ++i) o.t[i] = f.t[i];
-  return o;
-}
-
 // Two values as the sums of N bf16 values each, largest first, packed by term:
 // one conversion, two unpackings and two subtractions for a term of a pair.
 template <int N>
@@ -203,8 +195,8 @@ __device__ __forceinline__ void store_at(buf_t b, uint32_t off, float x) {
   else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), b, off, 0, 0);
 }
 
-// The first N of LD terms of a fragment whose lane has its place at `off`.
-template <int N, int LD = N>
+// A fragment of N terms whose lane has its place at `off`.
+template <int N>
 __device__ __forceinline__ Frag<N> frag_at(buf_t b, uint32_t off) {
   Frag<N> f;
 #pragma unroll
@@ -225,12 +217,12 @@ __device__ __forceinline__ Frag<NT> frag_of(const RawFrag<NT>& r) {
   }
 }
 
-// The first N of a stored fragment's LD terms.
-template <int N, int LD = N>
+// A stored fragment of N terms.
+template <int N>
 __device__ __forceinline__ Frag<N> load_frag(const uint4* p, int frag, int lane) {
   Frag<N> f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) f.t[i] = as_frag(p[((size_t)frag * LD + i) * 64 + lane]);
+  for (int i = 0; i < N; ++i) f.t[i] = as_frag(p[((size_t)frag * N + i) * 64 + lane]);
   return f;
 }
 

@@ -20,16 +20,15 @@ constexpr int kLd = 68;     // row stride (floats) of a 64 x 64 fp32 tile in LDS
 // Gates below this are this: e^-10000 is 0 in fp32, and G stays finite for -inf.
 constexpr float kLowestGate = -10000.f;
 
-// Four accumulator values of rows (k) row0 .. row0 + 3 of a column, as N terms
+// Four accumulator values of rows (k) row0 .. row0 + 3 of a column, as three terms
 // into stored fragments [column tile][row half]: the same places as in an LDS tile.
-template <int N, int LD>
 __device__ __forceinline__ void store_quad(uint4* frags, int tile, int column, int row, const float (&x)[4]) {
-  uint32_t lo[N], hi[N];
-  split2<N>(x[0], x[1], lo);
-  split2<N>(x[2], x[3], hi);
-  bh* to = reinterpret_cast<bh*>(frags + (size_t)(tile * 2 + row / 32) * LD * 64) + put_place(column, row % 32);
+  uint32_t lo[3], hi[3];
+  split2<3>(x[0], x[1], lo);
+  split2<3>(x[2], x[3], hi);
+  bh* to = reinterpret_cast<bh*>(frags + (size_t)(tile * 2 + row / 32) * 3 * 64) + put_place(column, row % 32);
 #pragma unroll
-  for (int i = 0; i < N; ++i) *reinterpret_cast<uint2*>(to + i * 512) = make_uint2(lo[i], hi[i]);
+  for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(to + i * 512) = make_uint2(lo[i], hi[i]);
 }
 
 // One workgroup per cell; wavefront w has rows (tokens) 16 w .. of the 64 x 64
@@ -159,8 +158,8 @@ __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_ker
                 x[r] = pi >= pj ? exp2_of((float)(Gs[pi] - Gs[pj])) * qk[j][r] : 0.f;
               }
             }
-            if constexpr (GRAD) store_quad<3, 3>(pp, j, lr, 16 * w + 4 * lg, x);          // P^T: row tile j, rows i
-            else store_quad<3, 3>(pp, w, lr, 16 * j + 4 * lg, x);                         // P: row tile w, columns j
+            if constexpr (GRAD) store_quad(pp, j, lr, 16 * w + 4 * lg, x);                // P^T: row tile j, rows i
+            else store_quad(pp, w, lr, 16 * j + 4 * lg, x);                               // P: row tile w, columns j
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -170,8 +169,8 @@ __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_ker
             // the fragments on the diagonal's block row hold a block above it
             const float z[4] = {0.f, 0.f, 0.f, 0.f};
             if (j / 2 == w / 2) {
-              if constexpr (GRAD) store_quad<3, 3>(pp, j, lr, 16 * w + 4 * lg, z);
-              else store_quad<3, 3>(pp, w, lr, 16 * j + 4 * lg, z);
+              if constexpr (GRAD) store_quad(pp, j, lr, 16 * w + 4 * lg, z);
+              else store_quad(pp, w, lr, 16 * j + 4 * lg, z);
             }
           }
         }
@@ -529,7 +528,7 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
         if constexpr (PT > 0) {
           const buf_t pb = buf(ws.p + ((slot + c) * p.hv + h) * tri, c <= last ? (uint32_t)tri * 16 : 0);
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) pf[set][ks] = frag_at<PT, 3>(pb, tri_off[ks]);
+          for (int ks = 0; ks < 2; ++ks) pf[set][ks] = frag_at<PT>(pb, tri_off[ks]);
         }
       };
       // a chunk's V goes into LDS a step ahead, as columns of four rows for the first half
@@ -625,7 +624,7 @@ __global__ __launch_bounds__(256, 2) void packed_scan_pairs_kernel(SeqProblem p,
   constexpr int PT = OB ? 3 : 0;                      // terms of the output products
   constexpr int NT = 1, NS = 2, KS = DKP / 32, MT = DKP >= 64 ? DKP / 64 : 1;
   constexpr int SP = 16 * DKP, TP = 16 * kC;          // elements of a term's tile
-  constexpr uint32_t es = NT == 1 ? 2 : 4;            // bytes of an input element
+  constexpr uint32_t es = 2;                          // bytes of an input element
   constexpr uint32_t os = OB;                         // of an output element
   __shared__ __align__(16) bh Sl[NS][3 * SP];
   __shared__ __align__(16) bh Nl[NS][3 * TP];
@@ -735,7 +734,7 @@ __global__ __launch_bounds__(256, 2) void packed_scan_pairs_kernel(SeqProblem p,
       if constexpr (PT > 0) {
         const buf_t pb = buf(ws.p + ((slot + c) * p.hv + h) * tri, c <= last ? (uint32_t)tri * 16 : 0);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) pf[ks] = frag_at<PT, 3>(pb, tri_off[ks]);
+        for (int ks = 0; ks < 2; ++ks) pf[ks] = frag_at<PT>(pb, tri_off[ks]);
       }
     };
     load_rows(0);
@@ -758,7 +757,7 @@ __global__ __launch_bounds__(256, 2) void packed_scan_pairs_kernel(SeqProblem p,
           for (int ks = 0; ks < KS; ++ks) {
             const Frag<3> sf = get<3, DKP>(Sl[i] + lane * 8, ks);
             mma_by_term<NT, 3>(frag_of<NT>(k[ks]), sf, a);
-            if constexpr (PT > 0) o[i] = mma<NT, PT>(frag_of<NT>(q[ks]), first_terms<PT>(sf), o[i]);
+            if constexpr (PT > 0) o[i] = mma<NT, PT>(frag_of<NT>(q[ks]), sf, o[i]);
           }
           float x[4];
 #pragma unroll
