@@ -292,3 +292,42 @@ def test_packed_calls_with_bad_offsets_write_nothing_else(G, sequences, hk, hv, 
     filled = good[-1].item()
     assert torch.equal(again[0][:filled], want[0][:filled]) and torch.equal(again[1], want[1])
     assert all(torch.equal(a[:filled], b[:filled]) for a, b in zip(againg[:5], wantg)) and torch.equal(againg[5], wantg[5])
+
+
+# ------------------------------------------------------------------ the most sequences
+
+@pytest.mark.parametrize("dtype,dv", [(BF16, 128), (F32, 128)])
+def test_packed_forward_of_the_most_sequences(G, dtype, dv):  # noqa: F811
+    """sequences * heads_v = 2^20 (65 to 76 GB of workspace): one token each, o = (q.k) beta v."""
+    n, h, dk = 32768, 32, 16
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(dtype)  # noqa: E731
+    q, k, v, beta = r(n, h, dk), r(n, h, dk), r(n, h, dv), torch.rand(n, h, generator=gen, device="cuda")
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    out, _ = G.packed_forward(q, k, v, -beta, beta, cu, want_state=False)
+    qk = (q.double() * k.double()).sum(-1) * beta.double()
+    size = (q.double() * k.double()).abs().sum(-1) * beta.double()
+    err = (out.double() - qk[..., None] * v.double()).abs()
+    # a product of d_k terms, its gate and beta, each rounded once or twice, on operands split to 24 bits
+    assert (err <= (dk + 8) * 2.0 ** -24 * size[..., None] * v.double().abs() + 1e-30).all()
+    del out, err
+    with pytest.raises(G.GdnError):
+        G.packed_forward(q, k, v, -beta, beta, torch.arange(n + 2, dtype=torch.int32, device="cuda"), want_state=False)
+
+
+def test_packed_backward_of_the_most_sequences(G):  # noqa: F811
+    """The same backward (91 GB): dq = beta (v.do) k, dk = beta (v.do) q, dv = beta (q.k) do, dbeta = (q.k) (v.do)."""
+    n, h, d = 32768, 32, 16
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    q, k, v, do = (torch.randn(n, h, d, generator=gen, device="cuda") for _ in range(4))
+    beta = torch.rand(n, h, generator=gen, device="cuda")
+    got = G.packed_backward(q, k, v, -beta, beta, torch.arange(n + 1, dtype=torch.int32, device="cuda"), do)
+    dot = lambda a, b: (a.double() * b.double()).sum(-1)  # noqa: E731
+    size = lambda a, b: (a.double() * b.double()).abs().sum(-1)  # noqa: E731
+    b, eps = beta.double(), 2 * (d + 8) * 2.0 ** -24
+    for x, want, scale in ((got[0], (b * dot(v, do))[..., None] * k.double(), (b * size(v, do))[..., None] * k.double().abs()),
+                           (got[1], (b * dot(v, do))[..., None] * q.double(), (b * size(v, do))[..., None] * q.double().abs()),
+                           (got[2], (b * dot(q, k))[..., None] * do.double(), (b * size(q, k))[..., None] * do.double().abs()),
+                           (got[4], dot(q, k) * dot(v, do), size(q, k) * size(v, do)),
+                           (got[3], torch.zeros_like(b), 4 * b * size(q, k) * size(v, do))):
+        assert ((x.double() - want).abs() <= eps * scale + 1e-30).all()
