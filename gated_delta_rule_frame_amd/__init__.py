@@ -100,6 +100,12 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"libgdn.so is not built ({LIB_PATH}); run "
                               "`python -m gated_delta_rule_frame_amd.build`")
+        # torch brings a HIP runtime of its own.  Loaded first, it serves the library too; two runtimes in
+        # one process see no device.  Without torch the host-only calls run on the system's.
+        try:
+            import torch  # noqa: F401
+        except ImportError:
+            pass
         L = ctypes.CDLL(LIB_PATH)
         vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
         P = ctypes.POINTER(Problem)

@@ -257,3 +257,14 @@ def test_packed_workspace_is_what_the_header_says(dtype, t):
         slots, D = tokens // 64 + sequences, 32 if dk <= 32 else 64 if dk <= 64 else 128
         for gradient, size in ((0, hv * 49920 + hk * 128 * t * D), (1, hv * (75008 + 512 * dv + 8 * D * dv) + hk * 256 * t * D)):
             assert G.lib().gdn_packed_workspace_size(p, gradient, ctypes.byref(n)) == G.OK and n.value == slots * size
+
+
+def test_library_loaded_before_torch_shares_its_hip_runtime():
+    """One HIP runtime in the process, whichever is loaded first: a second one sees no device."""
+    code = ("import gated_delta_rule_frame_amd as G\n"
+            "G.lib()\n"
+            "import torch\n"
+            "paths = {l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}\n"
+            "assert len(paths) == 1, paths\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=os.path.dirname(os.path.dirname(__file__)))
+    assert r.returncode == 0, r.stderr
