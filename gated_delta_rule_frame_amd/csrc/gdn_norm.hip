@@ -1038,7 +1038,8 @@ int vec_of(const NormProblem& p) {
 }
 
 // Lanes of a group on the S = 1 way and vectors per lane (0: the group is too
-// wide for the registers of one workgroup).  A wavefront has a group alone,
+// wide for the registers of one workgroup; the gradient of 8 bf16 vectors a lane spills
+// 26 of them, with a gate 105).  A wavefront has a group alone,
 // without an exchange through LDS, up to 16 values a lane (32 take the
 // gradient kernel's registers to one wavefront a SIMD: 16384 rows of one group
 // of 2048 bf16 278 us against 76 by a workgroup).

@@ -286,8 +286,9 @@ __device__ __forceinline__ void strip_of(int block, int strips, int* sh, int* st
 // The r-th sequence by length, longest first, in each wavefront for itself.  A
 // scan's workgroup lasts as long as its sequence, and where there are several
 // rounds of workgroups a long one that starts last leaves the card idle
-// (13 prompts of 35 to 1881 tokens, 32 heads of 128: scan 272 us in the order
-// given, 264 so; 6 training sequences of 762 to 2716: reverse scan 318 and 252).
+// (13 prompts of 35 to 1881 tokens, 32 heads of 128: scan 270 us in the order
+// given, 232 so; 6 training sequences of 762 to 2716: forward scan 241 and 193,
+// reverse scan 322 and 259).
 // More than 64 sequences even out by themselves and keep their order.
 __device__ __forceinline__ int by_length(const int* cu, int sequences, long long tokens, int r) {
   if (sequences == 1 || sequences > 64) return r;

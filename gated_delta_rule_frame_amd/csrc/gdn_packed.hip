@@ -34,8 +34,10 @@ __device__ __forceinline__ void store_quad(uint4* frags, int tile, int column, i
 // One workgroup per cell; wavefront w has rows (tokens) 16 w .. of the 64 x 64
 // matrices.  Accumulators hold four rows of a column, which is half a vector of
 // the transposed matrix's fragment; so the products are taken in the order that
-// makes each result leave its registers as it is stored.  What it writes
-// bounds it: 32768 tokens of 35 heads of 64 272 us, some 60 KB a cell, 4 TB/s.
+// makes each result leave its registers as it is stored.  What it reads and
+// writes bounds it: 32768 tokens of 35 heads of 64 274 us, some 67 KB a cell, 4.4
+// TB/s.  Of the 128 registers that four workgroups a CU leave a lane, d_k above
+// 64 spills 10.
 template <int NT, int DKP, bool GRAD>
 __global__ __launch_bounds__(256, NT == 1 && !GRAD ? 4 : 2) void packed_prep_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, long long slots, int heads) {
   constexpr int NM = GRAD ? 2 : 1, KS = DKP / 32;
@@ -293,9 +295,10 @@ __device__ __forceinline__ int next_of_slot(const int* slots, int sequences, int
 // 16 w .. of the chunk) run the first two phases; 4 - 7 have the output's
 // products, which fill the waits, and (all eight at d_k > 64) the rows of the
 // state.  Loads are issued SETS steps ahead, into registers that have just been
-// used.  One sequence of 32768 tokens, 35 heads of 64: 512 steps in 801 us, 1.56 us
-// a step, on 140 CUs (4009 us with four wavefronts, row-major LDS tiles and loads
-// of the step's own operands).
+// used.  One sequence of 32768 tokens, 35 heads of 64: 512 steps in 848 us, 1.66 us
+// a step, on 140 CUs (some 4000 with four wavefronts, row-major LDS tiles and loads
+// of the step's own operands).  fp32 at d_k above 64 spills 21 or 22 registers with
+// one strip (256 strips of 16 chunks 71 us against 42 of bf16).
 //
 // OB: bytes of an output element (2: bf16, 4: fp32), or 0: no outputs, but e and
 // the state before each chunk are left in the workspace for the gradients.  The
@@ -305,11 +308,11 @@ __device__ __forceinline__ int next_of_slot(const int* slots, int sequences, int
 // are the neighbour of what the fp32 result rounds to.
 //
 // NS: strips of 16 columns of a workgroup.  One where every strip can have a CU
-// to itself (d_k = d_v = 128, bf16, 16 chunks, 256 strips: 37 us against 46 in
-// pairs): only the step's own length counts, loads run two steps ahead.  Two
+// to itself (256 strips of 16 chunks, bf16: 42 us against 55 in pairs at d_k = d_v
+// = 128, 31 against 37 at 64, 29 against 36 at 32): only the step's own length counts, loads run two steps ahead.  Two
 // where there are more: the operands come through a CU's L1 once for both, which is
 // what bounds a full CU, and a step's waits have twice the products to fill them;
-// loads run one step ahead (384 strips 47 us against 69).
+// loads run one step ahead (384 strips 54 us against 73, 38 against 55, 39 against 53).
 template <int NT, int DKP, int OB, int NS>
 __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
   constexpr int PT = OB ? 3 : 0;                      // terms of the output products
@@ -615,10 +618,14 @@ __global__ __launch_bounds__(512, 2) void packed_scan_kernel(SeqProblem p, Packe
 // is the work of all CUs, not the length of a step, and four wavefronts that each
 // do every part of it, for two strips, leave two workgroups on a CU to fill each
 // other's waits.  K and Q share the state's operand reads, a lane's rows of V
-// need no staging.  13 prompts of 8191 tokens, 32 heads of 128: 200 us against
-// 264 by the eight wavefronts above in pairs; 2048 equal strips of 16 chunks 184
-// against 208, but 512 of them 59 against 48.  fp32 operands take the registers
-// of both workgroups (2048 strips 398 against 372), so they stay with those.
+// need no staging.  13 prompts of 8191 tokens, 32 heads of 128: 202 us against
+// 258 by the eight wavefronts above in pairs; equal strips of 16 chunks at d_k =
+// d_v = 128, 64, 32: 768 of them 89, 67, 96 against 103, 73, 102; 2048 196, 203, 253
+// against 235, 204, 247; but 512 of them 61, 48, 50 against 55, 40, 49.  The rule
+// counts strips, since the lengths are on the GPU: one long prompt among many short
+// ones runs its chain with this kernel's longer step.  fp32 operands take the
+// registers of both workgroups (2048 strips 398 against 372), so they stay with
+// the kernel above.
 template <int DKP, int OB>
 __global__ __launch_bounds__(256, 2) void packed_scan_pairs_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
   constexpr int PT = OB ? 3 : 0;                      // terms of the output products

@@ -45,10 +45,10 @@ struct GradIn {
 
 // NS: strips of 16 columns of a workgroup.  One where all of them are resident at
 // once, two to a CU; two where there are more: operands are fetched once for both
-// (d_k = d_v = 128, bf16, 16 chunks: 2048 strips 245 us against 353; 512 strips
-// of equal lengths 71 against 87, but 420 of three unequal sequences 32 against
-// 27, since the longest sequence's steps are what lasts).  Eight wavefronts in two
-// roles as in the forward scan gave 305 and 79.
+// (16 chunks, bf16: 2048 strips 250 us against 357 at d_k = d_v = 128, 225 against 285
+// at 64, 257 against 286 at 32; 512 strips of equal lengths 71 against 86, but 420
+// of three unequal sequences 32 against 27, since the longest sequence's steps are
+// what lasts).  Eight wavefronts in two roles as in the forward scan gave 305 and 79.
 template <int NT, int DKP, int NS>
 __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void packed_scan_grad_kernel(SeqProblem p, PackedTensors t, PackedSpace ws) {
   using In = GradIn<NT, DKP, NS>;
@@ -298,12 +298,13 @@ __device__ __forceinline__ float wave_sum(float x) {
 // ahead.  Wavefronts w and w + 4 have row tile w and each half of the columns of
 // d_k; the first four also have the 64 x 64 product D, the second M.
 //
-// Measured (8192 tokens, 16 key and 32 value heads of 128, bf16): 513 us, 31 us a
+// Measured (8192 tokens, 16 key and 32 value heads of 128, bf16): 503 us, 31 us a
 // chunk and value head on each CU, of which its 270 KB take 14 at the rate of a
 // large copy and the MFMAs 7: one workgroup has a CU's registers and LDS, so its
-// phases follow one another.  Sixteen wavefronts of 128 registers: 584 us; four
-// of 512: 738; eight that stay and fetch the next chunk's first operands ahead:
-// 590 (their registers spill).
+// phases follow one another.  It spills 38 registers itself (14 at fp32 and d_k =
+// 64, 141 above), which make most of the 249 MB that it writes; its outputs are 70.
+// Sixteen wavefronts of 128 registers: 584 us; four of 512: 738 (105 spilled);
+// eight that stay and fetch the next chunk's first operands ahead: 590 (81).
 template <int NT, int DKP>
 __global__ __launch_bounds__(512, 2) void packed_grads_kernel(SeqProblem p, PackedTensors t, PackedSpace ws, long long slots) {
   constexpr int NTI = DKP / 16, HT = NTI / 2;        // column tiles of d_k, and of a wavefront
