@@ -222,6 +222,8 @@ def packed_backward(q, k, v, log_gate, beta, cu_seqlens, dout, initial_state=Non
 
 def packed_workspace_size(q, v, sequences, *, gradient=False):
     """Bytes of workspace of ``packed_forward`` (or ``packed_backward``) for inputs like q and v."""
+    if q.dtype not in _CODE:
+        raise TypeError(f"unsupported dtype {q.dtype}")
     p = SeqProblem(ABI_VERSION, q.shape[1], v.shape[1], q.shape[2], v.shape[2], _CODE[q.dtype], F32, 0, q.shape[0])
     p.sequences = _fits("sequences", sequences)
     return _need("gdn_packed_workspace_size", SeqProblem, bytes(p), int(gradient))

@@ -434,7 +434,8 @@ gdn_status gdn_packed_backward(const gdn_seq_problem* problem,
  * have x's type and shape; mean and rstd [batch, groups] fp32.  All
  * statistics and sums are fp32, with no atomics.  RELU has slope 0 at 0; GELU
  * is u (1 + erf(u / sqrt 2)) / 2.  SILU, GELU and RELU and their slopes are 0 at
- * -inf (a masked gate lets nothing through), inf and 1 at +inf. */
+ * -inf (a masked gate lets nothing through), inf and 1 at +inf.  Pointers are
+ * 16-byte aligned, those of weight, bias, mean and rstd too. */
 enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU = 2, GDN_ACT_RELU = 3 };
 typedef struct gdn_norm_problem {
   int32_t abi_version;        /* must equal GDN_ABI_VERSION */

@@ -268,3 +268,10 @@ def test_library_loaded_before_torch_shares_its_hip_runtime():
             "assert len(paths) == 1, paths\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=os.path.dirname(os.path.dirname(__file__)))
     assert r.returncode == 0, r.stderr
+
+
+def test_packed_workspace_size_refuses_other_types():
+    x = torch.zeros(4, 2, 16)
+    assert G.packed_workspace_size(x, x, 3) == 3 * (2 * 49920 + 2 * 128 * 3 * 32)
+    with pytest.raises(TypeError):
+        G.packed_workspace_size(x.half(), x.half(), 3)
