@@ -331,3 +331,54 @@ def test_packed_backward_of_the_most_sequences(G):  # noqa: F811
                            (got[4], dot(q, k) * dot(v, do), size(q, k) * size(v, do)),
                            (got[3], torch.zeros_like(b), 4 * b * size(q, k) * size(v, do))):
         assert ((x.double() - want).abs() <= eps * scale + 1e-30).all()
+
+
+# ------------------------------------------------------------------ graphs whose inputs change
+
+def test_captured_calls_follow_new_lengths_slots_and_values(G):  # noqa: F811
+    """A graph of a prefill into a pool, a decoding step, their norm and the packed gradients, replayed on other offsets,
+    slots (padding and repeated ones among them) and values than it was captured with, two graphs on one workspace."""
+    n, hk, hv, d, pool, batch = 300, 2, 4, 64, 9, 6
+    gen = torch.Generator().manual_seed(5)
+    fresh = lambda seed: (rows(n, hk, hv, d, d, BF16, seed), rows(batch, hk, hv, d, d, BF16, seed + 1))  # noqa: E731
+    (x, y), z = fresh(1), torch.randn(batch, hv * d, generator=gen).to(BF16).cuda()
+    dout = torch.randn(n, hv, d, generator=gen).to(BF16).cuda()
+    cu, slots = cu_of([100, 0, 64, 136]), torch.tensor([3, 1, 0, 5], dtype=torch.int32, device="cuda")
+    rows_of = torch.arange(batch, dtype=torch.int32, device="cuda")
+    state, first = torch.randn(pool, hv, d, d, generator=gen).cuda(), torch.empty(pool, hv, d, d, device="cuda")
+    size = max(G.packed_workspace_size(x[0], x[2], 4, gradient=True), G.packed_workspace_size(x[0], x[2], 4))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def serve(workspace):
+        out, _ = G.packed_forward(*x, cu, state, slots=slots, out=torch.zeros(n, hv, d, device="cuda"), workspace=workspace)
+        one = G.decode(*y, state, rows_of, out=torch.zeros(batch, hv, d, device="cuda", dtype=BF16))
+        return (out, one, *G.group_norm(one.view(batch, hv * d), hv, None, None, z, activation="silu", center=False)[::2])
+
+    def train(workspace):
+        grads = [torch.zeros_like(t) for t in x]
+        return G.packed_backward(*x, cu, dout, grads=grads, workspace=workspace)[:5]
+
+    first.copy_(state)
+    graphs = []
+    for f in (serve, train):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = f(ws)
+        graphs.append((graph, got))
+    plans = [([100, 0, 64, 136], [3, 1, 0, 5], [0, 1, 2, 3, 4, 5]), ([1, 2, 3, 200], [8, 8, -1, 2], [4, -1, 9, 4, 8, 0]),
+             ([0, 300, 0, 0], [0, 6, 6, 6], [6] * 6), ([0, 0, 0, 0], [1, 2, 3, 4], [-1] * 6), ([64, 64, 64, 64], [1, 2, 3, 4], [7, 7, 1, 1, 0, 2])]
+    for i, (lengths, at, rows_at) in enumerate(plans):
+        new = fresh(10 + 2 * i)
+        for a, b in zip((*x, *y), (*new[0], *new[1])):
+            a.copy_(b)
+        cu.copy_(cu_of(lengths)), slots.copy_(torch.tensor(at)), rows_of.copy_(torch.tensor(rows_at))
+        state.copy_(first)
+        for graph, _ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        after = state.clone()
+        state.copy_(first)
+        want = (*serve(None), *train(None))
+        for a, b in zip((*graphs[0][1], *graphs[1][1]), want):
+            assert torch.equal(a, b)
+        assert torch.equal(after, state)
