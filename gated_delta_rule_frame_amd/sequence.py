@@ -80,7 +80,7 @@ def _problem(q, k, v, log_gate, beta, out_dtype):
     if q.dtype not in _CODE or out_dtype not in _CODE:
         raise TypeError(f"unsupported dtype {q.dtype} or {out_dtype}")
     device, (n, hk, dk), (hv, dv) = q.device, q.shape, v.shape[1:]
-    if max(hk, hv, dk, dv) > _MAX:
+    if (hk | hv | dk | dv) > _MAX:
         raise ValueError(f"heads and widths must be below 2^31 (got {hk}, {hv}, {dk}, {dv})")
     p = SeqProblem(ABI_VERSION, hk, hv, dk, dv, _CODE[q.dtype], _CODE[out_dtype], 0, n)
     p.q_stride = _rows("q", q, q.shape, q.dtype, device)
