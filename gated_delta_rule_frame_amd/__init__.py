@@ -6,7 +6,10 @@ stream.  The names mirror the C ABI in ``include/gdn.h``: ``forward`` wraps
 ``gdn_forward``, ``step`` wraps ``gdn_step``, ``workspace_size`` wraps
 ``gdn_workspace_size``.  The calls on sequences of tokens (``decode``,
 ``packed_forward``, ``packed_backward``) and the norm (``group_norm``,
-``group_norm_backward``) are in ``sequence``.
+``group_norm_backward``) are in ``sequence``, linear attention with a decay
+(``linear_decode``) is in ``linear``,
+rotary positions (``rotary``, ``rotary_backward``, ``rotary_frequencies``) in
+``positions``.
 
 There is no CPU fallback: if the library is not built, or a call is made with
 tensors that are not on a GPU, these functions raise.
@@ -21,6 +24,8 @@ import os
 
 __all__ = ["forward", "step", "step_noalloc", "workspace_size", "NOALLOC_SCRATCH_BYTES", "make_problem", "lib", "GdnError", "Tuning", "tuning",
            "decode", "packed_forward", "packed_backward", "packed_workspace_size", "group_norm", "group_norm_backward",
+           "linear_decode",
+           "rotary", "rotary_backward", "rotary_frequencies",
            "segment_plan", "profile_enable", "profile_reset", "profile_read",
            "FORWARD", "BACKWARD", "BIDIRECTIONAL", "CHUNK_CAUSAL", "ABI_VERSION", "LIB_PATH"]
 
@@ -374,11 +379,15 @@ def step_noalloc(q, k, v, log_gate, beta, state_in=None, state_out=None, *, key_
 
 
 def __getattr__(name):
-    # the sequence operators' binding needs torch at import; the rest of this module does not
-    if name in _SEQUENCE:
-        from . import sequence
-        return getattr(sequence, name)
+    # the sequence operators' bindings need torch at import; the rest of this module does not
+    if name in _LAZY:
+        import importlib
+        return getattr(importlib.import_module("." + _LAZY[name], __name__), name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
-_SEQUENCE = ("decode", "packed_forward", "packed_backward", "packed_workspace_size", "group_norm", "group_norm_backward")
+_LAZY = {name: module for module, names in {
+    "sequence": ("decode", "packed_forward", "packed_backward", "packed_workspace_size", "group_norm", "group_norm_backward"),
+    "linear": ("linear_decode",),
+    "positions": ("rotary", "rotary_backward", "rotary_frequencies"),
+}.items() for name in names}

@@ -113,6 +113,11 @@ const char* gdn_kernel_name(int32_t kernel) {
     case GDN_KERNEL_PACKED_SCAN: return "packed_scan_kernel";
     case GDN_KERNEL_PACKED_SCAN_GRAD: return "packed_scan_grad_kernel";
     case GDN_KERNEL_PACKED_GRADS: return "packed_grads_kernel";
+    case GDN_KERNEL_LINEAR_DECODE: return "linear_decode_kernel";
+    case GDN_KERNEL_LINEAR_STATES: return "linear_state_kernels";
+    case GDN_KERNEL_LINEAR_SCAN: return "linear_scan_kernels";
+    case GDN_KERNEL_LINEAR_GATES: return "linear_gate_kernels";
+    case GDN_KERNEL_ROTARY: return "rotary_kernel";
     default: return "";
   }
 }

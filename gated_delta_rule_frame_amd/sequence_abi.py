@@ -23,6 +23,24 @@ class NormProblem(ctypes.Structure):
                 ("reserved", ctypes.c_int32 * 4)]
 
 
+class LinearProblem(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("heads_k", ctypes.c_int32), ("heads_v", ctypes.c_int32),
+                ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("qkv_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("state_rows", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("sequences", ctypes.c_int32), ("gate_per_head", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32 * 5)]
+
+
+class RotaryProblem(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_int32), ("dtype", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("pairs", ctypes.c_int32), ("layout", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4), ("magnitude", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("k_out_stride", ctypes.c_int64), ("reserved", ctypes.c_int32 * 4)]
+
+
 def declare(L):
     """Argument types of the sequence entry points of a loaded libgdn."""
     vp, i32 = ctypes.c_void_p, ctypes.c_int32
@@ -42,3 +60,8 @@ def declare(L):
     L.gdn_group_norm.argtypes = [N, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.gdn_group_norm_backward.restype = i32
     L.gdn_group_norm_backward.argtypes = [N, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    X = ctypes.POINTER(LinearProblem)
+    L.gdn_linear_decode.restype = i32
+    L.gdn_linear_decode.argtypes = [X, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.gdn_rotary.restype = i32
+    L.gdn_rotary.argtypes = [ctypes.POINTER(RotaryProblem), vp, vp, vp, vp, vp, vp, vp]

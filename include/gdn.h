@@ -303,7 +303,12 @@ enum {
   GDN_KERNEL_PACKED_SCAN = 13,      /* packed sequences: chunks in order; outputs and final states */
   GDN_KERNEL_PACKED_SCAN_GRAD = 14, /* packed gradients: chunks in reverse order */
   GDN_KERNEL_PACKED_GRADS = 15,     /* packed gradients: every chunk's gradients of its inputs */
-  GDN_KERNEL_COUNT = 16
+  GDN_KERNEL_LINEAR_DECODE = 16,    /* linear attention: one token per row */
+  GDN_KERNEL_LINEAR_STATES = 17,    /* linear attention: the states between segments (all launches) */
+  GDN_KERNEL_LINEAR_SCAN = 18,      /* linear attention: outputs, or gradients of q, k and v (all launches) */
+  GDN_KERNEL_LINEAR_GATES = 19,     /* linear attention: gradients of gates, sums over shared heads (all launches) */
+  GDN_KERNEL_ROTARY = 20,           /* rotary positions and their gradients */
+  GDN_KERNEL_COUNT = 21
 };
 gdn_status gdn_profile_enable(int32_t on);
 gdn_status gdn_profile_reset(void);
@@ -467,6 +472,74 @@ gdn_status gdn_group_norm_backward(const gdn_norm_problem* problem, const void* 
                                    const float* mean, const float* rstd,
                                    void* dx, float* dweight, float* dbias, void* dgate,
                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head, for the same sequences, states,
+ * pools and layouts as the calls above.  For every token t of a value head,
+ * with the state S in R^{d_k x d_v} (fp32) and a_t = exp(g_t):
+ *     S   <- a_t S + k_t v_t^T                             decay and write
+ *     o_t  = scale S^T q_t                                 read after write
+ * log_gate is [tokens, heads_v], or [heads_v] where gate_per_head is 1 (a fixed
+ * decay for each head); g <= 0, and -inf drops a finite state.  q, k, v, out,
+ * states, strides, alignment and errors are as for the calls above. */
+typedef struct gdn_linear_problem {
+  int32_t abi_version;        /* must equal GDN_ABI_VERSION */
+  int32_t heads_k;            /* the fields up to v_stride as in gdn_seq_problem */
+  int32_t heads_v;
+  int32_t d_k;
+  int32_t d_v;
+  int32_t qkv_dtype;
+  int32_t out_dtype;
+  int32_t state_rows;
+  int64_t tokens;
+  int64_t q_stride, k_stride, v_stride;
+  int32_t sequences;          /* packed calls: sequences >= 0; gdn_linear_decode ignores it */
+  int32_t gate_per_head;      /* 1: log_gate is [heads_v]; 0: [tokens, heads_v] */
+  float scale;                /* finite; of the outputs */
+  int32_t reserved[5];        /* must be zero */
+} gdn_linear_problem;
+
+/* One token for each row of a serving batch; rows, slots, padding and repeated
+ * slots as in gdn_decode.  No aliasing. */
+gdn_status gdn_linear_decode(const gdn_linear_problem* problem,
+                             const void* q, const void* k, const void* v, const float* log_gate,
+                             float* state, const int32_t* slots, void* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions of queries and keys.  q [tokens, heads_q, width] and k
+ * [tokens, heads_k, width] have rows of dense heads, a stride apart.  The first
+ * 2 * pairs components of every head are turned: pair i, (x, y), by the angle
+ * a = p f_i becomes magnitude (x cos a - y sin a, x sin a + y cos a); the others
+ * are copied.  f_i = frequencies[i] (fp64, radians per position, device memory);
+ * p is the token's position on the pair's axis: positions [tokens, axes] int32,
+ * of which the first sections[0] pairs take axis 0, the next sections[1] axis 1,
+ * and so on.  The angle is reduced in fp64, so that positions up to 2^31 turn by
+ * the exact angle to 2^-24; products and sums are fp32, rounded once.  inverse = 1
+ * turns by -a: the gradients of q and k from those of the turned ones. */
+enum { GDN_ROTARY_HALF = 0,          /* pair i: components i and i + pairs */
+       GDN_ROTARY_INTERLEAVED = 1 }; /* pair i: components 2 i and 2 i + 1 */
+typedef struct gdn_rotary_problem {
+  int32_t abi_version;        /* must equal GDN_ABI_VERSION */
+  int32_t dtype;              /* GDN_F32 or GDN_BF16 */
+  int64_t tokens;             /* in [0, 2^31 - 256] */
+  int32_t heads_q;            /* in [1, 65535] */
+  int32_t heads_k;            /* in [0, 65535]; 0: there is no k */
+  int32_t width;              /* multiple of 8 in [8, 1024] */
+  int32_t pairs;              /* >= 1, 2 * pairs <= width */
+  int32_t layout;             /* GDN_ROTARY_* */
+  int32_t inverse;            /* 0 or 1 */
+  int32_t axes;               /* in [1, 4] */
+  int32_t sections[4];        /* pairs of each axis, >= 0, `pairs` in all; 0 behind the last axis */
+  float magnitude;            /* finite */
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;   /* elements between tokens: 0 = dense, or a multiple of 16 bytes up to 2^23 */
+  int32_t reserved[4];        /* must be zero */
+} gdn_rotary_problem;
+
+/* q_out, k_out: like q and k, or q and k themselves with the same strides (in
+ * place); no other aliasing.  k and k_out are ignored where heads_k is 0.
+ * Pointers are 16-byte aligned, positions 4-byte, frequencies 8-byte. */
+gdn_status gdn_rotary(const gdn_rotary_problem* problem, const void* q, const void* k, const int32_t* positions,
+                      const double* frequencies, void* q_out, void* k_out, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */
