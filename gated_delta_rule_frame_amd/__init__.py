@@ -7,7 +7,7 @@ stream.  The names mirror the C ABI in ``include/gdn.h``: ``forward`` wraps
 ``gdn_workspace_size``.  The calls on sequences of tokens (``decode``,
 ``packed_forward``, ``packed_backward``) and the norm (``group_norm``,
 ``group_norm_backward``) are in ``sequence``, linear attention with a decay
-(``linear_decode``) is in ``linear``,
+(``linear_decode``, ``linear_forward``, ``linear_backward``) is in ``linear``,
 rotary positions (``rotary``, ``rotary_backward``, ``rotary_frequencies``) in
 ``positions``.
 
@@ -24,7 +24,7 @@ import os
 
 __all__ = ["forward", "step", "step_noalloc", "workspace_size", "NOALLOC_SCRATCH_BYTES", "make_problem", "lib", "GdnError", "Tuning", "tuning",
            "decode", "packed_forward", "packed_backward", "packed_workspace_size", "group_norm", "group_norm_backward",
-           "linear_decode",
+           "linear_decode", "linear_forward", "linear_backward", "linear_workspace_size",
            "rotary", "rotary_backward", "rotary_frequencies",
            "segment_plan", "profile_enable", "profile_reset", "profile_read",
            "FORWARD", "BACKWARD", "BIDIRECTIONAL", "CHUNK_CAUSAL", "ABI_VERSION", "LIB_PATH"]
@@ -388,6 +388,6 @@ def __getattr__(name):
 
 _LAZY = {name: module for module, names in {
     "sequence": ("decode", "packed_forward", "packed_backward", "packed_workspace_size", "group_norm", "group_norm_backward"),
-    "linear": ("linear_decode",),
+    "linear": ("linear_decode", "linear_forward", "linear_backward", "linear_workspace_size"),
     "positions": ("rotary", "rotary_backward", "rotary_frequencies"),
 }.items() for name in names}

@@ -1,0 +1,185 @@
+// Linear attention with a decay for each head: outputs and final states, and the
+// states between segments.
+#include <type_traits>
+
+#include "gdn_linear_scan.h"
+
+namespace gdn {
+namespace {
+
+// The states between segments from their sums, for every element of the state by itself: forward S <- e^{G} S + sum from the
+// initial state, reversed R <- e^{G} R + sum from the final state's gradient.
+template <bool REV>
+__global__ __launch_bounds__(kScanThreads) void linear_chain_kernel(ScanArgs s, int cell, int parts) {
+  const int hv = s.hk * s.rep;
+  const long long items = (long long)s.sequences * hv * parts;
+  const bool in_place = s.from && s.from == s.to;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const int part = (int)(item % parts), h = (int)(item / parts % hv), seq = (int)(item / parts / hv);
+    int a, b;
+    seq_bounds(s.cu, seq, s.tokens, &a, &b);
+    const int count = segments_of(b - a, s.L);
+    if (count < 2) continue;
+    long long row = seq;
+    if (s.state_slots) {
+      row = s.state_slots[seq];
+      if (row < 0 || row >= s.state_rows) row = -1;
+      else if (in_place) {
+        bool earlier;
+        int next;
+        same_slot(s.state_slots, s.sequences, seq, &earlier, &next);
+        if (earlier || next < s.sequences) continue;
+      }
+    }
+    const int e = (part * kScanThreads + threadIdx.x) * 4;
+    if (e >= cell) continue;
+    const long long slot = a / s.L + (long long)seq;
+    const long long b0 = bound_of(a, 0, s.L);
+    float* at = s.between + (size_t)(b0 * hv + h) * cell + e;
+    const size_t step = (size_t)hv * cell;
+    f32x4 S = s.from && row >= 0 ? *reinterpret_cast<const f32x4*>(s.from + ((size_t)row * hv + h) * cell + e) : zero4();
+    if (!REV && in_place) *reinterpret_cast<f32x4*>(s.firsts + (size_t)(b0 * hv + h) * cell + e) = S;
+    constexpr int kAhead = 8;
+    for (int i0 = 0; i0 < count - 1; i0 += kAhead) {
+      f32x4 u[kAhead];
+      float d[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int k = REV ? count - 2 - i0 - i : i0 + i;            // bound k, between segments k and k + 1
+        if (i0 + i < count - 1) {
+          u[i] = *reinterpret_cast<const f32x4*>(at + k * step);
+          d[i] = s.decay[(slot + (REV ? k + 1 : k)) * hv + h];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int k = REV ? count - 2 - i0 - i : i0 + i;
+        if (i0 + i < count - 1) {
+          S = d[i] * S + u[i];
+          *reinterpret_cast<f32x4*>(at + k * step) = S;
+        }
+      }
+    }
+  }
+}
+
+// Segments.  Parallel work for the card, from some kSegments (segment, head) pairs, against the bytes of a state
+// between two segments and the second pass over K and V.
+constexpr long long kSegments = 1024;
+constexpr long long kShortest = 256;
+
+size_t carve(char** at, char* base, size_t* bytes, size_t n) {
+  const size_t from = align_up(*bytes, 256);
+  *at = base ? base + from : nullptr;
+  *bytes = from + n;
+  return n;
+}
+
+}  // namespace
+
+LinearPlan linear_plan(const LinearProblem& p) {
+  LinearPlan plan;
+  long long L = (p.tokens * p.hv + kSegments - 1) / kSegments;
+  L = L < kShortest ? kShortest : L;
+  L = (L + 63) / 64 * 64;
+  if (L >= p.tokens) L = (p.tokens + 64) / 64 * 64;       // one segment, and none behind it
+  plan.L = (int)L;
+  plan.slots = p.tokens / L + p.sequences;
+  plan.bounds = p.tokens / L;
+  return plan;
+}
+
+size_t linear_space(const LinearProblem& p, bool grad, void* base, LinearSpace* s) {
+  LinearSpace none;
+  LinearSpace& o = s ? *s : none;
+  o = {};
+  char* at = nullptr;
+  size_t bytes = 0;
+  const LinearPlan plan = linear_plan(p);
+  const auto take = [&](auto** to, size_t n) {
+    if (n == 0) return;
+    carve(&at, static_cast<char*>(base), &bytes, n * sizeof **to);
+    *to = reinterpret_cast<std::remove_reference_t<decltype(*to)>>(at);
+  };
+  const size_t cell = (size_t)p.dk * p.dv, states = (size_t)plan.bounds * p.hv * cell;
+  const size_t segments = plan.bounds ? (size_t)plan.slots * p.hv : 0;
+  take(&o.states, states);
+  take(&o.decay, segments);
+  if (!grad) {
+    take(&o.firsts, states);
+    return bytes;
+  }
+  take(&o.rstates, states);
+  take(&o.rdecay, segments);
+  take(&o.last, (size_t)p.sequences * p.hv * cell);
+  take(&o.qdq, (size_t)p.tokens * p.hv);
+  take(&o.vdv, (size_t)p.tokens * p.hv);
+  if (p.hv > p.hk) {
+    take(&o.dq, (size_t)p.tokens * p.hv * p.dk);
+    take(&o.dk, (size_t)p.tokens * p.hv * p.dk);
+  }
+  if (p.fixed) take(&o.dg, (size_t)plan.slots * p.hv);
+  return bytes;
+}
+
+hipError_t linear_states(const ScanArgs& s, bool bf16, bool reversed, hipStream_t stream) {
+  prof_begin(stream, GDN_KERNEL_LINEAR_STATES);
+  hipError_t e = reversed ? (bf16 ? scan_variant<1, 3, true, false, false>(s, stream) : scan_variant<3, 3, true, false, false>(s, stream))
+                          : (bf16 ? scan_variant<1, 3, false, false, false>(s, stream) : scan_variant<3, 3, false, false, false>(s, stream));
+  if (e == hipSuccess) {
+    const int cell = s.b.width * s.c.width, parts = (cell + kScanThreads * 4 - 1) / (kScanThreads * 4);
+    const long long items = (long long)s.sequences * s.hk * s.rep * parts;
+    const dim3 grid((unsigned)(items < kMaxBlocks ? items : kMaxBlocks));
+    if (reversed) hipLaunchKernelGGL(linear_chain_kernel<true>, grid, dim3(kScanThreads), 0, stream, s, cell, parts);
+    else hipLaunchKernelGGL(linear_chain_kernel<false>, grid, dim3(kScanThreads), 0, stream, s, cell, parts);
+    e = hipGetLastError();
+  }
+  prof_end(stream, GDN_KERNEL_LINEAR_STATES);
+  return e;
+}
+
+ScanArgs scan_args(const LinearProblem& p, const LinearTensors& t, const LinearPlan& plan) {
+  ScanArgs s = {};
+  s.g = t.g;
+  s.cu = t.cu;
+  s.tokens = p.tokens;
+  s.slots = plan.slots;
+  s.sequences = p.sequences;
+  s.hk = p.hk;
+  s.rep = p.hv / p.hk;
+  s.L = plan.L;
+  s.fixed = p.fixed;
+  s.scale = p.scale;
+  return s;
+}
+
+hipError_t linear_forward_launch(const LinearProblem& p, const LinearTensors& t, const LinearSpace& ws, hipStream_t stream) {
+  const LinearPlan plan = linear_plan(p);
+  const uint32_t es = p.in_bf16 ? 2 : 4;
+  ScanArgs s = scan_args(p, t, plan);
+  s.a = {static_cast<const char*>(t.q), (uint32_t)p.qs * es, p.dk, true};
+  s.b = {static_cast<const char*>(t.k), (uint32_t)p.ks * es, p.dk, true};
+  s.c = {static_cast<const char*>(t.v), (uint32_t)p.vs * es, p.dv, false};
+  s.out = static_cast<char*>(t.out);
+  s.out_bytes = p.out_bf16 ? 2 : 4;
+  s.out_row = (uint32_t)p.hv * p.dv * s.out_bytes;
+  s.from = t.h0;
+  s.to = t.hT;
+  s.state_slots = t.slots;
+  s.state_rows = p.state_rows;
+  s.between = ws.states;
+  s.firsts = ws.firsts;
+  s.decay = ws.decay;
+  if (plan.bounds) {
+    const hipError_t e = linear_states(s, p.in_bf16, false, stream);
+    if (e != hipSuccess) return e;
+  }
+  prof_begin(stream, GDN_KERNEL_LINEAR_SCAN);
+  const hipError_t e = !p.in_bf16     ? scan_variant<3, 3, false, true, false>(s, stream)
+                       : p.out_bf16 ? scan_variant<1, 2, false, true, false>(s, stream)
+                                    : scan_variant<1, 3, false, true, false>(s, stream);
+  prof_end(stream, GDN_KERNEL_LINEAR_SCAN);
+  return e;
+}
+
+}  // namespace gdn

@@ -101,6 +101,81 @@ gdn_status gdn_linear_decode(const gdn_linear_problem* pr, const void* q, const 
   }
 }
 
+gdn_status gdn_linear_workspace_size(const gdn_linear_problem* pr, int32_t gradient, size_t* bytes_out) {
+  try {
+    if (!bytes_out) return fail(GDN_ERR_INVALID_ARGUMENT, "bytes_out is NULL");
+    LinearProblem p;
+    const gdn_status s = check_linear(pr, true, false, &p);
+    if (s != GDN_OK) return s;
+    *bytes_out = linear_space(p, gradient != 0, nullptr, nullptr);
+    return finish(hipSuccess);
+  } catch (...) {
+    return fail(GDN_ERR_INVALID_ARGUMENT, "internal error while sizing the workspace");
+  }
+}
+
+gdn_status gdn_linear_forward(const gdn_linear_problem* pr, const void* q, const void* k, const void* v,
+                              const float* log_gate, const int32_t* cu_seqlens, const int32_t* slots,
+                              const float* initial_state, void* out, float* final_state, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  try {
+    LinearProblem p;
+    gdn_status s = check_linear(pr, true, slots != nullptr, &p);
+    if (s != GDN_OK) return s;
+    if (p.sequences == 0) return finish(hipSuccess);
+    s = check_needed({cu_seqlens}, "cu_seqlens");
+    if (s == GDN_OK && p.tokens > 0) s = check_needed({q, k, v, log_gate, out}, "q, k, v, log_gate and out");
+    if (s == GDN_OK)
+      s = check_aligned({q, k, v, initial_state, out, final_state, workspace}, {log_gate, cu_seqlens, slots});
+    if (s == GDN_OK) s = check_workspace(linear_space(p, false, nullptr, nullptr), workspace, workspace_bytes);
+    if (s != GDN_OK) return s;
+    LinearTensors t = {};
+    t.q = q;
+    t.k = k;
+    t.v = v;
+    t.g = log_gate;
+    t.cu = cu_seqlens;
+    t.slots = slots;
+    t.h0 = initial_state;
+    t.out = out;
+    t.hT = final_state;
+    LinearSpace ws;
+    linear_space(p, false, workspace, &ws);
+    return finish(linear_forward_launch(p, t, ws, reinterpret_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return fail(GDN_ERR_HIP, "internal error while enqueueing");
+  }
+}
+
+gdn_status gdn_linear_backward(const gdn_linear_problem* pr, const void* q, const void* k, const void* v,
+                               const float* log_gate, const int32_t* cu_seqlens, const float* initial_state,
+                               const void* dout, const float* dfinal_state, void* dq, void* dk, void* dv,
+                               float* dlog_gate, float* dinitial_state, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  try {
+    LinearProblem p;
+    gdn_status s = check_linear(pr, true, false, &p);
+    if (s != GDN_OK) return s;
+    if (p.sequences == 0 && !p.fixed) return finish(hipSuccess);
+    if (p.sequences > 0) s = check_needed({cu_seqlens}, "cu_seqlens");
+    if (s == GDN_OK && p.fixed) s = check_needed({log_gate, dlog_gate}, "log_gate and dlog_gate");
+    if (s == GDN_OK && p.sequences > 0 && p.tokens > 0)
+      s = check_needed({q, k, v, log_gate, dout, dq, dk, dv, dlog_gate}, "q, k, v, log_gate, dout, dq, dk, dv and dlog_gate");
+    if (s == GDN_OK)
+      s = check_aligned({q, k, v, initial_state, dout, dfinal_state, dq, dk, dv, dinitial_state, workspace},
+                        {log_gate, cu_seqlens, dlog_gate});
+    if (s == GDN_OK) s = check_workspace(linear_space(p, true, nullptr, nullptr), workspace, workspace_bytes);
+    if (s != GDN_OK) return s;
+    const LinearTensors t = {q, k, v, log_gate, cu_seqlens, nullptr, initial_state, nullptr, nullptr,
+                             dout, dfinal_state, dq, dk, dv, dlog_gate, dinitial_state};
+    LinearSpace ws;
+    linear_space(p, true, workspace, &ws);
+    return finish(linear_backward_launch(p, t, ws, reinterpret_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return fail(GDN_ERR_HIP, "internal error while enqueueing");
+  }
+}
+
 gdn_status gdn_rotary(const gdn_rotary_problem* pr, const void* q, const void* k, const int32_t* positions,
                       const double* frequencies, void* q_out, void* k_out, void* stream) {
   try {

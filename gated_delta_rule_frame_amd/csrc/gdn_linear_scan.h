@@ -1,0 +1,531 @@
+// Linear attention with a decay for each head over packed sequences, chunked, and
+// its gradients: the scan that the calls share.
+//
+// One scan serves all of them.  For operands A, B (width I) and C (width J), the
+// cumulative log-gate G of a chunk and a state S (I x J):
+//     forward:   out_x = s (e^{G_x} A_x S + sum_{y <= x} e^{G_x - G_y} (A_x.B_y) C_y)
+//                S    <- e^{G_n} S + sum_y e^{G_n - G_y} B_y C_y^T
+//     reversed:  out_x = e^{G_n - G_x} A_x S + s sum_{y >= x} e^{G_y - G_x} (A_x.B_y) C_y
+//                S    <- e^{G_n} S + s sum_y e^{G_y} B_y C_y^T
+//     outputs    forward  (A, B, C) = (q, k, v),  S from the initial state
+//     dq         forward  (dout, v, k),  S transposed
+//     dv         reversed (k, q, dout),  S from the final state's gradient
+//     dk         reversed (v, dout, q),  S transposed
+// so a gradient costs three scans over the same operands, and dlog_gate follows
+// from sums: q.dq and v.dv of a token are its place in the outputs and in the
+// writes, dlog_gate_t = <R, S> at the segment's end + sum_{s >= t} (q_s.dq_s -
+// v_s.dv_s), with the gradient R of the state there.
+//
+// Segments.  Sequences are cut into segments of L tokens that run in parallel:
+// a first launch sums what each segment adds to the state (its last line above
+// alone), a second one chains these sums into the states between segments, and
+// the scan starts every segment from its own.
+#pragma once
+
+#include "gdn_linear.h"
+#include "gdn_packed.h"
+
+namespace gdn {
+
+// ---------------------------------------------------------------- device
+
+constexpr int kScanThreads = 256;
+
+// Gates below this are this: e^-10000 is 0 in fp32, and G stays finite for -inf.
+constexpr float kLowestGate = -10000.f;
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef s16x4 __attribute__((address_space(3)))* lds_s16x4;
+
+// Operand tiles in LDS: rows (tokens) of U units of 16 bytes (8 bf16 values), unit
+// u of row r at place u ^ swizzle(r).  Row fragments (16 rows, the same unit) and
+// transposed ones (4 rows, 16 columns) both touch every bank once.
+template <int U>
+__device__ __forceinline__ int swizzle(int r) {
+  if constexpr (U == 16) return (r & 3) << 2 | (r >> 2 & 3);
+  else if constexpr (U == 8) return (r >> 1 & 1) << 2 | (r >> 2 & 3);
+  else return r >> 2 & 3;
+}
+
+// Rows row0 .. + 15, columns 32 ks + 8 (lane / 16) .. + 8: lane l has row l % 16.
+template <int NT, int U, int CH>
+__device__ __forceinline__ Frag<NT> row_frag(const char* tile, int row0, int ks, int lane) {
+  const int r = lane % 16;
+  const int at = (row0 + r) * U * 16 + ((ks * 4 + lane / 16) ^ swizzle<U>(r)) * 16;
+  Frag<NT> f;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) f.t[i] = as_frag(*reinterpret_cast<const uint4*>(tile + i * CH * U * 16 + at));
+  return f;
+}
+
+// The transpose: lane l has column l % 16 of a tile whose columns are four pieces of
+// four, rows 32 k2 + 8 (l / 16) .. + 8.  `unit`, `sub`: where piece l % 4 lies in a row.
+template <int NT, int U, int CH>
+__device__ __forceinline__ Frag<NT> column_frag(const char* tile, int k2, int unit, int sub, int lane) {
+  const int r0 = 8 * (lane / 16) + lane % 16 / 4;
+  Frag<NT> f;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    s16x4 h[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = r0 + 4 * j;
+      const char* at = tile + i * CH * U * 16 + (32 * k2 + r) * U * 16 + (unit ^ swizzle<U>(r)) * 16 + sub;
+      h[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)at);
+    }
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    f.t[i] = __builtin_bit_cast(frag_t, (s16x8)__builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  return f;
+}
+
+// A chunk's rows of one operand on their way into LDS.
+template <int NT, int U, int CH>
+struct Stage {
+  static constexpr int N = (CH * U + kScanThreads - 1) / kScanThreads;
+  uint4 r[N][NT == 1 ? 1 : 2];
+
+  __device__ __forceinline__ void load(buf_t b, uint32_t stride, int width, int tid) {
+    constexpr uint32_t es = NT == 1 ? 2 : 4;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = i * kScanThreads + tid, row = at / U, u = at % U;
+      const uint32_t off = at < CH * U && u * 8 < width ? row * stride + u * 8 * es : kNowhere;
+      r[i][0] = buf_load16(b, off);
+      if constexpr (NT == 3) r[i][1] = buf_load16(b, off + 16);
+    }
+  }
+
+  __device__ __forceinline__ void store(char* tile, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = i * kScanThreads + tid, row = at / U, u = at % U;
+      if (CH * U % kScanThreads && at >= CH * U) break;
+      char* to = tile + row * U * 16 + (u ^ swizzle<U>(row)) * 16;
+      if constexpr (NT == 1) {
+        *reinterpret_cast<uint4*>(to) = r[i][0];
+      } else {
+        RawFrag<3> raw;
+        raw.a = r[i][0];
+        raw.b = r[i][1];
+        const Frag<3> f = frag_of<3>(raw);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) *reinterpret_cast<uint4*>(to + t * CH * U * 16) = as_bits(f.t[t]);
+      }
+    }
+  }
+};
+
+// The sum of x over the lanes up to this one.
+__device__ __forceinline__ double prefix_sum(double x, int lane) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const double o = __shfl_up(x, m);
+    if (lane >= m) x += o;
+  }
+  return x;
+}
+
+// The segment of a slot; false for a slot without one.
+struct Segment {
+  int seq, c, count;        // segment c of `count` of this sequence
+  int first, n;             // its tokens
+  int start, length;        // those of the sequence
+};
+
+__device__ __forceinline__ int segments_of(int tokens, int L) { return (tokens + L - 1) / L; }
+
+__device__ __forceinline__ bool find_segment(const int* cu, int sequences, long long tokens, int L, long long slot, Segment* s) {
+  int lo = 0, hi = sequences - 1;
+  const int t = (int)tokens;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (min(max(cu[mid], 0), t) / L + (long long)mid <= slot) lo = mid;
+    else hi = mid - 1;
+  }
+  int a, b;
+  seq_bounds(cu, lo, tokens, &a, &b);
+  const long long c = slot - (a / L + (long long)lo);
+  const int count = max(1, segments_of(b - a, L));   // an empty sequence has one of no tokens
+  if (c < 0 || c >= count) return false;
+  s->seq = __builtin_amdgcn_readfirstlane(lo);
+  s->c = __builtin_amdgcn_readfirstlane((int)c);
+  s->start = __builtin_amdgcn_readfirstlane(a);
+  s->count = __builtin_amdgcn_readfirstlane(count);
+  s->length = __builtin_amdgcn_readfirstlane(b - a);
+  s->first = s->start + s->c * L;
+  s->n = __builtin_amdgcn_readfirstlane(min(L, b - s->first));
+  return true;
+}
+
+// Place of the state between segments c and c + 1 of a sequence that starts at `start`.  Such
+// bounds are L or more tokens apart, in one sequence and from one to the next.
+__device__ __forceinline__ long long bound_of(int start, int c, int L) { return ((long long)start + (c + 1LL) * L) / L - 1; }
+
+// Whether an earlier sequence uses this slot, and the next one that does (or `sequences`).  Every wavefront for itself.
+__device__ __forceinline__ void same_slot(const int* slots, int sequences, int seq, bool* earlier, int* next) {
+  const int lane = threadIdx.x % 64, slot = slots[seq];
+  int before = 0, after = sequences;
+  for (int i = lane; i < sequences; i += 64)
+    if (slots[i] == slot) {
+      before |= i < seq;
+      if (i > seq && i < after) after = i;
+    }
+  *earlier = __ballot(before) != 0;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) after = min(after, __shfl_xor(after, m));
+  *next = __builtin_amdgcn_readfirstlane(after);
+}
+
+// A state element (i, j) lies at i * si + j * sj.
+template <int KS, int CT>
+struct State {
+  f32x4 t[KS * 2][CT];                          // rows 32 ks + 8 lg + 4 half + r of column 16 or 32 w + ...
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < KS * 2; ++i)
+#pragma unroll
+      for (int j = 0; j < CT; ++j) t[i][j] = zero4();
+  }
+  template <bool LOAD>
+  __device__ __forceinline__ void move(float* p, int rows, int columns, bool transposed, int w, int lane) {
+    const int lr = lane % 16, lg = lane / 16;
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+      const int col = CT == 2 ? 32 * w + 8 * (lr / 4) + 4 * j + lr % 4 : 16 * w + lr;
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) {
+        const int row = 32 * (i / 2) + 8 * lg + 4 * (i % 2);
+        if (col < columns && row < rows) {
+          if (transposed) {
+            float4* at = reinterpret_cast<float4*>(p + (size_t)col * rows + row);
+            if constexpr (LOAD) t[i][j] = *reinterpret_cast<f32x4*>(at);
+            else *reinterpret_cast<f32x4*>(at) = t[i][j];
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float* at = p + (size_t)(row + r) * columns + col;
+              if constexpr (LOAD) t[i][j][r] = *at;
+              else *at = t[i][j][r];
+            }
+          }
+        } else if constexpr (LOAD) {
+          t[i][j] = zero4();
+        }
+      }
+    }
+  }
+};
+
+// TO: terms of the states and of P where they meet A and C in the outputs: three give fp32 outputs the accuracy of fp32
+// arithmetic; two (2^-17 of a product) are far below the rounding of a bf16 output.
+template <int NT, int TO, int KS, int CT, bool REV, bool OUT, bool DOT>
+__global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s) {
+  constexpr int CH = NT == 1 ? 64 : 32, RT = CH / 16, K2 = CH / 32;
+  constexpr int U = KS * 4, UC = CT * 8;
+  constexpr int es = NT == 1 ? 2 : 4;
+  __shared__ __align__(16) char As[OUT ? NT * CH * U * 16 : 16];
+  __shared__ __align__(16) char Bs[NT * CH * U * 16];
+  __shared__ __align__(16) char Cs[NT * CH * UC * 16];
+  __shared__ __align__(16) bh P[OUT ? RT * K2 * TO * 512 : 8];
+  __shared__ __align__(16) double Gs[2][64];
+  __shared__ __align__(16) float fo[2][64], fs[2][64];
+  __shared__ float red[DOT ? 4 : 1][CH];
+  const int tid = threadIdx.x, lane = tid % 64, w = __builtin_amdgcn_readfirstlane(tid / 64);
+  const int lr = lane % 16, lg = lane / 16;
+  const int I = s.b.width, J = s.c.width, hv = s.hk * s.rep;
+
+  if constexpr (OUT) {
+    // the blocks of P beside the diagonal that share a fragment with one that is used stay zero
+    for (int i = tid; i < RT * K2 * TO * 64; i += kScanThreads) reinterpret_cast<uint4*>(P)[i] = make_uint4(0, 0, 0, 0);
+  }
+  const long long units = s.slots * s.hk, blocks = (units + 7) / 8 * 8 * s.rep;
+  for (long long block = blockIdx.x; block < blocks; block += gridDim.x) {
+    // the value heads of a key head, which read the same rows, one after another on one XCD
+    const long long unit = block / 8 / s.rep * 8 + block % 8;
+    if (unit >= units) continue;
+    const int kh = (int)(unit % s.hk), h = kh * s.rep + (int)(block / 8 % s.rep);
+    const long long slot = unit / s.hk;
+    Segment seg;
+    if (!find_segment(s.cu, s.sequences, s.tokens, s.L, slot, &seg)) continue;
+    const size_t cell = (size_t)I * J;
+    const bool in_place = s.from && s.from == s.to;
+    bool keep = true;                           // the state after the last segment
+    int next = s.sequences;
+    long long row = seg.seq;
+    if (s.state_slots) {
+      row = s.state_slots[seg.seq];
+      if (row < 0 || row >= s.state_rows) row = -1;
+      else {
+        bool earlier;
+        same_slot(s.state_slots, s.sequences, seg.seq, &earlier, &next);
+        if (!in_place) {
+          keep = next == s.sequences;
+          next = s.sequences;
+        } else if (earlier || (next < s.sequences && (!OUT || seg.c > 0))) {
+          continue;                             // the first of them runs them all, one after another
+        }
+      }
+    }
+    if constexpr (!OUT) {
+      if (REV ? seg.c == 0 : seg.c == seg.count - 1) continue;
+    }
+    State<KS, CT> S;
+    double total = 0;                           // wavefront 3: of the gates
+    if constexpr (!OUT) {
+      S.zero();
+    } else {
+      float* p = const_cast<float*>(s.from);
+      const bool inner = REV ? seg.c < seg.count - 1 : seg.c > 0;
+      if (inner) p = s.between + (size_t)(bound_of(seg.start, REV ? seg.c : seg.c - 1, s.L) * hv + h) * cell;
+      else if (in_place && seg.count > 1 && next == s.sequences) p = s.firsts + (size_t)(bound_of(seg.start, 0, s.L) * hv + h) * cell;
+      else if (p && row >= 0) p += ((size_t)row * hv + h) * cell;
+      else p = nullptr;
+      if (p) S.template move<true>(p, I, J, s.transposed, w, lane);
+      else S.zero();
+    }
+    const bool serial = next < s.sequences;     // in place, with others that name this slot behind it
+    int seq = seg.seq, first = seg.first, n = serial ? seg.length : seg.n;
+    for (;;) {
+      const int chunks = (n + CH - 1) / CH;
+      Stage<NT, U, CH> ra, rb;
+      Stage<NT, UC, CH> rc;
+      float gate = 0.f;
+      auto fetch = [&](int i) {                 // the i-th chunk in the scan's order; behind the last: nothing
+        const int k = i < chunks ? (REV ? chunks - 1 - i : i) : 0, t0 = first + k * CH;
+        const int m = i < chunks ? min(CH, n - k * CH) : 0;
+        auto rows = [&](const Operand& o) {
+          return buf(o.p + (size_t)t0 * o.row + (size_t)(o.shared ? kh : h) * o.width * es,
+                     m > 0 ? (uint32_t)(m - 1) * o.row + o.width * es : 0);
+        };
+        if constexpr (OUT) ra.load(rows(s.a), s.a.row, I, tid);
+        rb.load(rows(s.b), s.b.row, I, tid);
+        rc.load(rows(s.c), s.c.row, J, tid);
+        if (w == 3) gate = lane < m ? s.g[s.fixed ? h : (size_t)(t0 + lane) * hv + h] : 0.f;
+      };
+      auto gates = [&](int at) {                // wavefront 3: cumulative gates and factors of the chunk that was fetched
+        gate = gate < kLowestGate ? kLowestGate : gate;
+        const double G = prefix_sum(gate * 1.4426950408889634, lane);   // in units of log 2
+        const double Gn = __shfl(G, 63);
+        const float up = exp2_of((float)G), down = exp2_of((float)(Gn - G));
+        Gs[at][lane] = G;
+        fo[at][lane] = REV ? down : s.scale * up;
+        fs[at][lane] = REV ? s.scale * up : down;
+        total += Gn;
+      };
+      fetch(0);
+      __syncthreads();                          // the gates and tiles of what ran before have been read
+      if (w == 3) gates(0);
+      for (int i = 0; i < chunks; ++i) {
+        const int k = REV ? chunks - 1 - i : i, at = i & 1;
+        const int t0 = first + k * CH, m = min(CH, n - k * CH);
+        if (i) __syncthreads();                 // the previous tiles have been read
+        if constexpr (OUT) ra.store(As, tid);
+        rb.store(Bs, tid);
+        rc.store(Cs, tid);
+        if constexpr (DOT) {
+          if (i && tid < CH) {
+            const int b0 = REV ? t0 + CH : t0 - CH;
+            if (b0 + tid < first + n) s.dot[(size_t)h * s.tokens + b0 + tid] = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
+          }
+        }
+        fetch(i + 1);
+        __syncthreads();
+
+        f32x4 o[RT][CT];
+        if constexpr (OUT) {
+          // P: rows x of A, y of B; a lane holds four y of one x, which is half a vector of P's fragment
+          for (int id = w; id < RT * (RT + 1) / 2; id += 4) {
+            const int hi = id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3, lo = id - hi * (hi + 1) / 2;
+            const int tx = REV ? lo : hi, ty = REV ? hi : lo;
+            f32x4 d = zero4();
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+              d = mma<NT, NT>(row_frag<NT, U, CH>(Bs, 16 * ty, ks, lane), row_frag<NT, U, CH>(As, 16 * tx, ks, lane), d);
+            const double Gx = Gs[at][16 * tx + lr];
+            float x[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const double e = Gx - Gs[at][16 * ty + 4 * lg + r];
+              const bool in = REV ? 16 * ty + 4 * lg + r >= 16 * tx + lr : 16 * ty + 4 * lg + r <= 16 * tx + lr;
+              x[r] = in ? s.scale * exp2_of((float)(REV ? -e : e)) * d[r] : 0.f;
+            }
+            uint32_t p0[TO], p1[TO];
+            split2<TO>(x[0], x[1], p0);
+            split2<TO>(x[2], x[3], p1);
+            bh* to = P + (tx * K2 + ty / 2) * TO * 512 + (((ty & 1) * 2 + lg / 2) * 16 + lr) * 8 + (lg & 1) * 4;
+#pragma unroll
+            for (int t = 0; t < TO; ++t) *reinterpret_cast<uint2*>(to + t * 512) = make_uint2(p0[t], p1[t]);
+          }
+          // the state's part
+#pragma unroll
+          for (int x = 0; x < RT; ++x)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) o[x][j] = zero4();
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            Frag<NT> af[RT];
+#pragma unroll
+            for (int x = 0; x < RT; ++x) af[x] = row_frag<NT, U, CH>(As, 16 * x, ks, lane);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+              const f32x4 u = S.t[2 * ks][j], v = S.t[2 * ks + 1][j];
+              const float e[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+              const Frag<TO> sf = split8<TO>(e);
+#pragma unroll
+              for (int x = 0; x < RT; ++x) o[x][j] = mma<TO, NT>(sf, af[x], o[x][j]);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < RT; ++x) {
+            const float f = fo[at][16 * x + lr];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) o[x][j] *= f;
+          }
+        }
+        // columns of C, as they are and as they go into the state
+        Frag<NT> cf[K2][CT];
+        const int piece = lane % 4;
+#pragma unroll
+        for (int k2 = 0; k2 < K2; ++k2)
+#pragma unroll
+          for (int j = 0; j < CT; ++j)
+            cf[k2][j] = column_frag<NT, UC, CH>(Cs, k2, CT == 2 ? 4 * w + piece : 2 * w + piece / 2, CT == 2 ? 8 * j : piece % 2 * 8, lane);
+        const float all = exp2_of((float)Gs[at][CH - 1]);
+#pragma unroll
+        for (int i2 = 0; i2 < KS * 2; ++i2)
+#pragma unroll
+          for (int j = 0; j < CT; ++j) S.t[i2][j] *= all;
+#pragma unroll
+        for (int k2 = 0; k2 < K2; ++k2) {
+          Frag<3> vf[CT];
+          const float* f = &fs[at][32 * k2 + 8 * lg];
+#pragma unroll
+          for (int j = 0; j < CT; ++j) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              x[e] = 0.f;
+#pragma unroll
+              for (int t = NT - 1; t >= 0; --t) {
+                const uint4 b = as_bits(cf[k2][j].t[t]);
+                const uint32_t word = e / 2 == 0 ? b.x : e / 2 == 1 ? b.y : e / 2 == 2 ? b.z : b.w;
+                x[e] += __uint_as_float(e % 2 ? word & 0xffff0000u : word << 16);
+              }
+              x[e] *= f[e];
+            }
+            vf[j] = split8<3>(x);
+          }
+#pragma unroll
+          for (int i2 = 0; i2 < KS * 2; ++i2) {
+            const Frag<NT> bf = column_frag<NT, U, CH>(Bs, k2, 4 * (i2 / 2) + piece, 8 * (i2 % 2), lane);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) S.t[i2][j] = mma<NT, 3>(bf, vf[j], S.t[i2][j]);
+          }
+        }
+        if constexpr (OUT) {
+          __syncthreads();                      // P is there
+          const uint32_t ob = s.out_bytes;
+          const buf_t to = buf(s.out + (size_t)t0 * s.out_row + (size_t)h * J * ob, (uint32_t)(m - 1) * s.out_row + J * ob);
+          const int col = CT == 2 ? 32 * w + 8 * lg : 16 * w + 4 * lg;
+          buf_t db = to;
+          if constexpr (DOT)
+            db = buf(s.d.p + (size_t)t0 * s.d.row + (size_t)(s.d.shared ? kh : h) * J * es, (uint32_t)(m - 1) * s.d.row + J * es);
+#pragma unroll
+          for (int x = 0; x < RT; ++x) {
+#pragma unroll
+            for (int k2 = REV ? x / 2 : 0; k2 < (REV ? K2 : x / 2 + 1); ++k2) {
+              Frag<TO> pf;
+#pragma unroll
+              for (int t = 0; t < TO; ++t)
+                pf.t[t] = as_frag(*reinterpret_cast<const uint4*>(P + ((x * K2 + k2) * TO + t) * 512 + lane * 8));
+#pragma unroll
+              for (int j = 0; j < CT; ++j) o[x][j] = mma<NT, TO>(cf[k2][j], pf, o[x][j]);
+            }
+            float v[4 * CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[4 * j + r] = o[x][j][r];
+            const uint32_t off = col < J ? (16 * x + lr) * s.out_row + col * ob : kNowhere;
+            if (ob == 2) {
+              uint32_t b[2 * CT];
+#pragma unroll
+              for (int r = 0; r < 2 * CT; ++r) {
+                uint32_t one[1];
+                split2<1>(v[2 * r], v[2 * r + 1], one);
+                b[r] = one[0];
+              }
+              typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+              typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+              if constexpr (CT == 2) __builtin_amdgcn_raw_buffer_store_b128(u32x4{b[0], b[1], b[2], b[3]}, to, off, 0, 0);
+              else __builtin_amdgcn_raw_buffer_store_b64(u32x2{b[0], b[1]}, to, off, 0, 0);
+            } else {
+              typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+              for (int j = 0; j < CT; ++j)
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                                             __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])},
+                                                       to, off + 16 * j, 0, 0);
+            }
+            if constexpr (DOT) {
+              const uint32_t at_d = col < J ? (16 * x + lr) * s.d.row + col * es : kNowhere;
+              float sum = 0.f;
+#pragma unroll
+              for (int r = 0; r < 4 * CT; ++r) sum = fmaf(v[r], raw_value(value_at<NT>(db, at_d + r * es)), sum);
+              sum += __shfl_xor(sum, 16);
+              sum += __shfl_xor(sum, 32);
+              if (lg == 0) red[w][16 * x + lr] = sum;
+            }
+          }
+        }
+        if (w == 3) gates(at ^ 1);
+      }
+      if constexpr (DOT) {
+        __syncthreads();
+        const int b0 = REV ? first : first + (chunks - 1) * CH;
+        if (chunks > 0 && tid < CH && b0 + tid < first + n)
+          s.dot[(size_t)h * s.tokens + b0 + tid] = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
+      }
+      if (!serial || next >= s.sequences) break;
+      seq = next;
+      bool earlier;
+      same_slot(s.state_slots, s.sequences, seq, &earlier, &next);
+      int a, b;
+      seq_bounds(s.cu, seq, s.tokens, &a, &b);
+      first = __builtin_amdgcn_readfirstlane(a);
+      n = __builtin_amdgcn_readfirstlane(b - a);
+    }
+    if constexpr (!OUT) {
+      S.template move<false>(s.between + (size_t)(bound_of(seg.start, REV ? seg.c - 1 : seg.c, s.L) * hv + h) * cell, I, J,
+                             s.transposed, w, lane);
+      if (tid == 3 * 64) s.decay[slot * hv + h] = exp2_of((float)total);
+    } else if (s.to && keep && row >= 0 && (serial || (REV ? seg.c == 0 : seg.c == seg.count - 1))) {
+      S.template move<false>(s.to + ((size_t)row * hv + h) * cell, I, J, s.transposed, w, lane);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+// Launches the scan of this variant for the widths of s.
+template <int NT, int TO, bool REV, bool OUT, bool DOT>
+hipError_t scan_variant(const ScanArgs& s, hipStream_t stream) {
+  const long long blocks = (s.slots * s.hk + 7) / 8 * 8 * s.rep;
+  const dim3 grid((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks));
+  const int ks = s.b.width <= 32 ? 1 : s.b.width <= 64 ? 2 : 4;
+  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kScanThreads), 0, stream, s); };
+  if (s.c.width <= 64) {
+    if (ks == 1) go(linear_scan_kernel<NT, TO, 1, 1, REV, OUT, DOT>);
+    else if (ks == 2) go(linear_scan_kernel<NT, TO, 2, 1, REV, OUT, DOT>);
+    else go(linear_scan_kernel<NT, TO, 4, 1, REV, OUT, DOT>);
+  } else {
+    if (ks == 1) go(linear_scan_kernel<NT, TO, 1, 2, REV, OUT, DOT>);
+    else if (ks == 2) go(linear_scan_kernel<NT, TO, 2, 2, REV, OUT, DOT>);
+    else go(linear_scan_kernel<NT, TO, 4, 2, REV, OUT, DOT>);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace gdn

@@ -1,14 +1,17 @@
 """Binding of libgdn's linear attention with a decay for each head (``include/gdn.h``, the section of that name).
 
-``linear_decode`` wraps ``gdn_linear_decode``.  It stands beside ``decode``, whose
-states, pools, checks and streams it shares; results carry no autograd graph.
+``linear_decode`` wraps ``gdn_linear_decode``, ``linear_forward`` and
+``linear_backward`` wrap ``gdn_linear_forward`` and its gradients.  They stand
+beside ``decode``, ``packed_forward`` and ``packed_backward``, whose states,
+pools, packed layout, checks and streams they share; results carry no autograd
+graph.
 """
 from __future__ import annotations
 
 import torch
 
-from . import ABI_VERSION, lib
-from .sequence import _CODE, _MAX, _dense, _fits, _on, _output, _ptr, _rows
+from . import ABI_VERSION, F32, lib
+from .sequence import _CODE, _MAX, _dense, _fits, _need, _on, _output, _ptr, _rows, _sequences, _space
 from .sequence_abi import LinearProblem
 
 
@@ -57,3 +60,88 @@ def linear_decode(q, k, v, log_gate, state, slots=None, *, scale=1.0, out_dtype=
     _on(device, lib().gdn_linear_decode, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), state.data_ptr(),
         _ptr(slots), out.data_ptr())
     return out
+
+
+def linear_forward(q, k, v, log_gate, cu_seqlens, initial_state=None, *, slots=None, scale=1.0, out_dtype=None, out=None,
+                   final_state=None, want_state=True, workspace=None):
+    """Linear attention with a decay over packed sequences (gdn_linear_forward); returns (out, final_state).
+
+    Per token of a value head: S <- exp(log_gate) S + k v^T, out = scale S^T q.
+    q, k: [tokens,heads_k,d_k]; v: [tokens,heads_v,d_v] (fp32 or bf16, one
+    dtype; heads_v a multiple of heads_k); log_gate: [tokens,heads_v] fp32, or
+    [heads_v], one decay for each head.  cu_seqlens, slots, states, outputs and
+    the reach of a NaN or infinity are ``packed_forward``'s.
+    """
+    odt = _output(out, out_dtype)
+    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, scale, odt)
+    seqs = p.sequences = _sequences(cu_seqlens, device)
+    states = seqs
+    if slots is not None:
+        _dense("slots", slots, (seqs,), torch.int32, device)
+        if final_state is None:
+            if initial_state is None:
+                raise ValueError("a call with slots needs initial_state or final_state, the pool")
+            if want_state:
+                final_state = initial_state
+        pool = initial_state if final_state is None else final_state
+        states = pool.shape[0] if isinstance(pool, torch.Tensor) and pool.dim() == 4 else 0
+        p.state_rows = _fits("the pool's rows", states)
+    shape = (states, hv, dk, dv)
+    if initial_state is not None:
+        _dense("initial_state", initial_state, shape, torch.float32, device)
+    if final_state is not None:
+        _dense("final_state", final_state, shape, torch.float32, device)
+    elif want_state and slots is None:
+        final_state = torch.empty(shape, dtype=torch.float32, device=device)
+    if out is None:
+        out = torch.empty((n, hv, dv), dtype=odt, device=device)
+    else:
+        _dense("out", out, (n, hv, dv), odt, device)
+    ws, ws_bytes = _space("gdn_linear_workspace_size", p, 0, workspace, device)
+    _on(device, lib().gdn_linear_forward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), cu_seqlens.data_ptr(),
+        _ptr(slots), _ptr(initial_state), out.data_ptr(), _ptr(final_state), _ptr(ws), ws_bytes)
+    return out, final_state
+
+
+def linear_backward(q, k, v, log_gate, cu_seqlens, dout, initial_state=None, dfinal_state=None, *, scale=1.0, grads=None,
+                    workspace=None):
+    """Gradients of ``linear_forward`` (gdn_linear_backward); returns (dq, dk, dv, dlog_gate, dinitial_state).
+
+    The inputs are linear_forward's (without slots); dout: like v, dense;
+    dfinal_state: like the final state, or None (zeros).  dq, dk and dv have
+    q's dtype and are dense, the others are fp32; dlog_gate has log_gate's
+    shape; dinitial_state is None where initial_state is.  Rows behind the
+    last sequence are not written: for a padded batch give ``grads``, four
+    tensors (dq, dk, dv, dlog_gate) to write into.
+    """
+    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, scale, torch.float32)
+    seqs = p.sequences = _sequences(cu_seqlens, device)
+    _dense("dout", dout, v.shape, q.dtype, device)
+    shape = (seqs, hv, dk, dv)
+    for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
+        if t is not None:
+            _dense(name, t, shape, torch.float32, device)
+    inputs = {"dq": q, "dk": k, "dv": v, "dlog_gate": log_gate}
+    if grads is None:
+        grads = [torch.empty(t.shape, dtype=t.dtype, device=device) for t in inputs.values()]
+    else:
+        if len(grads) != 4:
+            raise ValueError(f"grads must be four tensors (got {len(grads)})")
+        for (name, t), d in zip(inputs.items(), grads):
+            _dense(name, d, t.shape, t.dtype, device)
+    ws, ws_bytes = _space("gdn_linear_workspace_size", p, 1, workspace, device)
+    dstate = None if initial_state is None else torch.empty_like(initial_state)
+    _on(device, lib().gdn_linear_backward, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(),
+        cu_seqlens.data_ptr(), _ptr(initial_state), dout.data_ptr(), _ptr(dfinal_state), *(t.data_ptr() for t in grads),
+        _ptr(dstate), _ptr(ws), ws_bytes)
+    return (*grads, dstate)
+
+
+def linear_workspace_size(q, v, log_gate, sequences, *, gradient=False):
+    """Bytes of workspace of ``linear_forward`` (or ``linear_backward``) for inputs like q, v and log_gate."""
+    if q.dtype not in _CODE:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    p = LinearProblem(ABI_VERSION, q.shape[1], v.shape[1], q.shape[2], v.shape[2], _CODE[q.dtype], F32, 0, q.shape[0])
+    p.sequences = _fits("sequences", sequences)
+    p.gate_per_head = int(log_gate.dim() == 1)
+    return _need("gdn_linear_workspace_size", LinearProblem, bytes(p), int(gradient))

@@ -63,5 +63,11 @@ def declare(L):
     X = ctypes.POINTER(LinearProblem)
     L.gdn_linear_decode.restype = i32
     L.gdn_linear_decode.argtypes = [X, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.gdn_linear_workspace_size.restype = i32
+    L.gdn_linear_workspace_size.argtypes = [X, i32, ctypes.POINTER(sz)]
+    L.gdn_linear_forward.restype = i32
+    L.gdn_linear_forward.argtypes = [X, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.gdn_linear_backward.restype = i32
+    L.gdn_linear_backward.argtypes = [X, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.gdn_rotary.restype = i32
     L.gdn_rotary.argtypes = [ctypes.POINTER(RotaryProblem), vp, vp, vp, vp, vp, vp, vp]

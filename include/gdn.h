@@ -505,6 +505,39 @@ gdn_status gdn_linear_decode(const gdn_linear_problem* problem,
                              const void* q, const void* k, const void* v, const float* log_gate,
                              float* state, const int32_t* slots, void* out, void* stream);
 
+/* Bytes of device workspace of gdn_linear_forward (gradient = 0) or
+ * gdn_linear_backward (1); host only. */
+gdn_status gdn_linear_workspace_size(const gdn_linear_problem* problem, int32_t gradient, size_t* bytes_out);
+
+/* Packed sequences: cu_seqlens, slots, initial_state and final_state as in
+ * gdn_packed_forward.  fp32 results (states, and outputs of that type) have the
+ * accuracy of fp32 arithmetic, the range is that of bf16.  A NaN or infinity in
+ * a token's q spoils that token's outputs; in its k, v or log_gate, beside what
+ * the recurrence makes of it, also outputs of earlier tokens in its chunk of 64
+ * (0 times it is NaN), in the value heads that read it and, for v, in its
+ * column.  Rows behind the last sequence are neither read nor written.  No
+ * aliasing but of initial_state with final_state.  The workspace is as
+ * gdn_forward's. */
+gdn_status gdn_linear_forward(const gdn_linear_problem* problem,
+                              const void* q, const void* k, const void* v, const float* log_gate,
+                              const int32_t* cu_seqlens, const int32_t* slots,
+                              const float* initial_state, void* out, float* final_state,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(out dout) + sum(final_state dfinal_state) for every input,
+ * from the inputs alone; the arguments are gdn_packed_backward's without beta.
+ * dlog_gate has log_gate's shape; with gate_per_head it sums over all tokens of
+ * all sequences.  No atomics: every run gives the same bits.  A NaN or infinity
+ * may spoil every gradient of its sequence in the value heads that read it, and
+ * what is summed over them; other sequences are as without it (a dlog_gate of
+ * [heads_v] sums them all).  No aliasing. */
+gdn_status gdn_linear_backward(const gdn_linear_problem* problem,
+                               const void* q, const void* k, const void* v, const float* log_gate,
+                               const int32_t* cu_seqlens, const float* initial_state,
+                               const void* dout, const float* dfinal_state,
+                               void* dq, void* dk, void* dv, float* dlog_gate, float* dinitial_state,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Rotary positions of queries and keys.  q [tokens, heads_q, width] and k
  * [tokens, heads_k, width] have rows of dense heads, a stride apart.  The first
