@@ -36,7 +36,6 @@ struct ScanArgs {
   int sequences, hk, rep, L;
   bool fixed;
   float scale;
-  bool transposed;          // states are [J][I] in memory
   // outputs
   char* out;
   uint32_t out_row;

@@ -12,10 +12,11 @@ namespace {
 template <bool REV>
 __global__ __launch_bounds__(kScanThreads) void linear_chain_kernel(ScanArgs s, int cell, int parts) {
   const int hv = s.hk * s.rep;
-  const long long items = (long long)s.sequences * hv * parts;
+  const uint32_t items = (uint32_t)s.sequences * hv * parts;       // at most 2^20 * 16
   const bool in_place = s.from && s.from == s.to;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int part = (int)(item % parts), h = (int)(item / parts % hv), seq = (int)(item / parts / hv);
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint32_t pair = item / (uint32_t)parts;
+    const int part = item - pair * parts, seq = pair / (uint32_t)hv, h = pair - seq * (uint32_t)hv;
     int a, b;
     seq_bounds(s.cu, seq, s.tokens, &a, &b);
     const int count = segments_of(b - a, s.L);
@@ -33,7 +34,7 @@ __global__ __launch_bounds__(kScanThreads) void linear_chain_kernel(ScanArgs s, 
     }
     const int e = (part * kScanThreads + threadIdx.x) * 4;
     if (e >= cell) continue;
-    const long long slot = a / s.L + (long long)seq;
+    const long long slot = a / (uint32_t)s.L + seq;
     const long long b0 = bound_of(a, 0, s.L);
     float* at = s.between + (size_t)(b0 * hv + h) * cell + e;
     const size_t step = (size_t)hv * cell;

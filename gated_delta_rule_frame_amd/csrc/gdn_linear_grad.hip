@@ -34,10 +34,9 @@ struct GateArgs {
 __global__ __launch_bounds__(kThreads) void linear_gates_kernel(ScanArgs s, GateArgs a, int cell) {
   __shared__ double red[4];
   const int tid = threadIdx.x, lane = tid % 64, w = tid / 64, hv = s.hk * s.rep;
-  const long long items = s.slots * hv;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int h = (int)(item % hv);
-    const long long slot = item / hv;
+  const uint32_t items = s.slots * hv;
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int slot = item / (uint32_t)hv, h = item - slot * hv;
     Segment seg;
     if (!find_segment(s.cu, s.sequences, s.tokens, s.L, slot, &seg) || seg.n == 0) {
       if (a.sums && tid == 0) a.sums[item] = 0;
@@ -70,7 +69,7 @@ __global__ __launch_bounds__(kThreads) void linear_gates_kernel(ScanArgs s, Gate
         const size_t at = (size_t)h * s.tokens + seg.first + i;
         x = (double)a.qdq[at] - a.vdv[at];
       }
-      x = prefix_sum(x, lane);
+      x = prefix_sum(x);
       __syncthreads();
       if (lane == 63) red[w] = x;
       __syncthreads();
@@ -164,7 +163,6 @@ hipError_t linear_backward_launch(const LinearProblem& p, const LinearTensors& t
     s.b = v;
     s.c = k;
     s.d = q;
-    s.transposed = true;
     s.out = shared ? reinterpret_cast<char*>(ws.dq) : static_cast<char*>(t.dq);
     s.out_bytes = shared ? 4 : es;
     s.out_row = (uint32_t)(p.hv * p.dk) * s.out_bytes;
@@ -190,7 +188,6 @@ hipError_t linear_backward_launch(const LinearProblem& p, const LinearTensors& t
     s.a = v;
     s.b = dout;
     s.c = q;
-    s.transposed = true;
     s.out = shared ? reinterpret_cast<char*>(ws.dk) : static_cast<char*>(t.dk);
     s.out_bytes = shared ? 4 : es;
     s.out_row = (uint32_t)(p.hv * p.dk) * s.out_bytes;

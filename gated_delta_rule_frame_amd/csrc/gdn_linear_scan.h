@@ -87,12 +87,15 @@ struct Stage {
 
   __device__ __forceinline__ void load(buf_t b, uint32_t stride, int width, int tid) {
     constexpr uint32_t es = NT == 1 ? 2 : 4;
+    constexpr int step = kScanThreads / U;           // rows
+    asm volatile("" : "+v"(tid));                    // offsets are made here and not kept in registers through the chunk
+    const int row = tid / U, u = tid % U;
+    uint32_t off = (CH * U % kScanThreads == 0 || tid < CH * U) && u * 8 < width ? row * stride + u * 8 * es : kNowhere;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int at = i * kScanThreads + tid, row = at / U, u = at % U;
-      const uint32_t off = at < CH * U && u * 8 < width ? row * stride + u * 8 * es : kNowhere;
       r[i][0] = buf_load16(b, off);
       if constexpr (NT == 3) r[i][1] = buf_load16(b, off + 16);
+      off += step * stride;                          // behind kNowhere it stays there: 64 rows span less than 2^31 bytes
     }
   }
 
@@ -116,14 +119,57 @@ struct Stage {
   }
 };
 
-// The sum of x over the lanes up to this one.
-__device__ __forceinline__ double prefix_sum(double x, int lane) {
+// N (4 or 8) consecutive input values.
+template <int NT, int N>
+struct Values {
+  uint32_t b[NT == 1 ? N / 2 : N];
+  __device__ __forceinline__ void load(buf_t from, uint32_t off) {
+    if constexpr (NT == 1 && N == 4) {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(from, off, 0, 0));
+      b[0] = v[0];
+      b[1] = v[1];
+    } else {
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const double o = __shfl_up(x, m);
-    if (lane >= m) x += o;
+      for (int i = 0; i < (int)(sizeof b / 16); ++i) {
+        const uint4 v = buf_load16(from, off + 16 * i);
+        b[4 * i] = v.x;
+        b[4 * i + 1] = v.y;
+        b[4 * i + 2] = v.z;
+        b[4 * i + 3] = v.w;
+      }
+    }
   }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (NT == 1) return __uint_as_float(i % 2 ? b[i / 2] & 0xffff0000u : b[i / 2] << 16);
+    else return __uint_as_float(b[i]);
+  }
+};
+
+// The sum of x over the lanes up to this one, by shifts in rows of 16 lanes and
+// broadcasts of their last lanes (lane shuffles through LDS take several times as long).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lanes_before(double x) {      // 0 where no lane is
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  const i32x2 v = __builtin_bit_cast(i32x2, x);
+  return __builtin_bit_cast(double, i32x2{__builtin_amdgcn_update_dpp(0, v[0], CTRL, ROWS, 0xf, false),
+                                          __builtin_amdgcn_update_dpp(0, v[1], CTRL, ROWS, 0xf, false)});
+}
+
+__device__ __forceinline__ double prefix_sum(double x) {
+  x += lanes_before<0x111, 0xf>(x);    // row_shr:1, 2, 4, 8
+  x += lanes_before<0x112, 0xf>(x);
+  x += lanes_before<0x114, 0xf>(x);
+  x += lanes_before<0x118, 0xf>(x);
+  x += lanes_before<0x142, 0xa>(x);    // row_bcast:15 into rows 1 and 3
+  x += lanes_before<0x143, 0xc>(x);    // row_bcast:31 into rows 2 and 3
   return x;
+}
+
+__device__ __forceinline__ double last_lane(double x) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  const i32x2 v = __builtin_bit_cast(i32x2, x);
+  return __builtin_bit_cast(double, i32x2{__builtin_amdgcn_readlane(v[0], 63), __builtin_amdgcn_readlane(v[1], 63)});
 }
 
 // The segment of a slot; false for a slot without one.
@@ -133,23 +179,23 @@ struct Segment {
   int start, length;        // those of the sequence
 };
 
-__device__ __forceinline__ int segments_of(int tokens, int L) { return (tokens + L - 1) / L; }
+__device__ __forceinline__ int segments_of(int tokens, int L) { return ((uint32_t)tokens + L - 1) / (uint32_t)L; }
 
-__device__ __forceinline__ bool find_segment(const int* cu, int sequences, long long tokens, int L, long long slot, Segment* s) {
+__device__ __forceinline__ bool find_segment(const int* cu, int sequences, long long tokens, int L, int slot, Segment* s) {
   int lo = 0, hi = sequences - 1;
   const int t = (int)tokens;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (min(max(cu[mid], 0), t) / L + (long long)mid <= slot) lo = mid;
+    if (min(max(cu[mid], 0), t) / (uint32_t)L + mid <= (uint32_t)slot) lo = mid;
     else hi = mid - 1;
   }
   int a, b;
   seq_bounds(cu, lo, tokens, &a, &b);
-  const long long c = slot - (a / L + (long long)lo);
+  const int c = slot - (int)(a / (uint32_t)L + lo);
   const int count = max(1, segments_of(b - a, L));   // an empty sequence has one of no tokens
   if (c < 0 || c >= count) return false;
   s->seq = __builtin_amdgcn_readfirstlane(lo);
-  s->c = __builtin_amdgcn_readfirstlane((int)c);
+  s->c = __builtin_amdgcn_readfirstlane(c);
   s->start = __builtin_amdgcn_readfirstlane(a);
   s->count = __builtin_amdgcn_readfirstlane(count);
   s->length = __builtin_amdgcn_readfirstlane(b - a);
@@ -159,8 +205,8 @@ __device__ __forceinline__ bool find_segment(const int* cu, int sequences, long 
 }
 
 // Place of the state between segments c and c + 1 of a sequence that starts at `start`.  Such
-// bounds are L or more tokens apart, in one sequence and from one to the next.
-__device__ __forceinline__ long long bound_of(int start, int c, int L) { return ((long long)start + (c + 1LL) * L) / L - 1; }
+// bounds are L or more tokens apart, in one sequence and from one to the next: (start + (c + 1) L) / L - 1.
+__device__ __forceinline__ long long bound_of(int start, int c, int L) { return start / (uint32_t)L + c; }
 
 // Whether an earlier sequence uses this slot, and the next one that does (or `sequences`).  Every wavefront for itself.
 __device__ __forceinline__ void same_slot(const int* slots, int sequences, int seq, bool* earlier, int* next) {
@@ -188,30 +234,32 @@ struct State {
 #pragma unroll
       for (int j = 0; j < CT; ++j) t[i][j] = zero4();
   }
-  template <bool LOAD>
-  __device__ __forceinline__ void move(float* p, int rows, int columns, bool transposed, int w, int lane) {
+  // From or to [rows][columns] in memory, or its transpose (TR).  What is behind either width is zero, or dropped: its lanes'
+  // offsets are kNowhere, and the scalar offsets of the others stay inside.
+  template <bool LOAD, bool TR>
+  __device__ __forceinline__ void move(float* p, int rows, int columns, int w, int lane) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    asm volatile("" : "+v"(lane));               // offsets are made here and not kept in registers through the chunks
     const int lr = lane % 16, lg = lane / 16;
+    const buf_t b = buf(p, (uint32_t)rows * columns * 4);
 #pragma unroll
     for (int j = 0; j < CT; ++j) {
       const int col = CT == 2 ? 32 * w + 8 * (lr / 4) + 4 * j + lr % 4 : 16 * w + lr;
+      const uint32_t base = TR ? (uint32_t)(col * rows + 8 * lg) * 4 : (uint32_t)(8 * lg * columns + col) * 4;
 #pragma unroll
       for (int i = 0; i < KS * 2; ++i) {
-        const int row = 32 * (i / 2) + 8 * lg + 4 * (i % 2);
-        if (col < columns && row < rows) {
-          if (transposed) {
-            float4* at = reinterpret_cast<float4*>(p + (size_t)col * rows + row);
-            if constexpr (LOAD) t[i][j] = *reinterpret_cast<f32x4*>(at);
-            else *reinterpret_cast<f32x4*>(at) = t[i][j];
-          } else {
+        const uint32_t at = col < columns && 32 * (i / 2) + 8 * lg < rows ? base : kNowhere;
+        const int row = 32 * (i / 2) + 4 * (i % 2);
+        if constexpr (TR) {
+          if constexpr (LOAD) t[i][j] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at, row * 4, 0));
+          else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, t[i][j]), b, at, row * 4, 0);
+        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float* at = p + (size_t)(row + r) * columns + col;
-              if constexpr (LOAD) t[i][j][r] = *at;
-              else *at = t[i][j][r];
-            }
+          for (int r = 0; r < 4; ++r) {
+            const int to = (row + r) * columns * 4;
+            if constexpr (LOAD) t[i][j][r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, at, to, 0));
+            else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(t[i][j][r]), b, at, to, 0);
           }
-        } else if constexpr (LOAD) {
-          t[i][j] = zero4();
         }
       }
     }
@@ -225,6 +273,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
   constexpr int CH = NT == 1 ? 64 : 32, RT = CH / 16, K2 = CH / 32;
   constexpr int U = KS * 4, UC = CT * 8;
   constexpr int es = NT == 1 ? 2 : 4;
+  constexpr bool TR = OUT && REV != DOT;       // dq and dk: states are [J][I] in memory
   __shared__ __align__(16) char As[OUT ? NT * CH * U * 16 : 16];
   __shared__ __align__(16) char Bs[NT * CH * U * 16];
   __shared__ __align__(16) char Cs[NT * CH * UC * 16];
@@ -240,13 +289,13 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
     // the blocks of P beside the diagonal that share a fragment with one that is used stay zero
     for (int i = tid; i < RT * K2 * TO * 64; i += kScanThreads) reinterpret_cast<uint4*>(P)[i] = make_uint4(0, 0, 0, 0);
   }
-  const long long units = s.slots * s.hk, blocks = (units + 7) / 8 * 8 * s.rep;
-  for (long long block = blockIdx.x; block < blocks; block += gridDim.x) {
+  const uint32_t units = s.slots * s.hk, blocks = (units + 7) / 8 * 8 * s.rep;
+  for (uint32_t block = blockIdx.x; block < blocks; block += gridDim.x) {
     // the value heads of a key head, which read the same rows, one after another on one XCD
-    const long long unit = block / 8 / s.rep * 8 + block % 8;
+    const uint32_t group = block / 8 / (uint32_t)s.rep, unit = group * 8 + block % 8;
     if (unit >= units) continue;
-    const int kh = (int)(unit % s.hk), h = kh * s.rep + (int)(block / 8 % s.rep);
-    const long long slot = unit / s.hk;
+    const uint32_t slot = unit / (uint32_t)s.hk;
+    const int kh = unit - slot * s.hk, h = kh * s.rep + (block / 8 - group * s.rep);
     Segment seg;
     if (!find_segment(s.cu, s.sequences, s.tokens, s.L, slot, &seg)) continue;
     const size_t cell = (size_t)I * J;
@@ -282,7 +331,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
       else if (in_place && seg.count > 1 && next == s.sequences) p = s.firsts + (size_t)(bound_of(seg.start, 0, s.L) * hv + h) * cell;
       else if (p && row >= 0) p += ((size_t)row * hv + h) * cell;
       else p = nullptr;
-      if (p) S.template move<true>(p, I, J, s.transposed, w, lane);
+      if (p) S.template move<true, TR>(p, I, J, w, lane);
       else S.zero();
     }
     const bool serial = next < s.sequences;     // in place, with others that name this slot behind it
@@ -306,8 +355,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
       };
       auto gates = [&](int at) {                // wavefront 3: cumulative gates and factors of the chunk that was fetched
         gate = gate < kLowestGate ? kLowestGate : gate;
-        const double G = prefix_sum(gate * 1.4426950408889634, lane);   // in units of log 2
-        const double Gn = __shfl(G, 63);
+        const double G = prefix_sum(gate * 1.4426950408889634);         // in units of log 2
+        const double Gn = last_lane(G);
         const float up = exp2_of((float)G), down = exp2_of((float)(Gn - G));
         Gs[at][lane] = G;
         fo[at][lane] = REV ? down : s.scale * up;
@@ -429,9 +478,12 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
           const uint32_t ob = s.out_bytes;
           const buf_t to = buf(s.out + (size_t)t0 * s.out_row + (size_t)h * J * ob, (uint32_t)(m - 1) * s.out_row + J * ob);
           const int col = CT == 2 ? 32 * w + 8 * lg : 16 * w + 4 * lg;
-          buf_t db = to;
-          if constexpr (DOT)
-            db = buf(s.d.p + (size_t)t0 * s.d.row + (size_t)(s.d.shared ? kh : h) * J * es, (uint32_t)(m - 1) * s.d.row + J * es);
+          Values<NT, 4 * CT> drow[DOT ? RT : 1];
+          if constexpr (DOT) {
+            const buf_t db = buf(s.d.p + (size_t)t0 * s.d.row + (size_t)(s.d.shared ? kh : h) * J * es, (uint32_t)(m - 1) * s.d.row + J * es);
+#pragma unroll
+            for (int x = 0; x < RT; ++x) drow[x].load(db, col < J ? (16 * x + lr) * s.d.row + col * es : kNowhere);
+          }
 #pragma unroll
           for (int x = 0; x < RT; ++x) {
 #pragma unroll
@@ -470,10 +522,9 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
                                                        to, off + 16 * j, 0, 0);
             }
             if constexpr (DOT) {
-              const uint32_t at_d = col < J ? (16 * x + lr) * s.d.row + col * es : kNowhere;
               float sum = 0.f;
 #pragma unroll
-              for (int r = 0; r < 4 * CT; ++r) sum = fmaf(v[r], raw_value(value_at<NT>(db, at_d + r * es)), sum);
+              for (int r = 0; r < 4 * CT; ++r) sum = fmaf(v[r], drow[x].value(r), sum);
               sum += __shfl_xor(sum, 16);
               sum += __shfl_xor(sum, 32);
               if (lg == 0) red[w][16 * x + lr] = sum;
@@ -498,11 +549,11 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
       n = __builtin_amdgcn_readfirstlane(b - a);
     }
     if constexpr (!OUT) {
-      S.template move<false>(s.between + (size_t)(bound_of(seg.start, REV ? seg.c - 1 : seg.c, s.L) * hv + h) * cell, I, J,
-                             s.transposed, w, lane);
-      if (tid == 3 * 64) s.decay[slot * hv + h] = exp2_of((float)total);
+      S.template move<false, TR>(s.between + (size_t)(bound_of(seg.start, REV ? seg.c - 1 : seg.c, s.L) * hv + h) * cell, I, J,
+                                 w, lane);
+      if (tid == 3 * 64) s.decay[(size_t)slot * hv + h] = exp2_of((float)total);
     } else if (s.to && keep && row >= 0 && (serial || (REV ? seg.c == 0 : seg.c == seg.count - 1))) {
-      S.template move<false>(s.to + ((size_t)row * hv + h) * cell, I, J, s.transposed, w, lane);
+      S.template move<false, TR>(s.to + ((size_t)row * hv + h) * cell, I, J, w, lane);
     }
   }
 }
