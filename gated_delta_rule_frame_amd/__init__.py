@@ -182,7 +182,8 @@ def workspace_size(problem: Problem, direction=BIDIRECTIONAL) -> int:
 
 KERNELS = ("seg_map_kernel", "seg_chain_kernel", "seg_out_kernel", "recurrent_kernel", "jac_map_kernel",
            "jac_out_kernel", "prologue_kernel", "scan_prep_kernel", "scan_kernel", "decode_kernel", "norm_kernels", "norm_grad_kernels",
-           "packed_prep_kernel", "packed_scan_kernel", "packed_scan_grad_kernel", "packed_grads_kernel")
+           "packed_prep_kernel", "packed_scan_kernel", "packed_scan_grad_kernel", "packed_grads_kernel", "linear_decode_kernel",
+           "linear_state_kernels", "linear_scan_kernels", "linear_gate_kernels", "rotary_kernel")
 
 
 def profile_enable(on: bool = True) -> None:

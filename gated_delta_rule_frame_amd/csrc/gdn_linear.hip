@@ -7,10 +7,12 @@
 namespace gdn {
 namespace {
 
+constexpr int kThreads = 256;
+
 // The states between segments from their sums, for every element of the state by itself: forward S <- e^{G} S + sum from the
 // initial state, reversed R <- e^{G} R + sum from the final state's gradient.
 template <bool REV>
-__global__ __launch_bounds__(kScanThreads) void linear_chain_kernel(ScanArgs s, int cell, int parts) {
+__global__ __launch_bounds__(kThreads) void linear_chain_kernel(ScanArgs s, int cell, int parts) {
   const int hv = s.hk * s.rep;
   const uint32_t items = (uint32_t)s.sequences * hv * parts;       // at most 2^20 * 16
   const bool in_place = s.from && s.from == s.to;
@@ -32,7 +34,7 @@ __global__ __launch_bounds__(kScanThreads) void linear_chain_kernel(ScanArgs s, 
         if (earlier || next < s.sequences) continue;
       }
     }
-    const int e = (part * kScanThreads + threadIdx.x) * 4;
+    const int e = (part * kThreads + threadIdx.x) * 4;
     if (e >= cell) continue;
     const long long slot = a / (uint32_t)s.L + seq;
     const long long b0 = bound_of(a, 0, s.L);
@@ -128,11 +130,11 @@ hipError_t linear_states(const ScanArgs& s, bool bf16, bool reversed, hipStream_
   hipError_t e = reversed ? (bf16 ? scan_variant<1, 3, true, false, false>(s, stream) : scan_variant<3, 3, true, false, false>(s, stream))
                           : (bf16 ? scan_variant<1, 3, false, false, false>(s, stream) : scan_variant<3, 3, false, false, false>(s, stream));
   if (e == hipSuccess) {
-    const int cell = s.b.width * s.c.width, parts = (cell + kScanThreads * 4 - 1) / (kScanThreads * 4);
+    const int cell = s.b.width * s.c.width, parts = (cell + kThreads * 4 - 1) / (kThreads * 4);
     const long long items = (long long)s.sequences * s.hk * s.rep * parts;
     const dim3 grid((unsigned)(items < kMaxBlocks ? items : kMaxBlocks));
-    if (reversed) hipLaunchKernelGGL(linear_chain_kernel<true>, grid, dim3(kScanThreads), 0, stream, s, cell, parts);
-    else hipLaunchKernelGGL(linear_chain_kernel<false>, grid, dim3(kScanThreads), 0, stream, s, cell, parts);
+    if (reversed) hipLaunchKernelGGL(linear_chain_kernel<true>, grid, dim3(kThreads), 0, stream, s, cell, parts);
+    else hipLaunchKernelGGL(linear_chain_kernel<false>, grid, dim3(kThreads), 0, stream, s, cell, parts);
     e = hipGetLastError();
   }
   prof_end(stream, GDN_KERNEL_LINEAR_STATES);

@@ -31,6 +31,7 @@ namespace gdn {
 
 constexpr int kScanThreads = 256;
 
+
 // Gates below this are this: e^-10000 is 0 in fp32, and G stays finite for -inf.
 constexpr float kLowestGate = -10000.f;
 
@@ -41,7 +42,7 @@ typedef s16x4 __attribute__((address_space(3)))* lds_s16x4;
 // u of row r at place u ^ swizzle(r).  Row fragments (16 rows, the same unit) and
 // transposed ones (4 rows, 16 columns) both touch every bank once.
 template <int U>
-__device__ __forceinline__ int swizzle(int r) {
+__device__ __forceinline__ uint32_t swizzle(uint32_t r) {
   if constexpr (U == 16) return (r & 3) << 2 | (r >> 2 & 3);
   else if constexpr (U == 8) return (r >> 1 & 1) << 2 | (r >> 2 & 3);
   else return r >> 2 & 3;
@@ -49,9 +50,9 @@ __device__ __forceinline__ int swizzle(int r) {
 
 // Rows row0 .. + 15, columns 32 ks + 8 (lane / 16) .. + 8: lane l has row l % 16.
 template <int NT, int U, int CH>
-__device__ __forceinline__ Frag<NT> row_frag(const char* tile, int row0, int ks, int lane) {
-  const int r = lane % 16;
-  const int at = (row0 + r) * U * 16 + ((ks * 4 + lane / 16) ^ swizzle<U>(r)) * 16;
+__device__ __forceinline__ Frag<NT> row_frag(const char* tile, int row0, int ks, uint32_t lane) {
+  const uint32_t r = lane % 16;
+  const uint32_t at = row0 * U * 16 + r * U * 16 + ((ks * 4 + lane / 16) ^ swizzle<U>(r)) * 16;
   Frag<NT> f;
 #pragma unroll
   for (int i = 0; i < NT; ++i) f.t[i] = as_frag(*reinterpret_cast<const uint4*>(tile + i * CH * U * 16 + at));
@@ -61,16 +62,16 @@ __device__ __forceinline__ Frag<NT> row_frag(const char* tile, int row0, int ks,
 // The transpose: lane l has column l % 16 of a tile whose columns are four pieces of
 // four, rows 32 k2 + 8 (l / 16) .. + 8.  `unit`, `sub`: where piece l % 4 lies in a row.
 template <int NT, int U, int CH>
-__device__ __forceinline__ Frag<NT> column_frag(const char* tile, int k2, int unit, int sub, int lane) {
-  const int r0 = 8 * (lane / 16) + lane % 16 / 4;
+__device__ __forceinline__ Frag<NT> column_frag(const char* tile, int k2, uint32_t unit, uint32_t sub, uint32_t lane) {
+  const uint32_t r0 = 8 * (lane / 16) + lane % 16 / 4;
   Frag<NT> f;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     s16x4 h[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int r = r0 + 4 * j;
-      const char* at = tile + i * CH * U * 16 + (32 * k2 + r) * U * 16 + (unit ^ swizzle<U>(r)) * 16 + sub;
+      const uint32_t r = r0 + 4 * j;
+      const char* at = tile + (i * CH + 32 * k2) * U * 16 + (r * U * 16 + (unit ^ swizzle<U>(r)) * 16 + sub);
       h[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)at);
     }
     typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -80,17 +81,19 @@ __device__ __forceinline__ Frag<NT> column_frag(const char* tile, int k2, int un
 }
 
 // A chunk's rows of one operand on their way into LDS.
-template <int NT, int U, int CH>
-struct Stage {
-  static constexpr int N = (CH * U + kScanThreads - 1) / kScanThreads;
+template <int NT, int U, int CH, int TH>
+struct Stage {                                  // TH: threads
+  static constexpr int N = (CH * U + TH - 1) / TH;
   uint4 r[N][NT == 1 ? 1 : 2];
 
-  __device__ __forceinline__ void load(buf_t b, uint32_t stride, int width, int tid) {
+  static constexpr uint32_t step = TH / U;          // rows from one vector of a thread to its next: a multiple of 16
+
+  __device__ __forceinline__ void load(buf_t b, uint32_t stride, int width, uint32_t tid) {
     constexpr uint32_t es = NT == 1 ? 2 : 4;
-    constexpr int step = kScanThreads / U;           // rows
     asm volatile("" : "+v"(tid));                    // offsets are made here and not kept in registers through the chunk
-    const int row = tid / U, u = tid % U;
-    uint32_t off = (CH * U % kScanThreads == 0 || tid < CH * U) && u * 8 < width ? row * stride + u * 8 * es : kNowhere;
+    const uint32_t row = tid / U, u = tid % U;
+    const bool in = (CH * U % TH == 0 || tid < CH * U) && (int)u * 8 < width;
+    uint32_t off = in ? row * stride + u * 8 * es : kNowhere;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       r[i][0] = buf_load16(b, off);
@@ -99,25 +102,29 @@ struct Stage {
     }
   }
 
-  __device__ __forceinline__ void store(char* tile, int tid) const {
+  __device__ __forceinline__ void store(char* tile, uint32_t tid) const {
+    asm volatile("" : "+v"(tid));
+    const uint32_t row = tid / U, u = tid % U;
+    char* to = tile + row * U * 16 + (u ^ swizzle<U>(row)) * 16;
+    if (CH * U % TH && tid >= CH * U) return;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int at = i * kScanThreads + tid, row = at / U, u = at % U;
-      if (CH * U % kScanThreads && at >= CH * U) break;
-      char* to = tile + row * U * 16 + (u ^ swizzle<U>(row)) * 16;
       if constexpr (NT == 1) {
-        *reinterpret_cast<uint4*>(to) = r[i][0];
+        *reinterpret_cast<uint4*>(to + i * step * U * 16) = r[i][0];
       } else {
         RawFrag<3> raw;
         raw.a = r[i][0];
         raw.b = r[i][1];
         const Frag<3> f = frag_of<3>(raw);
 #pragma unroll
-        for (int t = 0; t < 3; ++t) *reinterpret_cast<uint4*>(to + t * CH * U * 16) = as_bits(f.t[t]);
+        for (int t = 0; t < 3; ++t) *reinterpret_cast<uint4*>(to + (i * step + t * CH) * U * 16) = as_bits(f.t[t]);
       }
     }
   }
 };
+
+// Keeps loads from LDS a step ahead of the products that use them: nothing is scheduled across.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
 // N (4 or 8) consecutive input values.
 template <int NT, int N>
@@ -237,18 +244,18 @@ struct State {
   // From or to [rows][columns] in memory, or its transpose (TR).  What is behind either width is zero, or dropped: its lanes'
   // offsets are kNowhere, and the scalar offsets of the others stay inside.
   template <bool LOAD, bool TR>
-  __device__ __forceinline__ void move(float* p, int rows, int columns, int w, int lane) {
+  __device__ __forceinline__ void move(float* p, int rows, int columns, int w, uint32_t lane) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     asm volatile("" : "+v"(lane));               // offsets are made here and not kept in registers through the chunks
-    const int lr = lane % 16, lg = lane / 16;
+    const uint32_t lr = lane % 16, lg = lane / 16;
     const buf_t b = buf(p, (uint32_t)rows * columns * 4);
 #pragma unroll
     for (int j = 0; j < CT; ++j) {
-      const int col = CT == 2 ? 32 * w + 8 * (lr / 4) + 4 * j + lr % 4 : 16 * w + lr;
+      const uint32_t col = CT == 2 ? 32 * w + 8 * (lr / 4) + 4 * j + lr % 4 : 16 * w + lr;
       const uint32_t base = TR ? (uint32_t)(col * rows + 8 * lg) * 4 : (uint32_t)(8 * lg * columns + col) * 4;
 #pragma unroll
       for (int i = 0; i < KS * 2; ++i) {
-        const uint32_t at = col < columns && 32 * (i / 2) + 8 * lg < rows ? base : kNowhere;
+        const uint32_t at = (int)col < columns && (int)(32 * (i / 2) + 8 * lg) < rows ? base : kNowhere;
         const int row = 32 * (i / 2) + 4 * (i % 2);
         if constexpr (TR) {
           if constexpr (LOAD) t[i][j] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at, row * 4, 0));
@@ -270,25 +277,23 @@ struct State {
 // arithmetic; two (2^-17 of a product) are far below the rounding of a bf16 output.
 template <int NT, int TO, int KS, int CT, bool REV, bool OUT, bool DOT>
 __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s) {
+  constexpr int TH = kScanThreads, NW = TH / 64;
   constexpr int CH = NT == 1 ? 64 : 32, RT = CH / 16, K2 = CH / 32;
-  constexpr int U = KS * 4, UC = CT * 8;
+  constexpr int U = KS * 4, UC = NW * CT * 2;
   constexpr int es = NT == 1 ? 2 : 4;
   constexpr bool TR = OUT && REV != DOT;       // dq and dk: states are [J][I] in memory
   __shared__ __align__(16) char As[OUT ? NT * CH * U * 16 : 16];
   __shared__ __align__(16) char Bs[NT * CH * U * 16];
   __shared__ __align__(16) char Cs[NT * CH * UC * 16];
   __shared__ __align__(16) bh P[OUT ? RT * K2 * TO * 512 : 8];
-  __shared__ __align__(16) double Gs[2][64];
-  __shared__ __align__(16) float fo[2][64], fs[2][64];
-  __shared__ float red[DOT ? 4 : 1][CH];
-  const int tid = threadIdx.x, lane = tid % 64, w = __builtin_amdgcn_readfirstlane(tid / 64);
-  const int lr = lane % 16, lg = lane / 16;
+  __shared__ __align__(16) float Gh[2][64], Gl[2][64];   // G = Gh + Gl to 48 bits: its differences have the accuracy of fp32
+  __shared__ __align__(16) float fo[2][64], fs[2][64], all[2];
+  __shared__ float red[DOT ? NW : 1][CH];
+  const uint32_t tid = threadIdx.x;
+  const int w = __builtin_amdgcn_readfirstlane(tid / 64);
+  uint32_t lane = tid % 64;
   const int I = s.b.width, J = s.c.width, hv = s.hk * s.rep;
 
-  if constexpr (OUT) {
-    // the blocks of P beside the diagonal that share a fragment with one that is used stay zero
-    for (int i = tid; i < RT * K2 * TO * 64; i += kScanThreads) reinterpret_cast<uint4*>(P)[i] = make_uint4(0, 0, 0, 0);
-  }
   const uint32_t units = s.slots * s.hk, blocks = (units + 7) / 8 * 8 * s.rep;
   for (uint32_t block = blockIdx.x; block < blocks; block += gridDim.x) {
     // the value heads of a key head, which read the same rows, one after another on one XCD
@@ -338,169 +343,273 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
     int seq = seg.seq, first = seg.first, n = serial ? seg.length : seg.n;
     for (;;) {
       const int chunks = (n + CH - 1) / CH;
-      Stage<NT, U, CH> ra, rb;
-      Stage<NT, UC, CH> rc;
+      Stage<NT, U, CH, TH> ra, rb;
+      Stage<NT, UC, CH, TH> rc;
       float gate = 0.f;
-      auto fetch = [&](int i) {                 // the i-th chunk in the scan's order; behind the last: nothing
+      // operands (bits: a, b, c) of the i-th chunk in the scan's order; behind the last: nothing
+      auto fetch = [&](int i, int which) {
         const int k = i < chunks ? (REV ? chunks - 1 - i : i) : 0, t0 = first + k * CH;
         const int m = i < chunks ? min(CH, n - k * CH) : 0;
         auto rows = [&](const Operand& o) {
           return buf(o.p + (size_t)t0 * o.row + (size_t)(o.shared ? kh : h) * o.width * es,
                      m > 0 ? (uint32_t)(m - 1) * o.row + o.width * es : 0);
         };
-        if constexpr (OUT) ra.load(rows(s.a), s.a.row, I, tid);
-        rb.load(rows(s.b), s.b.row, I, tid);
-        rc.load(rows(s.c), s.c.row, J, tid);
-        if (w == 3) gate = lane < m ? s.g[s.fixed ? h : (size_t)(t0 + lane) * hv + h] : 0.f;
+        if constexpr (OUT) {
+          if (which & 1) ra.load(rows(s.a), s.a.row, I, tid);
+        }
+        if (which & 2) rb.load(rows(s.b), s.b.row, I, tid);
+        if (which & 4) rc.load(rows(s.c), s.c.row, J, tid);
+        if ((which & 4) && w == 3) gate = (int)lane < m ? s.g[s.fixed ? h : (size_t)(t0 + lane) * hv + h] : 0.f;
       };
       auto gates = [&](int at) {                // wavefront 3: cumulative gates and factors of the chunk that was fetched
         gate = gate < kLowestGate ? kLowestGate : gate;
         const double G = prefix_sum(gate * 1.4426950408889634);         // in units of log 2
         const double Gn = last_lane(G);
         const float up = exp2_of((float)G), down = exp2_of((float)(Gn - G));
-        Gs[at][lane] = G;
+        const float hi = (float)G;
+        Gh[at][lane] = hi;
+        Gl[at][lane] = (float)(G - hi);
+        if (lane == 0) all[at] = exp2_of((float)Gn);
         fo[at][lane] = REV ? down : s.scale * up;
         fs[at][lane] = REV ? s.scale * up : down;
         total += Gn;
       };
-      fetch(0);
+      auto dot_of = [&] {                       // a token's sum over the columns
+        float x = red[0][tid];
+#pragma unroll
+        for (int j = 1; j < NW; ++j) x += red[j][tid];
+        return x;
+      };
+      fetch(0, 7);
       __syncthreads();                          // the gates and tiles of what ran before have been read
       if (w == 3) gates(0);
       for (int i = 0; i < chunks; ++i) {
         const int k = REV ? chunks - 1 - i : i, at = i & 1;
         const int t0 = first + k * CH, m = min(CH, n - k * CH);
+        asm volatile("" : "+v"(lane));         // addresses in LDS are made in each chunk and not kept in registers
+        const uint32_t lr = lane % 16, lg = lane / 16;
         if (i) __syncthreads();                 // the previous tiles have been read
         if constexpr (OUT) ra.store(As, tid);
         rb.store(Bs, tid);
-        rc.store(Cs, tid);
+        if constexpr (!OUT) rc.store(Cs, tid);
         if constexpr (DOT) {
           if (i && tid < CH) {
             const int b0 = REV ? t0 + CH : t0 - CH;
-            if (b0 + tid < first + n) s.dot[(size_t)h * s.tokens + b0 + tid] = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
+            if (b0 + (int)tid < first + n) s.dot[(size_t)h * s.tokens + b0 + tid] = dot_of();
           }
         }
-        fetch(i + 1);
         __syncthreads();
 
         f32x4 o[RT][CT];
         if constexpr (OUT) {
-          // P: rows x of A, y of B; a lane holds four y of one x, which is half a vector of P's fragment
-          for (int id = w; id < RT * (RT + 1) / 2; id += 4) {
-            const int hi = id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3, lo = id - hi * (hi + 1) / 2;
-            const int tx = REV ? lo : hi, ty = REV ? hi : lo;
-            f32x4 d = zero4();
+          rc.store(Cs, tid);
+          fetch(i + 1, 2);
+          // P: rows x of A, y of B; a lane holds four y of one x, which is half a vector of P's fragment.  Its blocks above the
+          // diagonal that share a fragment with one below are formed too, as zeros: three blocks a wavefront (one of four with
+          // chunks of 32).  Their gates run between the products of the state's part, out = A S, whose operands are read and
+          // split a step ahead.
+          constexpr int T = RT == 4 ? 3 : 1;
+          int tx[T], ty[T];
+          f32x4 d[T];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-              d = mma<NT, NT>(row_frag<NT, U, CH>(Bs, 16 * ty, ks, lane), row_frag<NT, U, CH>(As, 16 * tx, ks, lane), d);
-            const double Gx = Gs[at][16 * tx + lr];
-            float x[4];
+          for (int t = 0; t < T; ++t) {
+            if constexpr (RT == 4) {
+              tx[t] = w < 2 || t == 0 ? 2 + (w & 1) : w & 1;
+              ty[t] = w < 2 ? t : t == 0 ? 3 : t - 1;
+            } else {
+              tx[t] = w / 2;
+              ty[t] = w % 2;
+            }
+            if constexpr (REV) {
+              tx[t] = RT - 1 - tx[t];
+              ty[t] = RT - 1 - ty[t];
+            }
+            d[t] = zero4();
+          }
+          Frag<NT> fa[2][T], fb[2][T], af[2][RT];
+          const auto blocks_at = [&](int ks) {
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+              fb[ks % 2][t] = row_frag<NT, U, CH>(Bs, 16 * ty[t], ks, lane);
+              fa[ks % 2][t] = row_frag<NT, U, CH>(As, 16 * tx[t], ks, lane);
+            }
+          };
+          const auto rows_at = [&](int ks) {
+#pragma unroll
+            for (int x = 0; x < RT; ++x) af[ks % 2][x] = row_frag<NT, U, CH>(As, 16 * x, ks, lane);
+          };
+          const auto terms_of = [&](int ks, int j) {
+            const f32x4 u = S.t[2 * ks][j], v = S.t[2 * ks + 1][j];
+            const float e[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+            return split8<TO>(e);
+          };
+          blocks_at(0);
+          fence();
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            if (ks + 1 < KS) blocks_at(ks + 1);
+            else rows_at(0);
+            fence();
+#pragma unroll
+            for (int t = 0; t < T; ++t) d[t] = mma<NT, NT>(fb[ks % 2][t], fa[ks % 2][t], d[t]);
+            fence();
+          }
+          const auto gate_block = [&](int t) {
+            const uint32_t x = 16 * tx[t] + lr, y = 16 * ty[t] + 4 * lg;
+            const float hx = Gh[at][x], lx = Gl[at][x];
+            const f32x4 hy = *reinterpret_cast<const f32x4*>(&Gh[at][y]), ly = *reinterpret_cast<const f32x4*>(&Gl[at][y]);
+            float p[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const double e = Gx - Gs[at][16 * ty + 4 * lg + r];
-              const bool in = REV ? 16 * ty + 4 * lg + r >= 16 * tx + lr : 16 * ty + 4 * lg + r <= 16 * tx + lr;
-              x[r] = in ? s.scale * exp2_of((float)(REV ? -e : e)) * d[r] : 0.f;
+              const float e = REV ? (hy[r] - hx) + (ly[r] - lx) : (hx - hy[r]) + (lx - ly[r]);
+              p[r] = s.scale * exp2_of((REV ? y + r >= x : y + r <= x) ? e : -INFINITY) * d[t][r];
             }
             uint32_t p0[TO], p1[TO];
-            split2<TO>(x[0], x[1], p0);
-            split2<TO>(x[2], x[3], p1);
-            bh* to = P + (tx * K2 + ty / 2) * TO * 512 + (((ty & 1) * 2 + lg / 2) * 16 + lr) * 8 + (lg & 1) * 4;
+            split2<TO>(p[0], p[1], p0);
+            split2<TO>(p[2], p[3], p1);
+            bh* to = P + (tx[t] * K2 + ty[t] / 2) * TO * 512 + (((ty[t] & 1) * 2 + lg / 2) * 16 + lr) * 8 + (lg & 1) * 4;
 #pragma unroll
-            for (int t = 0; t < TO; ++t) *reinterpret_cast<uint2*>(to + t * 512) = make_uint2(p0[t], p1[t]);
-          }
-          // the state's part
+            for (int i2 = 0; i2 < TO; ++i2) *reinterpret_cast<uint2*>(to + i2 * 512) = make_uint2(p0[i2], p1[i2]);
+          };
 #pragma unroll
           for (int x = 0; x < RT; ++x)
 #pragma unroll
             for (int j = 0; j < CT; ++j) o[x][j] = zero4();
+          Frag<TO> sf[2];
+          sf[0] = terms_of(0, 0);
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            Frag<NT> af[RT];
+          for (int n = 0; n < KS * CT; ++n) {
+            const int ks = n / CT, j = n % CT;
+            if (j == 0 && ks + 1 < KS) rows_at(ks + 1);
+            if (n + 1 < KS * CT) sf[(n + 1) % 2] = terms_of((n + 1) / CT, (n + 1) % CT);
+            fence();
 #pragma unroll
-            for (int x = 0; x < RT; ++x) af[x] = row_frag<NT, U, CH>(As, 16 * x, ks, lane);
+            for (int x = 0; x < RT; ++x) o[x][j] = mma<TO, NT>(sf[n % 2], af[ks % 2][x], o[x][j]);
+            // T blocks over the KS * CT steps
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-              const f32x4 u = S.t[2 * ks][j], v = S.t[2 * ks + 1][j];
-              const float e[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
-              const Frag<TO> sf = split8<TO>(e);
-#pragma unroll
-              for (int x = 0; x < RT; ++x) o[x][j] = mma<TO, NT>(sf, af[x], o[x][j]);
-            }
+            for (int t = 0; t < T; ++t)
+              if (n == t * KS * CT / T) gate_block(t);
+            fence();
           }
+          fetch(i + 1, 4);
 #pragma unroll
           for (int x = 0; x < RT; ++x) {
             const float f = fo[at][16 * x + lr];
 #pragma unroll
             for (int j = 0; j < CT; ++j) o[x][j] *= f;
           }
+          __syncthreads();                      // P and C are there
+          fetch(i + 1, 1);
+        } else {
+          fetch(i + 1, 6);
         }
-        // columns of C, as they are and as they go into the state
-        Frag<NT> cf[K2][CT];
-        const int piece = lane % 4;
+        // Columns of C, as they are and, times the decay up to the chunk's end, as they go into the state: formed between the
+        // products of P C and of the state's update, whose operands are read a step ahead.
+        Frag<NT> cf[K2][CT], bf[2];
+        Frag<TO> pf[2][K2];
+        Frag<3> vf[2][CT];
+        float decays[2][8];
+        const uint32_t piece = lane % 4;
+        const auto decays_at = [&](int k2) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<f32x4*>(&decays[k2 % 2][4 * e]) = *reinterpret_cast<const f32x4*>(&fs[at][32 * k2 + 8 * lg + 4 * e]);
+        };
+        const auto columns_of = [&](int k2, int j, int pair) {        // values 2 pair, 2 pair + 1 of the eight
+          float x[2] = {0.f, 0.f};
+#pragma unroll
+          for (int t = NT - 1; t >= 0; --t) {
+            const uint4 b = as_bits(cf[k2][j].t[t]);
+            const uint32_t word = pair == 0 ? b.x : pair == 1 ? b.y : pair == 2 ? b.z : b.w;
+            x[0] += __uint_as_float(word << 16);
+            x[1] += __uint_as_float(word & 0xffff0000u);
+          }
+          uint32_t v[3];
+          split2<3>(x[0] * decays[k2 % 2][2 * pair], x[1] * decays[k2 % 2][2 * pair + 1], v);
+#pragma unroll
+          for (int t = 0; t < 3; ++t) {
+            uint4 b = as_bits(vf[k2 % 2][j].t[t]);
+            (pair == 0 ? b.x : pair == 1 ? b.y : pair == 2 ? b.z : b.w) = v[t];
+            vf[k2 % 2][j].t[t] = as_frag(b);
+          }
+        };
+        const auto p_at = [&](int x) {
+#pragma unroll
+          for (int k2 = REV ? x / 2 : 0; k2 < (REV ? K2 : x / 2 + 1); ++k2)
+#pragma unroll
+            for (int t = 0; t < TO; ++t)
+              pf[x % 2][k2].t[t] = as_frag(*reinterpret_cast<const uint4*>(P + ((x * K2 + k2) * TO + t) * 512 + lane * 8));
+        };
+        const auto b_at = [&](int n) {          // step n: rows of tile n % (2 KS), tokens of half n / (2 KS)
+          const int i2 = n % (2 * KS);
+          bf[n % 2] = column_frag<NT, U, CH>(Bs, n / (2 * KS), 4 * (i2 / 2) + piece, 8 * (i2 % 2), lane);
+        };
 #pragma unroll
         for (int k2 = 0; k2 < K2; ++k2)
 #pragma unroll
           for (int j = 0; j < CT; ++j)
             cf[k2][j] = column_frag<NT, UC, CH>(Cs, k2, CT == 2 ? 4 * w + piece : 2 * w + piece / 2, CT == 2 ? 8 * j : piece % 2 * 8, lane);
-        const float all = exp2_of((float)Gs[at][CH - 1]);
+        decays_at(0);
+        const float decay = all[at];
+        if constexpr (OUT) {
+          p_at(0);
+          fence();
 #pragma unroll
-        for (int i2 = 0; i2 < KS * 2; ++i2)
+          for (int x = 0; x < RT; ++x) {
+            if (x + 1 < RT) p_at(x + 1);
+            else b_at(0);
+            fence();
 #pragma unroll
-          for (int j = 0; j < CT; ++j) S.t[i2][j] *= all;
+            for (int k2 = REV ? x / 2 : 0; k2 < (REV ? K2 : x / 2 + 1); ++k2)
 #pragma unroll
-        for (int k2 = 0; k2 < K2; ++k2) {
-          Frag<3> vf[CT];
-          const float* f = &fs[at][32 * k2 + 8 * lg];
+              for (int j = 0; j < CT; ++j) o[x][j] = mma<NT, TO>(cf[k2][j], pf[x % 2][k2], o[x][j]);
 #pragma unroll
-          for (int j = 0; j < CT; ++j) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              x[e] = 0.f;
-#pragma unroll
-              for (int t = NT - 1; t >= 0; --t) {
-                const uint4 b = as_bits(cf[k2][j].t[t]);
-                const uint32_t word = e / 2 == 0 ? b.x : e / 2 == 1 ? b.y : e / 2 == 2 ? b.z : b.w;
-                x[e] += __uint_as_float(e % 2 ? word & 0xffff0000u : word << 16);
-              }
-              x[e] *= f[e];
-            }
-            vf[j] = split8<3>(x);
+            for (int n = x * 4 * CT / RT; n < (x + 1) * 4 * CT / RT; ++n) columns_of(0, n / 4, n % 4);
+            fence();
           }
+        } else {
+          b_at(0);
 #pragma unroll
-          for (int i2 = 0; i2 < KS * 2; ++i2) {
-            const Frag<NT> bf = column_frag<NT, U, CH>(Bs, k2, 4 * (i2 / 2) + piece, 8 * (i2 % 2), lane);
+          for (int n = 0; n < 4 * CT; ++n) columns_of(0, n / 4, n % 4);
+        }
 #pragma unroll
-            for (int j = 0; j < CT; ++j) S.t[i2][j] = mma<NT, 3>(bf, vf[j], S.t[i2][j]);
+        for (int n = 0; n < K2 * 2 * KS; ++n) {
+          const int i2 = n % (2 * KS), k2 = n / (2 * KS);
+          if (n + 1 < K2 * 2 * KS) b_at(n + 1);
+          if (i2 == 0 && k2 + 1 < K2) decays_at(k2 + 1);
+          if (k2 == 0) {
+#pragma unroll
+            for (int j = 0; j < CT; ++j) S.t[i2][j] *= decay;
           }
+          fence();
+#pragma unroll
+          for (int j = 0; j < CT; ++j) S.t[i2][j] = mma<NT, 3>(bf[n % 2], vf[k2 % 2][j], S.t[i2][j]);
+          if (k2 + 1 < K2) {
+#pragma unroll
+            for (int c = i2 * 4 * CT / (2 * KS); c < (i2 + 1) * 4 * CT / (2 * KS); ++c) columns_of(k2 + 1, c / 4, c % 4);
+          }
+          fence();
         }
         if constexpr (OUT) {
-          __syncthreads();                      // P is there
           const uint32_t ob = s.out_bytes;
           const buf_t to = buf(s.out + (size_t)t0 * s.out_row + (size_t)h * J * ob, (uint32_t)(m - 1) * s.out_row + J * ob);
-          const int col = CT == 2 ? 32 * w + 8 * lg : 16 * w + 4 * lg;
+          const uint32_t col = CT == 2 ? 32 * w + 8 * lg : 16 * w + 4 * lg;
           Values<NT, 4 * CT> drow[DOT ? RT : 1];
           if constexpr (DOT) {
             const buf_t db = buf(s.d.p + (size_t)t0 * s.d.row + (size_t)(s.d.shared ? kh : h) * J * es, (uint32_t)(m - 1) * s.d.row + J * es);
 #pragma unroll
-            for (int x = 0; x < RT; ++x) drow[x].load(db, col < J ? (16 * x + lr) * s.d.row + col * es : kNowhere);
+            for (int x = 0; x < RT; ++x) drow[x].load(db, (int)col < J ? (16 * x + lr) * s.d.row + col * es : kNowhere);
           }
 #pragma unroll
           for (int x = 0; x < RT; ++x) {
-#pragma unroll
-            for (int k2 = REV ? x / 2 : 0; k2 < (REV ? K2 : x / 2 + 1); ++k2) {
-              Frag<TO> pf;
-#pragma unroll
-              for (int t = 0; t < TO; ++t)
-                pf.t[t] = as_frag(*reinterpret_cast<const uint4*>(P + ((x * K2 + k2) * TO + t) * 512 + lane * 8));
-#pragma unroll
-              for (int j = 0; j < CT; ++j) o[x][j] = mma<NT, TO>(cf[k2][j], pf, o[x][j]);
-            }
             float v[4 * CT];
 #pragma unroll
             for (int j = 0; j < CT; ++j)
 #pragma unroll
               for (int r = 0; r < 4; ++r) v[4 * j + r] = o[x][j][r];
-            const uint32_t off = col < J ? (16 * x + lr) * s.out_row + col * ob : kNowhere;
+            const uint32_t off = (int)col < J ? (16 * x + lr) * s.out_row + col * ob : kNowhere;
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
             if (ob == 2) {
               uint32_t b[2 * CT];
 #pragma unroll
@@ -509,12 +618,9 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
                 split2<1>(v[2 * r], v[2 * r + 1], one);
                 b[r] = one[0];
               }
-              typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-              typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
               if constexpr (CT == 2) __builtin_amdgcn_raw_buffer_store_b128(u32x4{b[0], b[1], b[2], b[3]}, to, off, 0, 0);
               else __builtin_amdgcn_raw_buffer_store_b64(u32x2{b[0], b[1]}, to, off, 0, 0);
             } else {
-              typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
               for (int j = 0; j < CT; ++j)
                 __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
@@ -536,8 +642,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
       if constexpr (DOT) {
         __syncthreads();
         const int b0 = REV ? first : first + (chunks - 1) * CH;
-        if (chunks > 0 && tid < CH && b0 + tid < first + n)
-          s.dot[(size_t)h * s.tokens + b0 + tid] = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
+        if (chunks > 0 && tid < CH && b0 + (int)tid < first + n)
+          s.dot[(size_t)h * s.tokens + b0 + tid] = dot_of();
       }
       if (!serial || next >= s.sequences) break;
       seq = next;
