@@ -286,8 +286,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
   __shared__ __align__(16) char Bs[NT * CH * U * 16];
   __shared__ __align__(16) char Cs[NT * CH * UC * 16];
   __shared__ __align__(16) bh P[OUT ? RT * K2 * TO * 512 : 8];
-  __shared__ __align__(16) float Gh[2][64], Gl[2][64];   // G = Gh + Gl to 48 bits: its differences have the accuracy of fp32
-  __shared__ __align__(16) float fo[2][64], fs[2][64], all[2];
+  __shared__ __align__(16) float Gh[4][64], Gl[4][64];   // G = Gh + Gl to 48 bits: its differences have the accuracy of fp32
+  __shared__ __align__(16) float fo[4][64], fs[4][64], all[4];
   __shared__ float red[DOT ? NW : 1][CH];
   const uint32_t tid = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
       if (REV ? seg.c == 0 : seg.c == seg.count - 1) continue;
     }
     State<KS, CT> S;
-    double total = 0;                           // wavefront 3: of the gates
+    double total = 0;                           // of the gates of the wavefront's chunks
     if constexpr (!OUT) {
       S.zero();
     } else {
@@ -359,19 +359,24 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
         }
         if (which & 2) rb.load(rows(s.b), s.b.row, I, tid);
         if (which & 4) rc.load(rows(s.c), s.c.row, J, tid);
-        if ((which & 4) && w == 3) gate = (int)lane < m ? s.g[s.fixed ? h : (size_t)(t0 + lane) * hv + h] : 0.f;
       };
-      auto gates = [&](int at) {                // wavefront 3: cumulative gates and factors of the chunk that was fetched
+      // Four chunks at a time, the wavefront's one of them: its gates, loaded long before, then their sums and factors.
+      auto fetch_gates = [&](int i) {
+        const int k = i < chunks ? (REV ? chunks - 1 - i : i) : 0, t0 = first + k * CH;
+        const int m = i < chunks ? min(CH, n - k * CH) : 0;
+        gate = (int)lane < m ? s.g[s.fixed ? h : (size_t)(t0 + lane) * hv + h] : 0.f;
+      };
+      auto gates = [&] {
         gate = gate < kLowestGate ? kLowestGate : gate;
         const double G = prefix_sum(gate * 1.4426950408889634);         // in units of log 2
         const double Gn = last_lane(G);
         const float up = exp2_of((float)G), down = exp2_of((float)(Gn - G));
         const float hi = (float)G;
-        Gh[at][lane] = hi;
-        Gl[at][lane] = (float)(G - hi);
-        if (lane == 0) all[at] = exp2_of((float)Gn);
-        fo[at][lane] = REV ? down : s.scale * up;
-        fs[at][lane] = REV ? s.scale * up : down;
+        Gh[w][lane] = hi;
+        Gl[w][lane] = (float)(G - hi);
+        if (lane == 0) all[w] = exp2_of((float)Gn);
+        fo[w][lane] = REV ? down : s.scale * up;
+        fs[w][lane] = REV ? s.scale * up : down;
         total += Gn;
       };
       auto dot_of = [&] {                       // a token's sum over the columns
@@ -380,18 +385,21 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
         for (int j = 1; j < NW; ++j) x += red[j][tid];
         return x;
       };
+      fetch_gates(w);
       fetch(0, 7);
-      __syncthreads();                          // the gates and tiles of what ran before have been read
-      if (w == 3) gates(0);
       for (int i = 0; i < chunks; ++i) {
-        const int k = REV ? chunks - 1 - i : i, at = i & 1;
+        const int k = REV ? chunks - 1 - i : i, at = i & 3;
         const int t0 = first + k * CH, m = min(CH, n - k * CH);
         asm volatile("" : "+v"(lane));         // addresses in LDS are made in each chunk and not kept in registers
         const uint32_t lr = lane % 16, lg = lane / 16;
-        if (i) __syncthreads();                 // the previous tiles have been read
+        __syncthreads();                        // the previous tiles and gates have been read
         if constexpr (OUT) ra.store(As, tid);
         rb.store(Bs, tid);
         if constexpr (!OUT) rc.store(Cs, tid);
+        if (at == 0) {
+          gates();
+          fetch_gates(i + 4 + w);
+        }
         if constexpr (DOT) {
           if (i && tid < CH) {
             const int b0 = REV ? t0 + CH : t0 - CH;
@@ -402,8 +410,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
 
         f32x4 o[RT][CT];
         if constexpr (OUT) {
+          fetch(i + 1, 3);
           rc.store(Cs, tid);
-          fetch(i + 1, 2);
           // P: rows x of A, y of B; a lane holds four y of one x, which is half a vector of P's fragment.  Its blocks above the
           // diagonal that share a fragment with one below are formed too, as zeros: three blocks a wavefront (one of four with
           // chunks of 32).  Their gates run between the products of the state's part, out = A S, whose operands are read and
@@ -454,10 +462,18 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
             for (int t = 0; t < T; ++t) d[t] = mma<NT, NT>(fb[ks % 2][t], fa[ks % 2][t], d[t]);
             fence();
           }
+          fetch(i + 1, 4);
+          float hx, lx;
+          f32x4 hy, ly;
+          const auto gates_at = [&](int t) {
+            const uint32_t x = 16 * tx[t] + lr, y = 16 * ty[t] + 4 * lg;
+            hx = Gh[at][x];
+            lx = Gl[at][x];
+            hy = *reinterpret_cast<const f32x4*>(&Gh[at][y]);
+            ly = *reinterpret_cast<const f32x4*>(&Gl[at][y]);
+          };
           const auto gate_block = [&](int t) {
             const uint32_t x = 16 * tx[t] + lr, y = 16 * ty[t] + 4 * lg;
-            const float hx = Gh[at][x], lx = Gl[at][x];
-            const f32x4 hy = *reinterpret_cast<const f32x4*>(&Gh[at][y]), ly = *reinterpret_cast<const f32x4*>(&Gl[at][y]);
             float p[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -477,6 +493,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
             for (int j = 0; j < CT; ++j) o[x][j] = zero4();
           Frag<TO> sf[2];
           sf[0] = terms_of(0, 0);
+          gates_at(0);
+          constexpr int N = KS * CT, every = N > T ? N / T : 1;         // steps, and steps between P's blocks
 #pragma unroll
           for (int n = 0; n < KS * CT; ++n) {
             const int ks = n / CT, j = n % CT;
@@ -488,10 +506,12 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
             // T blocks over the KS * CT steps
 #pragma unroll
             for (int t = 0; t < T; ++t)
-              if (n == t * KS * CT / T) gate_block(t);
+              if (n == (N >= T ? t * every : 0)) {
+                gate_block(t);
+                if (t + 1 < T) gates_at(t + 1);
+              }
             fence();
           }
-          fetch(i + 1, 4);
 #pragma unroll
           for (int x = 0; x < RT; ++x) {
             const float f = fo[at][16 * x + lr];
@@ -499,13 +519,12 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
             for (int j = 0; j < CT; ++j) o[x][j] *= f;
           }
           __syncthreads();                      // P and C are there
-          fetch(i + 1, 1);
         } else {
           fetch(i + 1, 6);
         }
         // Columns of C, as they are and, times the decay up to the chunk's end, as they go into the state: formed between the
         // products of P C and of the state's update, whose operands are read a step ahead.
-        Frag<NT> cf[K2][CT], bf[2];
+        Frag<NT> cf[K2][CT], bf[3];
         Frag<TO> pf[2][K2];
         Frag<3> vf[2][CT];
         float decays[2][8];
@@ -542,7 +561,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
         };
         const auto b_at = [&](int n) {          // step n: rows of tile n % (2 KS), tokens of half n / (2 KS)
           const int i2 = n % (2 * KS);
-          bf[n % 2] = column_frag<NT, U, CH>(Bs, n / (2 * KS), 4 * (i2 / 2) + piece, 8 * (i2 % 2), lane);
+          bf[n % 3] = column_frag<NT, U, CH>(Bs, n / (2 * KS), 4 * (i2 / 2) + piece, 8 * (i2 % 2), lane);
         };
 #pragma unroll
         for (int k2 = 0; k2 < K2; ++k2)
@@ -558,6 +577,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
           for (int x = 0; x < RT; ++x) {
             if (x + 1 < RT) p_at(x + 1);
             else b_at(0);
+            if (x == RT - 1) b_at(1);
             fence();
 #pragma unroll
             for (int k2 = REV ? x / 2 : 0; k2 < (REV ? K2 : x / 2 + 1); ++k2)
@@ -569,13 +589,57 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
           }
         } else {
           b_at(0);
+          b_at(1);
 #pragma unroll
           for (int n = 0; n < 4 * CT; ++n) columns_of(0, n / 4, n % 4);
+        }
+        const uint32_t ob = s.out_bytes, col = CT == 2 ? 32 * w + 8 * lg : 16 * w + 4 * lg;
+        Values<NT, 4 * CT> drow[DOT ? RT : 1];
+        const auto rows_out = [&](int x) {        // outputs of 16 tokens
+          const buf_t to = buf(s.out + (size_t)t0 * s.out_row + (size_t)h * J * ob, (uint32_t)(m - 1) * s.out_row + J * ob);
+          float v[4 * CT];
+#pragma unroll
+          for (int j = 0; j < CT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[4 * j + r] = o[x][j][r];
+          const uint32_t off = (int)col < J ? (16 * x + lr) * s.out_row + col * ob : kNowhere;
+          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+          typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+          if (ob == 2) {
+            uint32_t b[2 * CT];
+#pragma unroll
+            for (int r = 0; r < 2 * CT; ++r) {
+              uint32_t one[1];
+              split2<1>(v[2 * r], v[2 * r + 1], one);
+              b[r] = one[0];
+            }
+            if constexpr (CT == 2) __builtin_amdgcn_raw_buffer_store_b128(u32x4{b[0], b[1], b[2], b[3]}, to, off, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b64(u32x2{b[0], b[1]}, to, off, 0, 0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < CT; ++j)
+              __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                                           __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])},
+                                                     to, off + 16 * j, 0, 0);
+          }
+          if constexpr (DOT) {
+            float sum = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4 * CT; ++r) sum = fmaf(v[r], drow[x].value(r), sum);
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (lg == 0) red[w][16 * x + lr] = sum;
+          }
+        };
+        if constexpr (DOT) {
+          const buf_t db = buf(s.d.p + (size_t)t0 * s.d.row + (size_t)(s.d.shared ? kh : h) * J * es, (uint32_t)(m - 1) * s.d.row + J * es);
+#pragma unroll
+          for (int x = 0; x < RT; ++x) drow[x].load(db, (int)col < J ? (16 * x + lr) * s.d.row + col * es : kNowhere);
         }
 #pragma unroll
         for (int n = 0; n < K2 * 2 * KS; ++n) {
           const int i2 = n % (2 * KS), k2 = n / (2 * KS);
-          if (n + 1 < K2 * 2 * KS) b_at(n + 1);
+          if (n + 2 < K2 * 2 * KS) b_at(n + 2);
           if (i2 == 0 && k2 + 1 < K2) decays_at(k2 + 1);
           if (k2 == 0) {
 #pragma unroll
@@ -583,61 +647,16 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
           }
           fence();
 #pragma unroll
-          for (int j = 0; j < CT; ++j) S.t[i2][j] = mma<NT, 3>(bf[n % 2], vf[k2 % 2][j], S.t[i2][j]);
+          for (int j = 0; j < CT; ++j) S.t[i2][j] = mma<NT, 3>(bf[n % 3], vf[k2 % 2][j], S.t[i2][j]);
           if (k2 + 1 < K2) {
 #pragma unroll
             for (int c = i2 * 4 * CT / (2 * KS); c < (i2 + 1) * 4 * CT / (2 * KS); ++c) columns_of(k2 + 1, c / 4, c % 4);
+          } else if constexpr (OUT) {
+#pragma unroll
+            for (int x = i2 * RT / (2 * KS); x < (i2 + 1) * RT / (2 * KS); ++x) rows_out(x);
           }
           fence();
         }
-        if constexpr (OUT) {
-          const uint32_t ob = s.out_bytes;
-          const buf_t to = buf(s.out + (size_t)t0 * s.out_row + (size_t)h * J * ob, (uint32_t)(m - 1) * s.out_row + J * ob);
-          const uint32_t col = CT == 2 ? 32 * w + 8 * lg : 16 * w + 4 * lg;
-          Values<NT, 4 * CT> drow[DOT ? RT : 1];
-          if constexpr (DOT) {
-            const buf_t db = buf(s.d.p + (size_t)t0 * s.d.row + (size_t)(s.d.shared ? kh : h) * J * es, (uint32_t)(m - 1) * s.d.row + J * es);
-#pragma unroll
-            for (int x = 0; x < RT; ++x) drow[x].load(db, (int)col < J ? (16 * x + lr) * s.d.row + col * es : kNowhere);
-          }
-#pragma unroll
-          for (int x = 0; x < RT; ++x) {
-            float v[4 * CT];
-#pragma unroll
-            for (int j = 0; j < CT; ++j)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) v[4 * j + r] = o[x][j][r];
-            const uint32_t off = (int)col < J ? (16 * x + lr) * s.out_row + col * ob : kNowhere;
-            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-            if (ob == 2) {
-              uint32_t b[2 * CT];
-#pragma unroll
-              for (int r = 0; r < 2 * CT; ++r) {
-                uint32_t one[1];
-                split2<1>(v[2 * r], v[2 * r + 1], one);
-                b[r] = one[0];
-              }
-              if constexpr (CT == 2) __builtin_amdgcn_raw_buffer_store_b128(u32x4{b[0], b[1], b[2], b[3]}, to, off, 0, 0);
-              else __builtin_amdgcn_raw_buffer_store_b64(u32x2{b[0], b[1]}, to, off, 0, 0);
-            } else {
-#pragma unroll
-              for (int j = 0; j < CT; ++j)
-                __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                                             __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])},
-                                                       to, off + 16 * j, 0, 0);
-            }
-            if constexpr (DOT) {
-              float sum = 0.f;
-#pragma unroll
-              for (int r = 0; r < 4 * CT; ++r) sum = fmaf(v[r], drow[x].value(r), sum);
-              sum += __shfl_xor(sum, 16);
-              sum += __shfl_xor(sum, 32);
-              if (lg == 0) red[w][16 * x + lr] = sum;
-            }
-          }
-        }
-        if (w == 3) gates(at ^ 1);
       }
       if constexpr (DOT) {
         __syncthreads();
@@ -657,7 +676,10 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
     if constexpr (!OUT) {
       S.template move<false, TR>(s.between + (size_t)(bound_of(seg.start, REV ? seg.c - 1 : seg.c, s.L) * hv + h) * cell, I, J,
                                  w, lane);
-      if (tid == 3 * 64) s.decay[(size_t)slot * hv + h] = exp2_of((float)total);
+      __shared__ double totals[NW];
+      if (lane == 0) totals[w] = total;
+      __syncthreads();
+      if (tid == 0) s.decay[(size_t)slot * hv + h] = exp2_of((float)(totals[0] + totals[1] + totals[2] + totals[3]));
     } else if (s.to && keep && row >= 0 && (serial || (REV ? seg.c == 0 : seg.c == seg.count - 1))) {
       S.template move<false, TR>(s.to + ((size_t)row * hv + h) * cell, I, J, w, lane);
     }
