@@ -21,7 +21,8 @@ __global__ __launch_bounds__(kThreads) void linear_chain_kernel(ScanArgs s, int 
     const int part = item - pair * parts, seq = pair / (uint32_t)hv, h = pair - seq * (uint32_t)hv;
     int a, b;
     seq_bounds(s.cu, seq, s.tokens, &a, &b);
-    const int count = segments_of(b - a, s.L);
+    int each;
+    const int count = segments_of(b - a, s.L, &each);
     if (count < 2) continue;
     long long row = seq;
     if (s.state_slots) {

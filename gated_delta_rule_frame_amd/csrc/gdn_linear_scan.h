@@ -186,7 +186,18 @@ struct Segment {
   int start, length;        // those of the sequence
 };
 
-__device__ __forceinline__ int segments_of(int tokens, int L) { return ((uint32_t)tokens + L - 1) / (uint32_t)L; }
+// Segments of a sequence, as many as its length needs at most L tokens each, and their length: equal ones of whole chunks, so
+// that the workgroups of a launch end together (the last may be shorter).
+__device__ __forceinline__ int segments_of(int tokens, int L, int* length) {
+  const uint32_t chunks = ((uint32_t)tokens + kC - 1) / kC, wanted = ((uint32_t)tokens + L - 1) / (uint32_t)L;
+  if (wanted == 0) {
+    *length = kC;
+    return 0;
+  }
+  const uint32_t each = (chunks + wanted - 1) / wanted;
+  *length = each * kC;
+  return (chunks + each - 1) / each;
+}
 
 __device__ __forceinline__ bool find_segment(const int* cu, int sequences, long long tokens, int L, int slot, Segment* s) {
   int lo = 0, hi = sequences - 1;
@@ -199,20 +210,21 @@ __device__ __forceinline__ bool find_segment(const int* cu, int sequences, long 
   int a, b;
   seq_bounds(cu, lo, tokens, &a, &b);
   const int c = slot - (int)(a / (uint32_t)L + lo);
-  const int count = max(1, segments_of(b - a, L));   // an empty sequence has one of no tokens
+  int each;
+  const int count = max(1, segments_of(b - a, L, &each));   // an empty sequence has one of no tokens
   if (c < 0 || c >= count) return false;
   s->seq = __builtin_amdgcn_readfirstlane(lo);
   s->c = __builtin_amdgcn_readfirstlane(c);
   s->start = __builtin_amdgcn_readfirstlane(a);
   s->count = __builtin_amdgcn_readfirstlane(count);
   s->length = __builtin_amdgcn_readfirstlane(b - a);
-  s->first = s->start + s->c * L;
-  s->n = __builtin_amdgcn_readfirstlane(min(L, b - s->first));
+  s->first = s->start + s->c * __builtin_amdgcn_readfirstlane(each);
+  s->n = __builtin_amdgcn_readfirstlane(min(each, b - s->first));
   return true;
 }
 
-// Place of the state between segments c and c + 1 of a sequence that starts at `start`.  Such
-// bounds are L or more tokens apart, in one sequence and from one to the next: (start + (c + 1) L) / L - 1.
+// Place of the state between segments c and c + 1 of a sequence that starts at `start`: a sequence of n tokens has at most
+// n / L of them (rounded down), so the next one's places are behind.
 __device__ __forceinline__ long long bound_of(int start, int c, int L) { return start / (uint32_t)L + c; }
 
 // Whether an earlier sequence uses this slot, and the next one that does (or `sequences`).  Every wavefront for itself.
