@@ -78,7 +78,7 @@ struct LinearPlan {
   long long bounds;         // between segments of one sequence, at most; 0: every sequence is one segment
 };
 
-LinearPlan linear_plan(const LinearProblem& p);
+LinearPlan linear_plan(const LinearProblem& p, bool grad);
 
 // Workspace of a call: what is not needed is null.
 struct LinearSpace {

@@ -1,5 +1,6 @@
 // Linear attention with a decay for each head: outputs and final states, and the
 // states between segments.
+#include <cmath>
 #include <type_traits>
 
 #include "gdn_linear_scan.h"
@@ -67,11 +68,6 @@ __global__ __launch_bounds__(kThreads) void linear_chain_kernel(ScanArgs s, int 
   }
 }
 
-// Segments.  Parallel work for the card, from some kSegments (segment, head) pairs, against the bytes of a state
-// between two segments and the second pass over K and V.
-constexpr long long kSegments = 1024;
-constexpr long long kShortest = 256;
-
 size_t carve(char** at, char* base, size_t* bytes, size_t n) {
   const size_t from = align_up(*bytes, 256);
   *at = base ? base + from : nullptr;
@@ -81,12 +77,24 @@ size_t carve(char** at, char* base, size_t* bytes, size_t n) {
 
 }  // namespace
 
-LinearPlan linear_plan(const LinearProblem& p) {
+// Segments.  A scan's workgroup takes about as long beside another on its CU as alone, and every segment costs the bytes of
+// a state, four times, and a start of some chunks' time: so there are about as many (segment, head) pairs as workgroups run at
+// once (LDS and registers: two a CU, three where no width is above 64, forward and bf16), with half a segment more for each
+// sequence's last one, or twice as many and so on where the sequences alone are that many.  Prompts of 8191 tokens in 13,
+// 32 heads of 128: 175 us at 256 tokens a segment, 155 at 512, 149 at 768, 165 at 1024; gradients of 8192 in 6: 578, 545, 515,
+// 588; one document of 32768, 35 heads of 64: 265, 247, 236, 247 and 226 at 1536; gradients of 16384: 459, 443, 401, 473, 447.
+// One workgroup alone takes 5 us for a chunk of 64 tokens, which bounds short calls: 880 tokens in 3 of fp32, 20 heads of 112
+// (gradients): 152 us at 128 tokens a segment, 231 at 256, 311 in one; but up to 384 tokens the two launches more cost more.
+LinearPlan linear_plan(const LinearProblem& p, bool grad) {
+  const bool wide = p.dk > 64 || p.dv > 64;
+  const double at_once = 256.0 * (wide || grad || !p.in_bf16 ? 2 : 3), each = at_once / p.hv, half = 0.5 * p.sequences;
+  const double wanted = p.sequences <= 1 ? std::fmax(1.0, std::floor(each))
+                                         : (std::floor(half / each + 0.5) + 1) * each - half;
+  double tokens = (double)p.tokens / wanted * (p.sequences <= 1 ? 1.0 : 1.03);
+  tokens = tokens < 128 ? 128 : tokens;
+  long long L = tokens < (double)p.tokens ? ((long long)std::ceil(tokens) + 63) / 64 * 64 : p.tokens;
+  if (p.tokens <= 384 || L >= p.tokens) L = (p.tokens + 64) / 64 * 64;       // one segment, and none behind it
   LinearPlan plan;
-  long long L = (p.tokens * p.hv + kSegments - 1) / kSegments;
-  L = L < kShortest ? kShortest : L;
-  L = (L + 63) / 64 * 64;
-  if (L >= p.tokens) L = (p.tokens + 64) / 64 * 64;       // one segment, and none behind it
   plan.L = (int)L;
   plan.slots = p.tokens / L + p.sequences;
   plan.bounds = p.tokens / L;
@@ -99,7 +107,7 @@ size_t linear_space(const LinearProblem& p, bool grad, void* base, LinearSpace* 
   o = {};
   char* at = nullptr;
   size_t bytes = 0;
-  const LinearPlan plan = linear_plan(p);
+  const LinearPlan plan = linear_plan(p, grad);
   const auto take = [&](auto** to, size_t n) {
     if (n == 0) return;
     carve(&at, static_cast<char*>(base), &bytes, n * sizeof **to);
@@ -158,7 +166,7 @@ ScanArgs scan_args(const LinearProblem& p, const LinearTensors& t, const LinearP
 }
 
 hipError_t linear_forward_launch(const LinearProblem& p, const LinearTensors& t, const LinearSpace& ws, hipStream_t stream) {
-  const LinearPlan plan = linear_plan(p);
+  const LinearPlan plan = linear_plan(p, false);
   const uint32_t es = p.in_bf16 ? 2 : 4;
   ScanArgs s = scan_args(p, t, plan);
   s.a = {static_cast<const char*>(t.q), (uint32_t)p.qs * es, p.dk, true};

@@ -125,7 +125,7 @@ unsigned blocks_of(long long n) { return (unsigned)(n < 1 ? 1 : n < kMaxBlocks ?
 }  // namespace
 
 hipError_t linear_backward_launch(const LinearProblem& p, const LinearTensors& t, const LinearSpace& ws, hipStream_t stream) {
-  const LinearPlan plan = linear_plan(p);
+  const LinearPlan plan = linear_plan(p, true);
   const uint32_t es = p.in_bf16 ? 2 : 4;
   const Operand q = {static_cast<const char*>(t.q), (uint32_t)p.qs * es, p.dk, true};
   const Operand k = {static_cast<const char*>(t.k), (uint32_t)p.ks * es, p.dk, true};

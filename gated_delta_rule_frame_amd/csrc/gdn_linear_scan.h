@@ -200,15 +200,23 @@ __device__ __forceinline__ int segments_of(int tokens, int L, int* length) {
 }
 
 __device__ __forceinline__ bool find_segment(const int* cu, int sequences, long long tokens, int L, int slot, Segment* s) {
-  int lo = 0, hi = sequences - 1;
-  const int t = (int)tokens;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (min(max(cu[mid], 0), t) / (uint32_t)L + mid <= (uint32_t)slot) lo = mid;
-    else hi = mid - 1;
+  // A wavefront looks at 64 sequences at once: one load where there are no more than that, and few otherwise.
+  const int t = (int)tokens, lane = threadIdx.x % 64;
+  int lo = 0, width = sequences, a, b;
+  for (;;) {
+    const int step = (width + 63) / 64, at = lo + lane * step;
+    const bool in = lane * (long long)step < width;
+    const int first = in ? min(max(cu[at], 0), t) : 0, end = in ? cu[at + 1] : 0;
+    const int before = __popcll(__ballot(in && first / (uint32_t)L + at <= (uint32_t)slot));
+    const int k = max(before - 1, 0);
+    lo += k * step;
+    if (step == 1) {
+      a = __builtin_amdgcn_readlane(first, k);
+      b = min(max(__builtin_amdgcn_readlane(end, k), a), t);
+      break;
+    }
+    width = min(step, width - k * step);
   }
-  int a, b;
-  seq_bounds(cu, lo, tokens, &a, &b);
   const int c = slot - (int)(a / (uint32_t)L + lo);
   int each;
   const int count = max(1, segments_of(b - a, L, &each));   // an empty sequence has one of no tokens
@@ -298,8 +306,9 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
   __shared__ __align__(16) char Bs[NT * CH * U * 16];
   __shared__ __align__(16) char Cs[NT * CH * UC * 16];
   __shared__ __align__(16) bh P[OUT ? RT * K2 * TO * 512 : 8];
-  __shared__ __align__(16) float Gh[4][64], Gl[4][64];   // G = Gh + Gl to 48 bits: its differences have the accuracy of fp32
-  __shared__ __align__(16) float fo[4][64], fs[4][64], all[4];
+  constexpr int GR = NT == 1 ? 4 : 2;          // chunks whose gates are there at once
+  __shared__ __align__(16) float Gh[GR][CH], Gl[GR][CH];  // G = Gh + Gl to 48 bits: its differences have the accuracy of fp32
+  __shared__ __align__(16) float fo[GR][CH], fs[GR][CH], all[GR];
   __shared__ float red[DOT ? NW : 1][CH];
   const uint32_t tid = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -372,7 +381,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
         if (which & 2) rb.load(rows(s.b), s.b.row, I, tid);
         if (which & 4) rc.load(rows(s.c), s.c.row, J, tid);
       };
-      // Four chunks at a time, the wavefront's one of them: its gates, loaded long before, then their sums and factors.
+      // GR chunks at a time, the wavefront's one of them: its gates, loaded long before, then their sums and factors.
       auto fetch_gates = [&](int i) {
         const int k = i < chunks ? (REV ? chunks - 1 - i : i) : 0, t0 = first + k * CH;
         const int m = i < chunks ? min(CH, n - k * CH) : 0;
@@ -384,11 +393,13 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
         const double Gn = last_lane(G);
         const float up = exp2_of((float)G), down = exp2_of((float)(Gn - G));
         const float hi = (float)G;
-        Gh[w][lane] = hi;
-        Gl[w][lane] = (float)(G - hi);
+        if (lane < CH) {
+          Gh[w][lane] = hi;
+          Gl[w][lane] = (float)(G - hi);
+          fo[w][lane] = REV ? down : s.scale * up;
+          fs[w][lane] = REV ? s.scale * up : down;
+        }
         if (lane == 0) all[w] = exp2_of((float)Gn);
-        fo[w][lane] = REV ? down : s.scale * up;
-        fs[w][lane] = REV ? s.scale * up : down;
         total += Gn;
       };
       auto dot_of = [&] {                       // a token's sum over the columns
@@ -397,10 +408,10 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
         for (int j = 1; j < NW; ++j) x += red[j][tid];
         return x;
       };
-      fetch_gates(w);
+      if (w < GR) fetch_gates(w);
       fetch(0, 7);
       for (int i = 0; i < chunks; ++i) {
-        const int k = REV ? chunks - 1 - i : i, at = i & 3;
+        const int k = REV ? chunks - 1 - i : i, at = i % GR;
         const int t0 = first + k * CH, m = min(CH, n - k * CH);
         asm volatile("" : "+v"(lane));         // addresses in LDS are made in each chunk and not kept in registers
         const uint32_t lr = lane % 16, lg = lane / 16;
@@ -408,9 +419,9 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
         if constexpr (OUT) ra.store(As, tid);
         rb.store(Bs, tid);
         if constexpr (!OUT) rc.store(Cs, tid);
-        if (at == 0) {
+        if (at == 0 && w < GR) {
           gates();
-          fetch_gates(i + 4 + w);
+          fetch_gates(i + GR + w);
         }
         if constexpr (DOT) {
           if (i && tid < CH) {
