@@ -383,7 +383,8 @@ def __getattr__(name):
     # the sequence operators' bindings need torch at import; the rest of this module does not
     if name in _LAZY:
         import importlib
-        return getattr(importlib.import_module("." + _LAZY[name], __name__), name)
+        value = globals()[name] = getattr(importlib.import_module("." + _LAZY[name], __name__), name)   # found at once from now on
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

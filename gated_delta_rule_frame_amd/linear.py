@@ -8,14 +8,23 @@ graph.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import ABI_VERSION, F32, lib
-from .sequence import _CODE, _MAX, _dense, _fits, _need, _on, _output, _ptr, _rows, _sequences, _space
+from . import sequence
+from .sequence import _CODE, _MAX, _dense, _fits, _need, _on, _output, _ptr, _rows, _space
 from .sequence_abi import LinearProblem
 
 
-def _problem(q, k, v, log_gate, scale, out_dtype):
+@functools.lru_cache(maxsize=1024)
+def _fields(hk, hv, dk, dv, code, out_code, n, qs, ks, vs, per_head, scale, sequences, state_rows):
+    """The problem of these fields; kept, as making one takes longer than a small launch.  Calls only read it."""
+    return LinearProblem(ABI_VERSION, hk, hv, dk, dv, code, out_code, state_rows, n, qs, ks, vs, sequences, per_head, scale)
+
+
+def _problem(q, k, v, log_gate, scale, out_dtype, sequences=0, state_rows=0):
     """Checks the inputs the calls share; returns (problem, device, tokens, heads_v, d_k, d_v)."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise ValueError("q must be a tensor on a GPU")
@@ -26,14 +35,23 @@ def _problem(q, k, v, log_gate, scale, out_dtype):
     device, (n, hk, dk), (hv, dv) = q.device, q.shape, v.shape[1:]
     if (hk | hv | dk | dv) > _MAX:
         raise ValueError(f"heads and widths must be below 2^31 (got {hk}, {hv}, {dk}, {dv})")
-    p = LinearProblem(ABI_VERSION, hk, hv, dk, dv, _CODE[q.dtype], _CODE[out_dtype], 0, n)
-    p.q_stride = _rows("q", q, q.shape, q.dtype, device)
-    p.k_stride = _rows("k", k, q.shape, q.dtype, device)
-    p.v_stride = _rows("v", v, (n, hv, dv), q.dtype, device)
-    p.scale = scale
-    p.gate_per_head = int(isinstance(log_gate, torch.Tensor) and log_gate.dim() == 1)
-    _dense("log_gate", log_gate, (hv,) if p.gate_per_head else (n, hv), torch.float32, device)
+    qs, ks = _rows("q", q, q.shape, q.dtype, device), _rows("k", k, q.shape, q.dtype, device)
+    vs = _rows("v", v, (n, hv, dv), q.dtype, device)
+    per_head = int(isinstance(log_gate, torch.Tensor) and log_gate.dim() == 1)
+    _dense("log_gate", log_gate, (hv,) if per_head else (n, hv), torch.float32, device)
+    p = _fields(hk, hv, dk, dv, _CODE[q.dtype], _CODE[out_dtype], n, qs, ks, vs, per_head, float(scale), sequences, state_rows)
     return p, device, n, hv, dk, dv
+
+
+def _sequences(cu_seqlens, q):
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be a tensor on a GPU")
+    return sequence._sequences(cu_seqlens, q.device)
+
+
+def _pool(t):
+    """Rows of a pool of states."""
+    return _fits("the pool's rows", t.shape[0] if isinstance(t, torch.Tensor) and t.dim() == 4 else 0)
 
 
 def linear_decode(q, k, v, log_gate, state, slots=None, *, scale=1.0, out_dtype=None, out=None):
@@ -46,12 +64,12 @@ def linear_decode(q, k, v, log_gate, state, slots=None, *, scale=1.0, out_dtype=
     ``decode``.
     """
     odt = _output(out, out_dtype)
-    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, scale, odt)
-    rows = n
-    if slots is not None:
+    rows = 0 if slots is None else _pool(state)
+    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, scale, odt, 0, rows)
+    if slots is None:
+        rows = n
+    else:
         _dense("slots", slots, (n,), torch.int32, device)
-        rows = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 4 else 0
-        p.state_rows = _fits("the pool's rows", rows)
     _dense("state", state, (rows, hv, dk, dv), torch.float32, device)
     if out is None:
         out = torch.empty((n, hv, dv), dtype=odt, device=device)
@@ -73,20 +91,18 @@ def linear_forward(q, k, v, log_gate, cu_seqlens, initial_state=None, *, slots=N
     the reach of a NaN or infinity are ``packed_forward``'s.
     """
     odt = _output(out, out_dtype)
-    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, scale, odt)
-    seqs = p.sequences = _sequences(cu_seqlens, device)
-    states = seqs
+    seqs, rows = _sequences(cu_seqlens, q), 0
     if slots is not None:
-        _dense("slots", slots, (seqs,), torch.int32, device)
         if final_state is None:
             if initial_state is None:
                 raise ValueError("a call with slots needs initial_state or final_state, the pool")
             if want_state:
                 final_state = initial_state
-        pool = initial_state if final_state is None else final_state
-        states = pool.shape[0] if isinstance(pool, torch.Tensor) and pool.dim() == 4 else 0
-        p.state_rows = _fits("the pool's rows", states)
-    shape = (states, hv, dk, dv)
+        rows = _pool(initial_state if final_state is None else final_state)
+    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, scale, odt, seqs, rows)
+    if slots is not None:
+        _dense("slots", slots, (seqs,), torch.int32, device)
+    shape = (seqs if slots is None else rows, hv, dk, dv)
     if initial_state is not None:
         _dense("initial_state", initial_state, shape, torch.float32, device)
     if final_state is not None:
@@ -114,8 +130,8 @@ def linear_backward(q, k, v, log_gate, cu_seqlens, dout, initial_state=None, dfi
     last sequence are not written: for a padded batch give ``grads``, four
     tensors (dq, dk, dv, dlog_gate) to write into.
     """
-    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, scale, torch.float32)
-    seqs = p.sequences = _sequences(cu_seqlens, device)
+    seqs = _sequences(cu_seqlens, q)
+    p, device, n, hv, dk, dv = _problem(q, k, v, log_gate, scale, torch.float32, seqs)
     _dense("dout", dout, v.shape, q.dtype, device)
     shape = (seqs, hv, dk, dv)
     for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
@@ -141,7 +157,6 @@ def linear_workspace_size(q, v, log_gate, sequences, *, gradient=False):
     """Bytes of workspace of ``linear_forward`` (or ``linear_backward``) for inputs like q, v and log_gate."""
     if q.dtype not in _CODE:
         raise TypeError(f"unsupported dtype {q.dtype}")
-    p = LinearProblem(ABI_VERSION, q.shape[1], v.shape[1], q.shape[2], v.shape[2], _CODE[q.dtype], F32, 0, q.shape[0])
-    p.sequences = _fits("sequences", sequences)
-    p.gate_per_head = int(log_gate.dim() == 1)
+    p = _fields(q.shape[1], v.shape[1], q.shape[2], v.shape[2], _CODE[q.dtype], F32, q.shape[0], 0, 0, 0, int(log_gate.dim() == 1),
+                1.0, _fits("sequences", sequences), 0)
     return _need("gdn_linear_workspace_size", LinearProblem, bytes(p), int(gradient))

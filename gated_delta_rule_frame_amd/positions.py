@@ -7,6 +7,7 @@ graph.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -53,12 +54,13 @@ def rotary_frequencies(width, base=10000.0, *, scaling="none", factor=1.0, train
     return f.to("cuda" if device is None else device), magnitude
 
 
-def _place(name, x, out, device):
-    """The output of x, its stride between tokens (0 = dense) and x's own."""
-    stride = _rows(name, x, x.shape, x.dtype, device)
-    if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=device), 0, stride
-    return out, _rows(f"{name}'s output", out, x.shape, x.dtype, device), stride
+@functools.lru_cache(maxsize=1024)
+def _problem(*fields):
+    """The problem of these fields; kept, as making one takes longer than a small launch.  Calls only read it."""
+    sections, rest = fields[0], fields[1:]
+    p = RotaryProblem(ABI_VERSION, *rest[:9], sections + (0,) * (4 - len(sections)), rest[9])
+    p.q_stride, p.k_stride, p.q_out_stride, p.k_out_stride = rest[10:]
+    return p
 
 
 def _turn(q, k, positions, frequencies, layout, magnitude, sections, out, inverse):
@@ -90,12 +92,20 @@ def _turn(q, k, positions, frequencies, layout, magnitude, sections, out, invers
         out = (None, None)
     elif len(out) != 2 or (k is None and out[1] is not None):
         raise ValueError("out must be a pair, the outputs of q and k")
-    p = RotaryProblem(ABI_VERSION, _CODE[q.dtype], n, hq, hk, width, pairs, LAYOUT[layout], int(inverse), len(parts),
-                      parts + (0,) * (4 - len(parts)), magnitude)
-    qo, p.q_out_stride, p.q_stride = _place("q", q, out[0], device)
-    ko = None
+    qs, ks, qos, kos = _rows("q", q, q.shape, q.dtype, device), 0, 0, 0
+    qo, ko = out
+    if qo is None:
+        qo = torch.empty(q.shape, dtype=q.dtype, device=device)
+    else:
+        qos = _rows("q's output", qo, q.shape, q.dtype, device)
     if k is not None:
-        ko, p.k_out_stride, p.k_stride = _place("k", k, out[1], device)
+        ks = _rows("k", k, k.shape, q.dtype, device)
+        if ko is None:
+            ko = torch.empty(k.shape, dtype=q.dtype, device=device)
+        else:
+            kos = _rows("k's output", ko, k.shape, q.dtype, device)
+    p = _problem(parts, _CODE[q.dtype], n, hq, hk, width, pairs, LAYOUT[layout], int(inverse), len(parts), float(magnitude),
+                 qs, ks, qos, kos)
     _on(device, lib().gdn_rotary, p, q.data_ptr(), _ptr(k), positions.data_ptr(), frequencies.data_ptr(), qo.data_ptr(), _ptr(ko))
     return qo, ko
 
