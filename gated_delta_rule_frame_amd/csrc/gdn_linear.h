@@ -40,6 +40,7 @@ struct ScanArgs {
   char* out;
   uint32_t out_row;
   int out_bytes;            // of a value
+  float* part;              // dq and dk of shared key heads: sums over value heads so far, [token][key head][J]; or null
   float* dot;               // [head][token]
   // states
   const float* from;        // of sequences, or rows of a pool; or null (zeros)
@@ -91,7 +92,7 @@ struct LinearSpace {
   float* last;              // [sequence][heads_v][d_k][d_v]: final states
   float* qdq;               // [heads_v][tokens]
   float* vdv;
-  float* dq;                // shared key heads: each value head's, [tokens][heads_v][d_k]
+  float* dq;                // shared key heads: sums so far, [tokens][heads_k][d_k]
   float* dk;
   double* dg;               // one gate a head: [slot][heads_v]
 };
@@ -103,8 +104,9 @@ ScanArgs scan_args(const LinearProblem& p, const LinearTensors& t, const LinearP
 hipError_t linear_forward_launch(const LinearProblem& p, const LinearTensors& t, const LinearSpace& s, hipStream_t stream);
 hipError_t linear_backward_launch(const LinearProblem& p, const LinearTensors& t, const LinearSpace& s, hipStream_t stream);
 
-// The sums of every segment's contributions to the state, and the states between segments from them (gdn_linear.hip).
-hipError_t linear_states(const ScanArgs& s, bool bf16, bool reversed, hipStream_t stream);
+// The sums of every segment's contributions to the state, and the states between segments from them (gdn_linear.hip): of the
+// forward scan, and of the reversed one where it is given.
+hipError_t linear_states(const ScanArgs& forward, const ScanArgs* reversed, bool bf16, hipStream_t stream);
 
 // ---------------------------------------------------------------- rotary positions
 

@@ -1,6 +1,7 @@
 // Linear attention with a decay for each head: outputs and final states, and the
 // states between segments.
 #include <cmath>
+#include <cstddef>
 #include <type_traits>
 
 #include "gdn_linear_scan.h"
@@ -10,61 +11,88 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The states between segments from their sums, for every element of the state by itself: forward S <- e^{G} S + sum from the
-// initial state, reversed R <- e^{G} R + sum from the final state's gradient.
+struct SumsArgs {
+  ScanArgs forward, reversed;
+  int directions;
+};
+
+template <int NT, int KS, int CT>
+__global__ __launch_bounds__(kScanThreads, 2) void linear_sums_kernel(SumsArgs a) {
+  __shared__ ScanSpace<NT, 3, KS, CT, false, false> z;
+  const uint32_t heads = a.forward.rep, parts = heads * a.directions, blocks = scan_blocks(a.forward) * a.directions;
+  for (uint32_t block = blockIdx.x; block < blocks; block += gridDim.x) {
+    const uint32_t group = block / 8 / parts, unit = group * 8 + block % 8, part = block / 8 - group * parts;
+    if (part < heads) {
+      const ScanArgs s = scan_args_at(offsetof(SumsArgs, forward));
+      scan_item<NT, 3, KS, CT, false, false, false>(s, unit, part, z);
+    } else {
+      const ScanArgs s = scan_args_at(offsetof(SumsArgs, reversed));
+      scan_item<NT, 3, KS, CT, true, false, false>(s, unit, part - heads, z);
+    }
+  }
+}
+
+// The states between the segments of a sequence from their sums, four elements of the state a lane: forward S <- e^G S + sum
+// from the initial state, reversed R <- e^G R + sum from the final state's gradient.
 template <bool REV>
-__global__ __launch_bounds__(kThreads) void linear_chain_kernel(ScanArgs s, int cell, int parts) {
+__device__ __forceinline__ void chain(const ScanArgs& s, int cell, int part, int seq, int h) {
   const int hv = s.hk * s.rep;
-  const uint32_t items = (uint32_t)s.sequences * hv * parts;       // at most 2^20 * 16
   const bool in_place = s.from && s.from == s.to;
-  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const uint32_t pair = item / (uint32_t)parts;
-    const int part = item - pair * parts, seq = pair / (uint32_t)hv, h = pair - seq * (uint32_t)hv;
-    int a, b;
-    seq_bounds(s.cu, seq, s.tokens, &a, &b);
-    int each;
-    const int count = segments_of(b - a, s.L, &each);
-    if (count < 2) continue;
-    long long row = seq;
-    if (s.state_slots) {
-      row = s.state_slots[seq];
-      if (row < 0 || row >= s.state_rows) row = -1;
-      else if (in_place) {
-        bool earlier;
-        int next;
-        same_slot(s.state_slots, s.sequences, seq, &earlier, &next);
-        if (earlier || next < s.sequences) continue;
-      }
-    }
-    const int e = (part * kThreads + threadIdx.x) * 4;
-    if (e >= cell) continue;
-    const long long slot = a / (uint32_t)s.L + seq;
-    const long long b0 = bound_of(a, 0, s.L);
-    float* at = s.between + (size_t)(b0 * hv + h) * cell + e;
-    const size_t step = (size_t)hv * cell;
-    f32x4 S = s.from && row >= 0 ? *reinterpret_cast<const f32x4*>(s.from + ((size_t)row * hv + h) * cell + e) : zero4();
-    if (!REV && in_place) *reinterpret_cast<f32x4*>(s.firsts + (size_t)(b0 * hv + h) * cell + e) = S;
-    constexpr int kAhead = 8;
-    for (int i0 = 0; i0 < count - 1; i0 += kAhead) {
-      f32x4 u[kAhead];
-      float d[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int k = REV ? count - 2 - i0 - i : i0 + i;            // bound k, between segments k and k + 1
-        if (i0 + i < count - 1) {
-          u[i] = *reinterpret_cast<const f32x4*>(at + k * step);
-          d[i] = s.decay[(slot + (REV ? k + 1 : k)) * hv + h];
+      int a, b;
+      seq_bounds(s.cu, seq, s.tokens, &a, &b);
+      int each;
+      const int count = segments_of(b - a, s.L, &each);
+      if (count < 2) return;
+      long long row = seq;
+      if (s.state_slots) {
+        row = s.state_slots[seq];
+        if (row < 0 || row >= s.state_rows) row = -1;
+        else if (in_place) {
+          bool earlier;
+          int next;
+          same_slot(s.state_slots, s.sequences, seq, &earlier, &next);
+          if (earlier || next < s.sequences) return;
         }
       }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int k = REV ? count - 2 - i0 - i : i0 + i;
-        if (i0 + i < count - 1) {
-          S = d[i] * S + u[i];
-          *reinterpret_cast<f32x4*>(at + k * step) = S;
+      const int e = (part * kThreads + threadIdx.x) * 4;
+      if (e >= cell) return;
+      const long long slot = a / (uint32_t)s.L + seq;
+      const long long b0 = bound_of(a, 0, s.L);
+      float* at = s.between + (size_t)(b0 * hv + h) * cell + e;
+      const size_t step = (size_t)hv * cell;
+      f32x4 S = s.from && row >= 0 ? *reinterpret_cast<const f32x4*>(s.from + ((size_t)row * hv + h) * cell + e) : zero4();
+      if (!REV && in_place) *reinterpret_cast<f32x4*>(s.firsts + (size_t)(b0 * hv + h) * cell + e) = S;
+      constexpr int kAhead = 8;
+      for (int i0 = 0; i0 < count - 1; i0 += kAhead) {
+        f32x4 u[kAhead];
+        float d[kAhead];
+  #pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int k = REV ? count - 2 - i0 - i : i0 + i;            // bound k, between segments k and k + 1
+          if (i0 + i < count - 1) {
+            u[i] = *reinterpret_cast<const f32x4*>(at + k * step);
+            d[i] = s.decay[(slot + (REV ? k + 1 : k)) * hv + h];
+          }
+        }
+  #pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int k = REV ? count - 2 - i0 - i : i0 + i;
+          if (i0 + i < count - 1) {
+            S = d[i] * S + u[i];
+            *reinterpret_cast<f32x4*>(at + k * step) = S;
+          }
         }
       }
-    }
+}
+
+__global__ __launch_bounds__(kThreads) void linear_chain_kernel(ScanArgs f, ScanArgs r, int directions, int cell, int parts) {
+  const uint32_t hv = f.hk * f.rep, each = f.sequences * hv * parts;       // at most 2^20 * 16
+  for (uint32_t item = blockIdx.x; item < each * directions; item += gridDim.x) {
+    const bool reversed = item >= each;
+    const uint32_t i = reversed ? item - each : item, pair = i / (uint32_t)parts;
+    const int part = i - pair * parts, seq = pair / hv, h = pair - seq * hv;
+    if (reversed) chain<true>(r, cell, part, seq, h);
+    else chain<false>(f, cell, part, seq, h);
   }
 }
 
@@ -127,23 +155,31 @@ size_t linear_space(const LinearProblem& p, bool grad, void* base, LinearSpace* 
   take(&o.qdq, (size_t)p.tokens * p.hv);
   take(&o.vdv, (size_t)p.tokens * p.hv);
   if (p.hv > p.hk) {
-    take(&o.dq, (size_t)p.tokens * p.hv * p.dk);
-    take(&o.dk, (size_t)p.tokens * p.hv * p.dk);
+    take(&o.dq, (size_t)p.tokens * p.hk * p.dk);
+    take(&o.dk, (size_t)p.tokens * p.hk * p.dk);
   }
   if (p.fixed) take(&o.dg, (size_t)plan.slots * p.hv);
   return bytes;
 }
 
-hipError_t linear_states(const ScanArgs& s, bool bf16, bool reversed, hipStream_t stream) {
+hipError_t linear_states(const ScanArgs& forward, const ScanArgs* reversed, bool bf16, hipStream_t stream) {
+  const int directions = reversed ? 2 : 1;
+  const ScanArgs& r = reversed ? *reversed : forward;
+  const SumsArgs a = {forward, r, directions};
   prof_begin(stream, GDN_KERNEL_LINEAR_STATES);
-  hipError_t e = reversed ? (bf16 ? scan_variant<1, 3, true, false, false>(s, stream) : scan_variant<3, 3, true, false, false>(s, stream))
-                          : (bf16 ? scan_variant<1, 3, false, false, false>(s, stream) : scan_variant<3, 3, false, false, false>(s, stream));
+  by_width(forward.b.width, [&](auto ks, auto) {
+    by_width(forward.c.width, [&](auto, auto ct) {
+      constexpr int KS = decltype(ks)::value, CT = decltype(ct)::value;
+      const dim3 grid = scan_grid((long long)scan_blocks(forward) * directions), threads(kScanThreads);
+      if (bf16) hipLaunchKernelGGL((linear_sums_kernel<1, KS, CT>), grid, threads, 0, stream, a);
+      else hipLaunchKernelGGL((linear_sums_kernel<3, KS, CT>), grid, threads, 0, stream, a);
+    });
+  });
+  hipError_t e = hipGetLastError();
   if (e == hipSuccess) {
-    const int cell = s.b.width * s.c.width, parts = (cell + kThreads * 4 - 1) / (kThreads * 4);
-    const long long items = (long long)s.sequences * s.hk * s.rep * parts;
-    const dim3 grid((unsigned)(items < kMaxBlocks ? items : kMaxBlocks));
-    if (reversed) hipLaunchKernelGGL(linear_chain_kernel<true>, grid, dim3(kThreads), 0, stream, s, cell, parts);
-    else hipLaunchKernelGGL(linear_chain_kernel<false>, grid, dim3(kThreads), 0, stream, s, cell, parts);
+    const int cell = forward.b.width * forward.c.width, parts = (cell + kThreads * 4 - 1) / (kThreads * 4);
+    const long long items = (long long)forward.sequences * forward.hk * forward.rep * parts * directions;
+    hipLaunchKernelGGL(linear_chain_kernel, scan_grid(items), dim3(kThreads), 0, stream, forward, r, directions, cell, parts);
     e = hipGetLastError();
   }
   prof_end(stream, GDN_KERNEL_LINEAR_STATES);
@@ -183,13 +219,20 @@ hipError_t linear_forward_launch(const LinearProblem& p, const LinearTensors& t,
   s.firsts = ws.firsts;
   s.decay = ws.decay;
   if (plan.bounds) {
-    const hipError_t e = linear_states(s, p.in_bf16, false, stream);
+    const hipError_t e = linear_states(s, nullptr, p.in_bf16, stream);
     if (e != hipSuccess) return e;
   }
   prof_begin(stream, GDN_KERNEL_LINEAR_SCAN);
-  const hipError_t e = !p.in_bf16     ? scan_variant<3, 3, false, true, false>(s, stream)
-                       : p.out_bf16 ? scan_variant<1, 2, false, true, false>(s, stream)
-                                    : scan_variant<1, 3, false, true, false>(s, stream);
+  by_width(p.dk, [&](auto ks, auto) {
+    by_width(p.dv, [&](auto, auto ct) {
+      constexpr int KS = decltype(ks)::value, CT = decltype(ct)::value;
+      const dim3 grid = scan_grid(scan_blocks(s)), threads(kScanThreads);
+      if (!p.in_bf16) hipLaunchKernelGGL((linear_scan_kernel<3, 3, KS, CT>), grid, threads, 0, stream, s);
+      else if (p.out_bf16) hipLaunchKernelGGL((linear_scan_kernel<1, 2, KS, CT>), grid, threads, 0, stream, s);
+      else hipLaunchKernelGGL((linear_scan_kernel<1, 3, KS, CT>), grid, threads, 0, stream, s);
+    });
+  });
+  const hipError_t e = hipGetLastError();
   prof_end(stream, GDN_KERNEL_LINEAR_SCAN);
   return e;
 }

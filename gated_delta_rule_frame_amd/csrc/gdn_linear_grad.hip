@@ -1,5 +1,7 @@
 // Gradients of linear attention with a decay for each head: three scans over the
 // same operands, then the gates' gradients from sums of theirs.
+#include <cstddef>
+
 #include "gdn_linear_scan.h"
 
 namespace gdn {
@@ -100,22 +102,36 @@ __global__ __launch_bounds__(kThreads) void linear_gate_sums_kernel(const double
   if (threadIdx.x == 0) dg[h] = (float)x;
 }
 
-// Gradients of a key head: the sums of its value heads', four values a lane.
-__global__ __launch_bounds__(kThreads) void linear_heads_kernel(ScanArgs s, const float* parts, void* out, int width, bool bf16) {
-  const int t0 = min(max(s.cu[0], 0), (int)s.tokens), t1 = min(max(s.cu[s.sequences], t0), (int)s.tokens);
-  const long long quads = (long long)(t1 - t0) * s.hk * width / 4;
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < quads; i += (long long)gridDim.x * kThreads) {
-    const long long e = (long long)t0 * s.hk * width + i * 4, head = e / width;     // head: of tokens * hk
-    const float* p = parts + head * s.rep * width + e % width;
-    f32x4 x = *reinterpret_cast<const f32x4*>(p);
-    for (int r = 1; r < s.rep; ++r) x += *reinterpret_cast<const f32x4*>(p + (size_t)r * width);
-    if (bf16) {
-      uint32_t lo[1], hi[1];
-      split2<1>(x[0], x[1], lo);
-      split2<1>(x[2], x[3], hi);
-      reinterpret_cast<uint2*>(out)[e / 4] = make_uint2(lo[0], hi[0]);
+struct GradArgs {
+  ScanArgs dq, dk, dv;
+};
+
+// dq, dk and dv in one launch: a unit's workgroups (of a segment and key head) one after another on one XCD, as they read the
+// same rows; those that sum over value heads, the longest, first.  KSK, CTK and KSV, CTV: by_width of d_k and d_v.
+template <int NT, int KSK, int CTK, int KSV, int CTV>
+__global__ __launch_bounds__(kScanThreads, 2) void linear_grad_kernel(GradArgs g) {
+  constexpr int TO = NT == 1 ? 2 : 3;
+  using Q = ScanSpace<NT, 3, KSV, CTK, true, true>;
+  using K = ScanSpace<NT, TO, KSV, CTK, true, false>;
+  using V = ScanSpace<NT, 3, KSK, CTV, true, true>;
+  __shared__ union {
+    Q q;
+    K k;
+    V v;
+  } z;
+  const uint32_t keys = g.dq.part ? 1 : g.dq.rep, parts = 2 * keys + g.dv.rep;
+  const uint32_t blocks = scan_blocks(g.dv) / g.dv.rep * parts;
+  for (uint32_t block = blockIdx.x; block < blocks; block += gridDim.x) {
+    const uint32_t group = block / 8 / parts, unit = group * 8 + block % 8, part = block / 8 - group * parts;
+    if (part < keys) {
+      const ScanArgs s = scan_args_at(offsetof(GradArgs, dq));
+      scan_item<NT, 3, KSV, CTK, false, true, true>(s, unit, part, z.q);
+    } else if (part < 2 * keys) {
+      const ScanArgs s = scan_args_at(offsetof(GradArgs, dk));
+      scan_item<NT, TO, KSV, CTK, true, true, false>(s, unit, part - keys, z.k);
     } else {
-      reinterpret_cast<f32x4*>(out)[e / 4] = x;
+      const ScanArgs s = scan_args_at(offsetof(GradArgs, dv));
+      scan_item<NT, 3, KSK, CTV, true, true, true>(s, unit, part - 2 * keys, z.v);
     }
   }
 }
@@ -144,66 +160,55 @@ hipError_t linear_backward_launch(const LinearProblem& p, const LinearTensors& t
     return hipGetLastError();
   }
   if (plan.bounds) {
-    ScanArgs s = forward;
-    s.b = k;
-    s.c = v;
-    e = linear_states(s, p.in_bf16, false, stream);
-    if (e != hipSuccess) return e;
-    s = reversed;
-    s.b = q;
-    s.c = dout;
-    e = linear_states(s, p.in_bf16, true, stream);
+    ScanArgs f = forward, r = reversed;
+    f.b = k;
+    f.c = v;
+    r.b = q;
+    r.c = dout;
+    e = linear_states(f, &r, p.in_bf16, stream);
     if (e != hipSuccess) return e;
   }
   const bool shared = p.hv > p.hk;
+  GradArgs g = {forward, reversed, reversed};
+  g.dq.a = dout;
+  g.dq.b = v;
+  g.dq.c = k;
+  g.dq.d = q;
+  g.dq.out = static_cast<char*>(t.dq);
+  g.dq.part = shared ? ws.dq : nullptr;
+  g.dq.dot = ws.qdq;
+  g.dq.to = t.dhT ? ws.last : nullptr;
+  g.dk.a = v;
+  g.dk.b = dout;
+  g.dk.c = q;
+  g.dk.out = static_cast<char*>(t.dk);
+  g.dk.part = shared ? ws.dk : nullptr;
+  g.dv.a = k;
+  g.dv.b = q;
+  g.dv.c = dout;
+  g.dv.d = v;
+  g.dv.out = static_cast<char*>(t.dv);
+  g.dv.dot = ws.vdv;
+  g.dv.to = t.dh0;
+  g.dq.out_bytes = g.dk.out_bytes = g.dv.out_bytes = es;
+  g.dq.out_row = g.dk.out_row = (uint32_t)(p.hk * p.dk) * es;
+  g.dv.out_row = (uint32_t)(p.hv * p.dv) * es;
   prof_begin(stream, GDN_KERNEL_LINEAR_SCAN);
-  {
-    ScanArgs s = forward;
-    s.a = dout;
-    s.b = v;
-    s.c = k;
-    s.d = q;
-    s.out = shared ? reinterpret_cast<char*>(ws.dq) : static_cast<char*>(t.dq);
-    s.out_bytes = shared ? 4 : es;
-    s.out_row = (uint32_t)(p.hv * p.dk) * s.out_bytes;
-    s.dot = ws.qdq;
-    s.to = t.dhT ? ws.last : nullptr;
-    e = p.in_bf16 ? scan_variant<1, 3, false, true, true>(s, stream) : scan_variant<3, 3, false, true, true>(s, stream);
-  }
-  if (e == hipSuccess) {
-    ScanArgs s = reversed;
-    s.a = k;
-    s.b = q;
-    s.c = dout;
-    s.d = v;
-    s.out = static_cast<char*>(t.dv);
-    s.out_bytes = es;
-    s.out_row = (uint32_t)(p.hv * p.dv) * es;
-    s.dot = ws.vdv;
-    s.to = t.dh0;
-    e = p.in_bf16 ? scan_variant<1, 3, true, true, true>(s, stream) : scan_variant<3, 3, true, true, true>(s, stream);
-  }
-  if (e == hipSuccess) {
-    ScanArgs s = reversed;
-    s.a = v;
-    s.b = dout;
-    s.c = q;
-    s.out = shared ? reinterpret_cast<char*>(ws.dk) : static_cast<char*>(t.dk);
-    s.out_bytes = shared ? 4 : es;
-    s.out_row = (uint32_t)(p.hv * p.dk) * s.out_bytes;
-    e = p.in_bf16 ? scan_variant<1, 2, true, true, false>(s, stream) : scan_variant<3, 3, true, true, false>(s, stream);
-  }
+  by_width(p.dk, [&](auto ksk, auto ctk) {
+    by_width(p.dv, [&](auto ksv, auto ctv) {
+      constexpr int KSK = decltype(ksk)::value, CTK = decltype(ctk)::value, KSV = decltype(ksv)::value, CTV = decltype(ctv)::value;
+      const dim3 grid = scan_grid((long long)scan_blocks(g.dv) + 2LL * scan_blocks(g.dq)), threads(kScanThreads);
+      if (p.in_bf16) hipLaunchKernelGGL((linear_grad_kernel<1, KSK, CTK, KSV, CTV>), grid, threads, 0, stream, g);
+      else hipLaunchKernelGGL((linear_grad_kernel<3, KSK, CTK, KSV, CTV>), grid, threads, 0, stream, g);
+    });
+  });
+  e = hipGetLastError();
   prof_end(stream, GDN_KERNEL_LINEAR_SCAN);
   if (e != hipSuccess) return e;
   prof_begin(stream, GDN_KERNEL_LINEAR_GATES);
   const GateArgs a = {ws.qdq, ws.vdv, ws.states, ws.rstates, ws.last, t.dhT, t.h0 == nullptr, t.dg, p.fixed ? ws.dg : nullptr};
   hipLaunchKernelGGL(linear_gates_kernel, dim3(blocks_of(plan.slots * p.hv)), dim3(kThreads), 0, stream, forward, a, p.dk * p.dv);
   if (p.fixed) hipLaunchKernelGGL(linear_gate_sums_kernel, dim3(p.hv), dim3(kThreads), 0, stream, ws.dg, plan.slots, p.hv, t.dg);
-  if (shared) {
-    const dim3 grid(blocks_of((p.tokens * p.hk * p.dk / 4 + kThreads - 1) / kThreads));
-    hipLaunchKernelGGL(linear_heads_kernel, grid, dim3(kThreads), 0, stream, forward, ws.dq, t.dq, p.dk, p.in_bf16);
-    hipLaunchKernelGGL(linear_heads_kernel, grid, dim3(kThreads), 0, stream, forward, ws.dk, t.dk, p.dk, p.in_bf16);
-  }
   e = hipGetLastError();
   prof_end(stream, GDN_KERNEL_LINEAR_GATES);
   return e;

@@ -22,6 +22,8 @@
 // the scan starts every segment from its own.
 #pragma once
 
+#include <type_traits>
+
 #include "gdn_linear.h"
 #include "gdn_packed.h"
 
@@ -293,37 +295,69 @@ struct State {
   }
 };
 
+// What a scan keeps in LDS.
+template <int NT, int TO, int KS, int CT, bool OUT, bool DOT>
+struct ScanSpace {
+  static constexpr int NW = kScanThreads / 64;
+  static constexpr int CH = NT == 1 ? 64 : 32, RT = CH / 16, K2 = CH / 32;   // tokens of a chunk, in tiles of 16 and 32
+  static constexpr int U = KS * 4, UC = NW * CT * 2;                         // 16-byte units of a row of A and B, and of C
+  static constexpr int GR = NT == 1 ? 4 : 2;                                 // chunks whose gates are there at once
+  alignas(16) char As[OUT ? NT * CH * U * 16 : 16];
+  alignas(16) char Bs[NT * CH * U * 16];
+  alignas(16) char Cs[NT * CH * UC * 16];
+  alignas(16) bh P[OUT ? RT * K2 * TO * 512 : 8];
+  alignas(16) float Gh[GR][CH];                // G = Gh + Gl to 48 bits: its differences have the accuracy of fp32
+  alignas(16) float Gl[GR][CH];
+  alignas(16) float fo[GR][CH];
+  alignas(16) float fs[GR][CH];
+  float all[GR];
+  float red[DOT ? NW : 1][DOT ? CH : 1];
+  double totals[OUT ? 1 : NW];
+};
+
+// The arguments of one of a kernel's scans, read where that scan begins: those of all of them at once do not fit the scalar
+// registers.  They lie `offset` bytes behind the kernel's first argument.
+__device__ __forceinline__ ScanArgs scan_args_at(uint32_t offset) {
+  auto p = (const __attribute__((address_space(4))) char*)__builtin_amdgcn_kernarg_segment_ptr() + offset;
+  asm volatile("" : "+s"(p));
+  return *(const ScanArgs*)(const char*)p;
+}
+
+// Workgroups of a scan: one for each (segment, value head), or (segment, key head) where the heads' outputs are summed.
+__host__ __device__ inline uint32_t scan_blocks(const ScanArgs& s) {
+  return (uint32_t)(s.slots * s.hk + 7) / 8 * 8 * (s.part ? 1 : s.rep);
+}
+
+// One workgroup's scan.  Units of the same remainder mod 8 run on one XCD: `unit` is a (slot, key head), `part` one of its value
+// heads (all of them, one after another, where their outputs are summed).
 // TO: terms of the states and of P where they meet A and C in the outputs: three give fp32 outputs the accuracy of fp32
 // arithmetic; two (2^-17 of a product) are far below the rounding of a bf16 output.
 template <int NT, int TO, int KS, int CT, bool REV, bool OUT, bool DOT>
-__global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s) {
-  constexpr int TH = kScanThreads, NW = TH / 64;
-  constexpr int CH = NT == 1 ? 64 : 32, RT = CH / 16, K2 = CH / 32;
-  constexpr int U = KS * 4, UC = NW * CT * 2;
+__device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int part, ScanSpace<NT, TO, KS, CT, OUT, DOT>& z) {
+  using Z = ScanSpace<NT, TO, KS, CT, OUT, DOT>;
+  constexpr int TH = kScanThreads, NW = Z::NW, CH = Z::CH, RT = Z::RT, K2 = Z::K2, U = Z::U, UC = Z::UC, GR = Z::GR;
   constexpr int es = NT == 1 ? 2 : 4;
-  constexpr bool TR = OUT && REV != DOT;       // dq and dk: states are [J][I] in memory
-  __shared__ __align__(16) char As[OUT ? NT * CH * U * 16 : 16];
-  __shared__ __align__(16) char Bs[NT * CH * U * 16];
-  __shared__ __align__(16) char Cs[NT * CH * UC * 16];
-  __shared__ __align__(16) bh P[OUT ? RT * K2 * TO * 512 : 8];
-  constexpr int GR = NT == 1 ? 4 : 2;          // chunks whose gates are there at once
-  __shared__ __align__(16) float Gh[GR][CH], Gl[GR][CH];  // G = Gh + Gl to 48 bits: its differences have the accuracy of fp32
-  __shared__ __align__(16) float fo[GR][CH], fs[GR][CH], all[GR];
-  __shared__ float red[DOT ? NW : 1][CH];
+  constexpr bool TR = OUT && REV != DOT;       // dq and dk: states are [J][I] in memory, and shared heads' outputs are summed
+  auto& As = z.As;
+  auto& Bs = z.Bs;
+  auto& Cs = z.Cs;
+  auto& P = z.P;
+  auto& Gh = z.Gh;
+  auto& Gl = z.Gl;
+  auto& fo = z.fo;
+  auto& fs = z.fs;
+  auto& all = z.all;
+  auto& red = z.red;
   const uint32_t tid = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(tid / 64);
   uint32_t lane = tid % 64;
   const int I = s.b.width, J = s.c.width, hv = s.hk * s.rep;
-
-  const uint32_t units = s.slots * s.hk, blocks = (units + 7) / 8 * 8 * s.rep;
-  for (uint32_t block = blockIdx.x; block < blocks; block += gridDim.x) {
-    // the value heads of a key head, which read the same rows, one after another on one XCD
-    const uint32_t group = block / 8 / (uint32_t)s.rep, unit = group * 8 + block % 8;
-    if (unit >= units) continue;
-    const uint32_t slot = unit / (uint32_t)s.hk;
-    const int kh = unit - slot * s.hk, h = kh * s.rep + (block / 8 - group * s.rep);
+  if (unit >= (uint32_t)(s.slots * s.hk)) return;
+  const uint32_t slot = unit / (uint32_t)s.hk;
+  const int kh = unit - slot * s.hk;
+  const bool summed = TR && s.part;
     Segment seg;
-    if (!find_segment(s.cu, s.sequences, s.tokens, s.L, slot, &seg)) continue;
+    if (!find_segment(s.cu, s.sequences, s.tokens, s.L, slot, &seg)) return;
     const size_t cell = (size_t)I * J;
     const bool in_place = s.from && s.from == s.to;
     bool keep = true;                           // the state after the last segment
@@ -339,13 +373,15 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
           keep = next == s.sequences;
           next = s.sequences;
         } else if (earlier || (next < s.sequences && (!OUT || seg.c > 0))) {
-          continue;                             // the first of them runs them all, one after another
+          return;                               // the first of them runs them all, one after another
         }
       }
     }
     if constexpr (!OUT) {
-      if (REV ? seg.c == 0 : seg.c == seg.count - 1) continue;
+      if (REV ? seg.c == 0 : seg.c == seg.count - 1) return;
     }
+    for (int r = summed ? 0 : part; r < (summed ? s.rep : part + 1); ++r) {
+    const int h = kh * s.rep + r;
     State<KS, CT> S;
     double total = 0;                           // of the gates of the wavefront's chunks
     if constexpr (!OUT) {
@@ -548,7 +584,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
         // Columns of C, as they are and, times the decay up to the chunk's end, as they go into the state: formed between the
         // products of P C and of the state's update, whose operands are read a step ahead.
         Frag<NT> cf[K2][CT], bf[3];
-        Frag<TO> pf[2][K2];
+        Frag<TO> pf[2];
         Frag<3> vf[2][CT];
         float decays[2][8];
         const uint32_t piece = lane % 4;
@@ -575,12 +611,14 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
             vf[k2 % 2][j].t[t] = as_frag(b);
           }
         };
-        const auto p_at = [&](int x) {
+        // P's fragments in turn: tokens 16 x .., by 32 k2 ..
+        constexpr int PN = RT == 4 ? 6 : 2;
+        const auto p_x = [](int n) { return RT == 4 ? (REV ? (n < 4 ? n / 2 : n - 2) : (n < 2 ? n : n / 2 + 1)) : n; };
+        const auto p_k2 = [](int n) { return RT == 4 ? (REV ? (n < 4 ? n % 2 : 1) : (n < 2 ? 0 : n % 2)) : 0; };
+        const auto p_at = [&](int n) {
 #pragma unroll
-          for (int k2 = REV ? x / 2 : 0; k2 < (REV ? K2 : x / 2 + 1); ++k2)
-#pragma unroll
-            for (int t = 0; t < TO; ++t)
-              pf[x % 2][k2].t[t] = as_frag(*reinterpret_cast<const uint4*>(P + ((x * K2 + k2) * TO + t) * 512 + lane * 8));
+          for (int t = 0; t < TO; ++t)
+            pf[n % 2].t[t] = as_frag(*reinterpret_cast<const uint4*>(P + ((p_x(n) * K2 + p_k2(n)) * TO + t) * 512 + lane * 8));
         };
         const auto b_at = [&](int n) {          // step n: rows of tile n % (2 KS), tokens of half n / (2 KS)
           const int i2 = n % (2 * KS);
@@ -592,49 +630,57 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
           for (int j = 0; j < CT; ++j)
             cf[k2][j] = column_frag<NT, UC, CH>(Cs, k2, CT == 2 ? 4 * w + piece : 2 * w + piece / 2, CT == 2 ? 8 * j : piece % 2 * 8, lane);
         decays_at(0);
-        const float decay = all[at];
-        if constexpr (OUT) {
-          p_at(0);
-          fence();
-#pragma unroll
-          for (int x = 0; x < RT; ++x) {
-            if (x + 1 < RT) p_at(x + 1);
-            else b_at(0);
-            if (x == RT - 1) b_at(1);
-            fence();
-#pragma unroll
-            for (int k2 = REV ? x / 2 : 0; k2 < (REV ? K2 : x / 2 + 1); ++k2)
-#pragma unroll
-              for (int j = 0; j < CT; ++j) o[x][j] = mma<NT, TO>(cf[k2][j], pf[x % 2][k2], o[x][j]);
-#pragma unroll
-            for (int n = x * 4 * CT / RT; n < (x + 1) * 4 * CT / RT; ++n) columns_of(0, n / 4, n % 4);
-            fence();
+        // Shared heads: the sums so far in fp32, and the last head's go out
+        const bool last = !summed || r == s.rep - 1;
+        char* const out = last ? s.out : reinterpret_cast<char*>(s.part);
+        const uint32_t part_row = (uint32_t)(s.hk * J) * 4, out_row = last ? s.out_row : part_row, ob = last ? s.out_bytes : 4;
+        const uint32_t col = CT == 2 ? 32 * w + 8 * lg : 16 * w + 4 * lg;
+        // What the outputs of 16 tokens need: their rows of d, and the sums so far
+        Values<3, 4 * CT> sums[TR ? 2 : 1];
+        Values<NT, 4 * CT> drow[DOT ? 2 : 1];
+        const auto out_at = [&](int x) {
+          if constexpr (DOT) {
+            const buf_t from = buf(s.d.p + (size_t)t0 * s.d.row + (size_t)(s.d.shared ? kh : h) * J * es, (uint32_t)(m - 1) * s.d.row + J * es);
+            drow[x % 2].load(from, (int)col < J ? (16 * x + lr) * s.d.row + col * es : kNowhere);
           }
-        } else {
-          b_at(0);
-          b_at(1);
-#pragma unroll
-          for (int n = 0; n < 4 * CT; ++n) columns_of(0, n / 4, n % 4);
-        }
-        const uint32_t ob = s.out_bytes, col = CT == 2 ? 32 * w + 8 * lg : 16 * w + 4 * lg;
-        Values<NT, 4 * CT> drow[DOT ? RT : 1];
+          if constexpr (TR) {
+            if (summed && r > 0) {
+              const buf_t from = buf(reinterpret_cast<char*>(s.part) + (size_t)t0 * part_row + (size_t)kh * J * 4, (uint32_t)(m - 1) * part_row + J * 4);
+              sums[x % 2].load(from, (int)col < J ? (16 * x + lr) * part_row + col * 4 : kNowhere);
+            }
+          }
+        };
         const auto rows_out = [&](int x) {        // outputs of 16 tokens
-          const buf_t to = buf(s.out + (size_t)t0 * s.out_row + (size_t)h * J * ob, (uint32_t)(m - 1) * s.out_row + J * ob);
+          const buf_t to = buf(out + (size_t)t0 * out_row + (size_t)(summed ? kh : h) * J * ob, (uint32_t)(m - 1) * out_row + J * ob);
           float v[4 * CT];
 #pragma unroll
           for (int j = 0; j < CT; ++j)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[4 * j + r] = o[x][j][r];
-          const uint32_t off = (int)col < J ? (16 * x + lr) * s.out_row + col * ob : kNowhere;
+            for (int e = 0; e < 4; ++e) v[4 * j + e] = o[x][j][e];
+          if constexpr (DOT) {
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4 * CT; ++e) sum = fmaf(v[e], drow[x % 2].value(e), sum);
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (lg == 0) red[w][16 * x + lr] = sum;
+          }
+          if constexpr (TR) {
+            if (summed && r > 0) {
+#pragma unroll
+              for (int e = 0; e < 4 * CT; ++e) v[e] += sums[x % 2].value(e);
+            }
+          }
+          const uint32_t off = (int)col < J ? (16 * x + lr) * out_row + col * ob : kNowhere;
           typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
           typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
           if (ob == 2) {
             uint32_t b[2 * CT];
 #pragma unroll
-            for (int r = 0; r < 2 * CT; ++r) {
+            for (int e = 0; e < 2 * CT; ++e) {
               uint32_t one[1];
-              split2<1>(v[2 * r], v[2 * r + 1], one);
-              b[r] = one[0];
+              split2<1>(v[2 * e], v[2 * e + 1], one);
+              b[e] = one[0];
             }
             if constexpr (CT == 2) __builtin_amdgcn_raw_buffer_store_b128(u32x4{b[0], b[1], b[2], b[3]}, to, off, 0, 0);
             else __builtin_amdgcn_raw_buffer_store_b64(u32x2{b[0], b[1]}, to, off, 0, 0);
@@ -645,19 +691,32 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
                                                            __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])},
                                                      to, off + 16 * j, 0, 0);
           }
-          if constexpr (DOT) {
-            float sum = 0.f;
-#pragma unroll
-            for (int r = 0; r < 4 * CT; ++r) sum = fmaf(v[r], drow[x].value(r), sum);
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
-            if (lg == 0) red[w][16 * x + lr] = sum;
-          }
         };
-        if constexpr (DOT) {
-          const buf_t db = buf(s.d.p + (size_t)t0 * s.d.row + (size_t)(s.d.shared ? kh : h) * J * es, (uint32_t)(m - 1) * s.d.row + J * es);
+        const float decay = all[at];
+        if constexpr (OUT) {
+          p_at(0);
+          fence();
 #pragma unroll
-          for (int x = 0; x < RT; ++x) drow[x].load(db, (int)col < J ? (16 * x + lr) * s.d.row + col * es : kNowhere);
+          for (int n = 0; n < PN; ++n) {
+            if (n + 1 < PN) p_at(n + 1);
+            else b_at(0);
+            if (n + 1 == PN) b_at(1);
+            fence();
+#pragma unroll
+            for (int j = 0; j < CT; ++j) o[p_x(n)][j] = mma<NT, TO>(cf[p_k2(n)][j], pf[n % 2], o[p_x(n)][j]);
+#pragma unroll
+            for (int c = n * 4 * CT / PN; c < (n + 1) * 4 * CT / PN; ++c) columns_of(0, c / 4, c % 4);
+            fence();
+          }
+        } else {
+          b_at(0);
+          b_at(1);
+#pragma unroll
+          for (int n = 0; n < 4 * CT; ++n) columns_of(0, n / 4, n % 4);
+        }
+        if constexpr (OUT) {
+          out_at(0);
+          out_at(1);
         }
 #pragma unroll
         for (int n = 0; n < K2 * 2 * KS; ++n) {
@@ -674,9 +733,15 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
           if (k2 + 1 < K2) {
 #pragma unroll
             for (int c = i2 * 4 * CT / (2 * KS); c < (i2 + 1) * 4 * CT / (2 * KS); ++c) columns_of(k2 + 1, c / 4, c % 4);
-          } else if constexpr (OUT) {
+          }
+          if constexpr (OUT) {
+            constexpr int N = K2 * 2 * KS;                             // outputs in the later steps
 #pragma unroll
-            for (int x = i2 * RT / (2 * KS); x < (i2 + 1) * RT / (2 * KS); ++x) rows_out(x);
+            for (int x = 0; x < RT; ++x)
+              if (n == N - 1 - (RT - 1 - x) * (N * 3 / (4 * RT))) {
+                rows_out(x);
+                if (x + 2 < RT) out_at(x + 2);
+              }
           }
           fence();
         }
@@ -699,35 +764,37 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s
     if constexpr (!OUT) {
       S.template move<false, TR>(s.between + (size_t)(bound_of(seg.start, REV ? seg.c - 1 : seg.c, s.L) * hv + h) * cell, I, J,
                                  w, lane);
-      __shared__ double totals[NW];
-      if (lane == 0) totals[w] = total;
+      if (lane == 0) z.totals[w] = total;
       __syncthreads();
-      if (tid == 0) s.decay[(size_t)slot * hv + h] = exp2_of((float)(totals[0] + totals[1] + totals[2] + totals[3]));
+      if (tid == 0) s.decay[(size_t)slot * hv + h] = exp2_of((float)(z.totals[0] + z.totals[1] + z.totals[2] + z.totals[3]));
     } else if (s.to && keep && row >= 0 && (serial || (REV ? seg.c == 0 : seg.c == seg.count - 1))) {
       S.template move<false, TR>(s.to + ((size_t)row * hv + h) * cell, I, J, w, lane);
     }
+    }
+}
+
+template <int NT, int TO, int KS, int CT>
+__global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s) {
+  __shared__ ScanSpace<NT, TO, KS, CT, true, false> z;
+  const uint32_t blocks = scan_blocks(s);
+  for (uint32_t block = blockIdx.x; block < blocks; block += gridDim.x) {
+    const uint32_t group = block / 8 / (uint32_t)s.rep;
+    scan_item<NT, TO, KS, CT, false, true, false>(s, group * 8 + block % 8, block / 8 - group * s.rep, z);
   }
 }
 
 // ---------------------------------------------------------------- host
 
-// Launches the scan of this variant for the widths of s.
-template <int NT, int TO, bool REV, bool OUT, bool DOT>
-hipError_t scan_variant(const ScanArgs& s, hipStream_t stream) {
-  const long long blocks = (s.slots * s.hk + 7) / 8 * 8 * s.rep;
-  const dim3 grid((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks));
-  const int ks = s.b.width <= 32 ? 1 : s.b.width <= 64 ? 2 : 4;
-  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kScanThreads), 0, stream, s); };
-  if (s.c.width <= 64) {
-    if (ks == 1) go(linear_scan_kernel<NT, TO, 1, 1, REV, OUT, DOT>);
-    else if (ks == 2) go(linear_scan_kernel<NT, TO, 2, 1, REV, OUT, DOT>);
-    else go(linear_scan_kernel<NT, TO, 4, 1, REV, OUT, DOT>);
-  } else {
-    if (ks == 1) go(linear_scan_kernel<NT, TO, 1, 2, REV, OUT, DOT>);
-    else if (ks == 2) go(linear_scan_kernel<NT, TO, 2, 2, REV, OUT, DOT>);
-    else go(linear_scan_kernel<NT, TO, 4, 2, REV, OUT, DOT>);
-  }
-  return hipGetLastError();
+// Calls f with the steps of 32 rows and the column tiles of a wavefront that widths up to 32, 64 and 128 take, as types.
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <class F>
+void by_width(int width, F f) {
+  if (width <= 32) f(Int<1>(), Int<1>());
+  else if (width <= 64) f(Int<2>(), Int<1>());
+  else f(Int<4>(), Int<2>());
 }
+
+inline dim3 scan_grid(long long blocks) { return dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)); }
 
 }  // namespace gdn
