@@ -566,7 +566,10 @@ __device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int 
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float e = REV ? (hy[r] - hx) + (ly[r] - lx) : (hx - hy[r]) + (lx - ly[r]);
-              p[r] = s.scale * exp2_of((REV ? y + r >= x : y + r <= x) ? e : -INFINITY) * d[t][r];
+              // The exponent carries the mask: no branch around the exponential.  Outputs mask the product too, which may be of a
+              // later key that is not finite; gradients, which such a key spoils anyhow, do not (it costs them registers, 10 %).
+              const bool in = REV ? y + r >= x : y + r <= x;
+              p[r] = s.scale * exp2_of(in ? e : -INFINITY) * (in || REV || DOT ? d[t][r] : 0.f);
             }
             uint32_t p0[TO], p1[TO];
             split2<TO>(p[0], p[1], p0);

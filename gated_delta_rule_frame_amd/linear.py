@@ -87,8 +87,10 @@ def linear_forward(q, k, v, log_gate, cu_seqlens, initial_state=None, *, slots=N
     Per token of a value head: S <- exp(log_gate) S + k v^T, out = scale S^T q.
     q, k: [tokens,heads_k,d_k]; v: [tokens,heads_v,d_v] (fp32 or bf16, one
     dtype; heads_v a multiple of heads_k); log_gate: [tokens,heads_v] fp32, or
-    [heads_v], one decay for each head.  cu_seqlens, slots, states, outputs and
-    the reach of a NaN or infinity are ``packed_forward``'s.
+    [heads_v], one decay for each head.  cu_seqlens, slots, states and outputs
+    are ``packed_forward``'s.  A NaN or infinity in v can make outputs of up to 63
+    earlier tokens of its sequence NaN (those in its chunk of 64), in its head and
+    column; in k or log_gate it reaches later tokens alone.
     """
     odt = _output(out, out_dtype)
     seqs, rows = _sequences(cu_seqlens, q), 0

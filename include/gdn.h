@@ -506,18 +506,23 @@ gdn_status gdn_linear_decode(const gdn_linear_problem* problem,
                              float* state, const int32_t* slots, void* out, void* stream);
 
 /* Bytes of device workspace of gdn_linear_forward (gradient = 0) or
- * gdn_linear_backward (1); host only. */
+ * gdn_linear_backward (1); host only.  Sequences are cut into segments of L
+ * tokens, L >= 128 by the number of (sequence, head) pairs (some 512 segments
+ * and heads in all, or one more for each pair); with cell = 4 heads_v d_k d_v:
+ *   forward    2 tokens / L cell: the states between segments, 0 for calls of
+ *              up to 384 tokens
+ *   gradients  as much, sequences cell, and tokens (8 heads_v, and 8 heads_k d_k
+ *              where value heads share key heads) */
 gdn_status gdn_linear_workspace_size(const gdn_linear_problem* problem, int32_t gradient, size_t* bytes_out);
 
 /* Packed sequences: cu_seqlens, slots, initial_state and final_state as in
  * gdn_packed_forward.  fp32 results (states, and outputs of that type) have the
  * accuracy of fp32 arithmetic, the range is that of bf16.  A NaN or infinity in
- * a token's q spoils that token's outputs; in its k, v or log_gate, beside what
- * the recurrence makes of it, also outputs of earlier tokens in its chunk of 64
- * (0 times it is NaN), in the value heads that read it and, for v, in its
- * column.  Rows behind the last sequence are neither read nor written.  No
- * aliasing but of initial_state with final_state.  The workspace is as
- * gdn_forward's. */
+ * a token's q spoils that token's outputs; in its k or log_gate it does what the
+ * recurrence makes of it; in its v it also reaches outputs of earlier tokens in
+ * its chunk of 64 (0 times it is NaN), in its head and column.  Rows behind the
+ * last sequence are neither read nor written.  No aliasing but of initial_state
+ * with final_state.  The workspace is as gdn_forward's. */
 gdn_status gdn_linear_forward(const gdn_linear_problem* problem,
                               const void* q, const void* k, const void* v, const float* log_gate,
                               const int32_t* cu_seqlens, const int32_t* slots,

@@ -329,7 +329,7 @@ def test_not_finite_values_stay_where_they_are_documented(G):
             same = torch.ones(cu[-1], hv, d, dtype=torch.bool, device="cuda")
             heads = [1] if which == "v" else [2, 3]
             cols = [3] if which == "v" else list(range(d))
-            rows = range(100, 101) if which == "q" else range(64, 200)
+            rows = range(100, 101) if which == "q" else range(100, 200) if which == "k" else range(64, 200)
             for h in heads:
                 for r in rows:
                     same[r, h, cols] = False
@@ -338,6 +338,16 @@ def test_not_finite_values_stay_where_they_are_documented(G):
             if which != "q":
                 assert torch.isnan(got[199, heads][:, cols]).all() and torch.isnan(fin[0, heads][:, :, cols]).any()
             assert torch.equal(fin[1], end[1])
+        for value in (float("nan"), float("inf")):             # in k: later tokens alone, also where its products are masked
+            y = [a.clone() for a in x]
+            y[1][100, 0, 5] = value
+            got, _ = G.linear_forward(*y, cu_tensor(cu))
+            assert torch.equal(got[:100], want[:100]) and torch.equal(got[200:], want[200:])
+        y = [a.clone() for a in x]
+        y[3][100, 2] = float("nan")
+        got, fin = G.linear_forward(*y, cu_tensor(cu))
+        assert torch.equal(got[:100], want[:100]) and torch.equal(got[200:], want[200:]) and torch.equal(got[:, [0, 1, 3]], want[:, [0, 1, 3]])
+        assert torch.isnan(got[100:200, 2]).all() and torch.isnan(fin[0, 2]).all()
 
 
 def test_malformed_offsets_stay_in_range(G):
