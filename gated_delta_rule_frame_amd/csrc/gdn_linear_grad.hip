@@ -8,6 +8,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr float kNoGate = -104.f;             // exp of less is 0 in fp32
 
 // The sum of x over the workgroup, in every lane; `red`: four values.
 __device__ __forceinline__ double block_sum(double x, double* red) {
@@ -32,7 +33,8 @@ struct GateArgs {
 };
 
 // dlog_gate of a segment's tokens: <R, S> at its end and the sums of q.dq - v.dv behind each token, in fp64.  The first
-// gate of a sequence that starts from zeros scales nothing: its gradient is 0, not what the sums' roundings leave.
+// gate of a sequence that starts from zeros scales nothing, and one whose exponential is 0 in fp32 (-inf, a mask's lowest
+// value) drops what it scales: their gradients are 0, not what the sums' roundings leave.
 __global__ __launch_bounds__(kThreads) void linear_gates_kernel(ScanArgs s, GateArgs a, int cell) {
   __shared__ double red[4];
   const int tid = threadIdx.x, lane = tid % 64, w = tid / 64, hv = s.hk * s.rep;
@@ -79,7 +81,8 @@ __global__ __launch_bounds__(kThreads) void linear_gates_kernel(ScanArgs s, Gate
       x += carry;
       carry += red[0] + red[1] + red[2] + red[3];
       if (i >= 0) {
-        if (a.from_zero && seg.first + i == seg.start) x = 0;
+        const float g = s.g[s.fixed ? h : (size_t)(seg.first + i) * hv + h];
+        if ((a.from_zero && seg.first + i == seg.start) || g < kNoGate) x = 0;
         if (a.sums) sum += x;
         else a.dg[(size_t)(seg.first + i) * hv + h] = (float)x;
       }

@@ -532,7 +532,7 @@ gdn_status gdn_linear_forward(const gdn_linear_problem* problem,
 /* Gradients of sum(out dout) + sum(final_state dfinal_state) for every input,
  * from the inputs alone; the arguments are gdn_packed_backward's without beta.
  * dlog_gate has log_gate's shape; with gate_per_head it sums over all tokens of
- * all sequences.  No atomics: every run gives the same bits.  A NaN or infinity
+ * all sequences; it is 0 where exp(log_gate) is 0 in fp32.  No atomics: every run gives the same bits.  A NaN or infinity
  * may spoil every gradient of its sequence in the value heads that read it, and
  * what is summed over them; other sequences are as without it (a dlog_gate of
  * [heads_v] sums them all).  No aliasing. */

@@ -315,6 +315,35 @@ def test_gates_at_their_ends(G):
     assert torch.allclose(a[3].double(), b[3].double().sum(0), rtol=1e-5)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gates_that_drop_the_state_have_no_gradient(G, dtype):
+    """exp(log_gate) is 0 in fp32: so is its gradient, exactly, in one segment, in several and for a fixed gate; the others keep theirs."""
+    lengths, d = [130, 900], 32
+    cu = bounds_of(lengths)
+    x = inputs(cu[-1], 1, 2, d, d, dtype, 25)
+    dropped = [(7, 0), (129, 1), (200, 0), (130, 1), (640, 1), (900, 0)]
+    low = [float("-inf"), torch.finfo(F32).min, -1e4, -105.0, float("-inf"), -200.0]
+    for (t, h), g in zip(dropped, low):
+        x[3][t, h] = g
+    S0, dS = states(2, 2, d, d, 1), states(2, 2, d, d, 2)
+    dout = x[2] + 1
+    dg = G.linear_backward(*x, cu_tensor(cu), dout, S0, dS)[3]
+    args = [R.f64(t) for t in x]
+    want = L.packed_grads(*args, cu, R.f64(S0), R.f64(dout), R.f64(dS), 1.0)[3]
+    for t, h in dropped:
+        assert dg[t, h].item() == 0
+    # the sums of q.dq and v.dv behind a token and <R, S> at the end, as in test_backward
+    mag = L.packed_grads(*[t.abs() for t in args[:3]], args[3], cu, R.f64(S0).abs(), R.f64(dout).abs(), R.f64(dS).abs(), 1.0)
+    terms = (args[2].abs() * mag[2]).sum(-1)
+    mend = reference(x, cu, S0, 1.0)[3]
+    m = torch.cat([terms[a:b].flip(0).cumsum(0).flip(0) + (R.f64(dS).abs() * mend).sum((-1, -2))[i]
+                   for i, (a, b) in enumerate(zip(cu, cu[1:]))])
+    assert (R.f64(dg) - want).norm() <= 2.0 ** -20 * 3 * m.norm()
+    fixed = torch.tensor([float("-inf"), -0.05], device="cuda")
+    dg = G.linear_backward(*x[:3], fixed, cu_tensor(cu), dout, S0, dS)[3]
+    assert dg[0].item() == 0 and dg[1].item() != 0
+
+
 def test_not_finite_values_stay_where_they_are_documented(G):
     """A NaN reaches back at most to its chunk of 64, in the heads that read it and, in v, in its column; other sequences are whole."""
     lengths, hk, hv, d = [200, 90], 2, 4, 32
