@@ -157,7 +157,8 @@ hipError_t launch(const SeqProblem& p, const void* q, const void* k, const void*
   prof_begin(stream, id);
   // 64 columns a workgroup: 440 rows x 32 heads x 128^2 407 us (4.55 TB/s; a copy of its size reaches 4.7), against 449 at 32
   // (128-byte pieces of the rows), 417 at 128 (a register more for every row held) and 650 at 16; 48 rows 43.5, 45.8, 45.2 and
-  // 69.7 (the delta rule).  Narrower values leave less than half of 64 columns' lanes idle at 32.
+  // 69.7 (the delta rule; linear attention, with half of the sums, 381 to 397 for 440 rows).  Narrower values leave less than
+  // half of 64 columns' lanes idle at 32.
   auto kernel = p.in_bf16 ? (p.dv > 32 ? go<true, 64, DELTA> : go<true, 32, DELTA>)
                           : (p.dv > 32 ? go<false, 64, DELTA> : go<false, 32, DELTA>);
   kernel(p, q, k, v, g, beta, state, slots, out, scale, fixed, stream);

@@ -109,10 +109,13 @@ size_t carve(char** at, char* base, size_t* bytes, size_t n) {
 // a state, four times, and a start of some chunks' time: so there are about as many (segment, head) pairs as workgroups run at
 // once (LDS and registers: two a CU, three where no width is above 64, forward and bf16), with half a segment more for each
 // sequence's last one, or twice as many and so on where the sequences alone are that many.  Prompts of 8191 tokens in 13,
-// 32 heads of 128: 175 us at 256 tokens a segment, 155 at 512, 149 at 768, 165 at 1024; gradients of 8192 in 6: 578, 545, 515,
-// 588; one document of 32768, 35 heads of 64: 265, 247, 236, 247 and 226 at 1536; gradients of 16384: 459, 443, 401, 473, 447.
+// 32 heads of 128: 180 us at 256 tokens a segment, 156 at 512, 148 at 768, 154 at 1024; gradients of 8192 in 6: 568, 510, 548,
+// 559; one document of 32768, 35 heads of 64: 265 at 512, 265 at 1024, 246 at 1536, 268 at 2048, 321 at 4096.
 // One workgroup alone takes 5 us for a chunk of 64 tokens, which bounds short calls: 880 tokens in 3 of fp32, 20 heads of 112
-// (gradients): 152 us at 128 tokens a segment, 231 at 256, 311 in one; but up to 384 tokens the two launches more cost more.
+// (gradients): 91 us at 128 tokens a segment, 117 at 256, 123 at 512; but up to 384 tokens the two launches more cost more
+// (203 tokens: 18 us in one, 28 at 128).
+// The errors of gates' gradients grow with a segment (linear_gates_kernel), those of one gate a head twice over: their
+// segments end at 1536 and 512 tokens (16384 tokens, 35 heads of 64 with a gate each: 390 us at 512, 370 at 1536).
 LinearPlan linear_plan(const LinearProblem& p, bool grad) {
   const bool wide = p.dk > 64 || p.dv > 64;
   const double at_once = 256.0 * (wide || grad || !p.in_bf16 ? 2 : 3), each = at_once / p.hv, half = 0.5 * p.sequences;
@@ -120,6 +123,7 @@ LinearPlan linear_plan(const LinearProblem& p, bool grad) {
                                          : (std::floor(half / each + 0.5) + 1) * each - half;
   double tokens = (double)p.tokens / wanted * (p.sequences <= 1 ? 1.0 : 1.03);
   tokens = tokens < 128 ? 128 : tokens;
+  if (grad && tokens > (p.fixed ? 512 : 1536)) tokens = p.fixed ? 512 : 1536;
   long long L = tokens < (double)p.tokens ? ((long long)std::ceil(tokens) + 63) / 64 * 64 : p.tokens;
   if (p.tokens <= 384 || L >= p.tokens) L = (p.tokens + 64) / 64 * 64;       // one segment, and none behind it
   LinearPlan plan;

@@ -508,7 +508,8 @@ gdn_status gdn_linear_decode(const gdn_linear_problem* problem,
 /* Bytes of device workspace of gdn_linear_forward (gradient = 0) or
  * gdn_linear_backward (1); host only.  Sequences are cut into segments of L
  * tokens, L >= 128 by the number of (sequence, head) pairs (some 512 segments
- * and heads in all, or one more for each pair); with cell = 4 heads_v d_k d_v:
+ * and heads in all, or one more for each pair; gradients: L <= 1536, or 512 with
+ * gate_per_head); with cell = 4 heads_v d_k d_v:
  *   forward    2 tokens / L cell: the states between segments, 0 for calls of
  *              up to 384 tokens
  *   gradients  as much, sequences cell, and tokens (8 heads_v, and 8 heads_k d_k

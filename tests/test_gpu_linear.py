@@ -315,6 +315,32 @@ def test_gates_at_their_ends(G):
     assert torch.allclose(a[3].double(), b[3].double().sum(0), rtol=1e-5)
 
 
+def test_gradients_of_fixed_gates_over_many_tokens(G):
+    """Each token's q.dq and v.dv have roundings of 2^-22 of their size at most in the 2-norm, independent ones.  A gate's gradient sums
+    what they leave behind every token, up to known ends of segments of at most 512 tokens: a bridge, whose sum has L^2 / 12 of a
+    step's variance for each; the ends' own roundings, 2^-22, count L / 2 in the two segments beside them."""
+    n, h, d = 20000, 32, 32
+    g = torch.tensor([1 - 2.0 ** (-2 - 6 * i / h) for i in range(h)], dtype=torch.float64).log().float().cuda()
+    q, k, v, _ = inputs(n, h, h, d, d, BF16, 77)
+    q, k = (torch.nn.functional.normalize(t.float(), dim=-1).to(BF16) for t in (q, k))
+    dout = inputs(n, h, h, d, d, BF16, 78)[2]
+    got = G.linear_backward(q, k, v, g, cu_tensor([0, n]), dout)[3]
+    a, (Q, K, V, D) = torch.exp(g.double())[:, None, None], (t.double() for t in (q, k, v, dout))
+    S, R = torch.zeros(2, h, d, d, dtype=torch.float64, device="cuda")
+    u, w = torch.empty(2, n, h, dtype=torch.float64, device="cuda")
+    for t in range(n):
+        S = S * a + K[t][:, :, None] * V[t][:, None, :]
+        u[t] = (Q[t][:, :, None] * S * D[t][:, None, :]).sum((-1, -2))
+        s = n - 1 - t
+        R = R * a + Q[s][:, :, None] * D[s][:, None, :] if t else Q[s][:, :, None] * D[s][:, None, :]
+        w[s] = (K[s][:, :, None] * R * V[s][:, None, :]).sum((-1, -2))
+    dg = (u - w).flip(0).cumsum(0).flip(0)                     # of each token
+    dg[0] = 0
+    ends = dg[64::64].square().mean(0) * (n / 512)             # <R, S> of the segments' ends, by their mean square
+    tol = 2.0 ** -22 * (512.0 ** 2 / 12 * (u * u + w * w).sum(0) + 512.0 ** 2 * ends).sum().sqrt()
+    assert (got.double() - dg.sum(0)).norm() <= tol
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_gates_that_drop_the_state_have_no_gradient(G, dtype):
     """exp(log_gate) is 0 in fp32: so is its gradient, exactly, in one segment, in several and for a fixed gate; the others keep theirs."""
