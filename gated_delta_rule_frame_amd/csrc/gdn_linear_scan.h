@@ -27,12 +27,12 @@
 // LDS once (the next chunk's are in flight meanwhile); P = A B^T, gated and split,
 // passes through LDS to the wavefronts' columns.  fp32 values are three bf16 terms,
 // products six of the nine term products.  What bounds it: with d = 128 and bf16
-// a wavefront has 196 matrix instructions of 16 clocks a chunk, and the chunk takes
-// 9.8 thousand clocks for a workgroup alone and 10.8 for two on a CU (at 1.65 to
-// 1.8 GHz; 3.2 us a chunk and CU, 58 % of the matrix instructions' rate): the rest is
-// the splitting of the state and of P, of which a matrix instruction hides two
-// instructions, and the waits at the chunk's three barriers.  8191 tokens of 32 heads: 99 us, 2.6 TB/s; 32768 of 35
-// heads of 64: 150, 3.4 TB/s.
+// a wavefront has 196 matrix instructions of 16 clocks a chunk.  A chunk takes 6 us
+// for a workgroup alone on a CU and 8.4 for two (16 sequences of 2048 tokens, 32
+// heads: 292 us), of which the matrix instructions would take 3.7 at 1.7 GHz: the rest
+// is the splitting of the state and of P, of which a matrix instruction hides two
+// instructions, and the waits at the chunk's three barriers.  8191 tokens of 32 heads
+// in segments: 99 us, 2.6 TB/s; 32768 of 35 heads of 64: 150, 3.4 TB/s.
 #pragma once
 
 #include <type_traits>
