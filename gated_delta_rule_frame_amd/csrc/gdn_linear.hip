@@ -32,67 +32,79 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_sums_kernel(SumsArgs a
   }
 }
 
-// The states between the segments of a sequence from their sums, four elements of the state a lane: forward S <- e^G S + sum
-// from the initial state, reversed R <- e^G R + sum from the final state's gradient.
-template <bool REV>
+// The states between the segments of a sequence from their sums, V times four elements of the state a lane: forward S <- e^G S +
+// sum from the initial state, reversed R <- e^G R + sum from the final state's gradient.
+template <bool REV, int V>
 __device__ __forceinline__ void chain(const ScanArgs& s, int cell, int part, int seq, int h) {
   const int hv = s.hk * s.rep;
   const bool in_place = s.from && s.from == s.to;
-      int a, b;
-      seq_bounds(s.cu, seq, s.tokens, &a, &b);
-      int each;
-      const int count = segments_of(b - a, s.L, &each);
-      if (count < 2) return;
-      long long row = seq;
-      if (s.state_slots) {
-        row = s.state_slots[seq];
-        if (row < 0 || row >= s.state_rows) row = -1;
-        else if (in_place) {
-          bool earlier;
-          int next;
-          same_slot(s.state_slots, s.sequences, seq, &earlier, &next);
-          if (earlier || next < s.sequences) return;
+  int a, b;
+  seq_bounds(s.cu, seq, s.tokens, &a, &b);
+  int each;
+  const int count = segments_of(b - a, s.L, &each);
+  if (count < 2) return;
+  long long row = seq;
+  if (s.state_slots) {
+    row = s.state_slots[seq];
+    if (row < 0 || row >= s.state_rows) row = -1;
+    else if (in_place) {
+      bool earlier;
+      int next;
+      same_slot(s.state_slots, s.sequences, seq, &earlier, &next);
+      if (earlier || next < s.sequences) return;
+    }
+  }
+  const int e = (part * V * kThreads + threadIdx.x) * 4;
+  constexpr int kNext = kThreads * 4;
+  if (V == 1 && e >= cell) return;                                // V = 2: cell is a multiple of what a workgroup has
+  const long long slot = a / (uint32_t)s.L + seq;
+  const long long b0 = bound_of(a, 0, s.L);
+  float* at = s.between + (size_t)(b0 * hv + h) * cell + e;
+  const size_t step = (size_t)hv * cell;
+  f32x4 S[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    S[v] = s.from && row >= 0 ? *reinterpret_cast<const f32x4*>(s.from + ((size_t)row * hv + h) * cell + e + v * kNext) : zero4();
+    if (!REV && in_place) *reinterpret_cast<f32x4*>(s.firsts + (size_t)(b0 * hv + h) * cell + e + v * kNext) = S[v];
+  }
+  // Two bounds at once: more cost instructions and registers where sequences have few (8191 tokens in 13, sums and states 40.5 us
+  // at 2, 42 at 8, 48 at 16, 55 at 24), and gain nothing along 21 of them
+  constexpr int kAhead = 2;
+  for (int i0 = 0; i0 < count - 1; i0 += kAhead) {
+    f32x4 u[kAhead][V];
+    float d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = REV ? count - 2 - i0 - i : i0 + i;            // bound k, between segments k and k + 1
+      if (i0 + i < count - 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) u[i][v] = *reinterpret_cast<const f32x4*>(at + k * step + v * kNext);
+        d[i] = s.decay[(slot + (REV ? k + 1 : k)) * hv + h];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = REV ? count - 2 - i0 - i : i0 + i;
+      if (i0 + i < count - 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          S[v] = d[i] * S[v] + u[i][v];
+          *reinterpret_cast<f32x4*>(at + k * step + v * kNext) = S[v];
         }
       }
-      const int e = (part * kThreads + threadIdx.x) * 4;
-      if (e >= cell) return;
-      const long long slot = a / (uint32_t)s.L + seq;
-      const long long b0 = bound_of(a, 0, s.L);
-      float* at = s.between + (size_t)(b0 * hv + h) * cell + e;
-      const size_t step = (size_t)hv * cell;
-      f32x4 S = s.from && row >= 0 ? *reinterpret_cast<const f32x4*>(s.from + ((size_t)row * hv + h) * cell + e) : zero4();
-      if (!REV && in_place) *reinterpret_cast<f32x4*>(s.firsts + (size_t)(b0 * hv + h) * cell + e) = S;
-      constexpr int kAhead = 8;
-      for (int i0 = 0; i0 < count - 1; i0 += kAhead) {
-        f32x4 u[kAhead];
-        float d[kAhead];
-  #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int k = REV ? count - 2 - i0 - i : i0 + i;            // bound k, between segments k and k + 1
-          if (i0 + i < count - 1) {
-            u[i] = *reinterpret_cast<const f32x4*>(at + k * step);
-            d[i] = s.decay[(slot + (REV ? k + 1 : k)) * hv + h];
-          }
-        }
-  #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int k = REV ? count - 2 - i0 - i : i0 + i;
-          if (i0 + i < count - 1) {
-            S = d[i] * S + u[i];
-            *reinterpret_cast<f32x4*>(at + k * step) = S;
-          }
-        }
-      }
+    }
+  }
 }
 
+template <int V>
 __global__ __launch_bounds__(kThreads) void linear_chain_kernel(ScanArgs f, ScanArgs r, int directions, int cell, int parts) {
   const uint32_t hv = f.hk * f.rep, each = f.sequences * hv * parts;       // at most 2^20 * 16
   for (uint32_t item = blockIdx.x; item < each * directions; item += gridDim.x) {
     const bool reversed = item >= each;
     const uint32_t i = reversed ? item - each : item, pair = i / (uint32_t)parts;
     const int part = i - pair * parts, seq = pair / hv, h = pair - seq * hv;
-    if (reversed) chain<true>(r, cell, part, seq, h);
-    else chain<false>(f, cell, part, seq, h);
+    if (reversed) chain<true, V>(r, cell, part, seq, h);
+    else chain<false, V>(f, cell, part, seq, h);
   }
 }
 
@@ -181,9 +193,14 @@ hipError_t linear_states(const ScanArgs& forward, const ScanArgs* reversed, bool
   });
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) {
+    // Two vectors a lane where that divides a state and there are more workgroups than run at once: 8191 tokens in 13, 32 heads of
+    // 128: 38 us with the sums against 42; but 35 heads of 64 in one sequence 88 against 84.
     const int cell = forward.b.width * forward.c.width, parts = (cell + kThreads * 4 - 1) / (kThreads * 4);
     const long long items = (long long)forward.sequences * forward.hk * forward.rep * parts * directions;
-    hipLaunchKernelGGL(linear_chain_kernel, scan_grid(items), dim3(kThreads), 0, stream, forward, r, directions, cell, parts);
+    if (items > 2048 && cell % (kThreads * 8) == 0)
+      hipLaunchKernelGGL(linear_chain_kernel<2>, scan_grid(items / 2), dim3(kThreads), 0, stream, forward, r, directions, cell, parts / 2);
+    else
+      hipLaunchKernelGGL(linear_chain_kernel<1>, scan_grid(items), dim3(kThreads), 0, stream, forward, r, directions, cell, parts);
     e = hipGetLastError();
   }
   prof_end(stream, GDN_KERNEL_LINEAR_STATES);

@@ -234,6 +234,32 @@ def test_pools_repeated_slots_and_padding(G, lengths):
         assert torch.equal(p, state)
 
 
+def test_many_sequences_and_heads_with_a_long_one(G):
+    """More states between segments than run at once: two vectors a lane in the chain; a pool in place, gradients against the formula's."""
+    lengths, hv, d = [700] + [20 + i % 7 for i in range(32)], 16, 64
+    cu, n = bounds_of(lengths), len(lengths)
+    x = inputs(cu[-1], 8, hv, d, d, BF16, 41)
+    S0, dS = states(n, hv, d, d, 1), states(n, hv, d, d, 2)
+    o, end, mo, mend = reference(x, cu, S0, 0.125)
+    slots = torch.randperm(n, generator=torch.Generator().manual_seed(4)).to(torch.int32).cuda()
+    pool = torch.empty_like(S0)
+    pool[slots.long()] = S0
+    eps = steps(d, d, lengths) + 2
+    got, final = G.linear_forward(*x, cu_tensor(cu), pool, slots=slots, scale=0.125)
+    assert final.data_ptr() == pool.data_ptr()
+    check(got, o, mo, eps)
+    check(final[slots.long()], end, mend, eps)
+    dout = x[2] + 1
+    args = [R.f64(t) for t in x]
+    want = L.packed_grads(*args, cu, R.f64(S0), R.f64(dout), R.f64(dS), 0.125)
+    mag = L.packed_grads(*[t.abs() for t in args[:3]], args[3], cu, R.f64(S0).abs(), R.f64(dout).abs(), R.f64(dS).abs(), 0.125)
+    dq, dk, dv, _, d0 = G.linear_backward(*x, cu_tensor(cu), dout, S0, dS, scale=0.125)
+    check(dq, want[0], mag[0], eps)
+    check(dk, want[1], mag[1], eps, two_terms=True)
+    check(dv, want[2], mag[2], eps)
+    check(d0, want[4], mag[4], eps)
+
+
 def test_in_place_without_slots(G):
     cu, d = bounds_of([700, 0, 30]), 32
     x = inputs(cu[-1], 1, 1, d, d, F32, 2)
