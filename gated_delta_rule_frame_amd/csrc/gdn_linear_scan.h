@@ -32,7 +32,7 @@
 // heads: 292 us), of which the matrix instructions would take 3.7 at 1.7 GHz: the rest
 // is the splitting of the state and of P, of which a matrix instruction hides two
 // instructions, and the waits at the chunk's three barriers.  8191 tokens of 32 heads
-// in segments: 99 us, 2.6 TB/s; 32768 of 35 heads of 64: 150, 3.4 TB/s.
+// in segments: 99 to 104 us, 2.7 TB/s; 32768 of 35 heads of 64: 150 to 173, 3.5 to 4.
 #pragma once
 
 #include <type_traits>
