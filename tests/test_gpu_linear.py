@@ -341,6 +341,29 @@ def test_gates_at_their_ends(G):
     assert torch.allclose(a[3].double(), b[3].double().sum(0), rtol=1e-5)
 
 
+def test_gradients_without_the_initial_states(G):
+    """The C entry may leave them out: the other gradients are the same, the gates' to what the sums of the first segments leave."""
+    from gated_delta_rule_frame_amd import linear
+    lengths, d = [100, 700], 32
+    cu = bounds_of(lengths)
+    x = inputs(cu[-1], 1, 2, d, d, BF16, 51)
+    S0, dS = states(2, 2, d, d, 1), states(2, 2, d, d, 2)
+    dout = x[2] + 1
+    want = G.linear_backward(*x, cu_tensor(cu), dout, S0, dS)
+    bounds = cu_tensor(cu)
+    p, device = linear._problem(*x, 1.0, F32, 2)[:2]
+    ws, size = linear._space("gdn_linear_workspace_size", p, 1, None, device)
+    got = [torch.empty_like(t) for t in want[:4]]
+    linear._on(device, G.lib().gdn_linear_backward, p, *(t.data_ptr() for t in x), bounds.data_ptr(), S0.data_ptr(), dout.data_ptr(),
+               dS.data_ptr(), *(t.data_ptr() for t in got), None, ws.data_ptr(), size)
+    assert all(torch.equal(a, b) for a, b in zip(got[:3], want))
+    # 2^-22 of q.dq and v.dv at each token, twice their sums' magnitude at most (as in test_backward: 2^-20 of the magnitudes)
+    args = [R.f64(t) for t in x]
+    mag = L.packed_grads(*[t.abs() for t in args[:3]], args[3], cu, R.f64(S0).abs(), R.f64(dout).abs(), R.f64(dS).abs(), 1.0)
+    m = 3 * (args[2].abs() * mag[2]).sum(-1).sum(0)
+    assert ((got[3] - want[3]).double().norm(dim=0).cpu() <= 2.0 ** -20 * m).all()
+
+
 def test_gradients_of_fixed_gates_over_many_tokens(G):
     """Each token's q.dq and v.dv have roundings of 2^-22 of their size at most in the 2-norm, independent ones.  A gate's gradient sums
     what they leave behind every token, up to known ends of segments of at most 512 tokens: a bridge, whose sum has L^2 / 12 of a
