@@ -18,16 +18,16 @@ struct SumsArgs {
 
 template <int NT, int KS, int CT>
 __global__ __launch_bounds__(kScanThreads, 2) void linear_sums_kernel(SumsArgs a) {
-  __shared__ ScanSpace<NT, 3, KS, CT, false, false> z;
+  __shared__ ScanSpace<NT, KS, CT, false, false> z;
   const uint32_t heads = a.forward.rep, parts = heads * a.directions, blocks = scan_blocks(a.forward) * a.directions;
   for (uint32_t block = blockIdx.x; block < blocks; block += gridDim.x) {
     const uint32_t group = block / 8 / parts, unit = group * 8 + block % 8, part = block / 8 - group * parts;
     if (part < heads) {
       const ScanArgs s = scan_args_at(offsetof(SumsArgs, forward));
-      scan_item<NT, 3, KS, CT, false, false, false>(s, unit, part, z);
+      scan_item<NT, KS, CT, false, false, false>(s, unit, part, z);
     } else {
       const ScanArgs s = scan_args_at(offsetof(SumsArgs, reversed));
-      scan_item<NT, 3, KS, CT, true, false, false>(s, unit, part - heads, z);
+      scan_item<NT, KS, CT, true, false, false>(s, unit, part - heads, z);
     }
   }
 }
@@ -248,9 +248,8 @@ hipError_t linear_forward_launch(const LinearProblem& p, const LinearTensors& t,
     by_width(p.dv, [&](auto, auto ct) {
       constexpr int KS = decltype(ks)::value, CT = decltype(ct)::value;
       const dim3 grid = scan_grid(scan_blocks(s)), threads(kScanThreads);
-      if (!p.in_bf16) hipLaunchKernelGGL((linear_scan_kernel<3, 3, KS, CT>), grid, threads, 0, stream, s);
-      else if (p.out_bf16) hipLaunchKernelGGL((linear_scan_kernel<1, 2, KS, CT>), grid, threads, 0, stream, s);
-      else hipLaunchKernelGGL((linear_scan_kernel<1, 3, KS, CT>), grid, threads, 0, stream, s);
+      if (p.in_bf16) hipLaunchKernelGGL((linear_scan_kernel<1, KS, CT>), grid, threads, 0, stream, s);
+      else hipLaunchKernelGGL((linear_scan_kernel<3, KS, CT>), grid, threads, 0, stream, s);
     });
   });
   const hipError_t e = hipGetLastError();

@@ -141,10 +141,9 @@ struct GradArgs {
 // registers; 16384 tokens of 35 heads of 64 272 us, 880 of fp32 48.  KSK, CTK and KSV, CTV: by_width of d_k and d_v.
 template <int NT, int KSK, int CTK, int KSV, int CTV>
 __global__ __launch_bounds__(kScanThreads, 2) void linear_grad_kernel(GradArgs g) {
-  constexpr int TO = NT == 1 ? 2 : 3;
-  using Q = ScanSpace<NT, 3, KSV, CTK, true, true>;
-  using K = ScanSpace<NT, TO, KSV, CTK, true, false>;
-  using V = ScanSpace<NT, 3, KSK, CTV, true, true>;
+  using Q = ScanSpace<NT, KSV, CTK, true, true>;
+  using K = ScanSpace<NT, KSV, CTK, true, false>;
+  using V = ScanSpace<NT, KSK, CTV, true, true>;
   __shared__ union {
     Q q;
     K k;
@@ -156,13 +155,13 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_grad_kernel(GradArgs g
     const uint32_t group = block / 8 / parts, unit = group * 8 + block % 8, part = block / 8 - group * parts;
     if (part < keys) {
       const ScanArgs s = scan_args_at(offsetof(GradArgs, dq));
-      scan_item<NT, 3, KSV, CTK, false, true, true>(s, unit, part, z.q);
+      scan_item<NT, KSV, CTK, false, true, true>(s, unit, part, z.q);
     } else if (part < 2 * keys) {
       const ScanArgs s = scan_args_at(offsetof(GradArgs, dk));
-      scan_item<NT, TO, KSV, CTK, true, true, false>(s, unit, part - keys, z.k);
+      scan_item<NT, KSV, CTK, true, true, false>(s, unit, part - keys, z.k);
     } else {
       const ScanArgs s = scan_args_at(offsetof(GradArgs, dv));
-      scan_item<NT, 3, KSK, CTV, true, true, true>(s, unit, part - 2 * keys, z.v);
+      scan_item<NT, KSK, CTV, true, true, true>(s, unit, part - 2 * keys, z.v);
     }
   }
 }

@@ -45,6 +45,10 @@ namespace gdn {
 // ---------------------------------------------------------------- device
 
 constexpr int kScanThreads = 256;
+// bf16 terms of the states and of P where they meet A and C, whatever the outputs' type: with three a bf16 output is the fp32
+// output rounded once.  Two (2^-17 of a product) sent 0.23 % of a call's bf16 values to another neighbour than the plain fp32 form
+// has, against 0.02 %, for 99 us of the forward scan's 115 (8191 tokens of 32 heads of 128) and 385 of the gradients' 389.
+constexpr int kTerms = 3;
 constexpr int kAtOnce = 512;                   // workgroups of a scan that run at once, at least
 
 // Gates below this are this: e^-10000 is 0 in fp32, and G stays finite for -inf.
@@ -337,7 +341,7 @@ struct State {
 };
 
 // What a scan keeps in LDS.
-template <int NT, int TO, int KS, int CT, bool OUT, bool DOT>
+template <int NT, int KS, int CT, bool OUT, bool DOT>
 struct ScanSpace {
   static constexpr int NW = kScanThreads / 64;
   static constexpr int CH = NT == 1 ? 64 : 32, RT = CH / 16, K2 = CH / 32;   // tokens of a chunk, in tiles of 16 and 32
@@ -346,7 +350,7 @@ struct ScanSpace {
   alignas(16) char As[OUT ? NT * CH * U * 16 : 16];
   alignas(16) char Bs[NT * CH * U * 16];
   alignas(16) char Cs[NT * CH * UC * 16];
-  alignas(16) bh P[OUT ? RT * K2 * TO * 512 : 8];
+  alignas(16) bh P[OUT ? RT * K2 * kTerms * 512 : 8];
   alignas(16) float Gh[GR][CH];                // G = Gh + Gl to 48 bits: its differences have the accuracy of fp32
   alignas(16) float Gl[GR][CH];
   alignas(16) float fo[GR][CH];
@@ -371,11 +375,9 @@ __host__ __device__ inline uint32_t scan_blocks(const ScanArgs& s) {
 
 // One workgroup's scan.  Units of the same remainder mod 8 run on one XCD: `unit` is a (slot, key head), `part` one of its value
 // heads (all of them, one after another, where their outputs are summed).
-// TO: terms of the states and of P where they meet A and C in the outputs: three give fp32 outputs the accuracy of fp32
-// arithmetic; two (2^-17 of a product) are far below the rounding of a bf16 output.
-template <int NT, int TO, int KS, int CT, bool REV, bool OUT, bool DOT>
-__device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int part, ScanSpace<NT, TO, KS, CT, OUT, DOT>& z) {
-  using Z = ScanSpace<NT, TO, KS, CT, OUT, DOT>;
+template <int NT, int KS, int CT, bool REV, bool OUT, bool DOT>
+__device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int part, ScanSpace<NT, KS, CT, OUT, DOT>& z) {
+  using Z = ScanSpace<NT, KS, CT, OUT, DOT>;
   constexpr int TH = kScanThreads, NW = Z::NW, CH = Z::CH, RT = Z::RT, K2 = Z::K2, U = Z::U, UC = Z::UC, GR = Z::GR;
   constexpr int es = NT == 1 ? 2 : 4;
   constexpr bool TR = OUT && REV != DOT;       // dq and dk: states are [J][I] in memory, and shared heads' outputs are summed
@@ -549,7 +551,7 @@ __device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int 
           const auto terms_of = [&](int ks, int j) {
             const f32x4 u = S.t[2 * ks][j], v = S.t[2 * ks + 1][j];
             const float e[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
-            return split8<TO>(e);
+            return split8<kTerms>(e);
           };
           blocks_at(0);
           fence();
@@ -583,18 +585,18 @@ __device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int 
               const bool in = REV ? y + r >= x : y + r <= x;
               p[r] = s.scale * exp2_of(in ? e : -INFINITY) * (in || REV || DOT ? d[t][r] : 0.f);
             }
-            uint32_t p0[TO], p1[TO];
-            split2<TO>(p[0], p[1], p0);
-            split2<TO>(p[2], p[3], p1);
-            bh* to = P + (tx[t] * K2 + ty[t] / 2) * TO * 512 + (((ty[t] & 1) * 2 + lg / 2) * 16 + lr) * 8 + (lg & 1) * 4;
+            uint32_t p0[kTerms], p1[kTerms];
+            split2<kTerms>(p[0], p[1], p0);
+            split2<kTerms>(p[2], p[3], p1);
+            bh* to = P + (tx[t] * K2 + ty[t] / 2) * kTerms * 512 + (((ty[t] & 1) * 2 + lg / 2) * 16 + lr) * 8 + (lg & 1) * 4;
 #pragma unroll
-            for (int i2 = 0; i2 < TO; ++i2) *reinterpret_cast<uint2*>(to + i2 * 512) = make_uint2(p0[i2], p1[i2]);
+            for (int i2 = 0; i2 < kTerms; ++i2) *reinterpret_cast<uint2*>(to + i2 * 512) = make_uint2(p0[i2], p1[i2]);
           };
 #pragma unroll
           for (int x = 0; x < RT; ++x)
 #pragma unroll
             for (int j = 0; j < CT; ++j) o[x][j] = zero4();
-          Frag<TO> sf[2];
+          Frag<kTerms> sf[2];
           sf[0] = terms_of(0, 0);
           gates_at(0);
           constexpr int N = KS * CT, every = N > T ? N / T : 1;         // steps, and steps between P's blocks
@@ -605,7 +607,7 @@ __device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int 
             if (n + 1 < KS * CT) sf[(n + 1) % 2] = terms_of((n + 1) / CT, (n + 1) % CT);
             fence();
 #pragma unroll
-            for (int x = 0; x < RT; ++x) o[x][j] = mma<TO, NT>(sf[n % 2], af[ks % 2][x], o[x][j]);
+            for (int x = 0; x < RT; ++x) o[x][j] = mma<kTerms, NT>(sf[n % 2], af[ks % 2][x], o[x][j]);
             // T blocks over the KS * CT steps
 #pragma unroll
             for (int t = 0; t < T; ++t)
@@ -628,7 +630,7 @@ __device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int 
         // Columns of C, as they are and, times the decay up to the chunk's end, as they go into the state: formed between the
         // products of P C and of the state's update, whose operands are read a step ahead.
         Frag<NT> cf[K2][CT], bf[3];
-        Frag<TO> pf[2];
+        Frag<kTerms> pf[2];
         Frag<3> vf[2][CT];
         float decays[2][8];
         const uint32_t piece = lane % 4;
@@ -661,8 +663,8 @@ __device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int 
         const auto p_k2 = [](int n) { return RT == 4 ? (REV ? (n < 4 ? n % 2 : 1) : (n < 2 ? 0 : n % 2)) : 0; };
         const auto p_at = [&](int n) {
 #pragma unroll
-          for (int t = 0; t < TO; ++t)
-            pf[n % 2].t[t] = as_frag(*reinterpret_cast<const uint4*>(P + ((p_x(n) * K2 + p_k2(n)) * TO + t) * 512 + lane * 8));
+          for (int t = 0; t < kTerms; ++t)
+            pf[n % 2].t[t] = as_frag(*reinterpret_cast<const uint4*>(P + ((p_x(n) * K2 + p_k2(n)) * kTerms + t) * 512 + lane * 8));
         };
         const auto b_at = [&](int n) {          // step n: rows of tile n % (2 KS), tokens of half n / (2 KS)
           const int i2 = n % (2 * KS);
@@ -747,7 +749,7 @@ __device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int 
             if (n + 1 == PN) b_at(1);
             fence();
 #pragma unroll
-            for (int j = 0; j < CT; ++j) o[p_x(n)][j] = mma<NT, TO>(cf[p_k2(n)][j], pf[n % 2], o[p_x(n)][j]);
+            for (int j = 0; j < CT; ++j) o[p_x(n)][j] = mma<NT, kTerms>(cf[p_k2(n)][j], pf[n % 2], o[p_x(n)][j]);
 #pragma unroll
             for (int c = n * 4 * CT / PN; c < (n + 1) * 4 * CT / PN; ++c) columns_of(0, c / 4, c % 4);
             fence();
@@ -817,13 +819,13 @@ __device__ __forceinline__ void scan_item(const ScanArgs& s, uint32_t unit, int 
     }
 }
 
-template <int NT, int TO, int KS, int CT>
+template <int NT, int KS, int CT>
 __global__ __launch_bounds__(kScanThreads, 2) void linear_scan_kernel(ScanArgs s) {
-  __shared__ ScanSpace<NT, TO, KS, CT, true, false> z;
+  __shared__ ScanSpace<NT, KS, CT, true, false> z;
   const uint32_t blocks = scan_blocks(s);
   for (uint32_t block = blockIdx.x; block < blocks; block += gridDim.x) {
     const uint32_t group = block / 8 / (uint32_t)s.rep;
-    scan_item<NT, TO, KS, CT, false, true, false>(s, group * 8 + block % 8, block / 8 - group * s.rep, z);
+    scan_item<NT, KS, CT, false, true, false>(s, group * 8 + block % 8, block / 8 - group * s.rep, z);
   }
 }
 

@@ -518,7 +518,8 @@ gdn_status gdn_linear_workspace_size(const gdn_linear_problem* problem, int32_t 
 
 /* Packed sequences: cu_seqlens, slots, initial_state and final_state as in
  * gdn_packed_forward.  fp32 results (states, and outputs of that type) have the
- * accuracy of fp32 arithmetic, the range is that of bf16.  A NaN or infinity in
+ * accuracy of fp32 arithmetic, the range is that of bf16; a bf16 output is the
+ * fp32 output rounded once.  A NaN or infinity in
  * a token's q spoils that token's outputs; in its k or log_gate it does what the
  * recurrence makes of it; in its v it also reaches outputs of earlier tokens in
  * its chunk of 64 (0 times it is NaN), in its head and column.  Rows behind the

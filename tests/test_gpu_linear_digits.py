@@ -1,0 +1,71 @@
+"""GPU: digits of linear attention's results where few are left by cancellation
+or by strong decays."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def G():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import gated_delta_rule_frame_amd as G
+    return G
+
+
+def normal(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).cuda()
+
+
+def bounds(cu):
+    return torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cu,hk,hv,dk,dv", [([0, 1], 1, 1, 16, 16), ([0, 130, 130, 203], 2, 4, 112, 112), ([0, 700, 900], 1, 2, 64, 48),
+                                            ([0, 65, 1000], 2, 2, 128, 128)])
+def test_a_bf16_output_is_the_fp32_output_rounded_once(G, dtype, cu, hk, hv, dk, dv):
+    n = cu[-1]
+    x = [normal(1, n, hk, dk).to(dtype), normal(2, n, hk, dk).to(dtype), normal(3, n, hv, dv).to(dtype), -0.1 * normal(4, n, hv).abs()]
+    S0 = normal(5, len(cu) - 1, hv, dk, dv)
+    out, end = G.linear_forward(*x, bounds(cu), S0, scale=dk ** -0.5)
+    short, same = G.linear_forward(*x, bounds(cu), S0, scale=dk ** -0.5, out_dtype=BF16)
+    assert torch.equal(short, out.to(BF16)) and torch.equal(same, end)
+
+
+def test_dk_takes_the_states_gradient_in_24_bits(G):
+    """dk = R v of a single token, R the final state's gradient: two columns that cancel to 2^-14 of their values."""
+    h, d = 16, 64
+    r = 1 + torch.rand(h, d, generator=torch.Generator().manual_seed(1)).cuda()
+    R = torch.zeros(1, h, d, d, device="cuda")
+    R[0, :, :, 3] = r
+    R[0, :, :, 41] = 2.0 ** -14 * normal(2, h, d) - r
+    v = torch.zeros(1, h, d, dtype=BF16, device="cuda")
+    v[:, :, 3] = v[:, :, 41] = 1.0
+    z = torch.zeros_like(v)
+    dk = G.linear_backward(normal(3, 1, h, d).to(BF16), normal(4, 1, h, d).to(BF16), v, torch.full((1, h), -0.1, device="cuda"),
+                           bounds([0, 1]), z, None, R)[1][0].double()
+    want = R[0].double().sum(-1)
+    # six products of bf16 terms, exact, and their sums below 2: at most a step of 2^-23 each; then the result's half step
+    assert ((dk - want).abs() / (6 * 2.0 ** -23 + 2.0 ** -8 * want.abs())).max().item() <= 1
+
+
+def test_dk_takes_the_products_of_v_and_dout_in_24_bits(G):
+    """dk of the first of two tokens, without a decay: (v.do) q of both, equal but for 2^-15 of their values, with opposite q."""
+    h, d, n = 16, 16, 8
+    rnd = lambda seed: (1 + torch.randint(0, 128, (n, h), generator=torch.Generator().manual_seed(seed)) / 128).cuda()  # noqa: E731
+    v, do, q = (torch.zeros(2 * n, h, d, device="cuda") for _ in range(3))
+    v[0::2, :, 0], v[0::2, :, 9] = rnd(1), rnd(2) / 256
+    do[0::2, :, 0], do[0::2, :, 9] = rnd(3), rnd(4)
+    do[1::2, :, 0], do[1::2, :, 9] = do[0::2, :, 0], rnd(5)
+    sign = normal(6, n, h, d).sign()
+    q[0::2], q[1::2] = sign, -sign
+    x = [t.to(BF16) for t in (q, normal(7, 2 * n, h, d), v, do)]
+    assert all(torch.equal(t.float(), u) for t, u in zip((x[0], x[2], x[3]), (q, v, do)))
+    dk = G.linear_backward(*x[:3], torch.zeros(2 * n, h, device="cuda"), bounds(list(range(0, 2 * n + 1, 2))), x[3])[1][0::2].double()
+    P = (v[0::2].double() * (do[0::2].double() - do[1::2].double())).sum(-1)
+    want = P[..., None] * sign.double()
+    # the products are below 4 + 2^-6 and exact in 24 bits; six products of their terms, whose sums have at most a step of 2^-21 each
+    assert ((dk - want).abs() / (6 * 2.0 ** -21 + 2.0 ** -8 * want.abs())).max().item() <= 1
