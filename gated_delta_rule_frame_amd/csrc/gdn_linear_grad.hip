@@ -37,7 +37,7 @@ struct GateArgs {
 };
 
 // dlog_gate of a segment's tokens, D_t = <R, S> before token t, in fp64: <R, S> at the segment's end and the sums of x = q.dq -
-// v.dv behind each token.  The x are rounded independently (1e-7 of them), so the sums' error grows like a random walk to the
+// v.dv behind each token, both without what a token reads of itself.  The x are rounded independently (1e-7 of them), so the sums' error grows like a random walk to the
 // segment's start, where it shows: the sum is not the <R, S> of that place.  What it is off by is taken back along the way, by
 // the parts of the walk's variance behind each token (16384 tokens, 35 heads of 64 with a gate each, six inputs: errors of the
 // gates' gradients 1.0 to 3.4e-6 without, 0.6 to 2.2e-6 with it, 3.5 to 8.7e-7 in segments of 512).  The first gate of a sequence that starts from zeros scales nothing, and one

@@ -128,7 +128,9 @@ def linear_backward(q, k, v, log_gate, cu_seqlens, dout, initial_state=None, dfi
     The inputs are linear_forward's (without slots); dout: like v, dense;
     dfinal_state: like the final state, or None (zeros).  dq, dk and dv have
     q's dtype and are dense, the others are fp32; dlog_gate has log_gate's
-    shape; dinitial_state is None where initial_state is.  Rows behind the
+    shape, and an error of some 2^-22 of what the tokens behind a gate read from
+    earlier ones and give to later ones, so that a gate stronger than those by
+    e^-15 has no digits; dinitial_state is None where initial_state is.  Rows behind the
     last sequence are not written: for a padded batch give ``grads``, four
     tensors (dq, dk, dv, dlog_gate) to write into.
     """

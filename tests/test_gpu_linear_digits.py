@@ -69,3 +69,49 @@ def test_dk_takes_the_products_of_v_and_dout_in_24_bits(G):
     want = P[..., None] * sign.double()
     # the products are below 4 + 2^-6 and exact in 24 bits; six products of their terms, whose sums have at most a step of 2^-21 each
     assert ((dk - want).abs() / (6 * 2.0 ** -21 + 2.0 ** -8 * want.abs())).max().item() <= 1
+
+
+def gate_gradients(q, k, v, g, do, scale):
+    """In 64 bits, of one sequence from zeros with heads of their own: e^g <R, S before> of each token and head, by the states
+    themselves, and what its error goes by: the magnitudes of what each token reads from earlier ones and gives to later ones."""
+    n, h, d = v.shape
+    a, (Q, K, V, D) = torch.exp(g.double())[..., None, None], (t.double() for t in (q, k, v, do))
+    outer = lambda x, y: x[:, :, None] * y[:, None, :]  # noqa: E731
+    S = R = A = B = torch.zeros(h, q.shape[2], d, dtype=torch.float64, device="cuda")
+    before, dg, mag = [], torch.zeros(n, h, dtype=torch.float64, device="cuda"), torch.zeros(n, h, dtype=torch.float64, device="cuda")
+    for t in range(n):
+        before.append(S * a[t])
+        A = A * a[t]
+        mag[t] += (scale * outer(Q[t].abs(), D[t].abs()) * A).sum((-1, -2)).square()
+        S, A = before[-1] + outer(K[t], V[t]), A + outer(K[t].abs(), V[t].abs())
+    for t in reversed(range(n)):
+        mag[t] += (B * outer(K[t].abs(), V[t].abs())).sum((-1, -2)).square()
+        R, B = R + scale * outer(Q[t], D[t]), B + scale * outer(Q[t].abs(), D[t].abs())
+        dg[t] = (R * before[t]).sum((-1, -2))
+        R, B = R * a[t], B * a[t]
+    return dg, mag.flip(0).cumsum(0).flip(0)          # the squares of all tokens behind
+
+
+STRONG = [-0.05, -1.0, -4.0, -8.0, -12.0, -16.0, -30.0, -60.0]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,dk,dv", [(60, 16, 16), (1500, 64, 64), (700, 128, 48)])
+def test_gradients_of_strong_gates_have_digits(G, dtype, n, dk, dv):
+    """One gate for all tokens of a head, and gates of every strength side by side.  What a token reads from earlier ones and what it
+    gives to later ones have roundings of 2^-22 of their magnitudes in the 2-norm, independent ones, and a gate's gradient sums those
+    behind it.  What a token reads of itself is in neither."""
+    h, scale = len(STRONG), dk ** -0.5
+    q, k, v, do = ((normal(i, n, h, d) / (8 if i < 3 else 1)).to(dtype) for i, d in ((1, dk), (2, dk), (3, dv), (4, dv)))
+    g = torch.tensor(STRONG, device="cuda")
+    want, var = gate_gradients(q, k, v, g.expand(n, h), do, scale)
+    got = G.linear_backward(q, k, v, g.expand(n, h).contiguous(), bounds([0, n]), do, scale=scale)[3]
+    assert ((got.double() - want).norm(dim=0) / (2.0 ** -22 * var.sum(0).sqrt())).max().item() <= 1
+    assert ((got.double() - want).norm(dim=0) / want.norm(dim=0)).max().item() <= 1e-4
+    got = G.linear_backward(q, k, v, g, bounds([0, n]), do, scale=scale)[3]
+    # the sum over the tokens: a token's roundings count for every gate before it
+    assert ((got.double() - want.sum(0)).abs() / (2.0 ** -22 * var.sqrt().sum(0))).max().item() <= 1
+    mixed = -16 * torch.rand(n, h, generator=torch.Generator().manual_seed(9)).cuda() ** 3
+    want, var = gate_gradients(q, k, v, mixed, do, scale)
+    got = G.linear_backward(q, k, v, mixed, bounds([0, n]), do, scale=scale)[3]
+    assert ((got.double() - want).norm(dim=0) / (2.0 ** -22 * var.sum(0).sqrt())).max().item() <= 1
