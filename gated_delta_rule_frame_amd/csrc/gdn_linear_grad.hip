@@ -8,7 +8,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr float kNoGate = -104.f;             // exp of less is 0 in fp32
+constexpr float kNoGate = -103.97207641601562f;   // exp of less rounds to 0 in fp32: it is below 2^-150, half of the smallest value
 
 // The sums of x and y over the workgroup, in every lane; `red`: four pairs.
 __device__ __forceinline__ double2 block_sum(double x, double y, double2* red) {

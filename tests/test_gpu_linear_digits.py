@@ -115,3 +115,22 @@ def test_gradients_of_strong_gates_have_digits(G, dtype, n, dk, dv):
     want, var = gate_gradients(q, k, v, mixed, do, scale)
     got = G.linear_backward(q, k, v, mixed, bounds([0, n]), do, scale=scale)[3]
     assert ((got.double() - want).norm(dim=0) / (2.0 ** -22 * var.sum(0).sqrt())).max().item() <= 1
+
+
+@pytest.mark.parametrize("fixed", [False, True])
+def test_gates_whose_exponential_rounds_to_0_have_no_gradient(G, fixed):
+    """In fp32, e^g is 0 at g = -103.972084 and below, its smallest value at -103.972076: 150 ln 2 lies between."""
+    n, d = 200, 32
+    low = [-103.98, -103.97208404541016, -103.9721, -104.0]
+    assert (torch.exp(torch.tensor(low, dtype=torch.float64)).float() == 0).all()
+    assert torch.exp(torch.tensor(-103.97207641601562, dtype=torch.float64)).float() > 0
+    x = [normal(i, n, 2, d) for i in (1, 2, 3)]
+    S0, dS = normal(4, 1, 2, d, d), normal(5, 1, 2, d, d)
+    for i, g in enumerate(low):
+        gates = torch.full((n, 2), -0.05, device="cuda")
+        gates[10 + 45 * i, 1] = g
+        if fixed:
+            gates = torch.tensor([-0.05, g], device="cuda")
+        dg = G.linear_backward(*x, gates, bounds([0, n]), x[2] + 1, S0, dS)[3]
+        assert (dg[1] if fixed else dg[10 + 45 * i, 1]).item() == 0
+        assert torch.count_nonzero(dg).item() == dg.numel() - 1
