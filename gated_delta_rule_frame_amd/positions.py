@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import functools
 import math
+import operator
 
 import torch
 
@@ -46,7 +47,7 @@ def rotary_frequencies(width, base=10000.0, *, scaling="none", factor=1.0, train
     if scaling == "linear":
         f = f / factor
     if scaling == "yarn":
-        if trained is None or trained < 1 or not 0 <= slow < fast:
+        if trained is None or not 1 <= trained < math.inf or not 0 <= slow < fast:
             raise ValueError(f"yarn needs trained >= 1 and 0 <= slow < fast (got {trained}, {slow}, {fast})")
         keep = ((trained * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
         f = f * (keep + (1 - keep) / factor)
@@ -61,6 +62,14 @@ def _problem(*fields):
     p = RotaryProblem(ABI_VERSION, *rest[:9], sections + (0,) * (4 - len(sections)), rest[9])
     p.q_stride, p.k_stride, p.q_out_stride, p.k_out_stride = rest[10:]
     return p
+
+
+def _sections(sections, pairs):
+    """The numbers of pairs of the axes."""
+    parts = (pairs,) if sections is None else tuple(operator.index(s) for s in sections)
+    if not 1 <= len(parts) <= 4 or min(parts) < 0 or sum(parts) != pairs:
+        raise ValueError(f"sections must be one to four numbers >= 0, {pairs} in all (got {parts})")
+    return parts
 
 
 def _turn(q, k, positions, frequencies, layout, magnitude, sections, out, inverse):
@@ -84,9 +93,7 @@ def _turn(q, k, positions, frequencies, layout, magnitude, sections, out, invers
         raise ValueError(f"frequencies must be a tensor of at most width / 2 = {width // 2} values")
     _dense("frequencies", frequencies, frequencies.shape, torch.float64, device)
     pairs = frequencies.shape[0]
-    parts = (pairs,) if sections is None else tuple(int(s) for s in sections)
-    if not 1 <= len(parts) <= 4 or min(parts) < 0 or sum(parts) != pairs:
-        raise ValueError(f"sections must be one to four numbers >= 0, {pairs} in all (got {parts})")
+    parts = _sections(sections, pairs)
     _dense("positions", positions, (n,) if sections is None else (n, len(parts)), torch.int32, device)
     if out is None:
         out = (None, None)

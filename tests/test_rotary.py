@@ -83,3 +83,18 @@ def test_cpu_tensors_are_refused():
     q = torch.zeros(4, 2, 64)
     with pytest.raises(ValueError):
         G.rotary(q, None, torch.zeros(4, dtype=torch.int32), G.rotary_frequencies(64, device="cpu")[0])
+
+
+def test_host_arguments_that_are_no_numbers_are_refused():
+    """Sections are counts: halves are not cut off.  A context of NaN positions has no frequencies."""
+    from gated_delta_rule_frame_amd import positions as P
+    assert P._sections((8, 0, 4), 12) == (8, 0, 4) and P._sections(None, 12) == (12,)
+    for bad in ((8.5, 4.5), (8, 4.0), ("8", 4), (8, None), 12):
+        with pytest.raises(TypeError):
+            P._sections(bad, 12)
+    for bad in ((), (8, 5), (13, -1), (4, 4, 2, 1, 1)):
+        with pytest.raises(ValueError):
+            P._sections(bad, 12)
+    for trained in (math.nan, math.inf):
+        with pytest.raises(ValueError):
+            G.rotary_frequencies(64, scaling="yarn", factor=4.0, trained=trained, device="cpu")
