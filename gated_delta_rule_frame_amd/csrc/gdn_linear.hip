@@ -121,13 +121,15 @@ size_t carve(char** at, char* base, size_t* bytes, size_t n) {
 // a state, four times, and a start of some chunks' time: so there are about as many (segment, head) pairs as workgroups run at
 // once (LDS and registers: two a CU, three where no width is above 64, forward and bf16), with half a segment more for each
 // sequence's last one, or twice as many and so on where the sequences alone are that many.  Prompts of 8191 tokens in 13,
-// 32 heads of 128: 180 us at 256 tokens a segment, 156 at 512, 148 at 768, 154 at 1024; gradients of 8192 in 6: 568, 510, 548,
-// 559; one document of 32768, 35 heads of 64: 265 at 512, 265 at 1024, 246 at 1536, 268 at 2048, 321 at 4096.
-// One workgroup alone takes 5 us for a chunk of 64 tokens, which bounds short calls: 880 tokens in 3 of fp32, 20 heads of 112
-// (gradients): 91 us at 128 tokens a segment, 117 at 256, 123 at 512; but up to 384 tokens the two launches more cost more
-// (203 tokens: 18 us in one, 28 at 128).
+// 32 heads of 128: 188 us at 256 tokens a segment, 170 at 512, 157 at 768, 167 at 1024, 152 to 159 as here; gradients of 8192 in 6:
+// 608, 538, 565, 583, 505; one document of 32768, 35 heads of 64: 281 at 512, 280 at 1024, 264 at 1536, 287 at 2048, 346 at 4096,
+// 243 as here.  One workgroup alone takes 7 us for a chunk of 64 tokens, which bounds short calls: 880 tokens in 3 of fp32, 20 heads
+// of 112 (gradients): 94 us at 128 tokens a segment, 121 at 256, 128 at 512; but up to 384 tokens the two launches more cost more
+// (203 tokens: 20 us in one, 30 at 128).  Heads are counted by the value: where many share a key head, whose workgroups sum them
+// one after another in the gradients, there are too few of those (8000 tokens, 32 heads of 64: 191 us with as many key heads, 230
+// with 16, 383 with 4, 1122 with one).
 // The errors of gates' gradients grow with a segment (linear_gates_kernel), those of one gate a head twice over: their
-// segments end at 1536 and 512 tokens (16384 tokens, 35 heads of 64 with a gate each: 390 us at 512, 370 at 1536).
+// segments end at 1536 and 512 tokens (16384 tokens, 35 heads of 64 with a gate each: 409 us at 512, 394 at 1536).
 LinearPlan linear_plan(const LinearProblem& p, bool grad) {
   const bool wide = p.dk > 64 || p.dv > 64;
   const double at_once = 256.0 * (wide || grad || !p.in_bf16 ? 2 : 3), each = at_once / p.hv, half = 0.5 * p.sequences;

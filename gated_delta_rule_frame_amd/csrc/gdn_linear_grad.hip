@@ -40,7 +40,7 @@ struct GateArgs {
 // v.dv behind each token, both without what a token reads of itself.  The x are rounded independently (1e-7 of them), so the sums' error grows like a random walk to the
 // segment's start, where it shows: the sum is not the <R, S> of that place.  What it is off by is taken back along the way, by
 // the parts of the walk's variance behind each token (16384 tokens, 35 heads of 64 with a gate each, six inputs: errors of the
-// gates' gradients 1.0 to 3.4e-6 without, 0.6 to 2.2e-6 with it, 3.5 to 8.7e-7 in segments of 512).  The first gate of a sequence that starts from zeros scales nothing, and one
+// gates' gradients 0.6 to 4.5e-6 without, 0.7 to 2.1e-6 with it, 2.3 to 9.1e-7 in segments of 512, 3.4e-7 to 1.7e-6 there without).  The first gate of a sequence that starts from zeros scales nothing, and one
 // whose exponential is 0 in fp32 (-inf, a mask's lowest value) drops what it scales: their gradients are 0, not what the
 // sums' roundings leave.
 __global__ __launch_bounds__(kThreads) void linear_gates_kernel(ScanArgs s, GateArgs a, int cell) {
@@ -136,9 +136,10 @@ struct GradArgs {
 
 // dq, dk and dv in one launch: a unit's workgroups (of a segment and key head) one after another on one XCD, as they read the
 // same rows; those that sum over value heads, the longest, first (three launches, and every value head's dq and dk summed
-// afterwards: 507 us a call against 474 for 8192 tokens in 6, 16 and 32 heads of 128; fp32, 880 in 3, 148 against 89).  That call
-// spends 390 us here, 1.14 GB at 2.9 TB/s: operands three times, the sums over value heads in fp32 out and back, 36 spilled
-// registers; 16384 tokens of 35 heads of 64 272 us, 880 of fp32 48.  KSK, CTK and KSV, CTV: by_width of d_k and d_v.
+// afterwards: 507 us a call against 474 for 8192 tokens in 6, 16 and 32 heads of 128; fp32, 880 in 3, 148 against 89; both with
+// two-term states).  That call spends 412 to 438 us here, 1.18 GB at 2.7 TB/s: operands three times, the sums over value heads in
+// fp32 out and back, 61 spilled vector and 300 scalar registers; 16384 tokens of 35 heads of 64 282 to 312 us, 880 of fp32 50.
+// KSK, CTK and KSV, CTV: by_width of d_k and d_v.
 template <int NT, int KSK, int CTK, int KSV, int CTV>
 __global__ __launch_bounds__(kScanThreads, 2) void linear_grad_kernel(GradArgs g) {
   using Q = ScanSpace<NT, KSV, CTK, true, true>;

@@ -32,12 +32,12 @@
 // LDS once (the next chunk's are in flight meanwhile); P = A B^T, gated and split,
 // passes through LDS to the wavefronts' columns.  fp32 values are three bf16 terms,
 // products six of the nine term products.  What bounds it: with d = 128 and bf16
-// a wavefront has 196 matrix instructions of 16 clocks a chunk.  A chunk takes 6 us
-// for a workgroup alone on a CU and 8.4 for two (16 sequences of 2048 tokens, 32
-// heads: 292 us), of which the matrix instructions would take 3.7 at 1.7 GHz: the rest
+// a wavefront has 240 matrix instructions of 16 clocks a chunk.  A chunk takes 6.9 us
+// for a workgroup alone on a CU and 9.6 for two (16 sequences of 2048 tokens, 32
+// heads: 338 us), of which the matrix instructions would take 4.5 at 1.7 GHz: the rest
 // is the splitting of the state and of P, of which a matrix instruction hides two
 // instructions, and the waits at the chunk's three barriers.  8191 tokens of 32 heads
-// in segments: 99 to 104 us, 2.7 TB/s; 32768 of 35 heads of 64: 150 to 173, 3.5 to 4.
+// in segments: 113 to 120 us, 2.5 TB/s; 32768 of 35 heads of 64: 159 to 201, 3 to 3.8.
 #pragma once
 
 #include <type_traits>
@@ -262,8 +262,8 @@ __device__ __forceinline__ bool find_segment(const int* cu, int sequences, long 
 }
 
 // The segment that a scan's workgroups take `at`-th: where they are more than run at once the longest first, so that the last
-// to start are short ones (13 prompts of 35 to 1881 tokens, 32 heads of 128: sums 51 -> 43 us, scan 102 -> 99; the order itself
-// costs a workgroup a microsecond).  More than 64 sequences even out by themselves and keep their order.
+// to start are short ones (13 prompts of 35 to 1881 tokens, 32 heads of 128: states 47 -> 39 us, scan 122 -> 120; the order itself
+// costs a workgroup a microsecond, and 6 training sequences of 762 to 2716 have 464 -> 490 us with it).  More than 64 sequences even out by themselves and keep their order.
 __device__ __forceinline__ bool find_in_order(const int* cu, int sequences, long long tokens, int L, bool several, int at,
                                               Segment* s) {
   if (!several || sequences == 1 || sequences > 64) return find_segment(cu, sequences, tokens, L, at, s);

@@ -71,7 +71,8 @@ struct Vec {                                   // 16 bytes of values
   }
 };
 
-// LAYOUT 0: halves with whole vectors of pairs (pairs a multiple of 16 bytes' values); 1: neighbours; 2: halves, pair by pair.
+// LAYOUT 0: halves with whole vectors of pairs (pairs a multiple of 16 bytes' values); 1: neighbours; 2: halves, pair by pair (16384
+// tokens of 48 heads of 128, bf16: 120 components turned 234 us, 128 in LAYOUT 0 78; fp32, 126 turned 242, 120 in LAYOUT 0 162).
 template <bool BF16, int LAYOUT, int TT>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(
     const void* q, const void* k, const int* __restrict__ positions, const double* __restrict__ frequencies, void* qo,
@@ -164,6 +165,7 @@ void go(const RotaryProblem& p, const void* q, const void* k, const int* positio
   // Four tokens a workgroup where there are enough of them to fill the card, so that a wavefront has several angles and more
   // loads in flight: 106480 tokens of 40 heads of 112 414 us at one, 381 at two, 371 at four, 385 at eight; 8192 of 10 heads of 64
   // 14.6, 12.6, 9.8, 9.8; 4096 of 48 heads of 128 20.6, 20.4, 20.7, 23.3; but 2048 14.5, 13.1, 15.0, 19.9 and 48 6.3, 8.0, 10.2, 16.0.
+  // Four tokens of narrow rows leave most lanes idle: a million of 2 heads of 16 255 us, 0.5 TB/s; 250000 of 3 heads of 64 80, 2.4.
   if (p.tokens >= 4096) launch(rotary_kernel<BF16, LAYOUT, 4>, 4);
   else launch(rotary_kernel<BF16, LAYOUT, 1>, 1);
 }

@@ -90,7 +90,8 @@ def linear_forward(q, k, v, log_gate, cu_seqlens, initial_state=None, *, slots=N
     [heads_v], one decay for each head.  cu_seqlens, slots, states and outputs
     are ``packed_forward``'s.  A NaN or infinity in v can make outputs of up to 63
     earlier tokens of its sequence NaN (those in its chunk of 64), in its head and
-    column; in k or log_gate it reaches later tokens alone.
+    column; in k or log_gate it reaches its own and later tokens alone.  An
+    infinity may come out as a NaN (``linear_decode`` keeps it).
     """
     odt = _output(out, out_dtype)
     seqs, rows = _sequences(cu_seqlens, q), 0
@@ -125,7 +126,9 @@ def linear_backward(q, k, v, log_gate, cu_seqlens, dout, initial_state=None, dfi
                     workspace=None):
     """Gradients of ``linear_forward`` (gdn_linear_backward); returns (dq, dk, dv, dlog_gate, dinitial_state).
 
-    The inputs are linear_forward's (without slots); dout: like v, dense;
+    The inputs are linear_forward's (without slots); dout: like v, dense, in
+    its dtype (with bf16 inputs ask linear_forward for ``out_dtype`` bf16, or
+    round the gradient of its fp32 output);
     dfinal_state: like the final state, or None (zeros).  dq, dk and dv have
     q's dtype and are dense, the others are fp32; dlog_gate has log_gate's
     shape, and an error of some 2^-22 of what the tokens behind a gate read from

@@ -305,8 +305,8 @@ enum {
   GDN_KERNEL_PACKED_GRADS = 15,     /* packed gradients: every chunk's gradients of its inputs */
   GDN_KERNEL_LINEAR_DECODE = 16,    /* linear attention: one token per row */
   GDN_KERNEL_LINEAR_STATES = 17,    /* linear attention: the states between segments (all launches) */
-  GDN_KERNEL_LINEAR_SCAN = 18,      /* linear attention: outputs, or gradients of q, k and v (all launches) */
-  GDN_KERNEL_LINEAR_GATES = 19,     /* linear attention: gradients of gates, sums over shared heads (all launches) */
+  GDN_KERNEL_LINEAR_SCAN = 18,      /* linear attention: outputs, or gradients of q, k and v with the sums over shared heads */
+  GDN_KERNEL_LINEAR_GATES = 19,     /* linear attention: gradients of gates (all launches) */
   GDN_KERNEL_ROTARY = 20,           /* rotary positions and their gradients */
   GDN_KERNEL_COUNT = 21
 };
@@ -519,12 +519,13 @@ gdn_status gdn_linear_workspace_size(const gdn_linear_problem* problem, int32_t 
 /* Packed sequences: cu_seqlens, slots, initial_state and final_state as in
  * gdn_packed_forward.  fp32 results (states, and outputs of that type) have the
  * accuracy of fp32 arithmetic, the range is that of bf16; a bf16 output is the
- * fp32 output rounded once.  A NaN or infinity in
- * a token's q spoils that token's outputs; in its k or log_gate it does what the
- * recurrence makes of it; in its v it also reaches outputs of earlier tokens in
- * its chunk of 64 (0 times it is NaN), in its head and column.  Rows behind the
- * last sequence are neither read nor written.  No aliasing but of initial_state
- * with final_state.  The workspace is as gdn_forward's. */
+ * fp32 output rounded once.  A NaN or infinity in a token's q spoils that token's
+ * outputs; in its k or log_gate those of that token and of later ones, with their
+ * states; in its v also those of earlier tokens in its chunk of 64 (0 times it is
+ * NaN), in its head and column.  What the recurrence and gdn_linear_decode make an
+ * infinity, of a value or of a state, may be a NaN here.  Rows behind the last
+ * sequence are neither read nor written.  No aliasing but of initial_state with
+ * final_state.  The workspace is as gdn_forward's. */
 gdn_status gdn_linear_forward(const gdn_linear_problem* problem,
                               const void* q, const void* k, const void* v, const float* log_gate,
                               const int32_t* cu_seqlens, const int32_t* slots,
@@ -533,7 +534,8 @@ gdn_status gdn_linear_forward(const gdn_linear_problem* problem,
 
 /* Gradients of sum(out dout) + sum(final_state dfinal_state) for every input,
  * from the inputs alone; the arguments are gdn_packed_backward's without beta.
- * dlog_gate has log_gate's shape; with gate_per_head it sums over all tokens of
+ * dout has qkv_dtype, whatever the outputs' type was: the gradient of an fp32
+ * output of bf16 inputs is rounded by the caller.  dlog_gate has log_gate's shape; with gate_per_head it sums over all tokens of
  * all sequences; it is 0 where exp(log_gate) is 0 in fp32.  It is formed from sums
  * over the tokens behind a gate, of what each reads from earlier tokens and gives
  * to later ones: its error is some 2^-22 of their decayed size (root of the sum of
