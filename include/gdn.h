@@ -535,15 +535,16 @@ gdn_status gdn_linear_forward(const gdn_linear_problem* problem,
 /* Gradients of sum(out dout) + sum(final_state dfinal_state) for every input,
  * from the inputs alone; the arguments are gdn_packed_backward's without beta.
  * dout has qkv_dtype, whatever the outputs' type was: the gradient of an fp32
- * output of bf16 inputs is rounded by the caller.  dlog_gate has log_gate's shape; with gate_per_head it sums over all tokens of
- * all sequences; it is 0 where exp(log_gate) is 0 in fp32.  It is formed from sums
- * over the tokens behind a gate, of what each reads from earlier tokens and gives
- * to later ones: its error is some 2^-22 of their decayed size (root of the sum of
- * squares), so a gate that is far stronger than those behind it, by e^-15 or more,
- * has no digits of its own, while heads that decay strongly all along have theirs.
- * No atomics: every run gives the same bits.  A NaN or infinity may spoil every
- * gradient of its sequence in the value heads that read it, and what is summed over
- * them; other sequences are as without it (a dlog_gate of [heads_v] sums them all).
+ * output of bf16 inputs is rounded by the caller.  dlog_gate has log_gate's shape;
+ * with gate_per_head it sums over all tokens of all sequences; it is 0 where
+ * exp(log_gate) is 0 in fp32.  It is formed from sums over the tokens behind a gate,
+ * of what each reads from earlier tokens and gives to later ones: its error is some
+ * 2^-22 of their decayed size (root of the sum of squares), so a gate that is far
+ * stronger than those behind it, by e^-15 or more, has no digits of its own, while
+ * heads that decay strongly all along have theirs.  No atomics: every run gives the
+ * same bits.  A NaN or infinity may spoil every gradient of its sequence in the
+ * value heads that read it, and what is summed over them; other sequences are as
+ * without it (a dlog_gate of [heads_v] sums them all).
  * No aliasing. */
 gdn_status gdn_linear_backward(const gdn_linear_problem* problem,
                                const void* q, const void* k, const void* v, const float* log_gate,
